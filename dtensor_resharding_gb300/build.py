@@ -11,6 +11,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB_PATH = os.path.join(HERE, "libreshard.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
+UNITS = ("execute", "route", "quantize", "product_fp8", "experts")   # CUDA translation units, compiled side by side
 
 
 def _nvcc() -> str:
@@ -42,11 +43,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags: List[str] = (
     os.makedirs(bdir, exist_ok=True)
     nvcc = _nvcc()
     common = ["-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
-    jobs = [
-        [nvcc, *common, *extra, "-x", "c++", "-c", os.path.join(CSRC, "plan.cpp"), "-o", os.path.join(bdir, "plan.o")],
-        [nvcc, *common, *ARCH, "-lineinfo", "-Xptxas", "-v" if verbose else "-O3", *extra,
-         "-c", os.path.join(CSRC, "execute.cu"), "-o", os.path.join(bdir, "execute.o")],
-    ]
+    jobs = [[nvcc, *common, *extra, "-x", "c++", "-c", os.path.join(CSRC, "plan.cpp"), "-o", os.path.join(bdir, "plan.o")]]
+    jobs += [[nvcc, *common, *ARCH, "-lineinfo", "-Xptxas", "-v" if verbose else "-O3", *extra,
+              "-c", os.path.join(CSRC, f"{unit}.cu"), "-o", os.path.join(bdir, f"{unit}.o")] for unit in UNITS]
     procs = [subprocess.Popen(j, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for j in jobs]
     logs = []
     for j, p in zip(jobs, procs):
@@ -55,7 +54,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: List[str] = (
         if p.returncode:
             raise RuntimeError(f"build failed: {' '.join(j)}\n{log}")
     tmp = out + f".tmp{os.getpid()}"
-    link = [nvcc, "-shared", *ARCH, os.path.join(bdir, "plan.o"), os.path.join(bdir, "execute.o"), "-o", tmp]
+    link = [nvcc, "-shared", *ARCH, *(os.path.join(bdir, f"{unit}.o") for unit in ("plan", *UNITS)), "-o", tmp]
     r = subprocess.run(link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
     if r.returncode:
         raise RuntimeError(f"link failed: {' '.join(link)}\n{r.stdout}")

@@ -1,0 +1,214 @@
+// The calls that put the operator kernels together: the product alone, with its rows' quantization, and the routed
+// expert feed-forward. Host code only; everything is enqueued on the caller's stream in the caller's workspace.
+#include <algorithm>
+
+#include "ops_common.cuh"
+
+namespace reshard {
+namespace ops {
+
+void Checks::pointer(const void *p, const char *name, uintptr_t align) {
+  if (!p) return add(true, RESHARD_ERR_INVALID_ARG, std::string(name) + " is NULL");
+  if (reinterpret_cast<uintptr_t>(p) % align)
+    return add(true, RESHARD_ERR_INVALID_ARG, std::string(name) + " is not aligned to " + std::to_string(align) + " bytes");
+  cudaPointerAttributes a{};
+  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return add(true, RESHARD_ERR_INVALID_ARG, std::string(name) + " is not a pointer the device can dereference");
+  }
+  if (a.type == cudaMemoryTypeUnregistered) return add(true, RESHARD_ERR_INVALID_ARG, std::string(name) + " is pageable host memory");
+  if (a.type == cudaMemoryTypeDevice) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) == cudaSuccess && a.device != dev)
+      add(true, RESHARD_ERR_INVALID_ARG, std::string(name) + " is memory of device " + std::to_string(a.device));
+  }
+}
+
+int device_sms(int *sms) {
+  static thread_local int dev_seen = -1, seen = 0;
+  int dev = 0;
+  OPS_CUDA(cudaGetDevice(&dev));
+  if (dev != dev_seen) {
+    OPS_CUDA(cudaDeviceGetAttribute(&seen, cudaDevAttrMultiProcessorCount, dev));
+    dev_seen = dev;
+  }
+  *sms = seen;
+  return RESHARD_OK;
+}
+
+namespace {
+
+constexpr int64_t kAlign = 256;
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+int64_t blocks_of(int64_t v) { return (v + kScaleBlock - 1) / kScaleBlock; }
+
+// Quantized rows in a workspace: values at a 16-byte pitch, scales block by block (a block's rows side by side, so that
+// the product's threads, one a row, read them in one line).
+struct QuantizedRows {
+  int64_t pitch, values, scales;
+  QuantizedRows(int64_t rows, int64_t cols) : pitch(up(cols, 16)), values(up(rows * pitch, kAlign)), scales(up(rows * blocks_of(cols) * 4, kAlign)) {}
+  int64_t bytes() const { return values + scales; }
+};
+
+struct ExpertLayout {
+  int64_t slots, offsets, order, position, y;
+  QuantizedRows x, h;
+  ExpertLayout(int64_t tokens, int k, int experts, int64_t hidden, int64_t ffn, int dtype)
+      : slots(tokens * k), offsets(up(4 * (experts + 1), kAlign)), order(up(4 * slots, kAlign)), position(order),
+        y(up(slots * up(hidden, 16) * element_bytes(dtype), kAlign)), x(slots, hidden), h(slots, ffn) {}
+  int64_t bytes() const { return offsets + order + position + y + x.bytes() + h.bytes(); }
+};
+
+void check_weight(Checks &c, const void *w, int64_t batch, int64_t batch_stride, int64_t rows, int64_t cols, int64_t stride, const char *name) {
+  c.pointer(w, name, 16);
+  c.invalid(stride < cols, "a weight row stride is shorter than the row");
+  c.unsupported(stride % 16 != 0, "a weight row stride is not a multiple of 16 bytes (lay the rows out with a padded pitch)");
+  if (batch > 1) {
+    c.invalid(batch_stride < (rows - 1) * stride + cols, "weight matrices overlap");
+    c.unsupported(batch_stride % 16 != 0, "a weight batch stride is not a multiple of 16 bytes");
+  }
+}
+
+// The batch stride a tensor map takes where there is one matrix only.
+int64_t map_batch(int64_t batch, int64_t batch_stride, int64_t rows, int64_t stride) { return batch > 1 ? batch_stride : rows * stride; }
+
+}  // namespace
+}  // namespace ops
+}  // namespace reshard
+
+using namespace reshard;
+using namespace reshard::ops;
+
+extern "C" int reshard_matmul_fp8(const void *a, int64_t a_stride, const float *a_scale, int64_t a_scale_row, int64_t a_scale_block,
+                                  const void *w, int64_t w_batch_stride, int64_t w_stride, const float *w_scale, const int32_t *offsets,
+                                  int groups, int64_t m, int64_t n, int64_t k, void *out, int out_dtype, int64_t out_stride,
+                                  reshard_stream_t stream) {
+  Checks c("reshard_matmul_fp8");
+  c.invalid(m < 0 || n < 0 || k < 1, "m and n must be >= 0 and k >= 1");
+  c.unsupported(m > RESHARD_MAX_EXTENT || n > RESHARD_MAX_EXTENT || k > RESHARD_MAX_EXTENT, "m, n or k above 2^30");
+  c.invalid(groups < 1 || (!offsets && groups != 1), "groups must be >= 1, and 1 without offsets");
+  c.unsupported(groups > RESHARD_MAX_GROUPS, "more than 512 groups");
+  c.invalid(!element_bytes(out_dtype), "out_dtype must be BF16, F16 or F32");
+  c.invalid(a_stride < k || out_stride < n, "a row stride is shorter than the row");
+  c.unsupported(a_stride % 16 != 0, "a's row stride is not a multiple of 16 bytes");
+  c.invalid(a_scale_row < 1 || a_scale_block < 1, "scale strides must be positive");
+  if (m > 0 && n > 0 && c.ok()) {
+    c.pointer(a, "a", 16);
+    c.pointer(a_scale, "a_scale", 4);
+    check_weight(c, w, groups, w_batch_stride, n, k, w_stride, "w");
+    c.pointer(w_scale, "w_scale", 4);
+    if (offsets) c.pointer(offsets, "offsets", 4);
+    c.pointer(out, "out", (uintptr_t)element_bytes(out_dtype));
+  }
+  if (!c.ok()) return c.report();
+  if (m == 0 || n == 0) return RESHARD_OK;
+  Product p{};
+  p.a = static_cast<const uint8_t *>(a), p.a_stride = a_stride, p.a_scale = a_scale, p.as_row = a_scale_row, p.as_block = a_scale_block;
+  p.w = static_cast<const uint8_t *>(w), p.w_batch = map_batch(groups, w_batch_stride, n, w_stride), p.w_stride = w_stride, p.w_scale = w_scale;
+  p.offsets = offsets, p.groups = groups, p.m = m, p.n = n, p.k = k;
+  p.out = out, p.out_dtype = out_dtype, p.out_stride = out_stride;
+  return enqueue_product(p, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" int64_t reshard_linear_fp8_workspace(int64_t m, int64_t k) { return m < 0 || k < 0 ? 0 : QuantizedRows(m, k).bytes(); }
+
+extern "C" int reshard_linear_fp8(const void *x, int dtype, int64_t m, int64_t k, int64_t row_stride, const void *w, int64_t w_stride,
+                                  const float *w_scale, int64_t n, void *out, int64_t out_stride, void *workspace, int64_t workspace_bytes,
+                                  reshard_stream_t stream_) {
+  Checks c("reshard_linear_fp8");
+  c.invalid(m < 0 || n < 0 || k < 1, "m and n must be >= 0 and k >= 1");
+  c.unsupported(m > RESHARD_MAX_EXTENT || n > RESHARD_MAX_EXTENT || k > RESHARD_MAX_EXTENT, "m, n or k above 2^30");
+  c.invalid(!element_bytes(dtype), "dtype must be BF16, F16 or F32");
+  c.invalid(row_stride < k || out_stride < n, "a row stride is shorter than the row");
+  if (m > 0 && n > 0 && c.ok()) {
+    c.pointer(x, "x", (uintptr_t)element_bytes(dtype));
+    check_weight(c, w, 1, 0, n, k, w_stride, "w");
+    c.pointer(w_scale, "w_scale", 4);
+    c.pointer(out, "out", (uintptr_t)element_bytes(dtype));
+    c.pointer(workspace, "workspace", kAlign);
+    c.invalid(workspace_bytes < reshard_linear_fp8_workspace(m, k), "the workspace is smaller than reshard_linear_fp8_workspace");
+  }
+  if (!c.ok()) return c.report();
+  if (m == 0 || n == 0) return RESHARD_OK;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const QuantizedRows l(m, k);
+  uint8_t *q = static_cast<uint8_t *>(workspace);
+  float *scale = reinterpret_cast<float *>(q + l.values);
+  Rows r{x, dtype, m, k, row_stride, q, l.pitch, scale, 1, m};
+  int rc = enqueue_quantize_rows(r, stream);
+  if (rc) return rc;
+  Product p{};
+  p.a = q, p.a_stride = l.pitch, p.a_scale = scale, p.as_row = 1, p.as_block = m;
+  p.w = static_cast<const uint8_t *>(w), p.w_batch = n * w_stride, p.w_stride = w_stride, p.w_scale = w_scale;
+  p.m = m, p.n = n, p.k = k;
+  p.out = out, p.out_dtype = dtype, p.out_stride = out_stride;
+  return enqueue_product(p, stream);
+}
+
+extern "C" int64_t reshard_experts_fp8_workspace(int64_t tokens, int k, int experts, int64_t hidden, int64_t ffn, int dtype) {
+  if (tokens < 0 || k < 1 || experts < 1 || hidden < 0 || ffn < 0 || !element_bytes(dtype)) return 0;
+  return ExpertLayout(tokens, k, experts, hidden, ffn, dtype).bytes();
+}
+
+extern "C" int reshard_experts_fp8(const void *x, int dtype, int64_t tokens, int64_t hidden, int64_t row_stride, const int32_t *ids,
+                                   const float *weights, int k, int first_expert, int experts, int64_t ffn, const void *w13,
+                                   int64_t w13_batch_stride, int64_t w13_stride, const float *w13_scale, const void *w2,
+                                   int64_t w2_batch_stride, int64_t w2_stride, const float *w2_scale, void *out, int64_t out_stride,
+                                   void *workspace, int64_t workspace_bytes, reshard_stream_t stream_) {
+  Checks c("reshard_experts_fp8");
+  c.invalid(tokens < 0 || hidden < 1 || ffn < 1 || k < 1, "tokens must be >= 0, hidden, ffn and k >= 1");
+  c.invalid(first_expert < 0 || experts < 1, "first_expert must be >= 0 and experts >= 1");
+  c.unsupported(experts > RESHARD_MAX_GROUPS, "more than 512 experts on this side");
+  c.unsupported(tokens > RESHARD_MAX_EXTENT || hidden > RESHARD_MAX_EXTENT / 2 || ffn > RESHARD_MAX_EXTENT / 2, "tokens, hidden or ffn above 2^29");
+  if (c.ok()) c.unsupported(tokens * k > RESHARD_MAX_SLOTS, "more than 2^30 slots");
+  c.unsupported(ffn % kScaleBlock != 0, "ffn is not a multiple of 128: a scale block would hold gate and up rows");
+  c.invalid(!element_bytes(dtype), "dtype must be BF16, F16 or F32");
+  c.invalid(row_stride < hidden || out_stride < hidden, "a row stride is shorter than the row");
+  if (tokens > 0 && c.ok()) {
+    c.pointer(x, "x", (uintptr_t)element_bytes(dtype));
+    c.pointer(ids, "ids", 4);
+    c.pointer(weights, "weights", 4);
+    check_weight(c, w13, experts, w13_batch_stride, 2 * ffn, hidden, w13_stride, "w13");
+    c.pointer(w13_scale, "w13_scale", 4);
+    check_weight(c, w2, experts, w2_batch_stride, hidden, ffn, w2_stride, "w2");
+    c.pointer(w2_scale, "w2_scale", 4);
+    c.pointer(out, "out", (uintptr_t)element_bytes(dtype));
+    c.pointer(workspace, "workspace", kAlign);
+    c.invalid(workspace_bytes < reshard_experts_fp8_workspace(tokens, k, experts, hidden, ffn, dtype),
+              "the workspace is smaller than reshard_experts_fp8_workspace");
+  }
+  if (!c.ok()) return c.report();
+  if (tokens == 0) return RESHARD_OK;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const ExpertLayout l(tokens, k, experts, hidden, ffn, dtype);
+  uint8_t *at = static_cast<uint8_t *>(workspace);
+  auto take = [&](int64_t bytes) { uint8_t *p = at; at += bytes; return p; };
+  int32_t *offsets = reinterpret_cast<int32_t *>(take(l.offsets));
+  int32_t *order = reinterpret_cast<int32_t *>(take(l.order));
+  int32_t *position = reinterpret_cast<int32_t *>(take(l.position));
+  uint8_t *y = take(l.y);
+  uint8_t *xq = take(l.x.values);
+  float *xs = reinterpret_cast<float *>(take(l.x.scales));
+  uint8_t *hq = take(l.h.values);
+  float *hs = reinterpret_cast<float *>(take(l.h.scales));
+  int rc = enqueue_dispatch(ids, l.slots, first_expert, experts, offsets, order, position, stream);
+  if (rc) return rc;
+  Rows r{x, dtype, l.slots, hidden, row_stride, xq, l.x.pitch, xs, 1, l.slots};
+  r.order = order;
+  r.count = offsets + experts;
+  r.per_row = k;
+  if ((rc = enqueue_quantize_rows(r, stream))) return rc;
+  Product p{};
+  p.a = xq, p.a_stride = l.x.pitch, p.a_scale = xs, p.as_row = 1, p.as_block = l.slots;
+  p.w = static_cast<const uint8_t *>(w13), p.w_batch = map_batch(experts, w13_batch_stride, 2 * ffn, w13_stride), p.w_stride = w13_stride;
+  p.w_scale = w13_scale, p.offsets = offsets, p.groups = experts, p.m = l.slots, p.n = ffn, p.k = hidden;
+  p.out = hq, p.out_stride = l.h.pitch, p.gated = true, p.out_scale = hs, p.os_row = 1, p.os_block = l.slots;
+  if ((rc = enqueue_product(p, stream))) return rc;
+  Product p2{};
+  p2.a = hq, p2.a_stride = l.h.pitch, p2.a_scale = hs, p2.as_row = 1, p2.as_block = l.slots;
+  p2.w = static_cast<const uint8_t *>(w2), p2.w_batch = map_batch(experts, w2_batch_stride, hidden, w2_stride), p2.w_stride = w2_stride;
+  p2.w_scale = w2_scale, p2.offsets = offsets, p2.groups = experts, p2.m = l.slots, p2.n = hidden, p2.k = ffn;
+  p2.out = y, p2.out_dtype = dtype, p2.out_stride = up(hidden, 16);
+  if ((rc = enqueue_product(p2, stream))) return rc;
+  return enqueue_combine(y, dtype, up(hidden, 16), position, weights, tokens, k, hidden, out, out_stride, stream);
+}

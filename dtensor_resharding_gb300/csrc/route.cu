@@ -1,0 +1,491 @@
+// Routing to experts: scores, selection and weights of each token, its gradient, and the order in which the chosen
+// (token, expert) slots reach the experts' products.
+//
+// Score s of logits z: softmax(z) or sigmoid(z) = 1 / (1 + exp(-z)). Experts are ordered by s + bias; without a bias
+// by z itself, which orders them as s does but has no ties that rounding made. The lowest index comes first among
+// equals. With groups (equal runs of experts) only those of the `kept` groups whose `group_top` best experts have the
+// largest sum of scores (+ bias) can be chosen. A logit of -inf or NaN, or a key that is one, is never chosen: the row's
+// missing slots get id -1 and weight 0. Everything is computed in 32 bits.
+//
+// One warp holds a row in registers (E / 32 values a lane), so that a row is read once and selection is k rounds of a
+// warp-wide integer maximum: keys are mapped to unsigned integers of the same order, removed ones to 0, and
+// redux.sync gives the maximum and then the lowest index that has it. Bound by instruction issue (about k rounds of
+// E / 32 compares and two redux), not by HBM, for the usual 128 to 256 experts.
+#include <algorithm>
+#include <climits>
+
+#include "ops_common.cuh"
+
+namespace reshard {
+namespace ops {
+
+namespace {
+
+constexpr int kRouteWarps = 4;     // rows of a CTA
+constexpr uint32_t kFull = 0xffffffffu;
+
+struct RouteArgs {
+  const void *logits;
+  int64_t tokens, stride;
+  int experts, k, groups, kept, group_top;
+  const float *bias;
+  bool sigmoid, renorm;
+  float scale;
+};
+
+// Unsigned integers in the order of the floats; 0 for what cannot be chosen (-inf, NaN). -0 counts as +0.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (!(v > -INFINITY)) return 0;
+  const uint32_t b = __float_as_uint(v + 0.0f);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float key_value(uint32_t u) { return __uint_as_float(u ^ (u >> 31 ? 0x80000000u : 0xffffffffu)); }
+
+// The rounding of each step is the one its formula names: __fadd_rn keeps the compiler from fusing the sum with
+// the exponential's last product, which would order near-equal scores by another rounding.
+__device__ __forceinline__ float sigmoid_score(float z) { return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-z))); }
+
+__device__ __forceinline__ float warp_max(float v) {
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+// A lane's V values of a row: vectors of W neighbours, dealt round the warp. e(i) is value i's expert.
+template <int V, int W>
+struct Lane {
+  static __device__ __forceinline__ int expert(int i, int lane) { return (i / W) * 32 * W + lane * W + i % W; }
+};
+
+template <typename T, int V, int W>
+__device__ __forceinline__ void load_row(const T *row, int E, int lane, float (&z)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; i += W) {
+    const int e = Lane<V, W>::expert(i, lane);
+    if (W > 1) {     // E and the row's start are multiples of W elements
+      struct alignas(sizeof(T) * W) Vec { T v[W]; };
+      if (e < E) {
+        const Vec x = *reinterpret_cast<const Vec *>(row + e);
+#pragma unroll
+        for (int j = 0; j < W; ++j) z[i + j] = to_f32(x.v[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j) z[i + j] = -INFINITY;
+      }
+    } else {
+      z[i] = e < E ? to_f32(row[e]) : -INFINITY;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (isnan(z[i])) z[i] = -INFINITY;
+}
+
+template <int V>
+__device__ __forceinline__ float row_max(const float (&z)[V]) {
+  float m = z[0];
+#pragma unroll
+  for (int i = 1; i < V; ++i) m = fmaxf(m, z[i]);
+  m = warp_max(m);
+  return m == -INFINITY ? 0.0f : m;   // a row with nothing to choose: exp(-inf - 0) = 0 everywhere
+}
+
+// Sets to 0 the keys of every group but the `kept` best. rank: the values that rank groups, as keys.
+template <int V, int W>
+__device__ __forceinline__ void keep_groups(const RouteArgs &a, int lane, const uint32_t (&rank)[V], uint32_t (&key)[V]) {
+  const int size = a.experts / a.groups;
+  uint32_t mine = 0;        // lane g: group g's key
+  for (int g = 0; g < a.groups; ++g) {
+    const int lo = g * size, hi = lo + size;
+    uint32_t b0 = 0, b1 = 0;       // this lane's two best of the group
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = Lane<V, W>::expert(i, lane);
+      const uint32_t u = e >= lo && e < hi ? rank[i] : 0;
+      b1 = max(b1, min(b0, u));
+      b0 = max(b0, u);
+    }
+    const uint32_t top = __reduce_max_sync(kFull, b0);
+    uint32_t total = top;
+    if (a.group_top > 1 && top) {
+      const uint32_t has = __ballot_sync(kFull, b0 == top);
+      const uint32_t next = __reduce_max_sync(kFull, lane == __ffs(has) - 1 ? b1 : b0);
+      if (next) total = order_key(__fadd_rn(key_value(top), key_value(next)));
+    }
+    if (lane == g) mine = total;
+  }
+  uint32_t kept = 0;        // bit g: group g stays
+  for (int j = 0; j < a.kept; ++j) {
+    const uint32_t left = lane < a.groups && !(kept >> lane & 1) ? mine : 0;
+    const uint32_t best = __reduce_max_sync(kFull, left);
+    if (!best) break;
+    kept |= 1u << (__ffs(__ballot_sync(kFull, left == best)) - 1);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (!(kept >> min(31, Lane<V, W>::expert(i, lane) / size) & 1)) key[i] = 0;
+}
+
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(kRouteWarps * 32) reshard_route_kernel(RouteArgs a, float *weights, int32_t *ids) {
+  grid_enter();
+  const int lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
+  if (t >= a.tokens) return;
+  const T *row = static_cast<const T *>(a.logits) + t * a.stride;
+  float z[V];
+  load_row<T, V, W>(row, a.experts, lane, z);
+
+  // what the score needs of the whole row
+  float top = 0.0f, total = 0.0f;
+  uint32_t key[V];
+  const bool whole = !a.sigmoid && (a.bias || !a.renorm), ranked = a.groups > 1 && a.group_top > 1;
+  if (!a.sigmoid && (whole || ranked)) top = row_max<V>(z);
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) total += expf(z[i] - top);
+    total = warp_sum(total);
+  }
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = Lane<V, W>::expert(i, lane);
+      const float s = a.sigmoid ? sigmoid_score(z[i]) : __fdiv_rn(expf(z[i] - top), total);
+      key[i] = z[i] > -INFINITY ? order_key(__fadd_rn(s, a.bias[e])) : 0;
+    }
+    if (a.groups > 1) keep_groups<V, W>(a, lane, key, key);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = order_key(z[i]);
+    if (ranked) {      // sums of scores; a softmax row's common divisor changes no order
+      uint32_t rank[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) rank[i] = key[i] ? order_key(a.sigmoid ? sigmoid_score(z[i]) : expf(z[i] - top)) : 0;
+      keep_groups<V, W>(a, lane, rank, key);
+    } else if (a.groups > 1) {
+      keep_groups<V, W>(a, lane, key, key);
+    }
+  }
+
+  int id = -1;              // lane j: the j-th choice
+  for (int j = 0; j < a.k; ++j) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) best = max(best, key[i]);
+    best = __reduce_max_sync(kFull, best);
+    if (!best) break;
+    int e = INT_MAX;
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i)
+      if (key[i] == best) e = Lane<V, W>::expert(i, lane);
+    e = __reduce_min_sync(kFull, e);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (Lane<V, W>::expert(i, lane) == e) key[i] = 0;
+    if (lane == j) id = e;
+  }
+
+  const float zc = id >= 0 ? to_f32(row[id]) : -INFINITY;
+  float w = 0.0f;
+  if (a.sigmoid) {
+    if (id >= 0) w = sigmoid_score(zc);
+  } else if (a.renorm) {    // relative to the largest chosen logit: no row's weights underflow together
+    const float m = warp_max(zc);
+    if (id >= 0) w = expf(zc - m);
+  } else if (id >= 0) {
+    w = __fdiv_rn(expf(zc - top), total);
+  }
+  if (a.renorm) {
+    const float sum = warp_sum(w);
+    w = sum == 0.0f ? 0.0f : __fdiv_rn(w, sum);
+  }
+  if (lane < a.k) {
+    weights[t * a.k + lane] = w * a.scale;
+    ids[t * a.k + lane] = id;
+  }
+}
+
+// The gradient to the logits, with g_j the gradient to weight j times scale, over the row's valid ids i_j:
+//   softmax:               d z_e = p_e (sum_j [i_j = e] g_j - sum_j g_j p_{i_j})
+//   softmax, renormalised: r = softmax over the chosen logits;  d z_{i_j} = r_j (g_j - sum g r), 0 elsewhere
+//   sigmoid:               d z_{i_j} = g_j s_j (1 - s_j)
+//   sigmoid, renormalised: r_j = s_j / sum s;  d z_{i_j} = (g_j - sum g r) r_j (1 - s_j)
+// 1 - s is computed as sigmoid(-z). The bias only selects and has no gradient. Written whole, one warp a row; bound by
+// the write of the rows (and, for the whole softmax, the read of the logits).
+template <typename T, int V, int W>
+__global__ void __launch_bounds__(kRouteWarps * 32)
+    reshard_route_backward_kernel(RouteArgs a, const float *grad, const int32_t *ids, T *out, int64_t out_stride) {
+  grid_enter();
+  const int lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * kRouteWarps + (threadIdx.x >> 5);
+  if (t >= a.tokens) return;
+  const T *row = static_cast<const T *>(a.logits) + t * a.stride;
+  int id = lane < a.k ? ids[t * a.k + lane] : -1;
+  if (id >= a.experts) id = -1;
+  const float g = id >= 0 ? grad[t * a.k + lane] * a.scale : 0.0f;
+  float zc = id >= 0 ? to_f32(row[id]) : -INFINITY;
+  if (isnan(zc)) zc = -INFINITY;
+  float d = 0.0f, dot = 0.0f;        // lane j: what expert i_j gets of slot j
+  float p[V];
+  const bool whole = !a.sigmoid && !a.renorm;
+  if (whole) {
+    load_row<T, V, W>(row, a.experts, lane, p);
+    const float top = row_max<V>(p);
+    float total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      p[i] = expf(p[i] - top);
+      total += p[i];
+    }
+    total = warp_sum(total);
+    const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] *= inv;
+    dot = warp_sum(g * (expf(zc - top) * inv));
+    d = g;
+  } else {
+    float r = 0.0f, tail = 1.0f;
+    if (a.sigmoid) {
+      if (id >= 0) {
+        r = sigmoid_score(zc);
+        tail = sigmoid_score(-zc);
+      }
+    } else {
+      const float m = warp_max(zc);
+      if (id >= 0 && m > -INFINITY) r = expf(zc - m);
+    }
+    if (a.renorm) {
+      const float sum = warp_sum(r);
+      r = sum == 0.0f ? 0.0f : __fdiv_rn(r, sum);
+      dot = warp_sum(g * r);
+    }
+    d = (g - dot) * r * tail;
+  }
+  float o[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) o[i] = 0.0f;
+  for (int j = 0; j < a.k; ++j) {
+    const int e = __shfl_sync(kFull, id, j);
+    const float v = __shfl_sync(kFull, d, j);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (Lane<V, W>::expert(i, lane) == e) o[i] += v;
+  }
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = p[i] * (o[i] - dot);
+  }
+  T *to = out + t * out_stride;
+#pragma unroll
+  for (int i = 0; i < V; i += W) {
+    const int e = Lane<V, W>::expert(i, lane);
+    if (e >= a.experts) continue;
+    if (W > 1) {
+      struct alignas(sizeof(T) * W) Vec { T v[W]; } x;
+#pragma unroll
+      for (int j = 0; j < W; ++j) x.v[j] = from_f32<T>(o[i + j]);
+      *reinterpret_cast<Vec *>(to + e) = x;
+    } else {
+      to[e] = from_f32<T>(o[i]);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------------------------------ dispatch --
+
+// The slots (token, choice) sorted by expert, in slot order within each: offsets[e] .. offsets[e + 1] are expert e's
+// places, order[place] its slot, position[slot] its place (-1: no expert of this range). One CTA an expert: a first
+// pass over the ids counts the slots of lower experts and of its own, a second places its own by ballot. No atomics:
+// the order is the same on every run. Every CTA reads all ids (from L2), so the cost is experts x slots x 4 bytes of L2
+// traffic; one launch and no workspace is worth that up to the sizes measured here.
+constexpr int kDispatchThreads = 512;
+
+__global__ void __launch_bounds__(kDispatchThreads)
+    reshard_dispatch_kernel(const int32_t *ids, int slots, int first, int experts, int32_t *offsets, int32_t *order, int32_t *position) {
+  grid_enter();
+  __shared__ int below_s, own_s, base_s;
+  __shared__ int warp_n[kDispatchThreads / 32];
+  const int e = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) below_s = own_s = 0;
+  __syncthreads();
+  int below = 0, own = 0;
+  for (int i = tid; i < slots; i += kDispatchThreads) {
+    const int x = ids[i] - first;
+    if (ids[i] >= 0 && x >= 0 && x < experts) {
+      below += x < e;
+      own += x == e;
+    } else if (e == 0) {
+      position[i] = -1;
+    }
+  }
+  below = __reduce_add_sync(kFull, below);
+  own = __reduce_add_sync(kFull, own);
+  if (lane == 0) {           // integer sums: their order changes nothing
+    atomicAdd(&below_s, below);
+    atomicAdd(&own_s, own);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    offsets[e] = below_s;
+    if (e == experts - 1) offsets[experts] = below_s + own_s;
+    base_s = below_s;
+  }
+  __syncthreads();
+  if (own_s == 0) return;
+  for (int i0 = 0; i0 < slots; i0 += kDispatchThreads) {
+    const int i = i0 + tid;
+    const bool hit = i < slots && ids[i] - first == e && ids[i] >= 0;
+    const uint32_t m = __ballot_sync(kFull, hit);
+    if (lane == 0) warp_n[warp] = __popc(m);
+    __syncthreads();
+    int at = base_s;
+    for (int w = 0; w < warp; ++w) at += warp_n[w];
+    if (hit) {
+      at += __popc(m & ((1u << lane) - 1));
+      order[at] = i;
+      position[i] = at;
+    }
+    __syncthreads();
+    if (tid == 0) {
+      int n = 0;
+      for (int w = 0; w < kDispatchThreads / 32; ++w) n += warp_n[w];
+      base_s += n;
+    }
+    __syncthreads();
+  }
+}
+
+// Calls f with the number of values a lane holds and the width of its vectors: four neighbours where E, the row
+// stride and the base allow it, one otherwise.
+template <typename F>
+void by_shape(int experts, bool wide, F &&f) {
+  if (wide) {
+    if (experts <= 128) f(std::integral_constant<int, 4>(), std::integral_constant<int, 4>());
+    else if (experts <= 256) f(std::integral_constant<int, 8>(), std::integral_constant<int, 4>());
+    else if (experts <= 512) f(std::integral_constant<int, 16>(), std::integral_constant<int, 4>());
+    else f(std::integral_constant<int, 32>(), std::integral_constant<int, 4>());
+  } else {
+    if (experts <= 64) f(std::integral_constant<int, 2>(), std::integral_constant<int, 1>());
+    else if (experts <= 256) f(std::integral_constant<int, 8>(), std::integral_constant<int, 1>());
+    else f(std::integral_constant<int, 32>(), std::integral_constant<int, 1>());
+  }
+}
+
+template <typename F>
+void by_type(int dtype, F &&f) {
+  if (dtype == RESHARD_F32) f(float());
+  else if (dtype == RESHARD_BF16) f(__nv_bfloat16());
+  else f(__half());
+}
+
+bool quads(const void *p, int dtype, int experts, int64_t stride) {
+  return experts % 4 == 0 && stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p) % (4 * element_bytes(dtype))) == 0;
+}
+
+void check_route(Checks &c, int64_t tokens, int experts, int64_t stride, int dtype, int k, int score) {
+  c.invalid(tokens < 0, "tokens < 0");
+  c.invalid(experts < 1 || k < 1 || k > experts, "experts and k must be positive, k at most experts");
+  c.unsupported(experts > RESHARD_ROUTE_MAX_EXPERTS || k > RESHARD_ROUTE_MAX_K, "more than 1024 experts or k above 32");
+  c.invalid(stride < experts, "a row stride is shorter than the row");
+  c.invalid(!element_bytes(dtype), "dtype must be BF16, F16 or F32");
+  c.invalid(score != RESHARD_SCORE_SOFTMAX && score != RESHARD_SCORE_SIGMOID, "unknown score function");
+  c.unsupported(tokens > (int64_t)INT32_MAX * kRouteWarps, "too many tokens for one launch");
+}
+
+}  // namespace
+
+int enqueue_dispatch(const int32_t *ids, int64_t slots, int first, int experts, int32_t *offsets, int32_t *order,
+                     int32_t *position, cudaStream_t stream) {
+  OPS_CUDA(launch(reshard_dispatch_kernel, dim3((unsigned)experts), kDispatchThreads, 0, 1, stream, ids, (int)slots, first, experts,
+                  offsets, order, position));
+  return RESHARD_OK;
+}
+
+}  // namespace ops
+}  // namespace reshard
+
+using namespace reshard;
+using namespace reshard::ops;
+
+extern "C" int reshard_route(const void *logits, int dtype, int64_t tokens, int experts, int64_t row_stride, const float *bias,
+                             int score, int groups, int groups_kept, int group_top, int k, int renormalize, float scale,
+                             float *weights, int32_t *ids, reshard_stream_t stream) {
+  Checks c("reshard_route");
+  check_route(c, tokens, experts, row_stride, dtype, k, score);
+  c.invalid(groups < 1 || (groups >= 1 && experts >= 1 && experts % groups), "groups must divide experts");
+  c.unsupported(groups > 32, "more than 32 groups");
+  c.invalid(groups_kept < 1 || groups_kept > groups, "groups_kept must be 1 .. groups");
+  c.invalid(group_top != 1 && group_top != 2, "group_top must be 1 or 2");
+  if (c.ok()) c.invalid((int64_t)groups_kept * (experts / groups) < k, "the kept groups hold fewer than k experts");
+  if (c.ok()) c.invalid(group_top > experts / groups, "group_top exceeds a group's experts");
+  if (tokens > 0 && c.ok()) {
+    c.pointer(logits, "logits", (uintptr_t)element_bytes(dtype));
+    if (bias) c.pointer(bias, "bias", 4);
+    c.pointer(weights, "weights", 4);
+    c.pointer(ids, "ids", 4);
+  }
+  if (!c.ok()) return c.report();
+  if (tokens == 0) return RESHARD_OK;
+  const RouteArgs a{logits, tokens, row_stride, experts, k, groups, groups_kept, group_top, bias,
+                    score == RESHARD_SCORE_SIGMOID, renormalize != 0, scale};
+  cudaError_t e = cudaSuccess;
+  by_type(dtype, [&](auto t) {
+    using T = decltype(t);
+    by_shape(experts, quads(logits, dtype, experts, row_stride), [&](auto v, auto w) {
+      e = launch(reshard_route_kernel<T, decltype(v)::value, decltype(w)::value>,
+                 dim3((unsigned)((tokens + kRouteWarps - 1) / kRouteWarps)), kRouteWarps * 32, 0, 1,
+                 reinterpret_cast<cudaStream_t>(stream), a, weights, ids);
+    });
+  });
+  return e == cudaSuccess ? RESHARD_OK : cuda_error(e, "launching reshard_route_kernel");
+}
+
+extern "C" int reshard_route_backward(const float *grad_weights, const void *logits, int dtype, int64_t tokens, int experts,
+                                      int64_t row_stride, const int32_t *ids, int k, int score, int renormalize, float scale,
+                                      void *grad_logits, int64_t grad_stride, reshard_stream_t stream) {
+  Checks c("reshard_route_backward");
+  check_route(c, tokens, experts, row_stride, dtype, k, score);
+  c.invalid(grad_stride < experts, "a row stride is shorter than the row");
+  if (tokens > 0 && c.ok()) {
+    c.pointer(grad_weights, "grad_weights", 4);
+    c.pointer(logits, "logits", (uintptr_t)element_bytes(dtype));
+    c.pointer(ids, "ids", 4);
+    c.pointer(grad_logits, "grad_logits", (uintptr_t)element_bytes(dtype));
+  }
+  if (!c.ok()) return c.report();
+  if (tokens == 0) return RESHARD_OK;
+  const RouteArgs a{logits, tokens, row_stride, experts, k, 1, 1, 1, nullptr, score == RESHARD_SCORE_SIGMOID, renormalize != 0, scale};
+  const bool wide = quads(logits, dtype, experts, row_stride) && quads(grad_logits, dtype, experts, grad_stride);
+  cudaError_t e = cudaSuccess;
+  by_type(dtype, [&](auto t) {
+    using T = decltype(t);
+    by_shape(experts, wide, [&](auto v, auto w) {
+      e = launch(reshard_route_backward_kernel<T, decltype(v)::value, decltype(w)::value>,
+                 dim3((unsigned)((tokens + kRouteWarps - 1) / kRouteWarps)), kRouteWarps * 32, 0, 1,
+                 reinterpret_cast<cudaStream_t>(stream), a, grad_weights, ids, static_cast<T *>(grad_logits), grad_stride);
+    });
+  });
+  return e == cudaSuccess ? RESHARD_OK : cuda_error(e, "launching reshard_route_backward_kernel");
+}
+
+extern "C" int reshard_dispatch(const int32_t *ids, int64_t slots, int first_expert, int experts, int32_t *offsets, int32_t *order,
+                                int32_t *position, reshard_stream_t stream) {
+  Checks c("reshard_dispatch");
+  c.invalid(slots < 0, "slots < 0");
+  c.unsupported(slots > RESHARD_MAX_SLOTS, "more than 2^30 slots");
+  c.invalid(first_expert < 0 || experts < 1, "first_expert must be >= 0 and experts >= 1");
+  c.unsupported(experts > RESHARD_MAX_GROUPS, "more than 512 experts on this side");
+  if (c.ok()) {
+    c.pointer(offsets, "offsets", 4);
+    if (slots > 0) {
+      c.pointer(ids, "ids", 4);
+      c.pointer(order, "order", 4);
+      c.pointer(position, "position", 4);
+    }
+  }
+  if (!c.ok()) return c.report();
+  return enqueue_dispatch(ids, slots, first_expert, experts, offsets, order, position, reinterpret_cast<cudaStream_t>(stream));
+}
