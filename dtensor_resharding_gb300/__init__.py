@@ -32,7 +32,8 @@ _OPS = ("reshard_route", "reshard_route_backward", "reshard_dispatch", "reshard_
 def __getattr__(name):
     if name in _OPS:
         from . import ops
-        return getattr(ops, name)
+        globals().update({n: getattr(ops, n) for n in _OPS})
+        return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

@@ -110,6 +110,9 @@ struct Product {              // out[m, n] = sum_k a[m, k] w[n, k], both as 8-bi
   const float *w_scale;
   const int32_t *offsets = nullptr;  // groups + 1 row offsets, on the device; NULL: one group of m rows
   int groups = 1;
+  const int32_t *order = nullptr;    // row r of the product is row order[r] / per_row of a's a_rows; NULL: row r
+  int per_row = 1;
+  int64_t a_rows = 0;
   int64_t m, n, k;
   void *out;
   int out_dtype;

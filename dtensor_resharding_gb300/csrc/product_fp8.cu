@@ -20,6 +20,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cstddef>
 #include <mutex>
 
 #include "tensor_core.cuh"
@@ -39,6 +40,8 @@ struct Args {
   int64_t as_row, as_block;
   const float *w_scale;
   const int32_t *offsets;
+  const int32_t *order; // NULL: row r of the product is row r of a; otherwise row order[r] / per_row
+  int per_row, a_rows;
   int groups, m, n, kblocks;
   int wblocks;          // blocks of w's rows in one group's scales
   void *out;
@@ -53,13 +56,12 @@ __device__ __forceinline__ int row_offset(const Args &p, int g) {
   return p.offsets ? min(max(p.offsets[g], 0), p.m) : g ? p.m : 0;
 }
 
-__device__ __forceinline__ float silu_times(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
-
-// 8 consecutive 32-bit words; p on a 32-byte boundary.
-__device__ __forceinline__ void store32(void *p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
-               "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+// The row of a (and of its scales) that the product's row r is. Places come from the device, too.
+__device__ __forceinline__ int source_row(const Args &p, int r) {
+  return p.order ? min(max(p.order[r], 0) / p.per_row, p.a_rows - 1) : r;
 }
+
+__device__ __forceinline__ float silu_times(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b);
@@ -76,32 +78,45 @@ __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
 
 // ---------------------------------------------------------------------------------------------------------- wide --
 
-constexpr int kWideM = 128, kWideN = 256, kWideStages = 4;
+constexpr int kWideM = 128, kWideN = 256, kWideStages = 3;
 constexpr int kWideStageBytes = (kWideM + kWideN) * kBlockK;
-constexpr int kWideThreads = 320;        // 8 epilogue warps, the loader, the issuer
+constexpr int kWideEpi = 8;              // epilogue warps: 4 row quarters x 2 column halves
+constexpr int kWideThreads = (kWideEpi + 4) * 32;        // behind a warpgroup: the issuer, the loader, the scales' loader, one idle
+constexpr int kWideCols = kWideN / 2;    // columns of a thread
+constexpr int kScaleSlots = 2 * kWideStages;
+constexpr int kRowBytes = 256;           // of a thread's row of output on its way, 16 more apart for the banks
+constexpr int kRowPitch = kRowBytes + 16;
+// Registers a thread: at launch, of the epilogue's two warpgroups and of the other. The epilogue holds 128 sums and two loads
+// of 16 columns.
+constexpr int kWideRegs = 168, kWideRegsEpi = 200, kWideRegsRest = 104;
+static_assert(kWideThreads * kWideRegs >= kWideEpi * 32 * kWideRegsEpi + 128 * kWideRegsRest, "more registers than the launch has");
 
 struct WideShared {
-  uint64_t full[kWideStages], empty[kWideStages], done[2], taken[2], paired[2], last;
+  alignas(16) uint64_t done[2];        // 16-byte pairs: the address of the other is this one's ^ 8
+  alignas(16) uint64_t taken[2];
+  uint64_t full[kWideStages], empty[kWideStages], paired[2], last;
   uint32_t tmem;
   int stop;
   uint32_t amax[2][2][kWideM];
+  alignas(16) uint8_t rows[2][kWideM][kRowPitch];
+  float a_scale[kScaleSlots][kWideM], w_scale[kScaleSlots][2];     // w: the column halves', or gate's and up's
   int off[RESHARD_MAX_GROUPS + 1], tiles[RESHARD_MAX_GROUPS + 1];   // row offsets; tiles of rows before each group
 };
-constexpr size_t kWideSmem = 1024 + (size_t)kWideStages * kWideStageBytes + sizeof(WideShared);
+constexpr size_t kWideSmem = (size_t)kWideStages * kWideStageBytes + sizeof(WideShared);
+static_assert(kWideSmem <= 232448, "shared memory of a CTA");
 
 struct WideTile {
   int g, row, rows, n;     // group, first row, rows of the group from there (can exceed the tile), column tile
 };
-__device__ __forceinline__ WideTile wide_tile(const WideShared &s, int groups, int ntiles, int64_t t) {
+__device__ __forceinline__ WideTile wide_tile(const WideShared &s, int groups, uint32_t ntiles, uint32_t t) {
   int lo = 0, hi = groups - 1;          // the last group whose first tile is <= t
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if ((int64_t)s.tiles[mid] * ntiles <= t) lo = mid;
+    if (s.tiles[mid] * ntiles <= t) lo = mid;
     else hi = mid - 1;
   }
-  const int here = s.tiles[lo + 1] - s.tiles[lo];
-  const int64_t l = t - (int64_t)s.tiles[lo] * ntiles;
-  const int n = (int)(l / here), m = (int)(l - (int64_t)n * here);     // row tiles first: neighbours share w's tile
+  const uint32_t here = s.tiles[lo + 1] - s.tiles[lo], l = t - s.tiles[lo] * ntiles;
+  const uint32_t n = l / here, m = l - n * here;     // row tiles first: neighbours share w's tile
   WideTile r;
   r.g = lo;
   r.row = s.off[lo] + m * kWideM;
@@ -110,56 +125,66 @@ __device__ __forceinline__ WideTile wide_tile(const WideShared &s, int groups, i
   return r;
 }
 
+// One thread's columns of its row, in T: 256 bytes at a time through its row of shared memory, from where the copy engine
+// takes them. All CTAs finish their tiles together and L2 takes 10 MB of a round's tiles no faster than it takes; plain
+// stores kept the epilogue (and with it the products) for 4,800 cycles a tile, this way for 1,000.
 template <typename T>
-__device__ __forceinline__ void store_row(T *to, const uint64_t (&acc)[64], int left) {
-  if (left >= 128 && (reinterpret_cast<uintptr_t>(to) & 31) == 0) {
-    constexpr int per = 32 / sizeof(T);
+__device__ __forceinline__ void store_columns(uint8_t *row, const float2 (&sum)[kWideCols / 2], T *to, int cols) {
+  constexpr int per = kRowBytes / sizeof(T);
+  const bool bulk = (reinterpret_cast<uintptr_t>(to) & 15) == 0 && (cols * sizeof(T)) % 16 == 0;
 #pragma unroll
-    for (int c = 0; c < 128; c += per) {
-      uint32_t v[8];
-      if constexpr (sizeof(T) == 4) {
+  for (int c = 0; c < kWideCols; c += per) {
+    if (!bulk) {             // a row that starts or ends inside 16 bytes
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = (uint32_t)(acc[(c + j) / 2] >> (32 * (j & 1)));
-      } else {
+      for (int j = 0; j < per; ++j)
+        if (c + j < cols) to[c + j] = from_f32<T>(j & 1 ? sum[(c + j) / 2].y : sum[(c + j) / 2].x);
+    } else if (c < cols) {
+      bulk_read();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = pack2<T>(lo32(acc[c / 2 + j]), hi32(acc[c / 2 + j]));
+      for (int j = 0; j < kRowBytes / 16; ++j) {
+        uint32_t v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (sizeof(T) == 4) v[i] = __float_as_uint(i & 1 ? sum[(c + 4 * j + i) / 2].y : sum[(c + 4 * j + i) / 2].x);
+          else v[i] = pack2<T>(sum[c / 2 + 4 * j + i].x, sum[c / 2 + 4 * j + i].y);
+        }
+        *reinterpret_cast<uint4 *>(row + 16 * j) = make_uint4(v[0], v[1], v[2], v[3]);
       }
-      store32(to + c, v);
+      bulk_store(to + c, smem_addr(row), (uint32_t)min(per, cols - c) * sizeof(T));
     }
-  } else {
-#pragma unroll
-    for (int c = 0; c < 128; ++c)
-      if (c < left) to[c] = from_f32<T>(c & 1 ? hi32(acc[c / 2]) : lo32(acc[c / 2]));
   }
 }
 
 template <bool Gated>
 __global__ void __launch_bounds__(kWideThreads, 1)
-    reshard_product_wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mw, const Args p) {
-  extern __shared__ uint8_t raw[];
-  uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    reshard_product_wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mw, const __grid_constant__ Args p) {
+  extern __shared__ __align__(1024) uint8_t stages[];
   WideShared &s = *reinterpret_cast<WideShared *>(stages + (size_t)kWideStages * kWideStageBytes);
+  if (smem_addr(stages) & 1023) {      // not seen: the swizzle needs it
+    atomicOr(&g_ops_status, 1);
+    return;
+  }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Stop stop{&s.stop, &g_ops_status};
   if (tid == 0) {
     for (int i = 0; i < kWideStages; ++i) {
-      bar_init(smem_addr(&s.full[i]), 1);
+      bar_init(smem_addr(&s.full[i]), 33);       // the loader, and a lane's copies of scales each
       bar_init(smem_addr(&s.empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       bar_init(smem_addr(&s.done[i]), 1);
-      bar_init(smem_addr(&s.taken[i]), 8);
-      bar_init(smem_addr(&s.paired[i]), 8);
+      bar_init(smem_addr(&s.taken[i]), kWideEpi);
+      bar_init(smem_addr(&s.paired[i]), kWideEpi);
     }
     bar_init(smem_addr(&s.last), 1);
     s.stop = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 9) tmem_alloc(smem_addr(&s.tmem), 512);
+  if (warp == 0) tmem_alloc(smem_addr(&s.tmem), 512);
   grid_enter();
   for (int g = tid; g <= p.groups; g += kWideThreads) s.off[g] = row_offset(p, g);
   __syncthreads();
-  if (warp == 0) {                     // running sum of the groups' row tiles
+  if (warp == 4) {                     // running sum of the groups' row tiles
     int base = 0;
     for (int g0 = 0; g0 < p.groups; g0 += 32) {
       const int g = g0 + lane;
@@ -180,162 +205,231 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const uint32_t tmem = s.tmem;
   constexpr int kCols = Gated ? kWideN / 2 : kWideN;      // output columns of a tile
   const int ntiles = (p.n + kCols - 1) / kCols;
-  const int64_t total = (int64_t)s.tiles[p.groups] * ntiles;
+  const uint32_t total = (uint32_t)s.tiles[p.groups] * ntiles;     // below 2^31: the caller's check
 
-  if (warp == 8) {
-    // ---- loader
-    if (elect_one()) {
-      uint32_t it = 0;
+  if (warp < 4) {
+    registers_down<kWideRegsRest>();
+    if (warp == 1) {
+      // ---- loader: one lane; where rows are gathered, four rows a lane
+      uint32_t it = 0, st = 0, phase = 1;
       bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
+      for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
         const WideTile w = wide_tile(s, p.groups, ntiles, t);
-        for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
-          const uint32_t st = it % kWideStages, bar = smem_addr(&s.full[st]);
-          if (!(ok = bar_wait(smem_addr(&s.empty[st]), (it / kWideStages & 1) ^ 1, stop))) break;
-          const uint32_t to = smem_addr(stages) + st * kWideStageBytes;
-          bar_expect(bar, kWideStageBytes);
-          tma_2d(to, &ma, kb * kBlockK, w.row, bar);
-          const uint32_t tw = to + kWideM * kBlockK;
-          if (Gated) {                 // columns 0-63: gate, 64-127: up, and the same for the tile's other half
+        int row[4];
+        if (p.order) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              tma_3d(tw + h * 16384, &mw, kb * kBlockK, w.n * kCols + h * 64, w.g, bar);
-              tma_3d(tw + h * 16384 + 8192, &mw, kb * kBlockK, p.n + w.n * kCols + h * 64, w.g, bar);
-            }
-          } else {
-            tma_3d(tw, &mw, kb * kBlockK, w.n * kCols, w.g, bar);
-            tma_3d(tw + 16384, &mw, kb * kBlockK, w.n * kCols + 128, w.g, bar);
+          for (int i = 0; i < 4; ++i) row[i] = source_row(p, w.row + min(4 * lane + i, w.rows - 1));
+        }
+        for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
+          const uint32_t bar = smem_addr(s.full) + st * 8;
+          ok = bar_wait(smem_addr(s.empty) + st * 8, phase, stop);
+          if (__any_sync(kFull, !ok)) {
+            ok = false;
+            break;
           }
+          const uint32_t to = smem_addr(stages) + st * kWideStageBytes;
+          if (lane == 0) {
+            bar_expect(bar, kWideStageBytes);
+            if (!p.order) tma_2d(to, &ma, kb * kBlockK, w.row, bar);
+            const uint32_t tw = to + kWideM * kBlockK;
+            if (Gated) {                 // of each half's columns the first 64 are gate, the others up
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                tma_3d(tw + h * 16384, &mw, kb * kBlockK, w.n * kCols + h * 64, w.g, bar);
+                tma_3d(tw + h * 16384 + 8192, &mw, kb * kBlockK, p.n + w.n * kCols + h * 64, w.g, bar);
+              }
+            } else {
+              tma_3d(tw, &mw, kb * kBlockK, w.n * kCols, w.g, bar);
+              tma_3d(tw + 16384, &mw, kb * kBlockK, w.n * kCols + 128, w.g, bar);
+            }
+          }
+          if (p.order) {
+            __syncwarp();
+            tma_rows4(to + lane * 4 * kBlockK, &ma, kb * kBlockK, row, bar);
+          }
+          if (++st == kWideStages) st = 0, phase ^= 1;
         }
       }
-      if (!ok)                         // stopped: what is on its way still lands in this CTA's memory
+      if (!ok && lane == 0)            // stopped: what is on its way still lands in this CTA's memory
         for (uint32_t i = it > kWideStages ? it - kWideStages : 0; i < it; ++i)
           bar_drain(smem_addr(&s.full[i % kWideStages]), i / kWideStages & 1);
-    }
-    __syncwarp();
-  } else if (warp == 9) {
-    // ---- issuer
-    if (elect_one()) {
-      const uint32_t idesc = instruction(kWideN);
-      uint32_t it = 0;
-      bool ok = true;
-      for (int64_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
-        for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
-          const uint32_t st = it % kWideStages, half = it & 1;
-          if (!(ok = bar_wait(smem_addr(&s.taken[half]), (it >> 1 & 1) ^ 1, stop))) break;
-          if (!(ok = bar_wait(smem_addr(&s.full[st]), it / kWideStages & 1, stop))) break;
+      __syncwarp();
+    } else if (warp == 0) {
+      // ---- issuer: the first warp, which the scheduler prefers
+
+      // The loop is kept to a few dependent steps: they, not the products, are what a block would wait for.
+      if (elect_one()) {
+        const uint32_t idesc = instruction(kWideN), full = smem_addr(s.full), empty = smem_addr(s.empty);
+        const uint64_t a0 = operand(smem_addr(stages));
+        uint32_t st = 0, phase = 0, d = tmem, done = smem_addr(s.done), taken = smem_addr(s.taken), free_phase = 1, second = 0;
+        const uint32_t mine = blockIdx.x < total ? (total - 1 - blockIdx.x) / gridDim.x + 1 : 0;
+        bool ok = true;
+        for (uint32_t n = mine * p.kblocks; n; --n) {
+          if (!(ok = bar_wait(full + st * 8, phase, stop))) break;
+          if (!(ok = bar_wait(taken, free_phase, stop))) break;
           tc_after_sync();
-          const uint32_t base = smem_addr(stages) + st * kWideStageBytes;
-          const uint64_t a = operand(base), b = operand(base + kWideM * kBlockK);
+          const uint64_t a = a0 + st * (kWideStageBytes / 16), b = a + kWideM * kBlockK / 16;
 #pragma unroll
-          for (int k = 0; k < kBlockK / 32; ++k) mma_e4m3(tmem + half * kWideN, a + 2 * k, b + 2 * k, idesc, k > 0);
-          mma_commit(smem_addr(&s.empty[st]));
-          mma_commit(smem_addr(&s.done[half]));
+          for (int k = 0; k < kBlockK / 32; ++k) mma_e4m3(d, a + 2 * k, b + 2 * k, idesc, k > 0);
+          mma_commit(done);
+          mma_commit(empty + st * 8);
+          if (++st == kWideStages) st = 0, phase ^= 1;
+          free_phase ^= second;
+          second ^= 1;
+          d ^= kWideN;
+          done ^= 8;
+          taken ^= 8;
+        }
+        if (!ok) {
+          mma_commit(smem_addr(&s.last));
+          bar_drain(smem_addr(&s.last), 0);
         }
       }
-      if (!ok) {
-        mma_commit(smem_addr(&s.last));
-        bar_drain(smem_addr(&s.last), 0);
+      __syncwarp();
+    } else if (warp == 2) {
+      // ---- scales of a stage's block, arriving with its operands. Two slots a stage: when a stage is free for block i,
+      // the products of block i - 4 are done, which began after the epilogue had taken block i - 6, so slot i % 8 is free too.
+      uint32_t st = 0, phase = 1, slot = 0;
+      bool ok = true;
+      for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
+        const WideTile w = wide_tile(s, p.groups, ntiles, t);
+        const float *sa[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sa[i] = p.a_scale + (int64_t)source_row(p, w.row + min(lane + 32 * i, w.rows - 1)) * p.as_row;
+        // lanes 0 and 1: gated, gate and up of the tile's one block; otherwise the two halves' blocks
+        const int wb = Gated ? w.n + (lane & 1) * (p.n / kScaleBlock) : min(w.n * 2 + (lane & 1), p.wblocks - 1);
+        const float *sw = p.w_scale + ((int64_t)w.g * p.wblocks + wb) * p.kblocks;
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          ok = bar_wait(smem_addr(s.empty) + st * 8, phase, stop);
+          if (__any_sync(kFull, !ok)) {
+            ok = false;
+            break;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            copy4(smem_addr(&s.a_scale[slot][lane + 32 * i]), sa[i]);
+            sa[i] += p.as_block;
+          }
+          if (lane < 2) copy4(smem_addr(&s.w_scale[slot][lane]), sw + kb);
+          bar_arrive_copied(smem_addr(s.full) + st * 8);
+          if (++st == kWideStages) st = 0, phase ^= 1;
+          if (++slot == kScaleSlots) slot = 0;
+        }
       }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
-    __syncwarp();
   } else {
-    // ---- epilogue: a row and 128 columns a thread
-    const int half_n = warp >> 2, r = (warp & 3) * 32 + lane;
-    const uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + half_n * 128;
-    uint32_t it = 0, tile_no = 0;
-    bool ok = true;
-    for (int64_t t = blockIdx.x; ok && t < total; t += gridDim.x, ++tile_no) {
-      const WideTile w = wide_tile(s, p.groups, ntiles, t);
-      const bool in = r < w.rows;
-      const float *sa = p.a_scale + (int64_t)(w.row + (in ? r : 0)) * p.as_row;
-      // gated: gate and up scales of the tile's one block; otherwise this half's block
-      const int wb = Gated ? w.n : min(w.n * 2 + half_n, p.wblocks - 1);
-      const float *sw = p.w_scale + ((int64_t)w.g * p.wblocks + wb) * p.kblocks;
-      const float *su = Gated ? sw + (int64_t)(p.n / kScaleBlock) * p.kblocks : sw;
-      uint64_t acc[64];
+    // ---- epilogue: a row and half of the columns a thread
+    registers_up<kWideRegsEpi>();
+    const int side = (warp >> 2) - 1, r = (warp & 3) * 32 + lane;
+    uint8_t *const out_row = s.rows[side][r];
+    // the next block's: tensor memory, barrier, parity, scales. tries: 1 once a wait gave up, so that the others pass
+    uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + side * kWideCols, done = smem_addr(s.done), phase = 0, second = 0;
+    uint32_t sa = smem_addr(&s.a_scale[0][r]), sw = smem_addr(&s.w_scale[0][Gated ? 0 : side]), tries = kTries;
+    const uint32_t sa_end = sa + sizeof s.a_scale;
+    constexpr uint32_t kToTaken = offsetof(WideShared, taken) - offsetof(WideShared, done);
+    for (uint32_t t = blockIdx.x, tile_no = 0; t < total; t += gridDim.x, ++tile_no) {
+      float2 sum[kWideCols / 2];       // pairs of columns
 #pragma unroll
-      for (int i = 0; i < 64; ++i) acc[i] = 0;
-      float a0 = sa[0], g0 = sw[0], u0 = su[0], a1 = 0, g1 = 0, u1 = 0;
-      if (p.kblocks > 1) a1 = sa[p.as_block], g1 = sw[1], u1 = su[1];
-      for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
-        float a2 = 0, g2 = 0, u2 = 0;        // two blocks ahead: their latency passes under the waits
-        if (kb + 2 < p.kblocks) a2 = sa[(int64_t)(kb + 2) * p.as_block], g2 = sw[kb + 2], u2 = su[kb + 2];
-        const float s0 = a0 * g0, s1 = Gated ? a0 * u0 : s0;
-        const uint32_t half = it & 1;
-        ok = bar_wait(smem_addr(&s.done[half]), it >> 1 & 1, stop);
-        if (__any_sync(kFull, !ok)) {
-          ok = false;
-          break;
-        }
+      for (int i = 0; i < kWideCols / 2; ++i) sum[i] = make_float2(0.0f, 0.0f);
+      uint32_t v[2][16];
+      float s0, s1;
+      // The first columns of a block are asked for as soon as its products are done, before the last sums of the block
+      // before, and its scales with them (they came with its operands): the sums hide both.
+      auto begin = [&]() {
+        if (!bar_spin(done, phase, tries)) tries = 1;
         tc_after_sync();
-        uint32_t v[2][16];
-        tmem_load16(from + half * kWideN, v[0]);
+        tmem_load(from, v[0]);
+        const float a = shared_f32(sa);
+        s0 = a * shared_f32(sw);
+        s1 = Gated ? a * shared_f32(sw + 4) : s0;
+      };
+      auto block = [&](bool more) {
+        const float by0 = s0, by1 = s1;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < kWideCols / 16; ++c) {
           tmem_loaded(v[c & 1]);
-          if (c < 7) {
-            tmem_load16(from + half * kWideN + (c + 1) * 16, v[(c + 1) & 1]);
+          if (c < kWideCols / 16 - 1) {
+            tmem_load(from + (c + 1) * 16, v[(c + 1) & 1]);
           } else {                     // the partial tile is in registers
             tc_before_sync();
             __syncwarp();
-            if (lane == 0) bar_arrive(smem_addr(&s.taken[half]));
+            if (lane == 0) bar_arrive(done + kToTaken);
+            from ^= kWideN;
+            done ^= 8;
+            phase ^= second;
+            second ^= 1;
+            sa += sizeof s.a_scale[0];
+            sw += sizeof s.w_scale[0];
+            if (sa == sa_end) sa -= sizeof s.a_scale, sw -= sizeof s.w_scale;
+            if (more) begin();
           }
-          const float sc = c < 4 ? s0 : s1;
+          const float by = c < kWideCols / 32 ? by0 : by1;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) fma2(acc[c * 8 + i], v[c & 1][2 * i], v[c & 1][2 * i + 1], sc);
+          for (int i = 0; i < 8; ++i)
+            sum[c * 8 + i] = __ffma2_rn(make_float2(__uint_as_float(v[c & 1][2 * i]), __uint_as_float(v[c & 1][2 * i + 1])), make_float2(by, by), sum[c * 8 + i]);
         }
-        a0 = a1, g0 = g1, u0 = u1;
-        a1 = a2, g1 = g2, u1 = u2;
-      }
-      if (!ok) break;
+      };
+      begin();
+#pragma unroll 1
+      for (int kb = 1; kb < p.kblocks; ++kb) block(true);
+      block(false);
+      if (__any_sync(kFull, tries == 1)) break;
+      const WideTile w = wide_tile(s, p.groups, ntiles, t);
       const int64_t row = w.row + r;
       if (!Gated) {
-        const int n0 = w.n * kCols + half_n * 128, left = p.n - n0;
-        if (in && left > 0) {
+        const int n0 = w.n * kCols + side * kWideCols, cols = min(kWideCols, p.n - n0);
+        if (r < w.rows && cols > 0) {
           const int64_t at = row * p.out_stride + n0;
-          if (p.out_dtype == RESHARD_BF16) store_row(static_cast<__nv_bfloat16 *>(p.out) + at, acc, left);
-          else if (p.out_dtype == RESHARD_F16) store_row(static_cast<__half *>(p.out) + at, acc, left);
-          else store_row(static_cast<float *>(p.out) + at, acc, left);
+          if (p.out_dtype == RESHARD_BF16) store_columns(out_row, sum, static_cast<__nv_bfloat16 *>(p.out) + at, cols);
+          else if (p.out_dtype == RESHARD_F16) store_columns(out_row, sum, static_cast<__half *>(p.out) + at, cols);
+          else store_columns(out_row, sum, static_cast<float *>(p.out) + at, cols);
         }
       } else {
-        // columns c of acc: gate 0 .. 63, up 64 .. 127; this thread's 64 of the row's 128 values
+        // of the sums the first half is gate, the second up: this thread's 64 of the row's 128 values
+        constexpr int kHalf = kWideCols / 4;
         uint32_t m = 0;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float x = silu_times(lo32(acc[i]), lo32(acc[32 + i])), y = silu_times(hi32(acc[i]), hi32(acc[32 + i]));
-          m = max(m, max(magnitude(x), magnitude(y)));
-          acc[i] = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
+        for (int i = 0; i < kHalf; ++i) {
+          sum[i] = make_float2(silu_times(sum[i].x, sum[kHalf + i].x), silu_times(sum[i].y, sum[kHalf + i].y));
+          m = max(m, max(magnitude(sum[i].x), magnitude(sum[i].y)));
         }
-        s.amax[tile_no & 1][half_n][r] = m;
+        s.amax[tile_no & 1][side][r] = m;
         __syncwarp();
-        if (lane == 0) bar_arrive(smem_addr(&s.paired[tile_no & 1]));
-        ok = bar_wait(smem_addr(&s.paired[tile_no & 1]), tile_no >> 1 & 1, stop);
-        if (__any_sync(kFull, !ok)) break;
-        m = max(m, s.amax[tile_no & 1][half_n ^ 1][r]);
+        const uint32_t paired = smem_addr(&s.paired[tile_no & 1]);
+        if (lane == 0) bar_arrive(paired);
+        if (!bar_spin(paired, tile_no >> 1 & 1, tries)) tries = 1;
+        if (__any_sync(kFull, tries == 1)) break;
+        m = max(m, s.amax[tile_no & 1][side ^ 1][r]);
         float scale, inv;
         block_scale(m, scale, inv);
-        if (in) {
-          if (half_n == 0) p.out_scale[row * p.os_row + w.n * p.os_block] = scale;
-          uint8_t *to = static_cast<uint8_t *>(p.out) + row * p.out_stride + w.n * kCols + half_n * 64;
+        if (r < w.rows) {
+          if (side == 0) p.out_scale[row * p.os_row + w.n * p.os_block] = scale;
+          bulk_read();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t q[8];
+          for (int j = 0; j < 4; ++j) {
+            uint32_t q[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint64_t x = acc[h * 16 + 2 * i], y = acc[h * 16 + 2 * i + 1];
-              q[i] = e4m3x4(lo32(x) * inv, hi32(x) * inv, lo32(y) * inv, hi32(y) * inv);
+            for (int i = 0; i < 4; ++i) {
+              const float2 x = sum[8 * j + 2 * i], y = sum[8 * j + 2 * i + 1];
+              q[i] = e4m3x4(x.x * inv, x.y * inv, y.x * inv, y.y * inv);
             }
-            store32(to + 32 * h, q);
+            *reinterpret_cast<uint4 *>(out_row + 16 * j) = make_uint4(q[0], q[1], q[2], q[3]);
           }
+          bulk_store(static_cast<uint8_t *>(p.out) + row * p.out_stride + w.n * kCols + side * 64, smem_addr(out_row), 64);
         }
       }
     }
+    if (tries == 1) {
+      s.stop = 1;
+      atomicOr(&g_ops_status, 1);
+    }
+    bulk_done();
   }
   tc_before_sync();
   __syncthreads();
   tc_after_sync();
-  if (warp == 9) tmem_free(tmem, 512);
+  if (warp == 0) tmem_free(tmem, 512);
 }
 
 // -------------------------------------------------------------------------------------------------------- narrow --
@@ -520,7 +614,7 @@ __global__ void __launch_bounds__(kNarrowThreads)
         for (int c = 0; c < NT; c += 16) {
           if (c < wide) {
             uint32_t v[16];
-            tmem_load16(from + (half * kParts + q) * NT + c, v);
+            tmem_load(from + (half * kParts + q) * NT + c, v);
             tmem_loaded(v);
             const float4 *sc = reinterpret_cast<const float4 *>(&s.scale[warp][half][q][c]);
 #pragma unroll
@@ -641,15 +735,21 @@ int encode(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, int64
   return RESHARD_OK;
 }
 
-// The dynamic shared memory of a kernel, allowed once per device.
+// The dynamic shared memory of a kernel, allowed once per device. regs: what its warpgroups share out among themselves; a
+// build that launches with another number would wait for registers that are not there.
 template <auto kernel>
-int allow_smem(size_t bytes) {
+int allow_smem(size_t bytes, int regs = 0) {
   static std::mutex mu;
   static uint64_t done = 0;
   int dev = 0;
   OPS_CUDA(cudaGetDevice(&dev));
   std::lock_guard<std::mutex> lock(mu);
   if (dev < 64 && (done >> dev & 1)) return RESHARD_OK;
+  if (regs) {
+    cudaFuncAttributes fa{};
+    OPS_CUDA(cudaFuncGetAttributes(&fa, kernel));
+    if (fa.numRegs != regs) return fail(RESHARD_ERR_UNSUPPORTED, "the product kernel was built with " + std::to_string(fa.numRegs) + " registers, not " + std::to_string(regs));
+  }
   OPS_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
   if (dev < 64) done |= 1ull << dev;
   return RESHARD_OK;
@@ -658,12 +758,13 @@ int allow_smem(size_t bytes) {
 template <bool Gated>
 int enqueue_wide(const Product &p, const Args &a, int sms, cudaStream_t stream) {
   CUtensorMap ma, mw;
-  int rc = encode(&ma, p.a, p.k, p.m, p.a_stride, 0, 0, kWideM);
+  int rc = encode(&ma, p.a, p.k, a.a_rows, p.a_stride, 0, 0, p.order ? 1 : kWideM);
   if (!rc) rc = encode(&mw, p.w, p.k, Gated ? 2 * p.n : p.n, p.w_stride, p.groups, p.w_batch, Gated ? 64 : 128);
-  if (!rc) rc = allow_smem<&reshard_product_wide_kernel<Gated>>(kWideSmem);
+  if (!rc) rc = allow_smem<&reshard_product_wide_kernel<Gated>>(kWideSmem, kWideRegs);
   if (rc) return rc;
   const int64_t cols = Gated ? kWideN / 2 : kWideN;
   const int64_t most = (p.m / kWideM + std::min<int64_t>(p.groups, p.m)) * ((p.n + cols - 1) / cols);
+  if (most > INT32_MAX) return fail(RESHARD_ERR_UNSUPPORTED, "too many tiles for one launch");
   const cudaError_t e = launch(reshard_product_wide_kernel<Gated>, dim3((unsigned)std::min<int64_t>(sms, most)), kWideThreads, kWideSmem, 1,
                                stream, ma, mw, a);
   return e == cudaSuccess ? RESHARD_OK : cuda_error(e, "launching reshard_product_wide_kernel");
@@ -708,6 +809,9 @@ int enqueue_product(const Product &p, cudaStream_t stream) {
   a.as_block = p.as_block;
   a.w_scale = p.w_scale;
   a.offsets = p.offsets;
+  a.order = p.order;
+  a.per_row = p.per_row;
+  a.a_rows = (int)(p.order ? p.a_rows : p.m);
   a.groups = p.groups;
   a.m = (int)p.m;
   a.n = (int)p.n;

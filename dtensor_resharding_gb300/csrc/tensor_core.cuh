@@ -10,12 +10,6 @@ namespace ops {
 
 #ifdef __CUDACC__
 
-__device__ __forceinline__ uint64_t now_ns() {
-  uint64_t t;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
-  return t;
-}
-
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
@@ -25,6 +19,13 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void bar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// 4 bytes to shared memory, and an arrival at `bar` when this thread's copies so far are there.
+__device__ __forceinline__ void copy4(uint32_t to, const void *from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void bar_arrive_copied(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
@@ -32,32 +33,33 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   return ok;
 }
 
-// A wait ends after a second at the latest: it then marks the CTA (so that its other roles stop too) and the status word.
-constexpr uint64_t kWaitNs = 1000000000ull;
+// Every wait is bounded: a try suspends the thread for some microseconds at most, and after kTries of them (seconds) the
+// wait gives up, marks the CTA (so that what it computed is not stored) and sets the status word. The loop is written
+// out because waits are on the path of every block: a clock read and a call in it cost more than the block's products.
+constexpr uint32_t kTries = 1u << 20;
 struct Stop {
   volatile int *cta;    // shared memory
   int *status;          // global memory
 };
+__device__ __forceinline__ bool bar_spin(uint32_t bar, uint32_t parity, uint32_t tries) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p, q;\n .reg .u32 n;\n mov.u32 n, %3;\n"
+               "again:\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n @p bra done;\n"
+               " sub.u32 n, n, 1;\n setp.ne.u32 q, n, 0;\n @q bra again;\n"
+               "done:\n selp.u32 %0, 1, 0, p;\n}"
+               : "=r"(ok) : "r"(bar), "r"(parity), "r"(tries) : "memory");
+  return ok;
+}
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Stop &s) {
-  if (bar_try(bar, parity)) return true;
-  const uint64_t t0 = now_ns();
-  for (;;) {
-    for (int i = 0; i < 32; ++i)
-      if (bar_try(bar, parity)) return true;
-    if (*s.cta) return false;
-    if (now_ns() - t0 > kWaitNs) {
-      *s.cta = 1;
-      atomicOr(s.status, 1);
-      return false;
-    }
+  const bool ok = bar_spin(bar, parity, kTries);
+  if (!ok) {
+    *s.cta = 1;
+    atomicOr(s.status, 1);
   }
+  return ok;
 }
-// The same for what is in flight when a CTA stops: the mark does not cut it short.
-__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) {
-  const uint64_t t0 = now_ns();
-  while (!bar_try(bar, parity) && now_ns() - t0 < kWaitNs) {
-  }
-}
+// The same for what is in flight when a CTA stops.
+__device__ __forceinline__ void bar_drain(uint32_t bar, uint32_t parity) { bar_spin(bar, parity, kTries); }
 
 // x (bytes) is a multiple of 16; what lies outside the tensor reads as 0.
 __device__ __forceinline__ void tma_2d(uint32_t to, const CUtensorMap *map, int x, int y, uint32_t bar) {
@@ -67,6 +69,12 @@ __device__ __forceinline__ void tma_2d(uint32_t to, const CUtensorMap *map, int 
 __device__ __forceinline__ void tma_3d(uint32_t to, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
   asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
                ::"r"(to), "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+
+// Four rows of a matrix, each as a tensor map whose box is one row describes it, one below the other.
+__device__ __forceinline__ void tma_rows4(uint32_t to, const CUtensorMap *map, int x, const int (&y)[4], uint32_t bar) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];"
+               ::"r"(to), "l"(map), "r"(x), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]), "r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void tmem_alloc(uint32_t slot, uint32_t columns) {   // a whole warp; a power of two, 32 .. 512
@@ -97,18 +105,51 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-// 16 columns of the warp's 32 lanes of tensor memory; the values are there after tmem_loaded().
-__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16]) {
+// Columns of the warp's 32 lanes of tensor memory; the values are there after tmem_loaded(), which the compiler keeps
+// before every use of them.
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-                 "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                : "r"(addr));
 }
-// Orders the loaded registers after the wait: the compiler may not use them before it.
 __device__ __forceinline__ void tmem_loaded(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                 "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                 "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+                 "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+                 "=r"(r[30]), "=r"(r[31])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+// Shared memory to global memory by the copy engine, 16-byte aligned and a multiple of 16 bytes; the thread's own writes
+// to `from` are ordered before it. bulk_read(): the engine is done reading what this thread has handed over.
+__device__ __forceinline__ void bulk_store(void *to, uint32_t from, uint32_t bytes) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(from), "r"(bytes) : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void bulk_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ float shared_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ bool elect_one() {     // one lane of a converged warp
@@ -117,15 +158,11 @@ __device__ __forceinline__ bool elect_one() {     // one lane of a converged war
   return p;
 }
 
-// Two fp32 multiply-adds in one instruction.
-__device__ __forceinline__ void fma2(uint64_t &acc, uint32_t x0, uint32_t x1, float s) {
-  uint64_t x, ss;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "r"(x0), "r"(x1));
-  asm("mov.b64 %0, {%1, %1};" : "=l"(ss) : "r"(__float_as_uint(s)));
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(x), "l"(ss));
-}
-__device__ __forceinline__ float lo32(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float hi32(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+// Registers of a warpgroup's threads from here on; the shares of a CTA's warpgroups sum to what it was launched with.
+template <int N>
+__device__ __forceinline__ void registers_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 #endif  // __CUDACC__
 

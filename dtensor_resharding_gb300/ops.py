@@ -51,6 +51,9 @@ def _bad(what: str) -> None:
     raise ReshardError(RESHARD_ERR_INVALID_ARG, what)
 
 
+# The checks below cover what the C call cannot see (types, shapes, layout and device of a tensor). They are on the path
+# of calls that take a few microseconds on the GPU, so each looks at a tensor once.
+
 def _code(t: torch.Tensor, name: str) -> int:
     code = _CODES.get(t.dtype)
     if code is None:
@@ -58,50 +61,59 @@ def _code(t: torch.Tensor, name: str) -> int:
     return code
 
 
-def _want(t: torch.Tensor, name: str, dim: int, dtype: Optional[torch.dtype] = None, dense: bool = False,
-          shape: Optional[tuple] = None, device: Optional[torch.device] = None) -> None:
-    """What ctypes cannot see: dimensions, type, layout and device of a tensor."""
-    if t.dim() != dim:
-        _bad(f"{name} must have {dim} dimensions, not {t.dim()}")
-    if dtype is not None and t.dtype != dtype:
-        _bad(f"{name} must be {dtype}, not {t.dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        _bad(f"{name} must have shape {shape}, not {tuple(t.shape)}")
-    if device is not None and t.device != device:
-        _bad(f"{name} is on {t.device}, not on {device}")
-    if dense:
-        if not t.is_contiguous():
-            _bad(f"{name} must be contiguous")
-    elif t.shape[-1] > 1 and t.stride(-1) != 1:
+def _matrix(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
+    """(rows, columns, row stride); a single row's stride may be anything."""
+    shape = t.shape
+    if len(shape) != 2:
+        _bad(f"{name} must have 2 dimensions, not {len(shape)}")
+    rows, cols = shape
+    step, inner = t.stride()
+    if inner != 1 and cols > 1:
         _bad(f"{name} must have contiguous rows")
+    return rows, cols, step if rows > 1 else max(step, cols)
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    """The distance of t's rows; that of a single row (or column) may be anything."""
-    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
+def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, like: torch.Tensor) -> int:
+    """The address of a contiguous tensor of that type and shape on `like`'s device."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != like.device:
+        _bad(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {like.device}, not {t.dtype} of shape "
+             f"{tuple(t.shape)}, strides {t.stride()} on {t.device}")
+    return t.data_ptr()
 
 
-class _On:
-    """The device and stream of a call: enters them only where they are not the current ones."""
+def _output(out: Optional[torch.Tensor], rows: int, cols: int, dtype: torch.dtype, like: torch.Tensor) -> torch.Tensor:
+    if out is None:
+        return torch.empty((rows, cols), dtype=dtype, device=like.device)
+    if out.dtype is not dtype or out.shape != (rows, cols) or out.device != like.device:
+        _bad(f"out must be {dtype} of shape {(rows, cols)} on {like.device}, not {out.dtype} of shape {tuple(out.shape)} on {out.device}")
+    return out
+
+
+def _here(t: torch.Tensor, stream) -> Optional[int]:
+    """The raw stream of a call if `t`'s device and that stream are the current ones; None otherwise."""
+    if not t.is_cuda:
+        _bad(f"tensors must be on a CUDA device, not on {t.device}")
+    index = t.get_device()
+    if index != torch._C._cuda_getDevice():
+        return None
+    raw = torch._C._cuda_getCurrentRawStream(index)
+    if stream is None or raw == (stream if isinstance(stream, int) else stream.cuda_stream):
+        return raw
+    return None
+
+
+class _on:
+    """Makes a tensor's device, and a stream, the current ones."""
 
     def __init__(self, t: torch.Tensor, stream):
-        if not t.is_cuda:
-            _bad(f"tensors must be on a CUDA device, not on {t.device}")
-        self.device = t.device
-        self.enter = []
-        if t.device.index != torch.cuda.current_device():
-            self.enter.append(torch.cuda.device(t.device))
-        if stream is None:
-            self.stream = torch._C._cuda_getCurrentRawStream(t.device.index)
-        else:
-            self.stream = stream if isinstance(stream, int) else stream.cuda_stream
-            if self.stream != torch._C._cuda_getCurrentRawStream(t.device.index):
-                self.enter.append(torch.cuda.stream(torch.cuda.ExternalStream(self.stream, device=t.device)))
+        self.enter = [torch.cuda.device(t.device)]
+        if stream is not None:
+            raw = stream if isinstance(stream, int) else stream.cuda_stream
+            self.enter.append(torch.cuda.stream(torch.cuda.ExternalStream(raw, device=t.device)))
 
     def __enter__(self):
         for e in self.enter:
             e.__enter__()
-        return self
 
     def __exit__(self, *exc):
         for e in reversed(self.enter):
@@ -125,52 +137,58 @@ def reshard_route(logits: torch.Tensor, k: int, *, score="softmax", bias: Option
     ``groups`` only the ``groups_kept`` groups whose ``group_top`` best experts have the largest sum take part. The weights are
     the chosen scores without the bias, divided by their sum if ``renormalize``, times ``scale``. A logit of -inf or NaN
     is never chosen: missing choices have id -1 and weight 0."""
-    _want(logits, "logits", 2)
-    T, E = logits.shape
-    with _On(logits, stream) as on:
-        if bias is not None:
-            _want(bias, "bias", 1, torch.float32, True, (E,), on.device)
-        weights = torch.empty((T, max(0, k)), dtype=torch.float32, device=on.device)
-        ids = torch.empty((T, max(0, k)), dtype=torch.int32, device=on.device)
-        _check(LIB.reshard_route(logits.data_ptr(), _code(logits, "logits"), T, E, _row_stride(logits),
-                                 None if bias is None else bias.data_ptr(), _score(score), groups, groups_kept, group_top, k,
-                                 renormalize, scale, weights.data_ptr(), ids.data_ptr(), on.stream))
+    here = _here(logits, stream)
+    if here is None:
+        with _on(logits, stream):
+            return reshard_route(logits, k, score=score, bias=bias, groups=groups, groups_kept=groups_kept, group_top=group_top,
+                                 renormalize=renormalize, scale=scale)
+    T, E, step = _matrix(logits, "logits")
+    code = _code(logits, "logits")
+    at_bias = None if bias is None else _dense(bias, "bias", torch.float32, (E,), logits)
+    device = logits.device
+    weights = torch.empty((T, max(0, k)), dtype=torch.float32, device=device)
+    ids = torch.empty((T, max(0, k)), dtype=torch.int32, device=device)
+    _check(LIB.reshard_route(logits.data_ptr(), code, T, E, step, at_bias, _score(score), groups, groups_kept, group_top, k,
+                             renormalize, scale, weights.data_ptr(), ids.data_ptr(), here))
     return weights, ids
 
 
 def reshard_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, *, score="softmax",
                            renormalize: bool = True, scale: float = 1.0, out: Optional[torch.Tensor] = None,
                            stream=None) -> torch.Tensor:
-    """The gradient to ``logits`` of ``reshard_route``'s weights, the choice ``ids`` held fixed, in the logits' type."""
-    _want(logits, "logits", 2)
-    _want(ids, "ids", 2, torch.int32, True)
-    T, E = logits.shape
-    k = ids.shape[1]
-    with _On(logits, stream) as on:
-        _want(ids, "ids", 2, shape=(T, k), device=on.device, dense=True)
-        _want(grad_weights, "grad_weights", 2, torch.float32, True, (T, k), on.device)
-        if out is None:
-            out = torch.empty((T, E), dtype=logits.dtype, device=on.device)
-        else:
-            _want(out, "out", 2, logits.dtype, False, (T, E), on.device)
-        _check(LIB.reshard_route_backward(grad_weights.data_ptr(), logits.data_ptr(), _code(logits, "logits"), T, E,
-                                          _row_stride(logits), ids.data_ptr(), k, _score(score), renormalize, scale,
-                                          out.data_ptr(), _row_stride(out), on.stream))
+    """The gradient to ``logits`` of ``reshard_route``'s weights, the choice ``ids`` held fixed, in the logits' type.
+
+    ``grad_weights`` is copied where it is not contiguous (a broadcast gradient)."""
+    here = _here(logits, stream)
+    if here is None:
+        with _on(logits, stream):
+            return reshard_route_backward(grad_weights, logits, ids, score=score, renormalize=renormalize, scale=scale, out=out)
+    T, E, step = _matrix(logits, "logits")
+    code = _code(logits, "logits")
+    k = _matrix(ids, "ids")[1]
+    at_ids = _dense(ids, "ids", torch.int32, (T, k), logits)
+    grad_weights = grad_weights.contiguous()
+    at_grad = _dense(grad_weights, "grad_weights", torch.float32, (T, k), logits)
+    out = _output(out, T, E, logits.dtype, logits)
+    _check(LIB.reshard_route_backward(at_grad, logits.data_ptr(), code, T, E, step, at_ids, k, _score(score), renormalize, scale,
+                                      out.data_ptr(), _matrix(out, "out")[2], here))
     return out
 
 
 def reshard_dispatch(ids: torch.Tensor, experts: int, first_expert: int = 0, stream=None) -> Tuple[torch.Tensor, ...]:
     """(offsets [experts + 1], order [slots], position [slots]) int32: the slots (flat indices of ``ids``) sorted by expert, for
     experts first_expert .. first_expert + experts - 1. Expert e's slots are order[offsets[e]:offsets[e + 1]], ascending;
-    position is a slot's place in order, -1 for an id outside the range."""
-    _want(ids, "ids", ids.dim(), torch.int32, True)
-    n = ids.numel()
-    with _On(ids, stream) as on:
-        offsets = torch.empty(max(0, experts) + 1, dtype=torch.int32, device=on.device)
-        order = torch.empty(n, dtype=torch.int32, device=on.device)
-        position = torch.empty(n, dtype=torch.int32, device=on.device)
-        _check(LIB.reshard_dispatch(ids.data_ptr(), n, first_expert, experts, offsets.data_ptr(), order.data_ptr(),
-                                    position.data_ptr(), on.stream))
+    position is a slot's place in order, -1 for an id outside the range. Places from offsets[experts] on are not written."""
+    here = _here(ids, stream)
+    if here is None:
+        with _on(ids, stream):
+            return reshard_dispatch(ids, experts, first_expert)
+    at_ids = _dense(ids, "ids", torch.int32, ids.shape, ids)
+    n, device = ids.numel(), ids.device
+    offsets = torch.empty(max(0, experts) + 1, dtype=torch.int32, device=device)
+    order = torch.empty(n, dtype=torch.int32, device=device)
+    position = torch.empty(n, dtype=torch.int32, device=device)
+    _check(LIB.reshard_dispatch(at_ids, n, first_expert, experts, offsets.data_ptr(), order.data_ptr(), position.data_ptr(), here))
     return offsets, order, position
 
 
@@ -186,39 +204,54 @@ def reshard_quantize_rows(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, t
     """(values [rows, cols] float8_e4m3fn, scale [rows, ceil(cols / 128)] float32) of x [rows, cols] in blocks of 1 x 128.
 
     The values' rows start every multiple of 16 bytes; the scales are stored block by block (a transposed view)."""
-    _want(x, "x", 2)
-    M, K = x.shape
-    with _On(x, stream) as on:
-        q = _pitched((M, K), on.device)
-        scale = torch.empty((-(-K // 128), M), dtype=torch.float32, device=on.device)
-        _check(LIB.reshard_quantize_rows(x.data_ptr(), _code(x, "x"), M, K, _row_stride(x), q.data_ptr(), q.stride(0),
-                                         scale.data_ptr(), 1, max(1, M), on.stream))
+    here = _here(x, stream)
+    if here is None:
+        with _on(x, stream):
+            return reshard_quantize_rows(x)
+    M, K, step = _matrix(x, "x")
+    code = _code(x, "x")
+    q = _pitched((M, K), x.device)
+    scale = torch.empty((-(-K // 128), M), dtype=torch.float32, device=x.device)
+    _check(LIB.reshard_quantize_rows(x.data_ptr(), code, M, K, step, q.data_ptr(), q.stride(0), scale.data_ptr(), 1, max(1, M), here))
     return q, scale.t()
 
 
 def reshard_quantize_blocks(w: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """(values float8_e4m3fn, scale float32) of w [rows, cols] or [batch, rows, cols] in blocks of 128 x 128: the scale has the
     last two extents divided by 128, rounded up, the layout that ``reshard_plan_blockwise_fp8`` moves."""
+    here = _here(w, stream)
+    if here is None:
+        with _on(w, stream):
+            return reshard_quantize_blocks(w)
     if w.dim() not in (2, 3):
         _bad(f"w must have 2 or 3 dimensions, not {w.dim()}")
-    _want(w, "w", w.dim())
     N, K = w.shape[-2:]
-    E = w.shape[0] if w.dim() == 3 else 1
-    with _On(w, stream) as on:
-        q = _pitched(tuple(w.shape), on.device)
-        scale = torch.empty((*w.shape[:-2], -(-N // 128), -(-K // 128)), dtype=torch.float32, device=on.device)
-        _check(LIB.reshard_quantize_blocks(w.data_ptr(), _code(w, "w"), E, N, K, w.stride(0) if w.dim() == 3 else 0,
-                                           _row_stride(w), q.data_ptr(), q.stride(0) if w.dim() == 3 else 0, q.stride(-2),
-                                           scale.data_ptr(), on.stream))
+    if K > 1 and w.stride(-1) != 1:
+        _bad("w must have contiguous rows")
+    E, batch = (w.shape[0], w.stride(0)) if w.dim() == 3 else (1, 0)
+    code = _code(w, "w")
+    q = _pitched(tuple(w.shape), w.device)
+    scale = torch.empty((*w.shape[:-2], -(-N // 128), -(-K // 128)), dtype=torch.float32, device=w.device)
+    _check(LIB.reshard_quantize_blocks(w.data_ptr(), code, E, N, K, batch, w.stride(-2) if N > 1 else max(K, w.stride(-2)), q.data_ptr(),
+                                       q.stride(0) if q.dim() == 3 else 0, q.stride(-2), scale.data_ptr(), here))
     return q, scale
 
 
-def _weights(w: torch.Tensor, scale: torch.Tensor, name: str, dim: int, device) -> None:
-    _want(w, name, dim, None, False, None, device)
-    if w.dtype not in (_FP8, torch.uint8):
+def _weights(w: torch.Tensor, scale: torch.Tensor, name: str, dim: int, like: torch.Tensor) -> Tuple[int, ...]:
+    """(address, batch stride, row stride, scale's address) of 8-bit weights."""
+    shape, stride = w.shape, w.stride()
+    if len(shape) != dim:
+        _bad(f"{name} must have {dim} dimensions, not {len(shape)}")
+    if w.dtype is not _FP8 and w.dtype is not torch.uint8:
         _bad(f"{name} must be float8_e4m3fn (or its bytes as uint8), not {w.dtype}")
-    N, K = w.shape[-2:]
-    _want(scale, f"{name}'s scale", dim, torch.float32, True, (*w.shape[:-2], -(-N // 128), -(-K // 128)), device)
+    N, K = shape[-2:]
+    if stride[-1] != 1 and K > 1:
+        _bad(f"{name} must have contiguous rows")
+    if w.device != like.device:
+        _bad(f"{name} is on {w.device}, not on {like.device}")
+    at_scale = _dense(scale, f"{name}'s scale", torch.float32, (*shape[:-2], -(-N // 128), -(-K // 128)), like)
+    # one row has no pitch of its own: the next multiple of 16
+    return w.data_ptr(), stride[0] if dim == 3 else 0, stride[-2] if N > 1 else -(-K // 16) * 16, at_scale
 
 
 def reshard_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *,
@@ -229,55 +262,46 @@ def reshard_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, 
     ``w`` is [n, k], or [groups, n, k] with ``offsets`` [groups + 1] int32 (on the device): rows offsets[g]:offsets[g + 1] of
     ``a`` meet w[g], rows beyond the last offset are left as they are in ``out``. float8 values may also come as the
     uint8 bytes that a reshard moved."""
-    _want(a, "a", 2)
-    if a.dtype not in (_FP8, torch.uint8):
+    here = _here(a, stream)
+    if here is None:
+        with _on(a, stream):
+            return reshard_matmul_fp8(a, a_scale, w, w_scale, offsets=offsets, out_dtype=out_dtype, out=out)
+    M, K, step = _matrix(a, "a")
+    if a.dtype is not _FP8 and a.dtype is not torch.uint8:
         _bad(f"a must be float8_e4m3fn (or its bytes as uint8), not {a.dtype}")
-    M, K = a.shape
-    with _On(a, stream) as on:
-        _weights(w, w_scale, "w", 2 if offsets is None else 3, on.device)
-        N = w.shape[-2]
-        if w.shape[-1] != K:
-            _bad(f"a has {K} columns, w {w.shape[-1]}")
-        groups = w.shape[0] if offsets is not None else 1
-        if offsets is not None:
-            _want(offsets, "offsets", 1, torch.int32, True, (groups + 1,), on.device)
-        if a_scale.dtype != torch.float32 or tuple(a_scale.shape) != (M, -(-K // 128)) or a_scale.device != on.device:
-            _bad(f"a_scale must be float32 [{M}, {-(-K // 128)}] on {on.device}")
-        if out is None:
-            out = torch.empty((M, N), dtype=out_dtype, device=on.device)
-        else:
-            _want(out, "out", 2, None, False, (M, N), on.device)
-        _check(LIB.reshard_matmul_fp8(a.data_ptr(), _row_stride(a) if M > 1 else -(-max(K, a.stride(0)) // 16) * 16,
-                                      a_scale.data_ptr(), max(1, a_scale.stride(0)), max(1, a_scale.stride(1)), w.data_ptr(),
-                                      w.stride(0) if offsets is not None else 0, _pitch_of(w), w_scale.data_ptr(),
-                                      None if offsets is None else offsets.data_ptr(), groups, M, N, K, out.data_ptr(),
-                                      _code(out, "out"), _row_stride(out), on.stream))
+    at_w, batch, pitch, at_ws = _weights(w, w_scale, "w", 2 if offsets is None else 3, a)
+    N = w.shape[-2]
+    if w.shape[-1] != K:
+        _bad(f"a has {K} columns, w {w.shape[-1]}")
+    groups = 1 if offsets is None else w.shape[0]
+    at_offsets = None if offsets is None else _dense(offsets, "offsets", torch.int32, (groups + 1,), a)
+    if a_scale.dtype is not torch.float32 or a_scale.shape != (M, -(-K // 128)) or a_scale.device != a.device:
+        _bad(f"a_scale must be float32 of shape {(M, -(-K // 128))} on {a.device}, not {a_scale.dtype} of shape {tuple(a_scale.shape)}")
+    out = _output(out, M, N, out_dtype if out is None else out.dtype, a)
+    _check(LIB.reshard_matmul_fp8(a.data_ptr(), step if M > 1 else -(-step // 16) * 16, a_scale.data_ptr(), max(1, a_scale.stride(0)),
+                                  max(1, a_scale.stride(1)), at_w, batch, pitch, at_ws, at_offsets, groups, M, N, K,
+                                  out.data_ptr(), _code(out, "out"), _matrix(out, "out")[2], here))
     return out
-
-
-def _pitch_of(w: torch.Tensor) -> int:
-    """The row pitch of weights; one row has none of its own, and takes the next multiple of 16."""
-    return w.stride(-2) if w.shape[-2] > 1 else -(-w.shape[-1] // 16) * 16
 
 
 def reshard_linear_fp8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *, out: Optional[torch.Tensor] = None,
                        stream=None) -> torch.Tensor:
     """out [m, n] = Q(x) w^T in x's type: x [m, k] is quantized by rows, ``w`` [n, k] holds 8-bit values and block scales."""
-    _want(x, "x", 2)
-    M, K = x.shape
-    with _On(x, stream) as on:
-        _weights(w, w_scale, "w", 2, on.device)
-        N = w.shape[0]
-        if w.shape[1] != K:
-            _bad(f"x has {K} columns, w {w.shape[1]}")
-        if out is None:
-            out = torch.empty((M, N), dtype=x.dtype, device=on.device)
-        else:
-            _want(out, "out", 2, x.dtype, False, (M, N), on.device)
-        need = LIB.reshard_linear_fp8_workspace(M, K)
-        space = torch.empty(need, dtype=torch.uint8, device=on.device)
-        _check(LIB.reshard_linear_fp8(x.data_ptr(), _code(x, "x"), M, K, _row_stride(x), w.data_ptr(), _pitch_of(w), w_scale.data_ptr(),
-                                      N, out.data_ptr(), _row_stride(out), space.data_ptr(), need, on.stream))
+    here = _here(x, stream)
+    if here is None:
+        with _on(x, stream):
+            return reshard_linear_fp8(x, w, w_scale, out=out)
+    M, K, step = _matrix(x, "x")
+    code = _code(x, "x")
+    at_w, _, pitch, at_ws = _weights(w, w_scale, "w", 2, x)
+    N = w.shape[0]
+    if w.shape[1] != K:
+        _bad(f"x has {K} columns, w {w.shape[1]}")
+    out = _output(out, M, N, x.dtype, x)
+    need = LIB.reshard_linear_fp8_workspace(M, K)
+    space = torch.empty(need, dtype=torch.uint8, device=x.device)
+    _check(LIB.reshard_linear_fp8(x.data_ptr(), code, M, K, step, at_w, pitch, at_ws, N, out.data_ptr(), _matrix(out, "out")[2],
+                                  space.data_ptr(), need, here))
     return out
 
 
@@ -289,31 +313,27 @@ def reshard_experts_fp8(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tenso
     x [tokens, hidden]; ids int32 and weights float32 [tokens, k] (``reshard_route``); w13 [experts, 2 ffn, hidden] (gate rows,
     then up rows) and w2 [experts, hidden, ffn] with their block scales; ffn a multiple of 128. Ids outside this
     rank's experts first_expert .. first_expert + experts - 1 add nothing."""
-    _want(x, "x", 2)
-    T, H = x.shape
-    with _On(x, stream) as on:
-        _want(ids, "ids", 2, torch.int32, True, None, on.device)
-        k = ids.shape[1]
-        if ids.shape[0] != T:
-            _bad(f"ids must have {T} rows, not {ids.shape[0]}")
-        _want(weights, "weights", 2, torch.float32, True, (T, k), on.device)
-        _weights(w13, w13_scale, "w13", 3, on.device)
-        _weights(w2, w2_scale, "w2", 3, on.device)
-        E, I = w2.shape[0], w2.shape[2]
-        if tuple(w13.shape) != (E, 2 * I, H) or w2.shape[1] != H:
-            _bad(f"w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} do not fit x with {H} columns: [experts, 2 ffn, hidden] and "
-                 "[experts, hidden, ffn]")
-        if out is None:
-            out = torch.empty((T, H), dtype=x.dtype, device=on.device)
-        else:
-            _want(out, "out", 2, x.dtype, False, (T, H), on.device)
-        code = _code(x, "x")
-        need = LIB.reshard_experts_fp8_workspace(T, k, E, H, I, code)
-        space = torch.empty(need, dtype=torch.uint8, device=on.device)
-        _check(LIB.reshard_experts_fp8(x.data_ptr(), code, T, H, _row_stride(x), ids.data_ptr(), weights.data_ptr(), k, first_expert, E, I,
-                                       w13.data_ptr(), w13.stride(0), _pitch_of(w13), w13_scale.data_ptr(), w2.data_ptr(),
-                                       w2.stride(0), _pitch_of(w2), w2_scale.data_ptr(), out.data_ptr(), _row_stride(out),
-                                       space.data_ptr(), need, on.stream))
+    here = _here(x, stream)
+    if here is None:
+        with _on(x, stream):
+            return reshard_experts_fp8(x, ids, weights, w13, w13_scale, w2, w2_scale, first_expert=first_expert, out=out)
+    T, H, step = _matrix(x, "x")
+    code = _code(x, "x")
+    k = _matrix(ids, "ids")[1]
+    at_ids = _dense(ids, "ids", torch.int32, (T, k), x)
+    at_weights = _dense(weights, "weights", torch.float32, (T, k), x)
+    at_w13, batch13, pitch13, at_s13 = _weights(w13, w13_scale, "w13", 3, x)
+    at_w2, batch2, pitch2, at_s2 = _weights(w2, w2_scale, "w2", 3, x)
+    E, _, I = w2.shape
+    if w13.shape != (E, 2 * I, H) or w2.shape[1] != H:
+        _bad(f"w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} do not fit x with {H} columns: [experts, 2 ffn, hidden] and "
+             "[experts, hidden, ffn]")
+    out = _output(out, T, H, x.dtype, x)
+    need = LIB.reshard_experts_fp8_workspace(T, k, E, H, I, code)
+    space = torch.empty(need, dtype=torch.uint8, device=x.device)
+    _check(LIB.reshard_experts_fp8(x.data_ptr(), code, T, H, step, at_ids, at_weights, k, first_expert, E, I, at_w13, batch13, pitch13,
+                                   at_s13, at_w2, batch2, pitch2, at_s2, out.data_ptr(), _matrix(out, "out")[2], space.data_ptr(), need,
+                                   here))
     return out
 
 
