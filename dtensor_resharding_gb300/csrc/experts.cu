@@ -55,7 +55,7 @@ struct ExpertLayout {
   QuantizedRows x, h;
   ExpertLayout(int64_t tokens, int k, int experts, int64_t hidden, int64_t ffn, int dtype)
       : slots(tokens * k), offsets(up(4 * (experts + 1), kAlign)), order(up(4 * slots, kAlign)), position(order),
-        y(up(slots * up(hidden, 16) * element_bytes(dtype), kAlign)), x(slots, hidden), h(slots, ffn) {}
+        y(up(slots * up(hidden, 16) * element_bytes(dtype), kAlign)), x(tokens, hidden), h(slots, ffn) {}
   int64_t bytes() const { return offsets + order + position + y + x.bytes() + h.bytes(); }
 };
 
@@ -141,6 +141,7 @@ extern "C" int reshard_linear_fp8(const void *x, int dtype, int64_t m, int64_t k
   p.a = q, p.a_stride = l.pitch, p.a_scale = scale, p.as_row = 1, p.as_block = m;
   p.w = static_cast<const uint8_t *>(w), p.w_batch = n * w_stride, p.w_stride = w_stride, p.w_scale = w_scale;
   p.m = m, p.n = n, p.k = k;
+  p.early = true;
   p.out = out, p.out_dtype = dtype, p.out_stride = out_stride;
   return enqueue_product(p, stream);
 }
@@ -193,21 +194,21 @@ extern "C" int reshard_experts_fp8(const void *x, int dtype, int64_t tokens, int
   float *hs = reinterpret_cast<float *>(take(l.h.scales));
   int rc = enqueue_dispatch(ids, l.slots, first_expert, experts, offsets, order, position, stream);
   if (rc) return rc;
-  Rows r{x, dtype, l.slots, hidden, row_stride, xq, l.x.pitch, xs, 1, l.slots};
-  r.order = order;
-  r.count = offsets + experts;
-  r.per_row = k;
-  if ((rc = enqueue_quantize_rows(r, stream))) return rc;
+  // tokens are quantized once; the first product gathers each expert's rows of them
+  if ((rc = enqueue_quantize_rows(Rows{x, dtype, tokens, hidden, row_stride, xq, l.x.pitch, xs, 1, tokens}, stream))) return rc;
   Product p{};
-  p.a = xq, p.a_stride = l.x.pitch, p.a_scale = xs, p.as_row = 1, p.as_block = l.slots;
+  p.a = xq, p.a_stride = l.x.pitch, p.a_scale = xs, p.as_row = 1, p.as_block = tokens;
+  p.order = order, p.per_row = k, p.a_rows = tokens;
   p.w = static_cast<const uint8_t *>(w13), p.w_batch = map_batch(experts, w13_batch_stride, 2 * ffn, w13_stride), p.w_stride = w13_stride;
   p.w_scale = w13_scale, p.offsets = offsets, p.groups = experts, p.m = l.slots, p.n = ffn, p.k = hidden;
+  p.early = true;      // behind the quantization; the sort before it has ended when that begins
   p.out = hq, p.out_stride = l.h.pitch, p.gated = true, p.out_scale = hs, p.os_row = 1, p.os_block = l.slots;
   if ((rc = enqueue_product(p, stream))) return rc;
   Product p2{};
   p2.a = hq, p2.a_stride = l.h.pitch, p2.a_scale = hs, p2.as_row = 1, p2.as_block = l.slots;
   p2.w = static_cast<const uint8_t *>(w2), p2.w_batch = map_batch(experts, w2_batch_stride, hidden, w2_stride), p2.w_stride = w2_stride;
   p2.w_scale = w2_scale, p2.offsets = offsets, p2.groups = experts, p2.m = l.slots, p2.n = hidden, p2.k = ffn;
+  p2.early = true;
   p2.out = y, p2.out_dtype = dtype, p2.out_stride = up(hidden, 16);
   if ((rc = enqueue_product(p2, stream))) return rc;
   return enqueue_combine(y, dtype, up(hidden, 16), position, weights, tokens, k, hidden, out, out_stride, stream);

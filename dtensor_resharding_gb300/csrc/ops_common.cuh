@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 #include <string>
 #include <utility>
 
@@ -81,6 +82,28 @@ cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, int block, size_t smem, 
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+#ifdef __CUDACC__
+// The dynamic shared memory of a kernel, allowed once per device. regs: what its warpgroups share out among themselves; a
+// build that launches with another number would wait for registers that are not there.
+template <auto kernel>
+int allow_smem(size_t bytes, int regs = 0) {
+  static std::mutex mu;
+  static uint64_t done = 0;
+  int dev = 0;
+  OPS_CUDA(cudaGetDevice(&dev));
+  std::lock_guard<std::mutex> lock(mu);
+  if (dev < 64 && (done >> dev & 1)) return RESHARD_OK;
+  if (regs) {
+    cudaFuncAttributes fa{};
+    OPS_CUDA(cudaFuncGetAttributes(&fa, kernel));
+    if (fa.numRegs != regs) return fail(RESHARD_ERR_UNSUPPORTED, "the kernel was built with " + std::to_string(fa.numRegs) + " registers, not " + std::to_string(regs));
+  }
+  OPS_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
+  if (dev < 64) done |= 1ull << dev;
+  return RESHARD_OK;
+}
+#endif
+
 // The enqueue halves of the public calls: arguments are checked by the caller.
 struct Rows {                 // a quantization by rows
   const void *x;
@@ -90,9 +113,6 @@ struct Rows {                 // a quantization by rows
   int64_t q_stride;
   float *scale;
   int64_t scale_row, scale_block;
-  const int32_t *order = nullptr;    // row r reads x row order[r] / per_row; NULL: row r
-  const int32_t *count = nullptr;    // rows in use, on the device; NULL: all
-  int per_row = 1;
 };
 int enqueue_quantize_rows(const Rows &r, cudaStream_t stream);
 int enqueue_dispatch(const int32_t *ids, int64_t slots, int first, int experts, int32_t *offsets, int32_t *order,
@@ -113,6 +133,7 @@ struct Product {              // out[m, n] = sum_k a[m, k] w[n, k], both as 8-bi
   const int32_t *order = nullptr;    // row r of the product is row order[r] / per_row of a's a_rows; NULL: row r
   int per_row = 1;
   int64_t a_rows = 0;
+  bool early = false;                // enqueued right behind a kernel of ours that wrote none of w, offsets, order
   int64_t m, n, k;
   void *out;
   int out_dtype;
@@ -128,9 +149,11 @@ int enqueue_product(const Product &p, cudaStream_t stream);
 
 #ifdef __CUDACC__
 
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_enter() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_wait();
+  grid_release();
 }
 
 __device__ __forceinline__ float to_f32(float v) { return v; }

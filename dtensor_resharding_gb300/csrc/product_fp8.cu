@@ -63,6 +63,24 @@ __device__ __forceinline__ int source_row(const Args &p, int r) {
 
 __device__ __forceinline__ float silu_times(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
+// tiles[g] = tiles of M rows before group g. One warp.
+template <int M>
+__device__ __forceinline__ void row_tiles(const int *off, int *tiles, int groups, int lane) {
+  int base = 0;
+  for (int g0 = 0; g0 < groups; g0 += 32) {
+    const int g = g0 + lane;
+    const int own = g < groups ? max(0, off[g + 1] - off[g] + M - 1) / M : 0;
+    int sum = own;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFull, sum, o);
+      if (lane >= o) sum += x;
+    }
+    if (g < groups) tiles[g] = base + sum - own;
+    base += __shfl_sync(kFull, sum, 31);
+  }
+  if (lane == 0) tiles[groups] = base;
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b);
 template <>
@@ -184,21 +202,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   grid_enter();
   for (int g = tid; g <= p.groups; g += kWideThreads) s.off[g] = row_offset(p, g);
   __syncthreads();
-  if (warp == 4) {                     // running sum of the groups' row tiles
-    int base = 0;
-    for (int g0 = 0; g0 < p.groups; g0 += 32) {
-      const int g = g0 + lane;
-      const int own = g < p.groups ? max(0, s.off[g + 1] - s.off[g] + kWideM - 1) / kWideM : 0;
-      int sum = own;
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(kFull, sum, o);
-        if (lane >= o) sum += x;
-      }
-      if (g < p.groups) s.tiles[g] = base + sum - own;
-      base += __shfl_sync(kFull, sum, 31);
-    }
-    if (lane == 0) s.tiles[p.groups] = base;
-  }
+  if (warp == 4) row_tiles<kWideM>(s.off, s.tiles, p.groups, lane);
   tc_before_sync();
   __syncthreads();
   tc_after_sync();
@@ -441,29 +445,53 @@ template <int NT, bool Gated>
 struct Narrow {
   static constexpr int kParts = Gated ? 2 : 1;
   static constexpr int kStageBytes = (kParts * kNarrowM + NT) * kBlockK;
-  static constexpr int kStages = 110592 / kStageBytes;     // two CTAs an SM
+  static constexpr int kPerSm = NT * kParts <= 64 ? 2 : 1;       // CTAs an SM: as many as the sums' registers allow
+  static constexpr int kStages = (kPerSm == 2 ? 107520 : 215040) / kStageBytes;
   static constexpr int kPartial = NT * kNarrowM * 4 * kParts;   // a CTA's sums, in stage memory, for the cluster
   static constexpr int kColumns = 2 * NT * kParts < 32 ? 32 : 2 * NT * kParts;
   static_assert(kStages >= 2 && kPartial <= kStages * kStageBytes, "stages");
   struct Shared {
-    uint64_t full[kStages], empty[kStages], done[2], taken[2], last;
+    uint64_t full[kStages], empty[kStages], done[2], taken[2], paired[2], last;
     uint32_t tmem;
     int stop;
-    int tile[4];                   // group, first row, rows, column tile
     alignas(16) float scale[4][2][kParts][NT];       // per epilogue warp, two blocks
-    uint32_t amax[4][NT];
+    uint32_t amax[2][4][NT];
+    int off[RESHARD_MAX_GROUPS + 1], tiles[RESHARD_MAX_GROUPS + 1];   // row offsets; tiles of rows before each group
   };
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + sizeof(Shared);
+  static constexpr size_t kSmem = (size_t)kStages * kStageBytes + sizeof(Shared);
+  static_assert(kSmem <= (kPerSm == 2 ? 115712 : 232448), "shared memory of a CTA");
 };
 
+struct NarrowTile {
+  int g, row, rows, n;     // group, first row, rows, column tile
+};
+template <int NT>
+__device__ __forceinline__ NarrowTile narrow_tile(const int *off, const int *tiles, int groups, uint32_t ntiles, uint32_t t) {
+  int lo = 0, hi = groups - 1;          // the last group whose first tile is <= t
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tiles[mid] * ntiles <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  const uint32_t l = t - tiles[lo] * ntiles, m = l / ntiles;      // column tiles first: w is read in order
+  NarrowTile r;
+  r.g = lo;
+  r.row = off[lo] + m * NT;
+  r.rows = min(NT, off[lo + 1] - r.row);
+  r.n = l - m * ntiles;
+  return r;
+}
+
+// early: the kernel before this one on the stream wrote neither weights nor offsets nor order, and had itself waited for
+// what did: their reads need not wait for its end, and the first weights are on their way while it runs.
 template <int NT, bool Gated>
-__global__ void __launch_bounds__(kNarrowThreads)
-    reshard_product_narrow_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mw, const Args p, const int split) {
+__global__ void __launch_bounds__(kNarrowThreads, Narrow<NT, Gated>::kPerSm)
+    reshard_product_narrow_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mw, const __grid_constant__ Args p,
+                                  const int split, const bool early) {
   using C = Narrow<NT, Gated>;
   using Shared = typename C::Shared;
   constexpr int kStages = C::kStages, kParts = C::kParts;
-  extern __shared__ uint8_t raw[];
-  uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) uint8_t stages[];
   Shared &s = *reinterpret_cast<Shared *>(stages + (size_t)kStages * C::kStageBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Stop stop{&s.stop, &g_ops_status};
@@ -475,92 +503,102 @@ __global__ void __launch_bounds__(kNarrowThreads)
     for (int i = 0; i < 2; ++i) {
       bar_init(smem_addr(&s.done[i]), 1);
       bar_init(smem_addr(&s.taken[i]), 4);
+      bar_init(smem_addr(&s.paired[i]), 4);
     }
     bar_init(smem_addr(&s.last), 1);
-    s.stop = 0;
+    s.stop = smem_addr(stages) & 1023;       // 0: the swizzle needs it
+    if (s.stop) atomicOr(&g_ops_status, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 5) tmem_alloc(smem_addr(&s.tmem), C::kColumns);
-  grid_enter();
-  const int ntiles = (p.n + kNarrowM - 1) / kNarrowM;
-  const int rank = (int)(blockIdx.x % split);       // consecutive CTAs are a cluster
-  if (warp == 0) {
-    const int64_t t = blockIdx.x / split;
-    int64_t base = 0;
-    bool found = false;
-    for (int g0 = 0; g0 < p.groups; g0 += 32) {
-      const int x = g0 + lane;
-      const int lo = x < p.groups ? row_offset(p, x) : 0, hi = x < p.groups ? row_offset(p, x + 1) : 0;
-      const int own = max(0, hi - lo + NT - 1) / NT;
-      int sum = own;
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(kFull, sum, o);
-        if (lane >= o) sum += y;
-      }
-      const int64_t first = (base + sum - own) * ntiles;
-      const bool mine = own > 0 && t >= first && t < first + (int64_t)own * ntiles;
-      found = __any_sync(kFull, mine);
-      if (mine) {
-        s.tile[0] = x;
-        s.tile[1] = lo + (int)((t - first) / ntiles) * NT;
-        s.tile[2] = hi;
-        s.tile[3] = (int)((t - first) % ntiles);
-      }
-      if (found) break;
-      base += __shfl_sync(kFull, sum, 31);
-    }
-    if (!found && lane == 0) s.tile[0] = -1;
-  }
+  if (!early) grid_wait();
+  grid_release();
+  for (int g = tid; g <= p.groups; g += kNarrowThreads) s.off[g] = row_offset(p, g);
+  __syncthreads();
+  if (warp == 0) row_tiles<NT>(s.off, s.tiles, p.groups, lane);
   tc_before_sync();
   __syncthreads();
   tc_after_sync();
   const uint32_t tmem = s.tmem;
-  const int group = s.tile[0], row0 = s.tile[1], nt = s.tile[3];
-  const int rows = group < 0 ? 0 : min(NT, s.tile[2] - row0);
-  const int kb0 = group < 0 ? 0 : (int)((int64_t)p.kblocks * rank / split), kb1 = group < 0 ? 0 : (int)((int64_t)p.kblocks * (rank + 1) / split);
-  const int wide = (rows + 15) & ~15;               // columns the products compute
+  const uint32_t ntiles = (p.n + kNarrowM - 1) / kNarrowM;
+  const int rank = (int)(blockIdx.x % split);       // consecutive CTAs are a cluster
+  const uint32_t first = blockIdx.x / split, step = gridDim.x / split;      // with a split, every cluster has one tile at most
+  const uint32_t total = s.stop ? 0 : (uint32_t)s.tiles[p.groups] * ntiles;
+  const int kb0 = (int)((int64_t)p.kblocks * rank / split), kb1 = (int)((int64_t)p.kblocks * (rank + 1) / split);
   float acc[kParts][NT];
-#pragma unroll
-  for (int q = 0; q < kParts; ++q)
-#pragma unroll
-    for (int c = 0; c < NT; ++c) acc[q][c] = 0.0f;
   bool ok = true;
+  auto tile = [&](uint32_t t) { return narrow_tile<NT>(s.off, s.tiles, p.groups, ntiles, t); };
 
   if (warp == 4) {
-    if (elect_one()) {
-      uint32_t it = 0;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const uint32_t st = it % kStages, bar = smem_addr(&s.full[st]);
-        if (!(ok = bar_wait(smem_addr(&s.empty[st]), (it / kStages & 1) ^ 1, stop))) break;
-        const uint32_t to = smem_addr(stages) + st * C::kStageBytes;
-        bar_expect(bar, C::kStageBytes);
+    // ---- loader: one lane; where rows are gathered, four rows a lane
+    auto weights = [&](const NarrowTile &w, int kb, uint32_t st) {
+      const uint32_t to = smem_addr(stages) + st * C::kStageBytes, bar = smem_addr(s.full) + st * 8;
+      bar_expect(bar, C::kStageBytes);
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) tma_3d(to + q * kNarrowM * kBlockK, &mw, kb * kBlockK, q * p.n + nt * kNarrowM, group, bar);
-        tma_2d(to + kParts * kNarrowM * kBlockK, &ma, kb * kBlockK, row0, bar);
+      for (int q = 0; q < kParts; ++q) tma_3d(to + q * kNarrowM * kBlockK, &mw, kb * kBlockK, q * p.n + w.n * kNarrowM, w.g, bar);
+    };
+    uint32_t sent = 0;                 // stages whose weights are on their way
+    if (early) {
+      for (uint32_t t = first; t < total && sent < kStages; t += step) {
+        const NarrowTile w = tile(t);
+        for (int kb = kb0; kb < kb1 && sent < kStages; ++kb, ++sent)
+          if (lane == 0) weights(w, kb, sent);
       }
-      if (!ok)
-        for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) bar_drain(smem_addr(&s.full[i % kStages]), i / kStages & 1);
+      grid_wait();
     }
+    uint32_t it = 0, st = 0, phase = 1;
+    for (uint32_t t = first; ok && t < total; t += step) {
+      const NarrowTile w = tile(t);
+      int row[4];
+      if (p.order) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) row[i] = source_row(p, w.row + min(4 * lane + i, w.rows - 1));
+      }
+      for (int kb = kb0; kb < kb1; ++kb, ++it) {
+        if (it >= sent) {
+          ok = bar_wait(smem_addr(s.empty) + st * 8, phase, stop);
+          if (__any_sync(kFull, !ok)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) weights(w, kb, st);
+          __syncwarp();
+        }
+        const uint32_t to = smem_addr(stages) + st * C::kStageBytes + kParts * kNarrowM * kBlockK, bar = smem_addr(s.full) + st * 8;
+        if (p.order) {
+          if (lane < NT / 4) tma_rows4(to + lane * 4 * kBlockK, &ma, kb * kBlockK, row, bar);
+        } else if (lane == 0) {
+          tma_2d(to, &ma, kb * kBlockK, w.row, bar);
+        }
+        if (++st == kStages) st = 0, phase ^= 1;
+      }
+    }
+    if (!ok && lane == 0)            // stopped: what is on its way still lands in this CTA's memory
+      for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i) bar_drain(smem_addr(&s.full[i % kStages]), i / kStages & 1);
     __syncwarp();
   } else if (warp == 5) {
+    // ---- issuer
     if (elect_one()) {
-      const uint32_t idesc = instruction(wide);
-      uint32_t it = 0;
-      for (int kb = kb0; kb < kb1; ++kb, ++it) {
-        const uint32_t st = it % kStages, half = it & 1;
-        if (!(ok = bar_wait(smem_addr(&s.taken[half]), (it >> 1 & 1) ^ 1, stop))) break;
-        if (!(ok = bar_wait(smem_addr(&s.full[st]), it / kStages & 1, stop))) break;
-        tc_after_sync();
-        const uint32_t base = smem_addr(stages) + st * C::kStageBytes;
-        const uint64_t b = operand(base + kParts * kNarrowM * kBlockK);
+      uint32_t st = 0, phase = 0, half = 0, free_phase = 1;
+      const uint64_t a0 = operand(smem_addr(stages));
+      for (uint32_t t = first; ok && t < total; t += step) {
+        const uint32_t idesc = instruction((tile(t).rows + 15) & ~15);
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!(ok = bar_wait(smem_addr(s.full) + st * 8, phase, stop))) break;
+          if (!(ok = bar_wait(smem_addr(s.taken) + half * 8, free_phase, stop))) break;
+          tc_after_sync();
+          const uint64_t a = a0 + st * (C::kStageBytes / 16), b = a + kParts * kNarrowM * kBlockK / 16;
 #pragma unroll
-        for (int q = 0; q < kParts; ++q) {
-          const uint64_t a = operand(base + q * kNarrowM * kBlockK);
+          for (int q = 0; q < kParts; ++q)
 #pragma unroll
-          for (int k = 0; k < kBlockK / 32; ++k) mma_e4m3(tmem + (half * kParts + q) * NT, a + 2 * k, b + 2 * k, idesc, k > 0);
+            for (int k = 0; k < kBlockK / 32; ++k)
+              mma_e4m3(tmem + (half * kParts + q) * NT, a + q * kNarrowM * kBlockK / 16 + 2 * k, b + 2 * k, idesc, k > 0);
+          mma_commit(smem_addr(s.empty) + st * 8);
+          mma_commit(smem_addr(s.done) + half * 8);
+          if (++st == kStages) st = 0, phase ^= 1;
+          free_phase ^= half;
+          half ^= 1;
         }
-        mma_commit(smem_addr(&s.empty[st]));
-        mma_commit(smem_addr(&s.done[half]));
       }
       if (!ok) {
         mma_commit(smem_addr(&s.last));
@@ -568,137 +606,150 @@ __global__ void __launch_bounds__(kNarrowThreads)
       }
     }
     __syncwarp();
-  } else if (group >= 0) {
-    // epilogue: one row of w a thread; the scales of the tile's rows of a are shared out by the warp
+  } else {
+    // ---- epilogue: one row of w a thread; the scales of the tile's rows of a are shared out by the warp
+    if (early) grid_wait();
     constexpr int kPer = (NT + 31) / 32;
-    const float *sw[kParts];
-#pragma unroll
-    for (int q = 0; q < kParts; ++q)
-      sw[q] = p.w_scale + ((int64_t)group * p.wblocks + q * (p.n / kScaleBlock) + nt) * p.kblocks;
-    float a0[kPer], a1[kPer], w0[kParts], w1[kParts];
-    auto fetch = [&](int kb, float (&a)[kPer], float (&w)[kParts]) {
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int c = lane + 32 * i;
-        a[i] = c < rows && kb < kb1 ? p.a_scale[(int64_t)(row0 + c) * p.as_row + (int64_t)kb * p.as_block] : 0.0f;
-      }
-#pragma unroll
-      for (int q = 0; q < kParts; ++q) w[q] = kb < kb1 ? sw[q][kb] : 0.0f;
-    };
-    fetch(kb0, a0, w0);
-    fetch(kb0 + 1, a1, w1);
     const uint32_t from = tmem + ((uint32_t)(warp * 32) << 16);
-    uint32_t it = 0;
-    for (int kb = kb0; kb < kb1; ++kb, ++it) {
-      const uint32_t half = it & 1;
+    uint32_t half = 0, phase = 0, tile_no = 0;
+    // The sums of a tile, whole or (with a split) of every split-th row of a.
+    auto finish = [&](const NarrowTile &w) {
+      const int n = w.n * kNarrowM + tid;
+      if (!Gated) {
 #pragma unroll
-      for (int q = 0; q < kParts; ++q)
+        for (int c = 0; c < NT; ++c) {
+          if (c < w.rows && n < p.n && (split == 1 || c % split == rank)) {
+            const int64_t at = (int64_t)(w.row + c) * p.out_stride + n;
+            if (p.out_dtype == RESHARD_BF16) static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(acc[0][c]);
+            else if (p.out_dtype == RESHARD_F16) static_cast<__half *>(p.out)[at] = __float2half_rn(acc[0][c]);
+            else static_cast<float *>(p.out)[at] = acc[0][c];
+          }
+        }
+      } else {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (lane + 32 * i < NT) s.scale[warp][half][q][lane + 32 * i] = a0[i] * w0[q];
+        for (int c = 0; c < NT; ++c) {
+          if (c < w.rows) {
+            acc[0][c] = silu_times(acc[0][c], acc[kParts - 1][c]);
+            const uint32_t m = __reduce_max_sync(kFull, magnitude(acc[0][c]));
+            if (lane == 0) s.amax[tile_no & 1][warp][c] = m;
+          }
+        }
+        __syncwarp();
+        const uint32_t paired = smem_addr(&s.paired[tile_no & 1]);
+        if (lane == 0) bar_arrive(paired);
+        ok = ok && bar_wait(paired, tile_no >> 1 & 1, stop);
+        if (__any_sync(kFull, !ok)) return;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) a0[i] = a1[i];
-#pragma unroll
-      for (int q = 0; q < kParts; ++q) w0[q] = w1[q];
-      fetch(kb + 2, a1, w1);
-      __syncwarp();
-      ok = bar_wait(smem_addr(&s.done[half]), it >> 1 & 1, stop);
-      if (__any_sync(kFull, !ok)) {
-        ok = false;
-        break;
-      }
-      tc_after_sync();
-#pragma unroll
-      for (int q = 0; q < kParts; ++q) {
-#pragma unroll
-        for (int c = 0; c < NT; c += 16) {
-          if (c < wide) {
-            uint32_t v[16];
-            tmem_load(from + (half * kParts + q) * NT + c, v);
-            tmem_loaded(v);
-            const float4 *sc = reinterpret_cast<const float4 *>(&s.scale[warp][half][q][c]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 f = sc[i];
-              acc[q][c + 4 * i] = fmaf(__uint_as_float(v[4 * i]), f.x, acc[q][c + 4 * i]);
-              acc[q][c + 4 * i + 1] = fmaf(__uint_as_float(v[4 * i + 1]), f.y, acc[q][c + 4 * i + 1]);
-              acc[q][c + 4 * i + 2] = fmaf(__uint_as_float(v[4 * i + 2]), f.z, acc[q][c + 4 * i + 2]);
-              acc[q][c + 4 * i + 3] = fmaf(__uint_as_float(v[4 * i + 3]), f.w, acc[q][c + 4 * i + 3]);
-            }
+        for (int c = 0; c < NT; ++c) {
+          if (c < w.rows && (split == 1 || c % split == rank)) {
+            const uint32_t(&am)[4][NT] = s.amax[tile_no & 1];
+            float scale, inv;
+            block_scale(max(max(am[0][c], am[1][c]), max(am[2][c], am[3][c])), scale, inv);
+            if (tid == 0) p.out_scale[(int64_t)(w.row + c) * p.os_row + (int64_t)w.n * p.os_block] = scale;
+            static_cast<uint8_t *>(p.out)[(int64_t)(w.row + c) * p.out_stride + n] = (uint8_t)e4m3x2(acc[0][c] * inv, 0.0f);
           }
         }
       }
-      tc_before_sync();
-      __syncwarp();
-      if (lane == 0) bar_arrive(smem_addr(&s.taken[half]));
+    };
+    for (uint32_t t = first; t < total; t += step, ++tile_no) {
+      const NarrowTile w = tile(t);
+      const int wide = (w.rows + 15) & ~15;               // columns the products compute
+      const float *sw[kParts], *sa[kPer];
+#pragma unroll
+      for (int q = 0; q < kParts; ++q)
+        sw[q] = p.w_scale + ((int64_t)w.g * p.wblocks + q * (p.n / kScaleBlock) + w.n) * p.kblocks;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) sa[i] = p.a_scale + (int64_t)source_row(p, w.row + min(lane + 32 * i, w.rows - 1)) * p.as_row;
+#pragma unroll
+      for (int q = 0; q < kParts; ++q)
+#pragma unroll
+        for (int c = 0; c < NT; ++c) acc[q][c] = 0.0f;
+      float a0[kPer], a1[kPer], w0[kParts], w1[kParts];
+      auto fetch = [&](int kb, float (&a)[kPer], float (&b)[kParts]) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) a[i] = kb < kb1 ? sa[i][(int64_t)kb * p.as_block] : 0.0f;
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) b[q] = kb < kb1 ? sw[q][kb] : 0.0f;
+      };
+      fetch(kb0, a0, w0);
+      fetch(kb0 + 1, a1, w1);
+      for (int kb = kb0; kb < kb1; ++kb) {
+#pragma unroll
+        for (int q = 0; q < kParts; ++q)
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+            if (lane + 32 * i < NT) s.scale[warp][half][q][lane + 32 * i] = a0[i] * w0[q];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) a0[i] = a1[i];
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) w0[q] = w1[q];
+        fetch(kb + 2, a1, w1);
+        __syncwarp();
+        ok = ok && bar_wait(smem_addr(s.done) + half * 8, phase, stop);
+        if (__any_sync(kFull, !ok)) {
+          ok = false;
+          break;
+        }
+        tc_after_sync();
+#pragma unroll
+        for (int q = 0; q < kParts; ++q) {
+#pragma unroll
+          for (int c = 0; c < NT; c += 16) {
+            if (c < wide) {
+              uint32_t v[16];
+              tmem_load(from + (half * kParts + q) * NT + c, v);
+              tmem_loaded(v);
+              const float4 *sc = reinterpret_cast<const float4 *>(&s.scale[warp][half][q][c]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float4 f = sc[i];
+                acc[q][c + 4 * i] = fmaf(__uint_as_float(v[4 * i]), f.x, acc[q][c + 4 * i]);
+                acc[q][c + 4 * i + 1] = fmaf(__uint_as_float(v[4 * i + 1]), f.y, acc[q][c + 4 * i + 1]);
+                acc[q][c + 4 * i + 2] = fmaf(__uint_as_float(v[4 * i + 2]), f.z, acc[q][c + 4 * i + 2]);
+                acc[q][c + 4 * i + 3] = fmaf(__uint_as_float(v[4 * i + 3]), f.w, acc[q][c + 4 * i + 3]);
+              }
+            }
+          }
+        }
+        tc_before_sync();
+        __syncwarp();
+        if (lane == 0) bar_arrive(smem_addr(s.taken) + half * 8);
+        phase ^= half;
+        half ^= 1;
+      }
+      if (!ok) break;
+      if (split == 1) finish(w);
+      if (!ok) break;
     }
-  }
-
-  if (split > 1) {
-    // Every CTA's products are done (its epilogue saw the last one), so its stages hold the sums from here; each rank
-    // then adds every split-th row of a, over the ranks in order.
-    float *part = reinterpret_cast<float *>(stages);
-    if (warp < 4) {
+    if (split > 1) {
+      // The CTA's products are done (its epilogue saw the last one), so its stages hold the sums from here; each rank then
+      // adds every split-th row of a, over the ranks in order.
+      float *part = reinterpret_cast<float *>(stages);
+      const NarrowTile w = first < total ? tile(first) : NarrowTile{0, 0, 0, 0};
 #pragma unroll
       for (int q = 0; q < kParts; ++q)
 #pragma unroll
         for (int c = 0; c < NT; ++c)
-          if (c < rows) part[(q * NT + c) * kNarrowM + tid] = acc[q][c];
-    }
-    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
-    if (warp < 4) {
+          if (c < w.rows) part[(q * NT + c) * kNarrowM + tid] = acc[q][c];
+      cluster_sync();
 #pragma unroll
       for (int c = 0; c < NT; ++c) {
-        if (c < rows && c % split == rank) {
+        if (c < w.rows && c % split == rank) {
 #pragma unroll
           for (int q = 0; q < kParts; ++q) {
             float sum = 0.0f;
-            for (int r = 0; r < split; ++r) {
-              uint32_t at;
-              float x;
-              asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(&part[(q * NT + c) * kNarrowM + tid])), "r"(r));
-              asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at) : "memory");
-              sum += x;
-            }
+            for (int r = 0; r < split; ++r) sum += cluster_f32(smem_addr(&part[(q * NT + c) * kNarrowM + tid]), r);
             acc[q][c] = sum;
           }
         }
       }
+      cluster_sync();
+      if (ok && w.rows > 0) finish(w);
     }
-    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
   }
-
-  if (warp < 4 && group >= 0) {
-    const bool whole = !s.stop;            // a stopped CTA's sums are incomplete: nothing of them is stored
-    const int n = nt * kNarrowM + tid;
-    if (!Gated) {
-#pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        if (whole && c < rows && n < p.n && (split == 1 || c % split == rank)) {
-          const int64_t at = (int64_t)(row0 + c) * p.out_stride + n;
-          if (p.out_dtype == RESHARD_BF16) static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(acc[0][c]);
-          else if (p.out_dtype == RESHARD_F16) static_cast<__half *>(p.out)[at] = __float2half_rn(acc[0][c]);
-          else static_cast<float *>(p.out)[at] = acc[0][c];
-        }
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        acc[0][c] = silu_times(acc[0][c], acc[kParts - 1][c]);
-        const uint32_t m = __reduce_max_sync(kFull, magnitude(acc[0][c]));
-        if (lane == 0) s.amax[warp][c] = m;
-      }
-      asm volatile("bar.sync 1, 128;" ::: "memory");
-#pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        if (whole && c < rows && (split == 1 || c % split == rank)) {
-          float scale, inv;
-          block_scale(max(max(s.amax[0][c], s.amax[1][c]), max(s.amax[2][c], s.amax[3][c])), scale, inv);
-          if (tid == 0) p.out_scale[(int64_t)(row0 + c) * p.os_row + (int64_t)nt * p.os_block] = scale;
-          static_cast<uint8_t *>(p.out)[(int64_t)(row0 + c) * p.out_stride + n] = (uint8_t)e4m3x2(acc[0][c] * inv, 0.0f);
-        }
-      }
-    }
+  if (split > 1 && warp >= 4) {        // the cluster's barriers count every thread
+    cluster_sync();
+    cluster_sync();
   }
   tc_before_sync();
   __syncthreads();
@@ -735,26 +786,6 @@ int encode(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, int64
   return RESHARD_OK;
 }
 
-// The dynamic shared memory of a kernel, allowed once per device. regs: what its warpgroups share out among themselves; a
-// build that launches with another number would wait for registers that are not there.
-template <auto kernel>
-int allow_smem(size_t bytes, int regs = 0) {
-  static std::mutex mu;
-  static uint64_t done = 0;
-  int dev = 0;
-  OPS_CUDA(cudaGetDevice(&dev));
-  std::lock_guard<std::mutex> lock(mu);
-  if (dev < 64 && (done >> dev & 1)) return RESHARD_OK;
-  if (regs) {
-    cudaFuncAttributes fa{};
-    OPS_CUDA(cudaFuncGetAttributes(&fa, kernel));
-    if (fa.numRegs != regs) return fail(RESHARD_ERR_UNSUPPORTED, "the product kernel was built with " + std::to_string(fa.numRegs) + " registers, not " + std::to_string(regs));
-  }
-  OPS_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
-  if (dev < 64) done |= 1ull << dev;
-  return RESHARD_OK;
-}
-
 template <bool Gated>
 int enqueue_wide(const Product &p, const Args &a, int sms, cudaStream_t stream) {
   CUtensorMap ma, mw;
@@ -774,17 +805,17 @@ template <int NT, bool Gated>
 int enqueue_narrow(const Product &p, const Args &a, int sms, cudaStream_t stream) {
   using C = Narrow<NT, Gated>;
   CUtensorMap ma, mw;
-  int rc = encode(&ma, p.a, p.k, p.m, p.a_stride, 0, 0, NT);
+  int rc = encode(&ma, p.a, p.k, a.a_rows, p.a_stride, 0, 0, p.order ? 1 : NT);
   if (!rc) rc = encode(&mw, p.w, p.k, Gated ? 2 * p.n : p.n, p.w_stride, p.groups, p.w_batch, kNarrowM);
   if (!rc) rc = allow_smem<&reshard_product_narrow_kernel<NT, Gated>>(C::kSmem);
   if (rc) return rc;
-  const int64_t tiles = (p.m / NT + std::min<int64_t>(p.groups, p.m)) * ((p.n + kNarrowM - 1) / kNarrowM);
-  // K is split while the tiles leave half of the GPU's places (two an SM) empty and a share keeps four blocks
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= 2 * sms && a.kblocks >= split * 8) split *= 2;
-  if (tiles * split > INT32_MAX) return fail(RESHARD_ERR_UNSUPPORTED, "too many tiles for one launch");
-  const cudaError_t e = launch(reshard_product_narrow_kernel<NT, Gated>, dim3((unsigned)(tiles * split)), kNarrowThreads, C::kSmem, split,
-                               stream, ma, mw, a, split);
+  const int64_t tiles = (p.offsets ? p.m / NT + std::min<int64_t>(p.groups, p.m) : (p.m + NT - 1) / NT) * ((p.n + kNarrowM - 1) / kNarrowM);
+  if (tiles > INT32_MAX) return fail(RESHARD_ERR_UNSUPPORTED, "too many tiles for one launch");
+  // K is split where the tiles leave places on the GPU empty, as far as each share keeps four blocks
+  const int64_t places = (int64_t)sms * C::kPerSm;
+  const int split = (int)std::max<int64_t>(1, std::min<int64_t>({8, places / tiles, a.kblocks / 4}));
+  const unsigned grid = (unsigned)(split > 1 ? tiles * split : std::min(tiles, places));
+  const cudaError_t e = launch(reshard_product_narrow_kernel<NT, Gated>, dim3(grid), kNarrowThreads, C::kSmem, split, stream, ma, mw, a, split, p.early);
   return e == cudaSuccess ? RESHARD_OK : cuda_error(e, "launching reshard_product_narrow_kernel");
 }
 
@@ -797,6 +828,9 @@ int enqueue_by_rows(const Product &p, const Args &a, cudaStream_t stream) {
   if (per <= 16) return enqueue_narrow<16, Gated>(p, a, sms, stream);
   if (per <= 32) return enqueue_narrow<32, Gated>(p, a, sms, stream);
   if (per <= 64) return enqueue_narrow<64, Gated>(p, a, sms, stream);
+  if constexpr (!Gated) {
+    if (per <= 128) return enqueue_narrow<128, Gated>(p, a, sms, stream);
+  }
   return enqueue_wide<Gated>(p, a, sms, stream);
 }
 

@@ -41,16 +41,14 @@ __global__ void __launch_bounds__(kQThreads) reshard_quantize_rows_kernel(Rows a
   grid_enter();
   const int lane = threadIdx.x & 31;
   const int64_t b = (int64_t)blockIdx.x * (kQThreads / 8) + threadIdx.x / 8;
-  const int64_t used = a.count ? (int64_t)*a.count * per_row_blocks : blocks;
-  if (b - (lane >> 3) >= used) return;         // the whole warp
-  const bool in = b < used;
+  if (b - (lane >> 3) >= blocks) return;       // the whole warp
+  const bool in = b < blocks;
   const int64_t r = in ? b / per_row_blocks : 0;
   const int kb = in ? (int)(b - r * per_row_blocks) : 0;
-  const int64_t from = a.order ? a.order[r] / a.per_row : r;
   const int at = kb * kScaleBlock + (lane & 7) * 16;
   const int left = in ? (int)min((int64_t)16, a.cols - at) : 0;
   float x[16];
-  load_values<T, 16>(static_cast<const T *>(a.x) + from * a.stride + at, left, wide, x);
+  load_values<T, 16>(static_cast<const T *>(a.x) + r * a.stride + at, left, wide, x);
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) m = max(m, magnitude(x[i]));

@@ -152,6 +152,17 @@ __device__ __forceinline__ float shared_f32(uint32_t addr) {
   return v;
 }
 
+// Every thread of every CTA of the cluster.
+__device__ __forceinline__ void cluster_sync() { asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory"); }
+// What another CTA of the cluster holds at this CTA's shared address.
+__device__ __forceinline__ float cluster_f32(uint32_t addr, int rank) {
+  uint32_t at;
+  float v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ bool elect_one() {     // one lane of a converged warp
   uint32_t p;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
