@@ -113,6 +113,8 @@ struct Rows {                 // a quantization by rows
   int64_t q_stride;
   float *scale;
   int64_t scale_row, scale_block;
+  const int32_t *position = nullptr; // row r goes to rows position[r * copies + j] >= 0, j < copies; NULL: to row r
+  int copies = 1;
 };
 int enqueue_quantize_rows(const Rows &r, cudaStream_t stream);
 int enqueue_dispatch(const int32_t *ids, int64_t slots, int first, int experts, int32_t *offsets, int32_t *order,
@@ -130,7 +132,8 @@ struct Product {              // out[m, n] = sum_k a[m, k] w[n, k], both as 8-bi
   const float *w_scale;
   const int32_t *offsets = nullptr;  // groups + 1 row offsets, on the device; NULL: one group of m rows
   int groups = 1;
-  const int32_t *order = nullptr;    // row r of the product is row order[r] / per_row of a's a_rows; NULL: row r
+  const int32_t *order = nullptr;    // row r of the product is row order[r] / per_row of a's a_rows; NULL: row r. Only
+                                     // where product_gathers()
   int per_row = 1;
   int64_t a_rows = 0;
   bool early = false;                // enqueued right behind a kernel of ours that wrote none of w, offsets, order
@@ -144,6 +147,7 @@ struct Product {              // out[m, n] = sum_k a[m, k] w[n, k], both as 8-bi
   int64_t os_row = 0, os_block = 0;
 };
 int enqueue_product(const Product &p, cudaStream_t stream);
+bool product_gathers(int64_t m, int groups);     // whether a product of m rows in so many groups can take `order`
 
 // ----------------------------------------------------------------------------------------------- device side --
 

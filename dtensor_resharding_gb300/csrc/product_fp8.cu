@@ -214,16 +214,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   if (warp < 4) {
     registers_down<kWideRegsRest>();
     if (warp == 1) {
-      // ---- loader: one lane; where rows are gathered, four rows a lane
+      // ---- loader
       uint32_t it = 0, st = 0, phase = 1;
       bool ok = true;
       for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
         const WideTile w = wide_tile(s, p.groups, ntiles, t);
-        int row[4];
-        if (p.order) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) row[i] = source_row(p, w.row + min(4 * lane + i, w.rows - 1));
-        }
         for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
           const uint32_t bar = smem_addr(s.full) + st * 8;
           ok = bar_wait(smem_addr(s.empty) + st * 8, phase, stop);
@@ -234,7 +229,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           const uint32_t to = smem_addr(stages) + st * kWideStageBytes;
           if (lane == 0) {
             bar_expect(bar, kWideStageBytes);
-            if (!p.order) tma_2d(to, &ma, kb * kBlockK, w.row, bar);
+            tma_2d(to, &ma, kb * kBlockK, w.row, bar);
             const uint32_t tw = to + kWideM * kBlockK;
             if (Gated) {                 // of each half's columns the first 64 are gate, the others up
 #pragma unroll
@@ -246,10 +241,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               tma_3d(tw, &mw, kb * kBlockK, w.n * kCols, w.g, bar);
               tma_3d(tw + 16384, &mw, kb * kBlockK, w.n * kCols + 128, w.g, bar);
             }
-          }
-          if (p.order) {
-            __syncwarp();
-            tma_rows4(to + lane * 4 * kBlockK, &ma, kb * kBlockK, row, bar);
           }
           if (++st == kWideStages) st = 0, phase ^= 1;
         }
@@ -299,7 +290,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const WideTile w = wide_tile(s, p.groups, ntiles, t);
         const float *sa[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sa[i] = p.a_scale + (int64_t)source_row(p, w.row + min(lane + 32 * i, w.rows - 1)) * p.as_row;
+        for (int i = 0; i < 4; ++i) sa[i] = p.a_scale + (int64_t)(w.row + min(lane + 32 * i, w.rows - 1)) * p.as_row;
         // lanes 0 and 1: gated, gate and up of the tile's one block; otherwise the two halves' blocks
         const int wb = Gated ? w.n + (lane & 1) * (p.n / kScaleBlock) : min(w.n * 2 + (lane & 1), p.wblocks - 1);
         const float *sw = p.w_scale + ((int64_t)w.g * p.wblocks + wb) * p.kblocks;
@@ -440,6 +431,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 
 constexpr int kNarrowM = 128;            // rows of w (of gate and of up, when gated)
 constexpr int kNarrowThreads = 192;      // 4 epilogue warps, the loader, the issuer
+constexpr int kMostSplit = 8;            // CTAs of a cluster that share a tile's K
 
 template <int NT, bool Gated>
 struct Narrow {
@@ -615,10 +607,13 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<NT, Gated>::kPerSm)
     // The sums of a tile, whole or (with a split) of every split-th row of a.
     auto finish = [&](const NarrowTile &w) {
       const int n = w.n * kNarrowM + tid;
+      int turn = split > 1 ? rank : 0;       // the next row of a that is this CTA's
       if (!Gated) {
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
-          if (c < w.rows && n < p.n && (split == 1 || c % split == rank)) {
+          if (c == turn && c < w.rows) {
+            turn += split;
+            if (n >= p.n) continue;
             const int64_t at = (int64_t)(w.row + c) * p.out_stride + n;
             if (p.out_dtype == RESHARD_BF16) static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(acc[0][c]);
             else if (p.out_dtype == RESHARD_F16) static_cast<__half *>(p.out)[at] = __float2half_rn(acc[0][c]);
@@ -641,7 +636,8 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<NT, Gated>::kPerSm)
         if (__any_sync(kFull, !ok)) return;
 #pragma unroll
         for (int c = 0; c < NT; ++c) {
-          if (c < w.rows && (split == 1 || c % split == rank)) {
+          if (c == turn && c < w.rows) {
+            turn += split;
             const uint32_t(&am)[4][NT] = s.amax[tile_no & 1];
             float scale, inv;
             block_scale(max(max(am[0][c], am[1][c]), max(am[2][c], am[3][c])), scale, inv);
@@ -732,13 +728,21 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<NT, Gated>::kPerSm)
         for (int c = 0; c < NT; ++c)
           if (c < w.rows) part[(q * NT + c) * kNarrowM + tid] = acc[q][c];
       cluster_sync();
+      int turn = rank;
 #pragma unroll
       for (int c = 0; c < NT; ++c) {
-        if (c < w.rows && c % split == rank) {
+        if (c == turn && c < w.rows) {
+          turn += split;
+          float x[kParts][kMostSplit];
+#pragma unroll
+          for (int r = 0; r < kMostSplit; ++r)
+#pragma unroll
+            for (int q = 0; q < kParts; ++q) x[q][r] = r < split ? cluster_f32(smem_addr(&part[(q * NT + c) * kNarrowM + tid]), r) : 0.0f;
 #pragma unroll
           for (int q = 0; q < kParts; ++q) {
-            float sum = 0.0f;
-            for (int r = 0; r < split; ++r) sum += cluster_f32(smem_addr(&part[(q * NT + c) * kNarrowM + tid]), r);
+            float sum = x[q][0];
+#pragma unroll
+            for (int r = 1; r < kMostSplit; ++r) sum += x[q][r];
             acc[q][c] = sum;
           }
         }
@@ -789,7 +793,7 @@ int encode(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, int64
 template <bool Gated>
 int enqueue_wide(const Product &p, const Args &a, int sms, cudaStream_t stream) {
   CUtensorMap ma, mw;
-  int rc = encode(&ma, p.a, p.k, a.a_rows, p.a_stride, 0, 0, p.order ? 1 : kWideM);
+  int rc = encode(&ma, p.a, p.k, p.m, p.a_stride, 0, 0, kWideM);
   if (!rc) rc = encode(&mw, p.w, p.k, Gated ? 2 * p.n : p.n, p.w_stride, p.groups, p.w_batch, Gated ? 64 : 128);
   if (!rc) rc = allow_smem<&reshard_product_wide_kernel<Gated>>(kWideSmem, kWideRegs);
   if (rc) return rc;
@@ -813,28 +817,34 @@ int enqueue_narrow(const Product &p, const Args &a, int sms, cudaStream_t stream
   if (tiles > INT32_MAX) return fail(RESHARD_ERR_UNSUPPORTED, "too many tiles for one launch");
   // K is split where the tiles leave places on the GPU empty, as far as each share keeps four blocks
   const int64_t places = (int64_t)sms * C::kPerSm;
-  const int split = (int)std::max<int64_t>(1, std::min<int64_t>({8, places / tiles, a.kblocks / 4}));
+  const int split = (int)std::max<int64_t>(1, std::min<int64_t>({kMostSplit, places / tiles, a.kblocks / 4}));
   const unsigned grid = (unsigned)(split > 1 ? tiles * split : std::min(tiles, places));
   const cudaError_t e = launch(reshard_product_narrow_kernel<NT, Gated>, dim3(grid), kNarrowThreads, C::kSmem, split, stream, ma, mw, a, split, p.early);
   return e == cudaSuccess ? RESHARD_OK : cuda_error(e, "launching reshard_product_narrow_kernel");
 }
+
+// Rows a group, on average: by them a product takes the narrow kernel or the wide one.
+int64_t rows_a_group(int64_t m, int groups) { return (m + groups - 1) / groups; }
+constexpr int64_t kMostNarrow = 64, kMostNarrowDense = 128;
 
 template <bool Gated>
 int enqueue_by_rows(const Product &p, const Args &a, cudaStream_t stream) {
   int sms = 0;
   int rc = device_sms(&sms);
   if (rc) return rc;
-  const int64_t per = (p.m + p.groups - 1) / p.groups;     // rows a group, on average
+  const int64_t per = rows_a_group(p.m, p.groups);
   if (per <= 16) return enqueue_narrow<16, Gated>(p, a, sms, stream);
   if (per <= 32) return enqueue_narrow<32, Gated>(p, a, sms, stream);
-  if (per <= 64) return enqueue_narrow<64, Gated>(p, a, sms, stream);
+  if (per <= kMostNarrow) return enqueue_narrow<64, Gated>(p, a, sms, stream);
   if constexpr (!Gated) {
-    if (per <= 128) return enqueue_narrow<128, Gated>(p, a, sms, stream);
+    if (!p.offsets && per <= kMostNarrowDense) return enqueue_narrow<128, Gated>(p, a, sms, stream);
   }
   return enqueue_wide<Gated>(p, a, sms, stream);
 }
 
 }  // namespace
+
+bool product_gathers(int64_t m, int groups) { return rows_a_group(m, groups) <= kMostNarrow; }
 
 int enqueue_product(const Product &p, cudaStream_t stream) {
   Args a{};

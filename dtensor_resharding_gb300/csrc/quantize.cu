@@ -57,17 +57,21 @@ __global__ void __launch_bounds__(kQThreads) reshard_quantize_rows_kernel(Rows a
   float scale, inv;
   block_scale(m, scale, inv);
   if (!in) return;
-  if ((lane & 7) == 0) a.scale[r * a.scale_row + kb * a.scale_block] = scale;
   uint32_t q[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) q[i] = e4m3x4(x[4 * i] * inv, x[4 * i + 1] * inv, x[4 * i + 2] * inv, x[4 * i + 3] * inv);
-  uint8_t *to = a.q + r * a.q_stride + at;
-  if (wide_q && left >= 16) {
-    *reinterpret_cast<uint4 *>(to) = make_uint4(q[0], q[1], q[2], q[3]);
-  } else {
+  for (int j = 0; j < a.copies; ++j) {
+    const int64_t to_row = a.position ? a.position[r * a.copies + j] : r;
+    if (to_row < 0) continue;
+    if ((lane & 7) == 0) a.scale[to_row * a.scale_row + kb * a.scale_block] = scale;
+    uint8_t *to = a.q + to_row * a.q_stride + at;
+    if (wide_q && left >= 16) {
+      *reinterpret_cast<uint4 *>(to) = make_uint4(q[0], q[1], q[2], q[3]);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (i < left) to[i] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
+      for (int i = 0; i < 16; ++i)
+        if (i < left) to[i] = (uint8_t)(q[i / 4] >> (8 * (i % 4)));
+    }
   }
 }
 

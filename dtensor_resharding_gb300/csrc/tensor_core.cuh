@@ -154,12 +154,12 @@ __device__ __forceinline__ float shared_f32(uint32_t addr) {
 
 // Every thread of every CTA of the cluster.
 __device__ __forceinline__ void cluster_sync() { asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory"); }
-// What another CTA of the cluster holds at this CTA's shared address.
+// What another CTA of the cluster holds at this CTA's shared address. Not a barrier to other loads: several are in flight.
 __device__ __forceinline__ float cluster_f32(uint32_t addr, int rank) {
   uint32_t at;
   float v;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at));
   return v;
 }
 
