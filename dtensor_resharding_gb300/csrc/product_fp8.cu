@@ -604,48 +604,18 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<NT, Gated>::kPerSm)
     constexpr int kPer = (NT + 31) / 32;
     const uint32_t from = tmem + ((uint32_t)(warp * 32) << 16);
     uint32_t half = 0, phase = 0, tile_no = 0;
-    // The sums of a tile, whole or (with a split) of every split-th row of a.
-    auto finish = [&](const NarrowTile &w) {
+    auto store = [&](const NarrowTile &w, int c, float v) {
       const int n = w.n * kNarrowM + tid;
-      int turn = split > 1 ? rank : 0;       // the next row of a that is this CTA's
-      if (!Gated) {
-#pragma unroll
-        for (int c = 0; c < NT; ++c) {
-          if (c == turn && c < w.rows) {
-            turn += split;
-            if (n >= p.n) continue;
-            const int64_t at = (int64_t)(w.row + c) * p.out_stride + n;
-            if (p.out_dtype == RESHARD_BF16) static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(acc[0][c]);
-            else if (p.out_dtype == RESHARD_F16) static_cast<__half *>(p.out)[at] = __float2half_rn(acc[0][c]);
-            else static_cast<float *>(p.out)[at] = acc[0][c];
-          }
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < NT; ++c) {
-          if (c < w.rows) {
-            acc[0][c] = silu_times(acc[0][c], acc[kParts - 1][c]);
-            const uint32_t m = __reduce_max_sync(kFull, magnitude(acc[0][c]));
-            if (lane == 0) s.amax[tile_no & 1][warp][c] = m;
-          }
-        }
-        __syncwarp();
-        const uint32_t paired = smem_addr(&s.paired[tile_no & 1]);
-        if (lane == 0) bar_arrive(paired);
-        ok = ok && bar_wait(paired, tile_no >> 1 & 1, stop);
-        if (__any_sync(kFull, !ok)) return;
-#pragma unroll
-        for (int c = 0; c < NT; ++c) {
-          if (c == turn && c < w.rows) {
-            turn += split;
-            const uint32_t(&am)[4][NT] = s.amax[tile_no & 1];
-            float scale, inv;
-            block_scale(max(max(am[0][c], am[1][c]), max(am[2][c], am[3][c])), scale, inv);
-            if (tid == 0) p.out_scale[(int64_t)(w.row + c) * p.os_row + (int64_t)w.n * p.os_block] = scale;
-            static_cast<uint8_t *>(p.out)[(int64_t)(w.row + c) * p.out_stride + n] = (uint8_t)e4m3x2(acc[0][c] * inv, 0.0f);
-          }
-        }
-      }
+      if (n >= p.n) return;
+      const int64_t at = (int64_t)(w.row + c) * p.out_stride + n;
+      if (p.out_dtype == RESHARD_F32) static_cast<float *>(p.out)[at] = v;
+      else static_cast<uint16_t *>(p.out)[at] = p.out_dtype == RESHARD_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+    };
+    auto store_gated = [&](const NarrowTile &w, int c, float h, uint32_t amax) {
+      float scale, inv;
+      block_scale(amax, scale, inv);
+      if (tid == 0) p.out_scale[(int64_t)(w.row + c) * p.os_row + (int64_t)w.n * p.os_block] = scale;
+      static_cast<uint8_t *>(p.out)[(int64_t)(w.row + c) * p.out_stride + w.n * kNarrowM + tid] = (uint8_t)e4m3x2(h * inv, 0.0f);
     };
     for (uint32_t t = first; t < total; t += step, ++tile_no) {
       const NarrowTile w = tile(t);
@@ -714,8 +684,33 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<NT, Gated>::kPerSm)
         half ^= 1;
       }
       if (!ok) break;
-      if (split == 1) finish(w);
-      if (!ok) break;
+      if (split > 1) continue;
+      if (!Gated) {
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+          if (c < w.rows) store(w, c, acc[0][c]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+          if (c < w.rows) {
+            acc[0][c] = silu_times(acc[0][c], acc[kParts - 1][c]);
+            const uint32_t m = __reduce_max_sync(kFull, magnitude(acc[0][c]));
+            if (lane == 0) s.amax[tile_no & 1][warp][c] = m;
+          }
+        }
+        __syncwarp();
+        const uint32_t paired = smem_addr(&s.paired[tile_no & 1]);
+        if (lane == 0) bar_arrive(paired);
+        ok = bar_wait(paired, tile_no >> 1 & 1, stop);
+        if (__any_sync(kFull, !ok)) {
+          ok = false;
+          break;
+        }
+        const uint32_t(&am)[4][NT] = s.amax[tile_no & 1];
+#pragma unroll
+        for (int c = 0; c < NT; ++c)
+          if (c < w.rows) store_gated(w, c, acc[0][c], max(max(am[0][c], am[1][c]), max(am[2][c], am[3][c])));
+      }
     }
     if (split > 1) {
       // The CTA's products are done (its epilogue saw the last one), so its stages hold the sums from here; each rank then
@@ -728,27 +723,31 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<NT, Gated>::kPerSm)
         for (int c = 0; c < NT; ++c)
           if (c < w.rows) part[(q * NT + c) * kNarrowM + tid] = acc[q][c];
       cluster_sync();
-      int turn = rank;
+      // a loop, not unrolled: code that runs once is fetched for as long as it runs
+#pragma unroll 1
+      for (int c = rank; c < w.rows; c += split) {
+        float x[kParts][kMostSplit], sum[kParts];
 #pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        if (c == turn && c < w.rows) {
-          turn += split;
-          float x[kParts][kMostSplit];
+        for (int r = 0; r < kMostSplit; ++r)
 #pragma unroll
-          for (int r = 0; r < kMostSplit; ++r)
+          for (int q = 0; q < kParts; ++q) x[q][r] = r < split ? cluster_f32(smem_addr(&part[(q * NT + c) * kNarrowM + tid]), r) : 0.0f;
 #pragma unroll
-            for (int q = 0; q < kParts; ++q) x[q][r] = r < split ? cluster_f32(smem_addr(&part[(q * NT + c) * kNarrowM + tid]), r) : 0.0f;
+        for (int q = 0; q < kParts; ++q) {
+          sum[q] = x[q][0];
 #pragma unroll
-          for (int q = 0; q < kParts; ++q) {
-            float sum = x[q][0];
-#pragma unroll
-            for (int r = 1; r < kMostSplit; ++r) sum += x[q][r];
-            acc[q][c] = sum;
-          }
+          for (int r = 1; r < kMostSplit; ++r) sum[q] += x[q][r];
+        }
+        if (!Gated) {
+          if (ok) store(w, c, sum[0]);
+        } else {
+          const float h = silu_times(sum[0], sum[kParts - 1]);
+          const uint32_t m = __reduce_max_sync(kFull, magnitude(h));
+          if (lane == 0) s.amax[0][warp][c] = m;
+          asm volatile("bar.sync 1, 128;" ::: "memory");       // the four warps, each once a row
+          if (ok) store_gated(w, c, h, max(max(s.amax[0][0][c], s.amax[0][1][c]), max(s.amax[0][2][c], s.amax[0][3][c])));
         }
       }
       cluster_sync();
-      if (ok && w.rows > 0) finish(w);
     }
   }
   if (split > 1 && warp >= 4) {        // the cluster's barriers count every thread
