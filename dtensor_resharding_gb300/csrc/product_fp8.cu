@@ -47,6 +47,7 @@ struct Args {
   void *out;
   int out_dtype;
   int64_t out_stride;
+  bool boxed;           // out has a tensor map
   float *out_scale;
   int64_t os_row, os_block;
 };
@@ -102,13 +103,16 @@ constexpr int kWideEpi = 8;              // epilogue warps: 4 row quarters x 2 c
 constexpr int kWideThreads = (kWideEpi + 4) * 32;        // behind a warpgroup: the issuer, the loader, the scales' loader, one idle
 constexpr int kWideCols = kWideN / 2;    // columns of a thread
 constexpr int kScaleSlots = 2 * kWideStages;
-constexpr int kRowBytes = 256;           // of a thread's row of output on its way, 16 more apart for the banks
-constexpr int kRowPitch = kRowBytes + 16;
+constexpr int kOutBox = 32 * 128;        // an epilogue warp's rows on their way out, 128 bytes of each; two of them a warp
+constexpr int kTileSlots = 8;            // tiles whose place the loader has written down: it is 6 blocks ahead at most
 // Registers a thread: at launch, of the epilogue's two warpgroups and of the other. The epilogue holds 128 sums and two loads
 // of 16 columns.
 constexpr int kWideRegs = 168, kWideRegsEpi = 200, kWideRegsRest = 104;
 static_assert(kWideThreads * kWideRegs >= kWideEpi * 32 * kWideRegsEpi + 128 * kWideRegsRest, "more registers than the launch has");
 
+struct WideTile {
+  int g, row, rows, n;     // group, first row, rows of the group from there (can exceed the tile), column tile
+};
 struct WideShared {
   alignas(16) uint64_t done[2];        // 16-byte pairs: the address of the other is this one's ^ 8
   alignas(16) uint64_t taken[2];
@@ -116,16 +120,14 @@ struct WideShared {
   uint32_t tmem;
   int stop;
   uint32_t amax[2][2][kWideM];
-  alignas(16) uint8_t rows[2][kWideM][kRowPitch];
+  alignas(16) WideTile tile[kTileSlots];
   float a_scale[kScaleSlots][kWideM], w_scale[kScaleSlots][2];     // w: the column halves', or gate's and up's
   int off[RESHARD_MAX_GROUPS + 1], tiles[RESHARD_MAX_GROUPS + 1];   // row offsets; tiles of rows before each group
 };
-constexpr size_t kWideSmem = (size_t)kWideStages * kWideStageBytes + sizeof(WideShared);
+constexpr size_t kWideOut = (size_t)kWideEpi * 2 * kOutBox;
+constexpr size_t kWideSmem = (size_t)kWideStages * kWideStageBytes + kWideOut + sizeof(WideShared);
 static_assert(kWideSmem <= 232448, "shared memory of a CTA");
 
-struct WideTile {
-  int g, row, rows, n;     // group, first row, rows of the group from there (can exceed the tile), column tile
-};
 __device__ __forceinline__ WideTile wide_tile(const WideShared &s, int groups, uint32_t ntiles, uint32_t t) {
   int lo = 0, hi = groups - 1;          // the last group whose first tile is <= t
   while (lo < hi) {
@@ -143,41 +145,91 @@ __device__ __forceinline__ WideTile wide_tile(const WideShared &s, int groups, u
   return r;
 }
 
-// One thread's columns of its row, in T: 256 bytes at a time through its row of shared memory, from where the copy engine
-// takes them. All CTAs finish their tiles together and L2 takes 10 MB of a round's tiles no faster than it takes; plain
-// stores kept the epilogue (and with it the products) for 4,800 cycles a tile, this way for 1,000.
+// An epilogue warp's 32 rows on their way to global memory: Boxes boxes of Bytes (128 or 64) of each row, in shared memory
+// as a tensor map of that box and swizzle has them (16-byte pieces spread over the banks by row). A lane writes its own
+// row's pieces; box_out() hands the boxes to the copy engine where all 32 rows are the group's, or else writes those that
+// are. The products go on meanwhile: all CTAs finish their tiles together, and 10 MB of a round's tiles reach L2 no
+// faster than it takes them (plain stores from the registers kept the epilogue 4,800 cycles a tile, a bulk copy for each
+// row 3,800).
+template <int Bytes>
+__device__ __forceinline__ void box_put(uint8_t *box, int lane, int piece, uint4 v) {
+  const int at = Bytes == 128 ? piece ^ (lane & 7) : piece ^ (lane >> 1 & 3);
+  *reinterpret_cast<uint4 *>(box + lane * Bytes + at * 16) = v;
+}
+template <int Bytes, int Boxes>
+__device__ __forceinline__ void box_out(const CUtensorMap *map, const uint8_t *box, int lane, uint8_t *out, int64_t pitch, int64_t x, int64_t row, int rows, int bytes) {
+  copy_fence();
+  __syncwarp();
+  if (rows >= 32) {
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < Boxes; ++i)
+        if (i * Bytes < bytes) tma_store_2d(map, smem_addr(box + i * kOutBox), (int)x + i * Bytes, (int)row);
+      bulk_commit();
+    }
+  } else {                       // a group's last rows
+#pragma unroll 1
+    for (int i = lane; i < rows * (Boxes * Bytes / 16); i += 32) {
+      const int r = i / (Boxes * Bytes / 16), c = i % (Boxes * Bytes / 16), b = c / (Bytes / 16), piece = c % (Bytes / 16);
+      const int at = Bytes == 128 ? piece ^ (r & 7) : piece ^ (r >> 1 & 3);
+      const uint4 v = *reinterpret_cast<const uint4 *>(box + b * kOutBox + r * Bytes + at * 16);
+      uint8_t *to = out + (row + r) * pitch + x + c * 16;
+      if (c * 16 + 16 <= bytes) {
+        *reinterpret_cast<uint4 *>(to) = v;
+      } else {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int e = 0; e < (bytes - c * 16) / 2; ++e) reinterpret_cast<uint16_t *>(to)[e] = (uint16_t)(w[e / 2] >> (16 * (e % 2)));
+      }
+    }
+    __syncwarp();
+  }
+}
+// The boxes are free again (their last copy has been read).
+__device__ __forceinline__ void box_free(int lane) {
+  if (lane == 0) bulk_read();
+  __syncwarp();
+}
+
+// A warp's 32 rows of 128 columns in T. boxed: out's rows start on 16 bytes (a tensor map describes it).
 template <typename T>
-__device__ __forceinline__ void store_columns(uint8_t *row, const float2 (&sum)[kWideCols / 2], T *to, int cols) {
-  constexpr int per = kRowBytes / sizeof(T);
-  const bool bulk = (reinterpret_cast<uintptr_t>(to) & 15) == 0 && (cols * sizeof(T)) % 16 == 0;
+__device__ __forceinline__ void store_tile(const CUtensorMap *map, bool boxed, uint8_t *box, int lane, const float2 (&sum)[kWideCols / 2], void *out, int64_t stride,
+                                           int64_t n0, int64_t row, int rows, int cols) {
+  if (!boxed) {
+    T *to = static_cast<T *>(out) + (row + lane) * stride + n0;
+    if (lane < rows) {
+#pragma unroll
+      for (int c = 0; c < kWideCols; ++c)
+        if (c < cols) to[c] = from_f32<T>(c & 1 ? sum[c / 2].y : sum[c / 2].x);
+    }
+    return;
+  }
+  constexpr int per = 256 / sizeof(T);       // columns of two boxes
 #pragma unroll
   for (int c = 0; c < kWideCols; c += per) {
-    if (!bulk) {             // a row that starts or ends inside 16 bytes
+    if (c >= cols) break;
+    box_free(lane);
 #pragma unroll
-      for (int j = 0; j < per; ++j)
-        if (c + j < cols) to[c + j] = from_f32<T>(j & 1 ? sum[(c + j) / 2].y : sum[(c + j) / 2].x);
-    } else if (c < cols) {
-      bulk_read();
+    for (int j = 0; j < 16; ++j) {
+      uint32_t v[4];
 #pragma unroll
-      for (int j = 0; j < kRowBytes / 16; ++j) {
-        uint32_t v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (sizeof(T) == 4) v[i] = __float_as_uint(i & 1 ? sum[(c + 4 * j + i) / 2].y : sum[(c + 4 * j + i) / 2].x);
-          else v[i] = pack2<T>(sum[c / 2 + 4 * j + i].x, sum[c / 2 + 4 * j + i].y);
-        }
-        *reinterpret_cast<uint4 *>(row + 16 * j) = make_uint4(v[0], v[1], v[2], v[3]);
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (sizeof(T) == 4) v[i] = __float_as_uint(i & 1 ? sum[(c + 4 * j + i) / 2].y : sum[(c + 4 * j + i) / 2].x);
+        else v[i] = pack2<T>(sum[c / 2 + 4 * j + i].x, sum[c / 2 + 4 * j + i].y);
       }
-      bulk_store(to + c, smem_addr(row), (uint32_t)min(per, cols - c) * sizeof(T));
+      box_put<128>(box + j / 8 * kOutBox, lane, j % 8, make_uint4(v[0], v[1], v[2], v[3]));
     }
+    box_out<128, 2>(map, box, lane, static_cast<uint8_t *>(out), stride * (int64_t)sizeof(T), (n0 + c) * (int64_t)sizeof(T), row, rows,
+                    min(per, cols - c) * (int)sizeof(T));
   }
 }
 
 template <bool Gated>
 __global__ void __launch_bounds__(kWideThreads, 1)
-    reshard_product_wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mw, const __grid_constant__ Args p) {
+    reshard_product_wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mo,
+                                const __grid_constant__ Args p) {
   extern __shared__ __align__(1024) uint8_t stages[];
-  WideShared &s = *reinterpret_cast<WideShared *>(stages + (size_t)kWideStages * kWideStageBytes);
+  uint8_t *const out_boxes = stages + (size_t)kWideStages * kWideStageBytes;
+  WideShared &s = *reinterpret_cast<WideShared *>(out_boxes + kWideOut);
   if (smem_addr(stages) & 1023) {      // not seen: the swizzle needs it
     atomicOr(&g_ops_status, 1);
     return;
@@ -215,9 +267,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     registers_down<kWideRegsRest>();
     if (warp == 1) {
       // ---- loader
-      uint32_t it = 0, st = 0, phase = 1;
+      uint32_t it = 0, st = 0, phase = 1, tile_no = 0;
       bool ok = true;
-      for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
+      for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x, ++tile_no) {
         const WideTile w = wide_tile(s, p.groups, ntiles, t);
         for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
           const uint32_t bar = smem_addr(s.full) + st * 8;
@@ -228,6 +280,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
           const uint32_t to = smem_addr(stages) + st * kWideStageBytes;
           if (lane == 0) {
+            if (kb == 0) s.tile[tile_no % kTileSlots] = w;      // for the epilogue, by way of this barrier
             bar_expect(bar, kWideStageBytes);
             tma_2d(to, &ma, kb * kBlockK, w.row, bar);
             const uint32_t tw = to + kWideM * kBlockK;
@@ -317,7 +370,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     // ---- epilogue: a row and half of the columns a thread
     registers_up<kWideRegsEpi>();
     const int side = (warp >> 2) - 1, r = (warp & 3) * 32 + lane;
-    uint8_t *const out_row = s.rows[side][r];
+    uint8_t *const box = out_boxes + (warp - 4) * 2 * kOutBox;
     // the next block's: tensor memory, barrier, parity, scales. tries: 1 once a wait gave up, so that the others pass
     uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + side * kWideCols, done = smem_addr(s.done), phase = 0, second = 0;
     uint32_t sa = smem_addr(&s.a_scale[0][r]), sw = smem_addr(&s.w_scale[0][Gated ? 0 : side]), tries = kTries;
@@ -370,15 +423,15 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       for (int kb = 1; kb < p.kblocks; ++kb) block(true);
       block(false);
       if (__any_sync(kFull, tries == 1)) break;
-      const WideTile w = wide_tile(s, p.groups, ntiles, t);
-      const int64_t row = w.row + r;
+      const WideTile w = s.tile[tile_no % kTileSlots];
+      const int64_t row0 = w.row + (warp & 3) * 32;      // the warp's rows
+      const int rows = w.rows - (warp & 3) * 32;
       if (!Gated) {
         const int n0 = w.n * kCols + side * kWideCols, cols = min(kWideCols, p.n - n0);
-        if (r < w.rows && cols > 0) {
-          const int64_t at = row * p.out_stride + n0;
-          if (p.out_dtype == RESHARD_BF16) store_columns(out_row, sum, static_cast<__nv_bfloat16 *>(p.out) + at, cols);
-          else if (p.out_dtype == RESHARD_F16) store_columns(out_row, sum, static_cast<__half *>(p.out) + at, cols);
-          else store_columns(out_row, sum, static_cast<float *>(p.out) + at, cols);
+        if (rows > 0 && cols > 0) {
+          if (p.out_dtype == RESHARD_BF16) store_tile<__nv_bfloat16>(&mo, p.boxed, box, lane, sum, p.out, p.out_stride, n0, row0, rows, cols);
+          else if (p.out_dtype == RESHARD_F16) store_tile<__half>(&mo, p.boxed, box, lane, sum, p.out, p.out_stride, n0, row0, rows, cols);
+          else store_tile<float>(&mo, p.boxed, box, lane, sum, p.out, p.out_stride, n0, row0, rows, cols);
         }
       } else {
         // of the sums the first half is gate, the second up: this thread's 64 of the row's 128 values
@@ -398,9 +451,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         m = max(m, s.amax[tile_no & 1][side ^ 1][r]);
         float scale, inv;
         block_scale(m, scale, inv);
-        if (r < w.rows) {
-          if (side == 0) p.out_scale[row * p.os_row + w.n * p.os_block] = scale;
-          bulk_read();
+        if (side == 0 && lane < rows) p.out_scale[(row0 + lane) * p.os_row + w.n * p.os_block] = scale;
+        if (rows > 0) {
+          box_free(lane);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t q[4];
@@ -409,9 +462,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               const float2 x = sum[8 * j + 2 * i], y = sum[8 * j + 2 * i + 1];
               q[i] = e4m3x4(x.x * inv, x.y * inv, y.x * inv, y.y * inv);
             }
-            *reinterpret_cast<uint4 *>(out_row + 16 * j) = make_uint4(q[0], q[1], q[2], q[3]);
+            box_put<64>(box, lane, j, make_uint4(q[0], q[1], q[2], q[3]));
           }
-          bulk_store(static_cast<uint8_t *>(p.out) + row * p.out_stride + w.n * kCols + side * 64, smem_addr(out_row), 64);
+          box_out<64, 1>(&mo, box, lane, static_cast<uint8_t *>(p.out), p.out_stride, w.n * kCols + side * 64, row0, rows, 64);
         }
       }
     }
@@ -775,32 +828,37 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return fn;
 }
 
-// Bytes [batch, rows, cols] in boxes of box_rows x 128, 128-byte swizzle; batch 0: a plain matrix.
-int encode(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, int64_t stride, int64_t batch, int64_t batch_stride, int box_rows) {
+// Bytes [batch, rows, cols] in boxes of box_rows x box_cols (128 or 64), swizzled over as many bytes; batch 0: a plain matrix.
+int encode(CUtensorMap *map, const void *base, int64_t cols, int64_t rows, int64_t stride, int64_t batch, int64_t batch_stride, int box_rows,
+           int box_cols = kBlockK) {
   PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
   if (!enc) return fail(RESHARD_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
   const cuuint64_t strides[2] = {(cuuint64_t)stride, (cuuint64_t)batch_stride};
-  const cuuint32_t box[3] = {(cuuint32_t)kBlockK, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1}, step[3] = {1, 1, 1};
   const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, batch ? 3 : 2, const_cast<void *>(base), dims, strides, box, step,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(RESHARD_ERR_CUDA, "cuTensorMapEncodeTiled failed with " + std::to_string((int)r));
   return RESHARD_OK;
 }
 
 template <bool Gated>
-int enqueue_wide(const Product &p, const Args &a, int sms, cudaStream_t stream) {
-  CUtensorMap ma, mw;
+int enqueue_wide(const Product &p, Args a, int sms, cudaStream_t stream) {
+  CUtensorMap ma, mw, mo{};
   int rc = encode(&ma, p.a, p.k, p.m, p.a_stride, 0, 0, kWideM);
   if (!rc) rc = encode(&mw, p.w, p.k, Gated ? 2 * p.n : p.n, p.w_stride, p.groups, p.w_batch, Gated ? 64 : 128);
+  const int64_t es = Gated ? 1 : element_bytes(p.out_dtype), pitch = p.out_stride * es;
+  a.boxed = Gated || ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)pitch) & 15) == 0;
+  if (!rc && a.boxed) rc = encode(&mo, p.out, p.n * es, p.m, pitch, 0, 0, 32, Gated ? 64 : 128);
   if (!rc) rc = allow_smem<&reshard_product_wide_kernel<Gated>>(kWideSmem, kWideRegs);
   if (rc) return rc;
   const int64_t cols = Gated ? kWideN / 2 : kWideN;
   const int64_t most = (p.m / kWideM + std::min<int64_t>(p.groups, p.m)) * ((p.n + cols - 1) / cols);
   if (most > INT32_MAX) return fail(RESHARD_ERR_UNSUPPORTED, "too many tiles for one launch");
   const cudaError_t e = launch(reshard_product_wide_kernel<Gated>, dim3((unsigned)std::min<int64_t>(sms, most)), kWideThreads, kWideSmem, 1,
-                               stream, ma, mw, a);
+                               stream, ma, mw, mo, a);
   return e == cudaSuccess ? RESHARD_OK : cuda_error(e, "launching reshard_product_wide_kernel");
 }
 

@@ -136,13 +136,14 @@ __device__ __forceinline__ void tmem_loaded(uint32_t (&r)[32]) {
                  "+r"(r[30]), "+r"(r[31])::"memory");
 }
 
-// Shared memory to global memory by the copy engine, 16-byte aligned and a multiple of 16 bytes; the thread's own writes
-// to `from` are ordered before it. bulk_read(): the engine is done reading what this thread has handed over.
-__device__ __forceinline__ void bulk_store(void *to, uint32_t from, uint32_t bytes) {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(to), "r"(from), "r"(bytes) : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+// A tile of shared memory to global memory by the copy engine: what lies outside the tensor is not written. Writes to
+// the tile come before it by copy_fence() of their threads and a barrier. bulk_read(): the engine is done reading what
+// this thread has handed over; bulk_done(): and writing it.
+__device__ __forceinline__ void copy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, uint32_t from, int x, int y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y), "r"(from) : "memory");
 }
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void bulk_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
