@@ -86,6 +86,27 @@ struct Blocks {
   int nb, kb;
 };
 
+// The CTA's amax, written as the block's scale and given back as the factor of its values.
+__device__ __forceinline__ void block_amax(uint32_t m, uint32_t (&part)[kQThreads / 32], float *scale, float &inv) {
+  m = __reduce_max_sync(kFull, m);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kQThreads / 32; ++i) m = max(m, part[i]);
+  float s;
+  block_scale(m, s, inv);
+  if (threadIdx.x == 0) *scale = s;
+}
+
+template <typename P>
+__device__ __forceinline__ P load_stream(const P *p) {      // read once: 16 bytes at a time, not kept
+  static_assert(sizeof(P) % 16 == 0, "16-byte pieces");
+  P r;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(P) / 16); ++i) reinterpret_cast<uint4 *>(&r)[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
+  return r;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kQThreads) reshard_quantize_blocks_kernel(Blocks a, bool wide, bool wide_q) {
   grid_enter();
@@ -96,6 +117,29 @@ __global__ void __launch_bounds__(kQThreads) reshard_quantize_blocks_kernel(Bloc
   const int col = (threadIdx.x & 15) * 8, row0 = threadIdx.x >> 4;
   const int64_t c0 = (int64_t)kb * kScaleBlock + col;
   const int left = (int)max((int64_t)0, min((int64_t)8, a.cols - c0));
+  // Whole blocks keep what they loaded as it came: eight loads in flight, and half the registers.
+  if (wide && wide_q && (int64_t)(kb + 1) * kScaleBlock <= a.cols && (int64_t)(nb + 1) * kScaleBlock <= a.rows) {
+    Pack<T, 8> x[8];
+    const T *from = static_cast<const T *>(a.w) + e * a.batch_stride + ((int64_t)nb * kScaleBlock + row0) * a.row_stride + c0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = load_stream(reinterpret_cast<const Pack<T, 8> *>(from + 16 * i * a.row_stride));
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, magnitude(to_f32(x[i].v[j])));
+    float inv;
+    block_amax(m, part, a.scale + b, inv);
+    uint8_t *to = a.q + e * a.q_batch_stride + ((int64_t)nb * kScaleBlock + row0) * a.q_row_stride + c0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float f[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = to_f32(x[i].v[j]) * inv;
+      *reinterpret_cast<uint2 *>(to + 16 * i * a.q_row_stride) = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+    }
+    return;
+  }
   float x[8][8];
   uint32_t m = 0;
 #pragma unroll
@@ -107,14 +151,8 @@ __global__ void __launch_bounds__(kQThreads) reshard_quantize_blocks_kernel(Bloc
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) m = max(m, magnitude(x[i][j]));
-  m = __reduce_max_sync(kFull, m);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kQThreads / 32; ++i) m = max(m, part[i]);
-  float scale, inv;
-  block_scale(m, scale, inv);
-  if (threadIdx.x == 0) a.scale[b] = scale;
+  float inv;
+  block_amax(m, part, a.scale + b, inv);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t r = (int64_t)nb * kScaleBlock + row0 + 16 * i;
@@ -148,15 +186,37 @@ __global__ void __launch_bounds__(kQThreads)
   float sum[8];
 #pragma unroll
   for (int u = 0; u < 8; ++u) sum[u] = 0.0f;
-#pragma unroll 4
-  for (int j = 0; j < k; ++j) {
-    const int p = position[t * k + j];
-    if (p < 0) continue;
-    const float w = weights[t * k + j];
-    float x[8];
-    load_values<T, 8>(y + p * y_stride + c, left, wide, x);
+  if (wide && left >= 8) {
+    // eight slots' places, then their values: two trips to memory for eight slots, not two for each
+    for (int j0 = 0; j0 < k; j0 += 8) {
+      int64_t p[8];
+      float w[8];
+      Pack<T, 8> x[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) sum[u] = fmaf(w, x[u], sum[u]);
+      for (int j = 0; j < 8; ++j) {
+        p[j] = j0 + j < k ? position[t * k + j0 + j] : -1;
+        w[j] = j0 + j < k ? weights[t * k + j0 + j] : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (p[j] >= 0) x[j] = *reinterpret_cast<const Pack<T, 8> *>(y + p[j] * y_stride + c);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (p[j] >= 0) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) sum[u] = fmaf(w[j], to_f32(x[j].v[u]), sum[u]);
+        }
+    }
+  } else {
+    for (int j = 0; j < k; ++j) {
+      const int p = position[t * k + j];
+      if (p < 0) continue;
+      const float w = weights[t * k + j];
+      float x[8];
+      load_values<T, 8>(y + p * y_stride + c, left, false, x);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) sum[u] = fmaf(w, x[u], sum[u]);
+    }
   }
   T *to = out + t * out_stride + c;
   if (wide && left >= 8) {
