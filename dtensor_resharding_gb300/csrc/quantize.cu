@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(kQThreads) reshard_quantize_rows_kernel(Rows a
   const int64_t b = (int64_t)blockIdx.x * (kQThreads / 8) + threadIdx.x / 8;
   if (b - (lane >> 3) >= blocks) return;       // the whole warp
   const bool in = b < blocks;
-  const int64_t r = in ? b / per_row_blocks : 0;
+  const int64_t r = !in ? 0 : blocks <= 0xffffffffll ? (uint32_t)b / (uint32_t)per_row_blocks : b / per_row_blocks;
   const int kb = in ? (int)(b - r * per_row_blocks) : 0;
   const int at = kb * kScaleBlock + (lane & 7) * 16;
   const int left = in ? (int)min((int64_t)16, a.cols - at) : 0;
@@ -178,45 +178,23 @@ __global__ void __launch_bounds__(kQThreads)
     reshard_combine_kernel(const T *y, int64_t y_stride, const int32_t *position, const float *weights, int64_t tokens, int k, int64_t cols,
                            T *out, int64_t out_stride, int chunks, bool wide) {
   grid_enter();
-  const int64_t i = (int64_t)blockIdx.x * kQThreads + threadIdx.x;
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   if (i >= tokens * chunks) return;
-  const int64_t t = i / chunks;
+  const int64_t t = tokens * chunks <= 0xffffffffll ? (uint32_t)i / (uint32_t)chunks : i / chunks;
   const int64_t c = (i - t * chunks) * 8;
   const int left = (int)min((int64_t)8, cols - c);
   float sum[8];
 #pragma unroll
   for (int u = 0; u < 8; ++u) sum[u] = 0.0f;
-  if (wide && left >= 8) {
-    // eight slots' places, then their values: two trips to memory for eight slots, not two for each
-    for (int j0 = 0; j0 < k; j0 += 8) {
-      int64_t p[8];
-      float w[8];
-      Pack<T, 8> x[8];
+#pragma unroll 4
+  for (int j = 0; j < k; ++j) {
+    const int p = position[t * k + j];
+    if (p < 0) continue;
+    const float w = weights[t * k + j];
+    float x[8];
+    load_values<T, 8>(y + (int64_t)p * y_stride + c, left, wide, x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        p[j] = j0 + j < k ? position[t * k + j0 + j] : -1;
-        w[j] = j0 + j < k ? weights[t * k + j0 + j] : 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (p[j] >= 0) x[j] = *reinterpret_cast<const Pack<T, 8> *>(y + p[j] * y_stride + c);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (p[j] >= 0) {
-#pragma unroll
-          for (int u = 0; u < 8; ++u) sum[u] = fmaf(w[j], to_f32(x[j].v[u]), sum[u]);
-        }
-    }
-  } else {
-    for (int j = 0; j < k; ++j) {
-      const int p = position[t * k + j];
-      if (p < 0) continue;
-      const float w = weights[t * k + j];
-      float x[8];
-      load_values<T, 8>(y + p * y_stride + c, left, false, x);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) sum[u] = fmaf(w, x[u], sum[u]);
-    }
+    for (int u = 0; u < 8; ++u) sum[u] = fmaf(w, x[u], sum[u]);
   }
   T *to = out + t * out_stride + c;
   if (wide && left >= 8) {
@@ -254,12 +232,13 @@ int enqueue_combine(const void *y, int dtype, int64_t y_stride, const int32_t *p
                     int k, int64_t cols, void *out, int64_t out_stride, cudaStream_t stream) {
   if (tokens == 0 || cols == 0) return RESHARD_OK;
   const int chunks = (int)((cols + 7) / 8), es = element_bytes(dtype);
-  const dim3 grid((unsigned)((tokens * chunks + kQThreads - 1) / kQThreads));
+  const int block = tokens * chunks <= 32768 ? 64 : kQThreads;      // a few tokens' columns spread over the SMs
+  const dim3 grid((unsigned)((tokens * chunks + block - 1) / block));
   const bool wide = aligned16(y, y_stride, es) && aligned16(out, out_stride, es);
   cudaError_t e;
   auto go = [&](auto t) {
     using T = decltype(t);
-    return launch(reshard_combine_kernel<T>, grid, kQThreads, 0, 1, stream, static_cast<const T *>(y), y_stride, position, weights,
+    return launch(reshard_combine_kernel<T>, grid, block, 0, 1, stream, static_cast<const T *>(y), y_stride, position, weights,
                   tokens, k, cols, static_cast<T *>(out), out_stride, chunks, wide);
   };
   if (dtype == RESHARD_F32) e = go(float());

@@ -195,10 +195,15 @@ __global__ void __launch_bounds__(kRouteWarps * 32) reshard_route_kernel(RouteAr
   }
   if (a.bias) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < V; i += W) {
       const int e = Lane<V, W>::expert(i, lane);
-      const float s = a.sigmoid ? sigmoid_score(z[i]) : __fdiv_rn(expf(z[i] - top), total);
-      key[i] = z[i] > -INFINITY ? order_key(__fadd_rn(s, a.bias[e])) : 0;
+      struct alignas(4 * W) Vec { float v[W]; } b{};
+      if (e < a.experts) b = *reinterpret_cast<const Vec *>(a.bias + e);
+#pragma unroll
+      for (int j = i; j < i + W; ++j) {
+        const float s = a.sigmoid ? sigmoid_score(z[j]) : __fdiv_rn(expf(z[j] - top), total);
+        key[j] = z[j] > -INFINITY ? order_key(__fadd_rn(s, b.v[j - i])) : 0;
+      }
     }
     if (a.groups > 1) keep_groups<V, W>(a, lane, key, key);
   } else {
@@ -215,24 +220,27 @@ __global__ void __launch_bounds__(kRouteWarps * 32) reshard_route_kernel(RouteAr
   }
 
   int id = -1;              // lane j: the j-th choice
-  for (int j = 0; j < a.k; ++j) {
-    uint32_t mine = key[0];
+  uint32_t mine = key[0];   // this lane's best; only the lane that gave the last choice looks for it again
 #pragma unroll
-    for (int i = 1; i < V; ++i) mine = max(mine, key[i]);
+  for (int i = 1; i < V; ++i) mine = max(mine, key[i]);
+  for (int j = 0; j < a.k; ++j) {
     const uint32_t best = __reduce_max_sync(kFull, mine);
     if (!best) break;
-    // Mostly one lane has it; several only where keys are equal.
+    const uint32_t has = __ballot_sync(kFull, mine == best);
     int e = INT_MAX;
     if (mine == best) {
 #pragma unroll
       for (int i = V - 1; i >= 0; --i)
         if (key[i] == best) e = Lane<V, W>::expert(i, lane);
     }
-    const int first = __reduce_min_sync(kFull, e);
+    const int first = has & (has - 1) ? __reduce_min_sync(kFull, e) : __shfl_sync(kFull, e, __ffs(has) - 1);
     if (e == first) {
+      mine = 0;
 #pragma unroll
-      for (int i = 0; i < V; ++i)
+      for (int i = 0; i < V; ++i) {
         if (Lane<V, W>::expert(i, lane) == first) key[i] = 0;
+        mine = max(mine, key[i]);
+      }
     }
     if (lane == j) id = first;
   }
@@ -369,12 +377,20 @@ __global__ void __launch_bounds__(kDispatchWarps * 32)
   const int run = ((slots + ctas * kDispatchWarps * 32 - 1) / (ctas * kDispatchWarps * 32)) * 32;     // slots a warp
   const int64_t lo = (int64_t)(cta * kDispatchWarps + warp) * run;
   const int64_t hi = min(lo + run, (int64_t)slots);
+  auto expert = [&](int64_t i) {       // slot i's expert here, -1 if it has none
+    const int id = i < hi ? ids[i] : -1;
+    return id >= first && id - first < experts ? id - first : -1;
+  };
   for (int i = tid; i < kDispatchWarps * experts; i += kDispatchWarps * 32) count[i] = 0;
   __syncthreads();
   int32_t *const mine = count + warp * experts;
-  for (int64_t i = lo + lane; i < hi; i += 32) {
-    const int id = ids[i];
-    if (id >= first && id - first < experts) atomicAdd(&mine[id - first], 1);
+  for (int64_t i0 = lo + lane; i0 < hi; i0 += 8 * 32) {      // eight loads in flight
+    int e[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) e[u] = expert(i0 + 32 * u);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (e[u] >= 0) atomicAdd(&mine[e[u]], 1);
   }
   __syncthreads();
   for (int e = tid; e < experts; e += kDispatchWarps * 32) {       // counts of the warps before, and the CTA's
@@ -388,51 +404,64 @@ __global__ void __launch_bounds__(kDispatchWarps * 32)
     sum[e] = n;
   }
   asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
-  // the experts' first places: a warp-wide running sum of the cluster's counts, and this CTA's share of each
-  if (warp == 0) {
-    int base = 0;
-    for (int e0 = 0; e0 < experts; e0 += 32) {
-      const int e = e0 + lane;
-      int all = 0, before = 0;
-      if (e < experts) {
-        for (int c = 0; c < ctas; ++c) {
-          uint32_t at;
-          int n;
-          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(&sum[e])), "r"(c));
-          asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(n) : "r"(at) : "memory");
-          if (c < cta) before += n;
-          all += n;
+  // the experts' first places: a running sum of the cluster's counts, one expert a thread, and this CTA's share of each
+  __shared__ int32_t warp_sum[RESHARD_MAX_GROUPS / 32];
+  int all = 0, before = 0, upto = 0;
+  if (tid < (experts + 31) / 32 * 32) {
+    if (tid < experts) {
+      int n[kDispatchCluster];
+#pragma unroll
+      for (int c = 0; c < kDispatchCluster; ++c) {
+        uint32_t at;
+        n[c] = 0;
+        if (c < ctas) {
+          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(&sum[tid])), "r"(c));
+          asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(n[c]) : "r"(at));
         }
       }
-      int upto = all;
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(kFull, upto, o);
-        if (lane >= o) upto += x;
+#pragma unroll
+      for (int c = 0; c < kDispatchCluster; ++c) {
+        if (c < cta) before += n[c];
+        all += n[c];
       }
-      if (e < experts) {
-        if (cta == 0) offsets[e] = base + upto - all;
-        sum[experts + e] = base + upto - all + before;        // this CTA's first place of expert e
-      }
-      base += __shfl_sync(kFull, upto, 31);
     }
-    if (cta == 0 && lane == 0) offsets[experts] = base;
+    upto = all;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFull, upto, o);
+      if (lane >= o) upto += x;
+    }
+    if (lane == 31) warp_sum[warp] = upto;
   }
   __syncthreads();
-  for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-    const int64_t i = i0 + lane;
-    const int id = i < hi ? ids[i] : -1;
-    const int e = id >= first && id - first < experts ? id - first : -1;
-    const uint32_t same = __match_any_sync(kFull, e);
-    if (e >= 0) {
-      const int at = sum[experts + e] + mine[e] + __popc(same & ((1u << lane) - 1));
-      order[at] = (int32_t)i;
-      position[i] = at;
-    } else if (i < hi) {
-      position[i] = -1;
+  if (tid < experts) {
+    for (int w = 0; w < warp; ++w) upto += warp_sum[w];
+    if (cta == 0) {
+      offsets[tid] = upto - all;
+      if (tid == experts - 1) offsets[experts] = upto;
     }
-    __syncwarp();
-    if (e >= 0 && (same >> lane) == 1) mine[e] += __popc(same);      // the last of each expert's lanes
-    __syncwarp();
+    sum[experts + tid] = upto - all + before;        // this CTA's first place of the expert
+  }
+  __syncthreads();
+  for (int64_t i0 = lo; i0 < hi; i0 += 4 * 32) {
+    int next[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) next[u] = expert(i0 + 32 * u + lane);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t i = i0 + 32 * u + lane;
+      const int e = next[u];
+      const uint32_t same = __match_any_sync(kFull, e);
+      if (e >= 0) {
+        const int at = sum[experts + e] + mine[e] + __popc(same & ((1u << lane) - 1));
+        order[at] = (int32_t)i;
+        position[i] = at;
+      } else if (i < hi) {
+        position[i] = -1;
+      }
+      __syncwarp();
+      if (e >= 0 && (same >> lane) == 1) mine[e] += __popc(same);      // the last of each expert's lanes
+      __syncwarp();
+    }
   }
   asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");   // others may still read `sum`
 }
@@ -518,7 +547,7 @@ extern "C" int reshard_route(const void *logits, int dtype, int64_t tokens, int 
   cudaError_t e = cudaSuccess;
   by_type(dtype, [&](auto t) {
     using T = decltype(t);
-    by_shape(experts, quads(logits, dtype, experts, row_stride), [&](auto v, auto w) {
+    by_shape(experts, quads(logits, dtype, experts, row_stride) && (reinterpret_cast<uintptr_t>(bias) & 15) == 0, [&](auto v, auto w) {
       e = launch(reshard_route_kernel<T, decltype(v)::value, decltype(w)::value>,
                  dim3((unsigned)((tokens + kRouteWarps - 1) / kRouteWarps)), kRouteWarps * 32, 0, 1,
                  reinterpret_cast<cudaStream_t>(stream), a, weights, ids);
