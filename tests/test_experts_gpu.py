@@ -547,3 +547,16 @@ def test_refusals_name_what_is_wrong():
     w, i = torch.zeros(4, 2, device="cuda"), torch.zeros(4, 2, dtype=torch.int32, device="cuda")
     rc = R.binding.LIB.reshard_route(host.data_ptr(), 3, 4, 8, 8, None, 0, 1, 1, 1, 2, 1, 1.0, w.data_ptr(), i.data_ptr(), None)
     assert rc == R.RESHARD_ERR_INVALID_ARG and "pageable" in R.reshard_last_error()
+
+
+def test_example_refits_and_computes():
+    """The example's generation ranks against the layer in one piece: a rank's share rounds to bf16 (2^-8 at most) once more."""
+    import importlib.util
+    import os
+
+    from conftest import ROOT
+    spec = importlib.util.spec_from_file_location("refit_experts", os.path.join(ROOT, "examples", "refit_experts.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    assert example.main([]) < 2 ** -7
+    assert example.main(["--tokens", "3", "--experts", "8", "--hidden", "384", "--ffn", "256", "--train", "4", "--gen", "4", "--k", "2"]) < 2 ** -7
