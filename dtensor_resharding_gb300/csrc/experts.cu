@@ -69,6 +69,9 @@ void check_weight(Checks &c, const void *w, int64_t batch, int64_t batch_stride,
   }
 }
 
+// A word as an int; what does not fit stays out of every range that the calls accept.
+int as_int(int64_t v) { return (int)std::max<int64_t>(INT32_MIN, std::min<int64_t>(INT32_MAX, v)); }
+
 // The batch stride a tensor map takes where there is one matrix only.
 int64_t map_batch(int64_t batch, int64_t batch_stride, int64_t rows, int64_t stride) { return batch > 1 ? batch_stride : rows * stride; }
 
@@ -217,4 +220,53 @@ extern "C" int reshard_experts_fp8(const void *x, int dtype, int64_t tokens, int
   p2.out = y, p2.out_dtype = dtype, p2.out_stride = up(hidden, 16);
   if ((rc = enqueue_product(p2, stream))) return rc;
   return enqueue_combine(y, dtype, up(hidden, 16), position, weights, tokens, k, hidden, out, out_stride, stream);
+}
+
+extern "C" int reshard_ops_call(int op, const reshard_word_t *a) {
+  if (!a) return fail(RESHARD_ERR_INVALID_ARG, "args is NULL");
+  switch (op) {
+    case RESHARD_OP_ROUTE:
+      return reshard_route(reinterpret_cast<const void *>(a[0].i), as_int(a[1].i), a[2].i, as_int(a[3].i), a[4].i,
+                           reinterpret_cast<const float *>(a[5].i), as_int(a[6].i), as_int(a[7].i), as_int(a[8].i), as_int(a[9].i),
+                           as_int(a[10].i), as_int(a[11].i), (float)a[12].f, reinterpret_cast<float *>(a[13].i),
+                           reinterpret_cast<int32_t *>(a[14].i), reinterpret_cast<reshard_stream_t>(a[15].i));
+    case RESHARD_OP_ROUTE_BACKWARD:
+      return reshard_route_backward(reinterpret_cast<const float *>(a[0].i), reinterpret_cast<const void *>(a[1].i),
+                                    as_int(a[2].i), a[3].i, as_int(a[4].i), a[5].i, reinterpret_cast<const int32_t *>(a[6].i),
+                                    as_int(a[7].i), as_int(a[8].i), as_int(a[9].i), (float)a[10].f, reinterpret_cast<void *>(a[11].i),
+                                    a[12].i, reinterpret_cast<reshard_stream_t>(a[13].i));
+    case RESHARD_OP_DISPATCH:
+      return reshard_dispatch(reinterpret_cast<const int32_t *>(a[0].i), a[1].i, as_int(a[2].i), as_int(a[3].i),
+                              reinterpret_cast<int32_t *>(a[4].i), reinterpret_cast<int32_t *>(a[5].i),
+                              reinterpret_cast<int32_t *>(a[6].i), reinterpret_cast<reshard_stream_t>(a[7].i));
+    case RESHARD_OP_QUANTIZE_ROWS:
+      return reshard_quantize_rows(reinterpret_cast<const void *>(a[0].i), as_int(a[1].i), a[2].i, a[3].i, a[4].i,
+                                   reinterpret_cast<void *>(a[5].i), a[6].i, reinterpret_cast<float *>(a[7].i), a[8].i, a[9].i,
+                                   reinterpret_cast<reshard_stream_t>(a[10].i));
+    case RESHARD_OP_QUANTIZE_BLOCKS:
+      return reshard_quantize_blocks(reinterpret_cast<const void *>(a[0].i), as_int(a[1].i), a[2].i, a[3].i, a[4].i, a[5].i,
+                                     a[6].i, reinterpret_cast<void *>(a[7].i), a[8].i, a[9].i,
+                                     reinterpret_cast<float *>(a[10].i), reinterpret_cast<reshard_stream_t>(a[11].i));
+    case RESHARD_OP_MATMUL_FP8:
+      return reshard_matmul_fp8(reinterpret_cast<const void *>(a[0].i), a[1].i, reinterpret_cast<const float *>(a[2].i),
+                                a[3].i, a[4].i, reinterpret_cast<const void *>(a[5].i), a[6].i, a[7].i,
+                                reinterpret_cast<const float *>(a[8].i), reinterpret_cast<const int32_t *>(a[9].i),
+                                as_int(a[10].i), a[11].i, a[12].i, a[13].i, reinterpret_cast<void *>(a[14].i), as_int(a[15].i),
+                                a[16].i, reinterpret_cast<reshard_stream_t>(a[17].i));
+    case RESHARD_OP_LINEAR_FP8:
+      return reshard_linear_fp8(reinterpret_cast<const void *>(a[0].i), as_int(a[1].i), a[2].i, a[3].i, a[4].i,
+                                reinterpret_cast<const void *>(a[5].i), a[6].i, reinterpret_cast<const float *>(a[7].i),
+                                a[8].i, reinterpret_cast<void *>(a[9].i), a[10].i, reinterpret_cast<void *>(a[11].i), a[12].i,
+                                reinterpret_cast<reshard_stream_t>(a[13].i));
+    case RESHARD_OP_EXPERTS_FP8:
+      return reshard_experts_fp8(reinterpret_cast<const void *>(a[0].i), as_int(a[1].i), a[2].i, a[3].i, a[4].i,
+                                 reinterpret_cast<const int32_t *>(a[5].i), reinterpret_cast<const float *>(a[6].i),
+                                 as_int(a[7].i), as_int(a[8].i), as_int(a[9].i), a[10].i, reinterpret_cast<const void *>(a[11].i),
+                                 a[12].i, a[13].i, reinterpret_cast<const float *>(a[14].i),
+                                 reinterpret_cast<const void *>(a[15].i), a[16].i, a[17].i,
+                                 reinterpret_cast<const float *>(a[18].i), reinterpret_cast<void *>(a[19].i), a[20].i,
+                                 reinterpret_cast<void *>(a[21].i), a[22].i, reinterpret_cast<reshard_stream_t>(a[23].i));
+    default:
+      return fail(RESHARD_ERR_INVALID_ARG, "unknown operator number");
+  }
 }

@@ -13,18 +13,20 @@ input made on another stream must be ready there (an event), as for any torch op
 from __future__ import annotations
 
 import ctypes
+from functools import lru_cache
+from struct import Struct
 from typing import Optional, Tuple
 
 import torch
 
-from .binding import LIB, ReshardError, RESHARD_ERR_INVALID_ARG, _check
+from .binding import LIB, ReshardError, RESHARD_ERR_INVALID_ARG, _check, reshard_last_error
 
 RESHARD_SCORE_SOFTMAX = 0
 RESHARD_SCORE_SIGMOID = 1
 SCORES = {"softmax": RESHARD_SCORE_SOFTMAX, "sigmoid": RESHARD_SCORE_SIGMOID}
 OPS_EXPORTED = ("reshard_route", "reshard_route_backward", "reshard_dispatch", "reshard_quantize_rows", "reshard_quantize_blocks",
                 "reshard_matmul_fp8", "reshard_linear_fp8_workspace", "reshard_linear_fp8", "reshard_experts_fp8_workspace",
-                "reshard_experts_fp8", "reshard_ops_status")
+                "reshard_experts_fp8", "reshard_ops_call", "reshard_ops_status")
 _CODES = {torch.bfloat16: 1, torch.float16: 2, torch.float32: 3}   # RESHARD_BF16, RESHARD_F16, RESHARD_F32
 _FP8 = torch.float8_e4m3fn
 
@@ -40,11 +42,29 @@ _SIGNATURES = {
     "reshard_linear_fp8": [_p, _i, _l, _l, _l, _p, _l, _p, _l, _p, _l, _p, _l, _p],
     "reshard_experts_fp8_workspace": [_l, _i, _i, _l, _l, _i],
     "reshard_experts_fp8": [_p, _i, _l, _l, _l, _p, _p, _i, _i, _i, _l, _p, _l, _l, _p, _p, _l, _l, _p, _p, _l, _p, _l, _p],
+    "reshard_ops_call": [_i, ctypes.c_char_p],
     "reshard_ops_status": [_p, _i],
 }
 for _name, _args in _SIGNATURES.items():
     getattr(LIB, _name).argtypes = _args
     getattr(LIB, _name).restype = _l if _name.endswith("_workspace") else _i
+
+
+# The calls' arguments as 64-bit words (reshard_ops_call): packing them takes a third of what ctypes takes for each.
+_ROUTE = Struct("=12qd3q").pack
+_ROUTE_BACKWARD = Struct("=10qd3q").pack
+_DISPATCH = Struct("=8q").pack
+_QUANTIZE_ROWS = Struct("=11q").pack
+_QUANTIZE_BLOCKS = Struct("=12q").pack
+_MATMUL_FP8 = Struct("=18q").pack
+_LINEAR_FP8 = Struct("=14q").pack
+_EXPERTS_FP8 = Struct("=24q").pack
+
+
+def _call(op: int, words: bytes) -> None:
+    rc = LIB.reshard_ops_call(op, words)
+    if rc:
+        raise ReshardError(rc, reshard_last_error())
 
 
 def _bad(what: str) -> None:
@@ -70,23 +90,29 @@ def _matrix(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
     step, inner = t.stride()
     if inner != 1 and cols > 1:
         _bad(f"{name} must have contiguous rows")
-    return rows, cols, step if rows > 1 else max(step, cols)
+    return rows, cols, step if rows > 1 or step > cols else cols
 
 
 def _dense(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, like: torch.Tensor) -> int:
     """The address of a contiguous tensor of that type and shape on `like`'s device."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != like.device:
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != like.get_device():
         _bad(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {like.device}, not {t.dtype} of shape "
              f"{tuple(t.shape)}, strides {t.stride()} on {t.device}")
     return t.data_ptr()
 
 
-def _output(out: Optional[torch.Tensor], rows: int, cols: int, dtype: torch.dtype, like: torch.Tensor) -> torch.Tensor:
+def _output(out: Optional[torch.Tensor], rows: int, cols: int, dtype: torch.dtype, like: torch.Tensor) -> Tuple[torch.Tensor, int]:
+    """(the output, its row stride)"""
     if out is None:
-        return torch.empty((rows, cols), dtype=dtype, device=like.device)
-    if out.dtype is not dtype or out.shape != (rows, cols) or out.device != like.device:
+        return torch.empty((rows, cols), dtype=dtype, device=like.device), cols
+    if out.dtype is not dtype or out.shape != (rows, cols) or out.get_device() != like.get_device():
         _bad(f"out must be {dtype} of shape {(rows, cols)} on {like.device}, not {out.dtype} of shape {tuple(out.shape)} on {out.device}")
-    return out
+    return out, _matrix(out, "out")[2]
+
+
+# Workspace sizes by sizes: asking the library each time costs a call.
+_linear_space = lru_cache(maxsize=4096)(LIB.reshard_linear_fp8_workspace)
+_experts_space = lru_cache(maxsize=4096)(LIB.reshard_experts_fp8_workspace)
 
 
 def _here(t: torch.Tensor, stream) -> Optional[int]:
@@ -144,12 +170,12 @@ def reshard_route(logits: torch.Tensor, k: int, *, score="softmax", bias: Option
                                  renormalize=renormalize, scale=scale)
     T, E, step = _matrix(logits, "logits")
     code = _code(logits, "logits")
-    at_bias = None if bias is None else _dense(bias, "bias", torch.float32, (E,), logits)
+    at_bias = 0 if bias is None else _dense(bias, "bias", torch.float32, (E,), logits)
     device = logits.device
     weights = torch.empty((T, max(0, k)), dtype=torch.float32, device=device)
     ids = torch.empty((T, max(0, k)), dtype=torch.int32, device=device)
-    _check(LIB.reshard_route(logits.data_ptr(), code, T, E, step, at_bias, _score(score), groups, groups_kept, group_top, k,
-                             renormalize, scale, weights.data_ptr(), ids.data_ptr(), here))
+    _call(0, _ROUTE(logits.data_ptr(), code, T, E, step, at_bias, _score(score), groups, groups_kept, group_top, k,
+                    renormalize, scale, weights.data_ptr(), ids.data_ptr(), here))
     return weights, ids
 
 
@@ -169,9 +195,9 @@ def reshard_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, ids
     at_ids = _dense(ids, "ids", torch.int32, (T, k), logits)
     grad_weights = grad_weights.contiguous()
     at_grad = _dense(grad_weights, "grad_weights", torch.float32, (T, k), logits)
-    out = _output(out, T, E, logits.dtype, logits)
-    _check(LIB.reshard_route_backward(at_grad, logits.data_ptr(), code, T, E, step, at_ids, k, _score(score), renormalize, scale,
-                                      out.data_ptr(), _matrix(out, "out")[2], here))
+    out, to_step = _output(out, T, E, logits.dtype, logits)
+    _call(1, _ROUTE_BACKWARD(at_grad, logits.data_ptr(), code, T, E, step, at_ids, k, _score(score), renormalize, scale,
+                             out.data_ptr(), to_step, here))
     return out
 
 
@@ -188,16 +214,8 @@ def reshard_dispatch(ids: torch.Tensor, experts: int, first_expert: int = 0, str
     offsets = torch.empty(max(0, experts) + 1, dtype=torch.int32, device=device)
     order = torch.empty(n, dtype=torch.int32, device=device)
     position = torch.empty(n, dtype=torch.int32, device=device)
-    _check(LIB.reshard_dispatch(at_ids, n, first_expert, experts, offsets.data_ptr(), order.data_ptr(), position.data_ptr(), here))
+    _call(2, _DISPATCH(at_ids, n, first_expert, experts, offsets.data_ptr(), order.data_ptr(), position.data_ptr(), here))
     return offsets, order, position
-
-
-def _pitched(shape, device) -> torch.Tensor:
-    """Bytes whose rows start every multiple of 16, as the products read them."""
-    cols = shape[-1]
-    pitch = -(-cols // 16) * 16
-    t = torch.empty((*shape[:-1], pitch), dtype=_FP8, device=device)
-    return t if pitch == cols else t[..., :cols]
 
 
 def reshard_quantize_rows(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -210,10 +228,11 @@ def reshard_quantize_rows(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, t
             return reshard_quantize_rows(x)
     M, K, step = _matrix(x, "x")
     code = _code(x, "x")
-    q = _pitched((M, K), x.device)
-    scale = torch.empty((-(-K // 128), M), dtype=torch.float32, device=x.device)
-    _check(LIB.reshard_quantize_rows(x.data_ptr(), code, M, K, step, q.data_ptr(), q.stride(0), scale.data_ptr(), 1, max(1, M), here))
-    return q, scale.t()
+    device, pitch, rows = x.device, -(-K // 16) * 16, M or 1
+    q = torch.empty_strided((M, K), (pitch, 1), dtype=_FP8, device=device)
+    scale = torch.empty_strided((M, -(-K // 128)), (1, rows), dtype=torch.float32, device=device)
+    _call(3, _QUANTIZE_ROWS(x.data_ptr(), code, M, K, step, q.data_ptr(), pitch, scale.data_ptr(), 1, rows, here))
+    return q, scale
 
 
 def reshard_quantize_blocks(w: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -223,17 +242,24 @@ def reshard_quantize_blocks(w: torch.Tensor, stream=None) -> Tuple[torch.Tensor,
     if here is None:
         with _on(w, stream):
             return reshard_quantize_blocks(w)
-    if w.dim() not in (2, 3):
-        _bad(f"w must have 2 or 3 dimensions, not {w.dim()}")
-    N, K = w.shape[-2:]
-    if K > 1 and w.stride(-1) != 1:
+    shape, stride = w.shape, w.stride()
+    if len(shape) not in (2, 3):
+        _bad(f"w must have 2 or 3 dimensions, not {len(shape)}")
+    N, K = shape[-2:]
+    if K > 1 and stride[-1] != 1:
         _bad("w must have contiguous rows")
-    E, batch = (w.shape[0], w.stride(0)) if w.dim() == 3 else (1, 0)
     code = _code(w, "w")
-    q = _pitched(tuple(w.shape), w.device)
-    scale = torch.empty((*w.shape[:-2], -(-N // 128), -(-K // 128)), dtype=torch.float32, device=w.device)
-    _check(LIB.reshard_quantize_blocks(w.data_ptr(), code, E, N, K, batch, w.stride(-2) if N > 1 else max(K, w.stride(-2)), q.data_ptr(),
-                                       q.stride(0) if q.dim() == 3 else 0, q.stride(-2), scale.data_ptr(), here))
+    pitch, blocks, device = -(-K // 16) * 16, (-(-N // 128), -(-K // 128)), w.device
+    step = stride[-2] if N > 1 or stride[-2] > K else K
+    if len(shape) == 3:
+        E, batch = shape[0], stride[0]
+        q = torch.empty_strided(shape, (N * pitch, pitch, 1), dtype=_FP8, device=device)
+        scale = torch.empty((E, *blocks), dtype=torch.float32, device=device)
+    else:
+        E, batch = 1, 0
+        q = torch.empty_strided(shape, (pitch, 1), dtype=_FP8, device=device)
+        scale = torch.empty(blocks, dtype=torch.float32, device=device)
+    _call(4, _QUANTIZE_BLOCKS(w.data_ptr(), code, E, N, K, batch, step, q.data_ptr(), N * pitch, pitch, scale.data_ptr(), here))
     return q, scale
 
 
@@ -247,7 +273,7 @@ def _weights(w: torch.Tensor, scale: torch.Tensor, name: str, dim: int, like: to
     N, K = shape[-2:]
     if stride[-1] != 1 and K > 1:
         _bad(f"{name} must have contiguous rows")
-    if w.device != like.device:
+    if w.get_device() != like.get_device():
         _bad(f"{name} is on {w.device}, not on {like.device}")
     at_scale = _dense(scale, f"{name}'s scale", torch.float32, (*shape[:-2], -(-N // 128), -(-K // 128)), like)
     # one row has no pitch of its own: the next multiple of 16
@@ -274,13 +300,13 @@ def reshard_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, 
     if w.shape[-1] != K:
         _bad(f"a has {K} columns, w {w.shape[-1]}")
     groups = 1 if offsets is None else w.shape[0]
-    at_offsets = None if offsets is None else _dense(offsets, "offsets", torch.int32, (groups + 1,), a)
+    at_offsets = 0 if offsets is None else _dense(offsets, "offsets", torch.int32, (groups + 1,), a)
     if a_scale.dtype is not torch.float32 or a_scale.shape != (M, -(-K // 128)) or a_scale.device != a.device:
         _bad(f"a_scale must be float32 of shape {(M, -(-K // 128))} on {a.device}, not {a_scale.dtype} of shape {tuple(a_scale.shape)}")
-    out = _output(out, M, N, out_dtype if out is None else out.dtype, a)
-    _check(LIB.reshard_matmul_fp8(a.data_ptr(), step if M > 1 else -(-step // 16) * 16, a_scale.data_ptr(), max(1, a_scale.stride(0)),
-                                  max(1, a_scale.stride(1)), at_w, batch, pitch, at_ws, at_offsets, groups, M, N, K,
-                                  out.data_ptr(), _code(out, "out"), _matrix(out, "out")[2], here))
+    out, to_step = _output(out, M, N, out_dtype if out is None else out.dtype, a)
+    _call(5, _MATMUL_FP8(a.data_ptr(), step if M > 1 else -(-step // 16) * 16, a_scale.data_ptr(), max(1, a_scale.stride(0)),
+                         max(1, a_scale.stride(1)), at_w, batch, pitch, at_ws, at_offsets, groups, M, N, K, out.data_ptr(), _code(out, "out"),
+                         to_step, here))
     return out
 
 
@@ -297,11 +323,11 @@ def reshard_linear_fp8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, 
     N = w.shape[0]
     if w.shape[1] != K:
         _bad(f"x has {K} columns, w {w.shape[1]}")
-    out = _output(out, M, N, x.dtype, x)
-    need = LIB.reshard_linear_fp8_workspace(M, K)
+    out, to_step = _output(out, M, N, x.dtype, x)
+    need = _linear_space(M, K)
     space = torch.empty(need, dtype=torch.uint8, device=x.device)
-    _check(LIB.reshard_linear_fp8(x.data_ptr(), code, M, K, step, at_w, pitch, at_ws, N, out.data_ptr(), _matrix(out, "out")[2],
-                                  space.data_ptr(), need, here))
+    _call(6, _LINEAR_FP8(x.data_ptr(), code, M, K, step, at_w, pitch, at_ws, N, out.data_ptr(), to_step, space.data_ptr(),
+                         need, here))
     return out
 
 
@@ -328,12 +354,11 @@ def reshard_experts_fp8(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tenso
     if w13.shape != (E, 2 * I, H) or w2.shape[1] != H:
         _bad(f"w13 {tuple(w13.shape)} and w2 {tuple(w2.shape)} do not fit x with {H} columns: [experts, 2 ffn, hidden] and "
              "[experts, hidden, ffn]")
-    out = _output(out, T, H, x.dtype, x)
-    need = LIB.reshard_experts_fp8_workspace(T, k, E, H, I, code)
+    out, to_step = _output(out, T, H, x.dtype, x)
+    need = _experts_space(T, k, E, H, I, code)
     space = torch.empty(need, dtype=torch.uint8, device=x.device)
-    _check(LIB.reshard_experts_fp8(x.data_ptr(), code, T, H, step, at_ids, at_weights, k, first_expert, E, I, at_w13, batch13, pitch13,
-                                   at_s13, at_w2, batch2, pitch2, at_s2, out.data_ptr(), _matrix(out, "out")[2], space.data_ptr(), need,
-                                   here))
+    _call(7, _EXPERTS_FP8(x.data_ptr(), code, T, H, step, at_ids, at_weights, k, first_expert, E, I, at_w13, batch13, pitch13,
+                          at_s13, at_w2, batch2, pitch2, at_s2, out.data_ptr(), to_step, space.data_ptr(), need, here))
     return out
 
 

@@ -124,6 +124,25 @@ int reshard_experts_fp8(const void *x, int dtype, int64_t tokens, int64_t hidden
                         void *workspace, int64_t workspace_bytes, reshard_stream_t stream);
 
 /*
+ * reshard_ops_call -- one of the calls above with its arguments, in order, as 64-bit words (integers and pointers in `i`,
+ * floats in `f`): for bindings in which marshalling each argument costs more than the call. op is a RESHARD_OP_* number;
+ * another one is INVALID_ARG.
+ */
+#define RESHARD_OP_ROUTE 0
+#define RESHARD_OP_ROUTE_BACKWARD 1
+#define RESHARD_OP_DISPATCH 2
+#define RESHARD_OP_QUANTIZE_ROWS 3
+#define RESHARD_OP_QUANTIZE_BLOCKS 4
+#define RESHARD_OP_MATMUL_FP8 5
+#define RESHARD_OP_LINEAR_FP8 6
+#define RESHARD_OP_EXPERTS_FP8 7
+typedef union {
+  int64_t i;
+  double f;
+} reshard_word_t;
+int reshard_ops_call(int op, const reshard_word_t *args);
+
+/*
  * reshard_ops_status -- the product kernels' status word on the current device (0 = fine; bit 0: a wait inside a
  * kernel gave up after its time limit and that launch's output is incomplete). Synchronizes the device, then reads
  * the word; reset != 0 clears it.

@@ -144,3 +144,18 @@ def test_route_groups_by_hand():
     masked[0, 7] = float("nan")
     w, ids = X.route(masked, 2)
     assert ids.tolist() == [[6, -1]] and w.tolist() == [[1.0, 0.0]]
+
+
+def test_packed_arguments_reach_the_same_calls():
+    """The word form refuses what the plain form refuses, and takes no number or value that it cannot hold."""
+    words = (ctypes.c_int64 * 24)()
+    refused(B.LIB.reshard_ops_call(99, bytes(words)), B.RESHARD_ERR_INVALID_ARG, "unknown operator")
+    refused(B.LIB.reshard_ops_call(0, None), B.RESHARD_ERR_INVALID_ARG, "NULL")
+    for op in range(8):
+        rc = B.LIB.reshard_ops_call(op, bytes(words))
+        assert rc == B.RESHARD_ERR_INVALID_ARG, (op, rc)
+    words[:5] = [0, 1, 1, 1 << 40, 1 << 40]         # experts beyond 32 bits
+    words[11] = 2
+    assert B.LIB.reshard_ops_call(0, bytes(words)) != 0
+    with pytest.raises(R.ReshardError):
+        ops._call(2, ops._DISPATCH(0, 4, -1, 0, 0, 0, 0, 0))
