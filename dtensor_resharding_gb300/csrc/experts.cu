@@ -113,7 +113,9 @@ extern "C" int reshard_matmul_fp8(const void *a, int64_t a_stride, const float *
   return enqueue_product(p, reinterpret_cast<cudaStream_t>(stream));
 }
 
-extern "C" int64_t reshard_linear_fp8_workspace(int64_t m, int64_t k) { return m < 0 || k < 0 ? 0 : QuantizedRows(m, k).bytes(); }
+extern "C" int64_t reshard_linear_fp8_workspace(int64_t m, int64_t k) {
+  return m < 0 || k < 0 || product_quantizes(m, k) ? 0 : QuantizedRows(m, k).bytes();
+}
 
 extern "C" int reshard_linear_fp8(const void *x, int dtype, int64_t m, int64_t k, int64_t row_stride, const void *w, int64_t w_stride,
                                   const float *w_scale, int64_t n, void *out, int64_t out_stride, void *workspace, int64_t workspace_bytes,
@@ -128,23 +130,26 @@ extern "C" int reshard_linear_fp8(const void *x, int dtype, int64_t m, int64_t k
     check_weight(c, w, 1, 0, n, k, w_stride, "w");
     c.pointer(w_scale, "w_scale", 4);
     c.pointer(out, "out", (uintptr_t)element_bytes(dtype));
-    c.pointer(workspace, "workspace", kAlign);
+    if (reshard_linear_fp8_workspace(m, k) > 0) c.pointer(workspace, "workspace", kAlign);
     c.invalid(workspace_bytes < reshard_linear_fp8_workspace(m, k), "the workspace is smaller than reshard_linear_fp8_workspace");
   }
   if (!c.ok()) return c.report();
   if (m == 0 || n == 0) return RESHARD_OK;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  const QuantizedRows l(m, k);
-  uint8_t *q = static_cast<uint8_t *>(workspace);
-  float *scale = reinterpret_cast<float *>(q + l.values);
-  Rows r{x, dtype, m, k, row_stride, q, l.pitch, scale, 1, m};
-  int rc = enqueue_quantize_rows(r, stream);
-  if (rc) return rc;
   Product p{};
-  p.a = q, p.a_stride = l.pitch, p.a_scale = scale, p.as_row = 1, p.as_block = m;
+  if (product_quantizes(m, k)) {
+    p.x = x, p.a_stride = row_stride;
+  } else {
+    const QuantizedRows l(m, k);
+    uint8_t *q = static_cast<uint8_t *>(workspace);
+    float *scale = reinterpret_cast<float *>(q + l.values);
+    const int rc = enqueue_quantize_rows(Rows{x, dtype, m, k, row_stride, q, l.pitch, scale, 1, m}, stream);
+    if (rc) return rc;
+    p.a = q, p.a_stride = l.pitch, p.a_scale = scale, p.as_row = 1, p.as_block = m;
+    p.early = true;
+  }
   p.w = static_cast<const uint8_t *>(w), p.w_batch = n * w_stride, p.w_stride = w_stride, p.w_scale = w_scale;
   p.m = m, p.n = n, p.k = k;
-  p.early = true;
   p.out = out, p.out_dtype = dtype, p.out_stride = out_stride;
   return enqueue_product(p, stream);
 }

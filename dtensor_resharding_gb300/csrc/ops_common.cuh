@@ -127,6 +127,8 @@ struct Product {              // out[m, n] = sum_k a[m, k] w[n, k], both as 8-bi
   int64_t a_stride;
   const float *a_scale;
   int64_t as_row, as_block;
+  const void *x = nullptr;           // rows in out's type, a_stride apart, that the product quantizes itself, in place of a and
+                                     // a_scale: dense and product_quantizes()
   const uint8_t *w;
   int64_t w_batch, w_stride;
   const float *w_scale;
@@ -147,6 +149,7 @@ struct Product {              // out[m, n] = sum_k a[m, k] w[n, k], both as 8-bi
   int64_t os_row = 0, os_block = 0;
 };
 int enqueue_product(const Product &p, cudaStream_t stream);
+bool product_quantizes(int64_t m, int64_t k);    // whether a dense product takes rows as `x`
 bool product_gathers(int64_t m, int groups);     // whether a product of m rows in so many groups can take `order`
 
 // ----------------------------------------------------------------------------------------------- device side --

@@ -22,6 +22,7 @@
 #include <algorithm>
 #include <cstddef>
 #include <mutex>
+#include <type_traits>
 
 #include "tensor_core.cuh"
 
@@ -38,6 +39,9 @@ __device__ int g_ops_status;
 struct Args {
   const float *a_scale;
   int64_t as_row, as_block;
+  const void *x;        // the few kernel's rows: values that it quantizes, or quantized ones
+  int64_t x_stride;
+  int cols;
   const float *w_scale;
   const int32_t *offsets;
   const int32_t *order; // NULL: row r of the product is row r of a; otherwise row order[r] / per_row
@@ -813,6 +817,166 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<NT, Gated>::kPerSm)
   if (warp == 5) tmem_free(tmem, C::kColumns);
 }
 
+// ----------------------------------------------------------------------------------------------------------- few --
+
+constexpr int kFewRows = 8;              // rows of a: the columns of one warp-wide product
+constexpr int kFewN = 16;                // rows of w a CTA
+constexpr int kFewWarps = 8;             // of a CTA: each has a share of K
+
+constexpr int kFewAhead = 3;             // blocks of w on their way to a warp
+constexpr int64_t kFewBytes = 64 << 10;  // of the rows of a, quantized, in shared memory
+
+// A lane's 32 bytes of a row of w.
+struct FewBytes {
+  uint4 v[2];
+  __device__ __forceinline__ void load(const uint8_t *p) {
+    v[0] = __ldcs(reinterpret_cast<const uint4 *>(p));
+    v[1] = __ldcs(reinterpret_cast<const uint4 *>(p) + 1);
+  }
+  __device__ __forceinline__ void load_some(const uint8_t *p, int left) {      // a row's end: what follows it is not the row's
+    uint64_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll 1
+      for (int j = 0; j < 8; ++j)
+        if (8 * i + j < left) w[i] |= (uint64_t)p[8 * i + j] << (8 * j);
+    v[0] = make_uint4((uint32_t)w[0], (uint32_t)(w[0] >> 32), (uint32_t)w[1], (uint32_t)(w[1] >> 32));
+    v[1] = make_uint4((uint32_t)w[2], (uint32_t)(w[2] >> 32), (uint32_t)w[3], (uint32_t)(w[3] >> 32));
+  }
+};
+
+// Few rows of a, dense, and often one: a matrix times a vector, bound by the read of w from HBM and, at the sizes where
+// that is short, by what a kernel has to do before its first load. So no tensor memory, barriers or staging of w here:
+// each warp streams w from global memory into registers, three blocks ahead, and multiplies on the warp-wide tensor
+// instruction (16 x 8 x 32), whose rate is far above what the read leaves to do. Lane (g, t) holds rows g and g + 8 of w
+// and row g of a at columns 32 t .. 32 t + 31 of a block: which columns a product takes from a lane is the same for both
+// operands, so that a lane's bytes can be neighbours. The CTA quantizes its rows of a into shared memory (X: their type, or
+// uint8_t where they come quantized) while the first loads of w are on their way: one launch for the whole call. The K
+// shares of a CTA's warps are added in order.
+template <typename X>
+__global__ void __launch_bounds__(kFewWarps * 32, 3) reshard_product_few_kernel(const __grid_constant__ Args p, const uint8_t *wq, int64_t w_stride) {
+  constexpr bool kGiven = std::is_same_v<X, uint8_t>;
+  grid_enter();
+  extern __shared__ __align__(16) uint8_t xq[];      // [row][pitch], then scales [row][block]
+  __shared__ float part[kFewWarps][kFewN][kFewRows + 1];
+  const int pitch = p.kblocks * kBlockK + 16;
+  float *const xs = reinterpret_cast<float *>(xq + p.m * pitch);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int n0 = blockIdx.x * kFewN;
+  const int kb0 = p.kblocks * warp / kFewWarps, kb1 = p.kblocks * (warp + 1) / kFewWarps, whole = min(kb1, p.cols / kBlockK);
+  const uint8_t *w0 = wq + (int64_t)min(n0 + g, p.n - 1) * w_stride + 32 * t, *w1 = wq + (int64_t)min(n0 + g + 8, p.n - 1) * w_stride + 32 * t;
+  FewBytes b[kFewAhead][2];
+#pragma unroll
+  for (int u = 0; u < kFewAhead; ++u)
+    if (kb0 + u < whole) {
+      b[u][0].load(w0 + (kb0 + u) * kBlockK);
+      b[u][1].load(w1 + (kb0 + u) * kBlockK);
+    }
+
+  // the rows of a: 8 lanes a block, 16 values each
+  const bool wide = ((reinterpret_cast<uintptr_t>(p.x) | (uintptr_t)(p.x_stride * (int64_t)sizeof(X))) & 15) == 0;
+#pragma unroll 1
+  for (int i = tid >> 3; i < (p.m * p.kblocks + 3) / 4 * 4; i += kFewWarps * 4) {      // four blocks a warp, all of it to the shuffles
+    const bool in = i < p.m * p.kblocks;
+    const int r = in ? i / p.kblocks : 0, kb = in ? i - r * p.kblocks : 0, at = kb * kBlockK + (lane & 7) * 16;
+    const X *from = static_cast<const X *>(p.x) + (int64_t)r * p.x_stride + at;
+    const int left = in ? p.cols - at : 0;
+    uint4 q;
+    float scale;
+    if constexpr (kGiven) {
+      FewBytes x;
+      if (left >= 16 && wide) x.v[0] = __ldg(reinterpret_cast<const uint4 *>(from));
+      else x.load_some(from, min(left, 16));
+      q = x.v[0];
+      scale = in ? p.a_scale[(int64_t)r * p.as_row + (int64_t)kb * p.as_block] : 0.0f;
+    } else {
+      float x[16];
+      if (left >= 16 && wide) {
+        constexpr int per = 16 / sizeof(X);
+#pragma unroll
+        for (int j = 0; j < 16 / per; ++j) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4 *>(from) + j);
+#pragma unroll
+          for (int e = 0; e < per; ++e) x[j * per + e] = to_f32(reinterpret_cast<const X *>(&v)[e]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = j < left ? to_f32(from[j]) : 0.0f;
+      }
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) m = max(m, magnitude(x[j]));
+#pragma unroll
+      for (int o = 4; o; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+      float inv;
+      block_scale(m, scale, inv);
+      q = make_uint4(e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv), e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv),
+                     e4m3x4(x[8] * inv, x[9] * inv, x[10] * inv, x[11] * inv), e4m3x4(x[12] * inv, x[13] * inv, x[14] * inv, x[15] * inv));
+    }
+    if (in) {
+      *reinterpret_cast<uint4 *>(xq + r * pitch + at) = q;
+      if ((lane & 7) == 0) xs[r * p.kblocks + kb] = scale;
+    }
+  }
+  __syncthreads();
+
+  const float *sw = p.w_scale + (int64_t)(n0 / kScaleBlock) * p.kblocks;
+  const uint8_t *mine = xq + min(g, p.m - 1) * pitch + 32 * t;
+  const float *s0 = xs + min(2 * t, p.m - 1) * p.kblocks, *s1 = xs + min(2 * t + 1, p.m - 1) * p.kblocks;      // this lane's sums are of rows 2 t and 2 t + 1
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto block = [&](const FewBytes (&w)[2], int kb) {
+    uint32_t q[8];
+    *reinterpret_cast<uint4 *>(q) = *reinterpret_cast<const uint4 *>(mine + kb * kBlockK);
+    *reinterpret_cast<uint4 *>(q + 4) = *reinterpret_cast<const uint4 *>(mine + kb * kBlockK + 16);
+    const uint32_t u0[8] = {w[0].v[0].x, w[0].v[0].y, w[0].v[0].z, w[0].v[0].w, w[0].v[1].x, w[0].v[1].y, w[0].v[1].z, w[0].v[1].w};
+    const uint32_t u1[8] = {w[1].v[0].x, w[1].v[0].y, w[1].v[0].z, w[1].v[0].w, w[1].v[1].x, w[1].v[1].y, w[1].v[1].z, w[1].v[1].w};
+    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 8; i += 2)
+      asm volatile("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                   : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                   : "r"(u0[i]), "r"(u1[i]), "r"(u0[i + 1]), "r"(u1[i + 1]), "r"(q[i]), "r"(q[i + 1]));
+    const float f = sw[kb], f0 = s0[kb] * f, f1 = s1[kb] * f;
+    acc[0] = fmaf(d[0], f0, acc[0]);
+    acc[1] = fmaf(d[1], f1, acc[1]);
+    acc[2] = fmaf(d[2], f0, acc[2]);
+    acc[3] = fmaf(d[3], f1, acc[3]);
+  };
+#pragma unroll 1
+  for (int kb = kb0; kb < whole; kb += kFewAhead) {
+#pragma unroll
+    for (int u = 0; u < kFewAhead; ++u) {
+      if (kb + u < whole) {
+        block(b[u], kb + u);
+        if (kb + u + kFewAhead < whole) {
+          b[u][0].load(w0 + (int64_t)(kb + u + kFewAhead) * kBlockK);
+          b[u][1].load(w1 + (int64_t)(kb + u + kFewAhead) * kBlockK);
+        }
+      }
+    }
+  }
+  if (whole < kb1) {                 // K's last block, if it is not whole, is the last warp's
+    const int left = p.cols - whole * kBlockK - 32 * t;
+    b[0][0].load_some(w0 + (int64_t)whole * kBlockK, left);
+    b[0][1].load_some(w1 + (int64_t)whole * kBlockK, left);
+    block(b[0], whole);
+  }
+  part[warp][g][2 * t] = acc[0];
+  part[warp][g][2 * t + 1] = acc[1];
+  part[warp][g + 8][2 * t] = acc[2];
+  part[warp][g + 8][2 * t + 1] = acc[3];
+  __syncthreads();
+  const int r = tid & 15, m = tid >> 4;
+  if (m < p.m && n0 + r < p.n) {
+    float v = part[0][r][m];
+#pragma unroll
+    for (int i = 1; i < kFewWarps; ++i) v += part[i][r][m];
+    const int64_t at = (int64_t)m * p.out_stride + n0 + r;
+    if (p.out_dtype == RESHARD_F32) static_cast<float *>(p.out)[at] = v;
+    else static_cast<uint16_t *>(p.out)[at] = p.out_dtype == RESHARD_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(v)) : __half_as_ushort(__float2half_rn(v));
+  }
+}
+
 // ----------------------------------------------------------------------------------------------------- host side --
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -899,8 +1063,18 @@ int enqueue_by_rows(const Product &p, const Args &a, cudaStream_t stream) {
   return enqueue_wide<Gated>(p, a, sms, stream);
 }
 
+template <typename X>
+int enqueue_few(const Product &p, const Args &a, cudaStream_t stream) {
+  const size_t smem = (size_t)p.m * (a.kblocks * (kBlockK + 4) + 16);
+  int rc = allow_smem<&reshard_product_few_kernel<X>>((size_t)(kFewBytes * 33 / 32 + 16 * kFewRows));
+  if (rc) return rc;
+  const cudaError_t e = launch(reshard_product_few_kernel<X>, dim3((unsigned)((p.n + kFewN - 1) / kFewN)), kFewWarps * 32, smem, 1, stream, a, p.w, p.w_stride);
+  return e == cudaSuccess ? RESHARD_OK : cuda_error(e, "launching reshard_product_few_kernel");
+}
+
 }  // namespace
 
+bool product_quantizes(int64_t m, int64_t k) { return m <= kFewRows && m * ((k + kBlockK - 1) / kBlockK * kBlockK) <= kFewBytes; }
 bool product_gathers(int64_t m, int groups) { return rows_a_group(m, groups) <= kMostNarrow; }
 
 int enqueue_product(const Product &p, cudaStream_t stream) {
@@ -908,6 +1082,9 @@ int enqueue_product(const Product &p, cudaStream_t stream) {
   a.a_scale = p.a_scale;
   a.as_row = p.as_row;
   a.as_block = p.as_block;
+  a.x = p.x ? p.x : p.a;
+  a.x_stride = p.a_stride;
+  a.cols = (int)p.k;
   a.w_scale = p.w_scale;
   a.offsets = p.offsets;
   a.order = p.order;
@@ -924,6 +1101,12 @@ int enqueue_product(const Product &p, cudaStream_t stream) {
   a.out_scale = p.out_scale;
   a.os_row = p.os_row;
   a.os_block = p.os_block;
+  if (!p.offsets && !p.gated && product_quantizes(p.m, p.k)) {
+    if (!p.x) return enqueue_few<uint8_t>(p, a, stream);
+    if (p.out_dtype == RESHARD_F32) return enqueue_few<float>(p, a, stream);
+    if (p.out_dtype == RESHARD_BF16) return enqueue_few<__nv_bfloat16>(p, a, stream);
+    return enqueue_few<__half>(p, a, stream);
+  }
   return p.gated ? enqueue_by_rows<true>(p, a, stream) : enqueue_by_rows<false>(p, a, stream);
 }
 

@@ -325,9 +325,9 @@ def reshard_linear_fp8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, 
         _bad(f"x has {K} columns, w {w.shape[1]}")
     out, to_step = _output(out, M, N, x.dtype, x)
     need = _linear_space(M, K)
-    space = torch.empty(need, dtype=torch.uint8, device=x.device)
-    _call(6, _LINEAR_FP8(x.data_ptr(), code, M, K, step, at_w, pitch, at_ws, N, out.data_ptr(), to_step, space.data_ptr(),
-                         need, here))
+    space = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
+    _call(6, _LINEAR_FP8(x.data_ptr(), code, M, K, step, at_w, pitch, at_ws, N, out.data_ptr(), to_step,
+                         space.data_ptr() if need else 0, need, here))
     return out
 
 

@@ -98,8 +98,9 @@ int reshard_matmul_fp8(const void *a, int64_t a_stride, const float *a_scale, in
                        int64_t out_stride, reshard_stream_t stream);
 
 /*
- * reshard_linear_fp8 -- out = Q(x) w^T: x [m, k] quantized by rows into the workspace, then the product with one
- * weight matrix w [n, k]. workspace: reshard_linear_fp8_workspace(m, k) bytes, 256-byte aligned. out has x's type.
+ * reshard_linear_fp8 -- out = Q(x) w^T: x [m, k] quantized by rows, then the product with one weight matrix w [n, k].
+ * workspace: reshard_linear_fp8_workspace(m, k) bytes, 256-byte aligned; 0 bytes (NULL will do) for the few rows that the
+ * product quantizes on its way. out has x's type.
  */
 int64_t reshard_linear_fp8_workspace(int64_t m, int64_t k);
 int reshard_linear_fp8(const void *x, int dtype, int64_t m, int64_t k, int64_t row_stride, const void *w, int64_t w_stride,
