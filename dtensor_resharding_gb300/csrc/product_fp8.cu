@@ -823,7 +823,7 @@ constexpr int kFewRows = 8;              // rows of a: the columns of one warp-w
 constexpr int kFewN = 16;                // rows of w a CTA
 constexpr int kFewWarps = 8;             // of a CTA: each has a share of K
 
-constexpr int kFewAhead = 3;             // blocks of w on their way to a warp
+constexpr int kFewAhead = 2;             // blocks of w on their way to a warp
 constexpr int64_t kFewBytes = 64 << 10;  // of the rows of a, quantized, in shared memory
 
 // A lane's 32 bytes of a row of w.
@@ -847,7 +847,7 @@ struct FewBytes {
 
 // Few rows of a, dense, and often one: a matrix times a vector, bound by the read of w from HBM and, at the sizes where
 // that is short, by what a kernel has to do before its first load. So no tensor memory, barriers or staging of w here:
-// each warp streams w from global memory into registers, three blocks ahead, and multiplies on the warp-wide tensor
+// each warp streams w from global memory into registers, two blocks ahead, and multiplies on the warp-wide tensor
 // instruction (16 x 8 x 32), whose rate is far above what the read leaves to do. Lane (g, t) holds rows g and g + 8 of w
 // and row g of a at columns 32 t .. 32 t + 31 of a block: which columns a product takes from a lane is the same for both
 // operands, so that a lane's bytes can be neighbours. The CTA quantizes its rows of a into shared memory (X: their type, or
