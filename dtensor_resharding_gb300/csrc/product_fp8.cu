@@ -194,20 +194,12 @@ __device__ __forceinline__ void box_free(int lane) {
   __syncwarp();
 }
 
-// A warp's 32 rows of 128 columns in T. boxed: out's rows start on 16 bytes (a tensor map describes it).
+// A warp's 32 rows of 128 columns in T. boxed: out's rows start on 16 bytes (a tensor map describes it); otherwise the warp
+// writes a row at a time from the boxes, an element a lane (rows from the registers, one a lane, took three times as long).
 template <typename T>
 __device__ __forceinline__ void store_tile(const CUtensorMap *map, bool boxed, uint8_t *box, int lane, const float2 (&sum)[kWideCols / 2], void *out, int64_t stride,
                                            int64_t n0, int64_t row, int rows, int cols) {
-  if (!boxed) {
-    T *to = static_cast<T *>(out) + (row + lane) * stride + n0;
-    if (lane < rows) {
-#pragma unroll
-      for (int c = 0; c < kWideCols; ++c)
-        if (c < cols) to[c] = from_f32<T>(c & 1 ? sum[c / 2].y : sum[c / 2].x);
-    }
-    return;
-  }
-  constexpr int per = 256 / sizeof(T);       // columns of two boxes
+  constexpr int per = 256 / sizeof(T), piece = 16 / sizeof(T);       // columns of two boxes, of 16 bytes
 #pragma unroll
   for (int c = 0; c < kWideCols; c += per) {
     if (c >= cols) break;
@@ -222,8 +214,21 @@ __device__ __forceinline__ void store_tile(const CUtensorMap *map, bool boxed, u
       }
       box_put<128>(box + j / 8 * kOutBox, lane, j % 8, make_uint4(v[0], v[1], v[2], v[3]));
     }
-    box_out<128, 2>(map, box, lane, static_cast<uint8_t *>(out), stride * (int64_t)sizeof(T), (n0 + c) * (int64_t)sizeof(T), row, rows,
-                    min(per, cols - c) * (int)sizeof(T));
+    if (boxed) {
+      box_out<128, 2>(map, box, lane, static_cast<uint8_t *>(out), stride * (int64_t)sizeof(T), (n0 + c) * (int64_t)sizeof(T), row, rows,
+                      min(per, cols - c) * (int)sizeof(T));
+    } else {
+      __syncwarp();
+      T *to = static_cast<T *>(out) + row * stride + n0 + c;
+#pragma unroll 2
+      for (int r = 0; r < min(rows, 32); ++r, to += stride) {
+#pragma unroll
+        for (int u = 0; u < per / 32; ++u) {
+          const int e = u * 32 + lane, at = e / (8 * piece) * kOutBox + r * 128 + ((e / piece % 8) ^ (r & 7)) * 16;
+          if (c + e < cols) to[e] = reinterpret_cast<const T *>(box + at)[e % piece];
+        }
+      }
+    }
   }
 }
 
@@ -845,6 +850,34 @@ struct FewBytes {
   }
 };
 
+// 16 bytes of values at p, those from `left` on 0; p may start anywhere.
+template <typename X>
+__device__ __forceinline__ uint4 load_piece(const X *p, int left) {
+  constexpr int per = 16 / sizeof(X);
+  uint64_t w[2] = {0, 0};
+#pragma unroll 1
+  for (int j = 0; j < min(left, per); ++j) {
+    uint64_t x;
+    if constexpr (sizeof(X) == 1) x = p[j];
+    else if constexpr (sizeof(X) == 2) x = reinterpret_cast<const uint16_t *>(p)[j];
+    else x = reinterpret_cast<const uint32_t *>(p)[j];
+    const int at = j * 8 * (int)sizeof(X);
+    if (at < 64) w[0] |= x << at;
+    else w[1] |= x << (at - 64);
+  }
+  return make_uint4((uint32_t)w[0], (uint32_t)(w[0] >> 32), (uint32_t)w[1], (uint32_t)(w[1] >> 32));
+}
+template <typename X>
+__device__ __forceinline__ void unpack(uint4 v, float *x) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < (int)(16 / sizeof(X)); ++j) {
+    if constexpr (sizeof(X) == 4) x[j] = __uint_as_float(w[j]);
+    else if constexpr (std::is_same_v<X, __nv_bfloat16>) x[j] = __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
+    else x[j] = __half2float(__ushort_as_half((uint16_t)(w[j / 2] >> (16 * (j & 1)))));
+  }
+}
+
 // Few rows of a, dense, and often one: a matrix times a vector, bound by the read of w from HBM and, at the sizes where
 // that is short, by what a kernel has to do before its first load. So no tensor memory, barriers or staging of w here:
 // each warp streams w from global memory into registers, two blocks ahead, and multiplies on the warp-wide tensor
@@ -873,49 +906,55 @@ __global__ void __launch_bounds__(kFewWarps * 32, 3) reshard_product_few_kernel(
       b[u][1].load(w1 + (kb0 + u) * kBlockK);
     }
 
-  // the rows of a: 8 lanes a block, 16 values each
+  // the rows of a: 8 lanes a block, 16 values each; the loads of two blocks a lane group are in flight together
   const bool wide = ((reinterpret_cast<uintptr_t>(p.x) | (uintptr_t)(p.x_stride * (int64_t)sizeof(X))) & 15) == 0;
+  const int blocks = p.m * p.kblocks;
+  constexpr int kBatch = kGiven || sizeof(X) == 2 ? 2 : 1, kPieces = kGiven ? 1 : (int)sizeof(X), kStep = kFewWarps * 4;
 #pragma unroll 1
-  for (int i = tid >> 3; i < (p.m * p.kblocks + 3) / 4 * 4; i += kFewWarps * 4) {      // four blocks a warp, all of it to the shuffles
-    const bool in = i < p.m * p.kblocks;
-    const int r = in ? i / p.kblocks : 0, kb = in ? i - r * p.kblocks : 0, at = kb * kBlockK + (lane & 7) * 16;
-    const X *from = static_cast<const X *>(p.x) + (int64_t)r * p.x_stride + at;
-    const int left = in ? p.cols - at : 0;
-    uint4 q;
-    float scale;
-    if constexpr (kGiven) {
-      FewBytes x;
-      if (left >= 16 && wide) x.v[0] = __ldg(reinterpret_cast<const uint4 *>(from));
-      else x.load_some(from, min(left, 16));
-      q = x.v[0];
-      scale = in ? p.a_scale[(int64_t)r * p.as_row + (int64_t)kb * p.as_block] : 0.0f;
-    } else {
-      float x[16];
+  for (int i0 = tid >> 3; i0 < (blocks + 3) / 4 * 4; i0 += kBatch * kStep) {      // four blocks a warp, all of it to the shuffles
+    uint4 v[kBatch][kPieces];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * kStep, r = i / p.kblocks, kb = i - r * p.kblocks, at = kb * kBlockK + (lane & 7) * 16;
+      const X *from = static_cast<const X *>(p.x) + (int64_t)r * p.x_stride + at;
+      const int left = i < blocks ? p.cols - at : 0;
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) v[u][j] = make_uint4(0, 0, 0, 0);
       if (left >= 16 && wide) {
-        constexpr int per = 16 / sizeof(X);
 #pragma unroll
-        for (int j = 0; j < 16 / per; ++j) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4 *>(from) + j);
+        for (int j = 0; j < kPieces; ++j) v[u][j] = __ldg(reinterpret_cast<const uint4 *>(from) + j);
+      } else if (left > 0) {
 #pragma unroll
-          for (int e = 0; e < per; ++e) x[j * per + e] = to_f32(reinterpret_cast<const X *>(&v)[e]);
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = j < left ? to_f32(from[j]) : 0.0f;
+        for (int j = 0; j < kPieces; ++j) v[u][j] = load_piece(from + j * (16 / (int)sizeof(X)), left - j * (16 / (int)sizeof(X)));
       }
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) m = max(m, magnitude(x[j]));
-#pragma unroll
-      for (int o = 4; o; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
-      float inv;
-      block_scale(m, scale, inv);
-      q = make_uint4(e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv), e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv),
-                     e4m3x4(x[8] * inv, x[9] * inv, x[10] * inv, x[11] * inv), e4m3x4(x[12] * inv, x[13] * inv, x[14] * inv, x[15] * inv));
     }
-    if (in) {
-      *reinterpret_cast<uint4 *>(xq + r * pitch + at) = q;
-      if ((lane & 7) == 0) xs[r * p.kblocks + kb] = scale;
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * kStep, r = i / p.kblocks, kb = i - r * p.kblocks, at = kb * kBlockK + (lane & 7) * 16;
+      if (i - (lane >> 3) >= blocks) break;            // the whole warp
+      uint4 q = v[u][0];
+      float scale = 0.0f;
+      if constexpr (kGiven) {
+        if (i < blocks) scale = p.a_scale[(int64_t)r * p.as_row + (int64_t)kb * p.as_block];
+      } else {
+        constexpr int per = 16 / sizeof(X);
+        float x[16];
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) unpack<X>(v[u][j], x + j * per);
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) m = max(m, magnitude(x[j]));
+#pragma unroll
+        for (int o = 4; o; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+        float inv;
+        block_scale(m, scale, inv);
+        q = make_uint4(e4m3x4(x[0] * inv, x[1] * inv, x[2] * inv, x[3] * inv), e4m3x4(x[4] * inv, x[5] * inv, x[6] * inv, x[7] * inv),
+                       e4m3x4(x[8] * inv, x[9] * inv, x[10] * inv, x[11] * inv), e4m3x4(x[12] * inv, x[13] * inv, x[14] * inv, x[15] * inv));
+      }
+      if (i < blocks) {
+        *reinterpret_cast<uint4 *>(xq + r * pitch + at) = q;
+        if ((lane & 7) == 0) xs[r * p.kblocks + kb] = scale;
+      }
     }
   }
   __syncthreads();

@@ -6,6 +6,7 @@
 // few roundings of 32 bits, far below the 2^-4 of an e4m3 step. A block holding an infinity or NaN gets scale and values NaN.
 // Both kernels read each value once, keep it in registers between the amax and the rounding, and are bound by HBM.
 #include <algorithm>
+#include <type_traits>
 
 #include "ops_common.cuh"
 
@@ -35,9 +36,52 @@ __device__ __forceinline__ void load_values(const T *p, int left, bool wide, flo
   }
 }
 
-// 8 lanes a block of 128 values, 16 each: two or four 16-byte loads, three shuffles and one 16-byte store a lane.
+// The 16-byte words that hold N values at p, wherever p is: ask() reads them (words that hold none of the `left` values
+// are not read, `any` is in their place), take() shifts the values into place and clears those from `left` on. Rows that
+// start anywhere are read as fast as aligned ones this way; value by value they took three times as long.
+template <typename T, int N>
+struct Shifted {
+  static constexpr int kWords = N * (int)sizeof(T) / 4;
+  static_assert(kWords % 4 == 0, "16-byte words");
+  uint32_t w[kWords + 4];
+  __device__ __forceinline__ void ask(const T *p, int left, const uint8_t *any) {
+    const uintptr_t skip = reinterpret_cast<uintptr_t>(p) & 15;
+    const uint8_t *from = reinterpret_cast<const uint8_t *>(p) - skip;
+    const int end = left > 0 ? (int)skip + min(left, N) * (int)sizeof(T) : 0;        // bytes from there to the last value
+#pragma unroll
+    for (int i = 0; i < kWords + 4; i += 4) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(4 * i < end ? from + 4 * i : any));
+      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+    }
+  }
+  __device__ __forceinline__ void take(const T *p, int left, uint32_t (&v)[kWords]) {
+    const uint32_t skip = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+#pragma unroll
+    for (int i = 0; i < kWords + 3; ++i) w[i] = skip & 4 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < kWords + 2; ++i) w[i] = skip & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      const uint32_t x = sizeof(T) < 4 ? __funnelshift_r(w[i], w[i + 1], 8 * (skip & 3)) : w[i];
+      const int have = left - i * (4 / (int)sizeof(T));          // values from this word on
+      v[i] = have >= 4 / (int)sizeof(T) ? x : have > 0 ? x & 0xffffu : 0;
+    }
+  }
+};
 template <typename T>
-__global__ void __launch_bounds__(kQThreads) reshard_quantize_rows_kernel(Rows a, int64_t blocks, int per_row_blocks, bool wide, bool wide_q) {
+__device__ __forceinline__ float value_of(const uint32_t *v, int i) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(v[i]);
+  else if constexpr (std::is_same_v<T, __nv_bfloat16>) return __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
+  else return __half2float(__ushort_as_half((uint16_t)(v[i / 2] >> (16 * (i & 1)))));
+}
+// A 16-byte word that holds a tensor's first value.
+__device__ __forceinline__ const uint8_t *first_word(const void *p) {
+  return reinterpret_cast<const uint8_t *>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15);
+}
+
+// 8 lanes a block of 128 values, 16 each: two or four 16-byte loads, three shuffles and one 16-byte store a lane.
+template <typename T, bool Wide>
+__global__ void __launch_bounds__(kQThreads) reshard_quantize_rows_kernel(Rows a, int64_t blocks, int per_row_blocks, bool wide_q) {
   grid_enter();
   const int lane = threadIdx.x & 31;
   const int64_t b = (int64_t)blockIdx.x * (kQThreads / 8) + threadIdx.x / 8;
@@ -47,8 +91,18 @@ __global__ void __launch_bounds__(kQThreads) reshard_quantize_rows_kernel(Rows a
   const int kb = in ? (int)(b - r * per_row_blocks) : 0;
   const int at = kb * kScaleBlock + (lane & 7) * 16;
   const int left = in ? (int)min((int64_t)16, a.cols - at) : 0;
+  const T *const from = static_cast<const T *>(a.x) + r * a.stride + at;
   float x[16];
-  load_values<T, 16>(static_cast<const T *>(a.x) + r * a.stride + at, left, wide, x);
+  if constexpr (Wide) {
+    load_values<T, 16>(from, left, true, x);
+  } else {
+    Shifted<T, 16> s;
+    uint32_t v[Shifted<T, 16>::kWords];
+    s.ask(from, left, first_word(a.x));
+    s.take(from, left, v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = value_of<T>(v, i);
+  }
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 16; ++i) m = max(m, magnitude(x[i]));
@@ -140,27 +194,34 @@ __global__ void __launch_bounds__(kQThreads) reshard_quantize_blocks_kernel(Bloc
     }
     return;
   }
-  float x[8][8];
-  uint32_t m = 0;
+  using S = Shifted<T, 8>;
+  constexpr int kBatch = sizeof(T) == 4 ? 4 : 8;      // rows whose words are in flight together
+  uint32_t v[8][S::kWords];
+  const T *from = static_cast<const T *>(a.w) + e * a.batch_stride + ((int64_t)nb * kScaleBlock + row0) * a.row_stride + c0;
+  const int rows = (int)min((int64_t)kScaleBlock, a.rows - (int64_t)nb * kScaleBlock) - row0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = (int64_t)nb * kScaleBlock + row0 + 16 * i;
-    load_values<T, 8>(static_cast<const T *>(a.w) + e * a.batch_stride + r * a.row_stride + c0, r < a.rows ? left : 0, wide, x[i]);
+  for (int i0 = 0; i0 < 8; i0 += kBatch) {
+    S s[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) s[i].ask(from + 16 * (i0 + i) * a.row_stride, 16 * (i0 + i) < rows ? left : 0, first_word(a.w));
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) s[i].take(from + 16 * (i0 + i) * a.row_stride, 16 * (i0 + i) < rows ? left : 0, v[i0 + i]);
   }
+  uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, magnitude(x[i][j]));
+    for (int j = 0; j < 8; ++j) m = max(m, magnitude(value_of<T>(v[i], j)));
   float inv;
   block_amax(m, part, a.scale + b, inv);
+  uint8_t *to = a.q + e * a.q_batch_stride + ((int64_t)nb * kScaleBlock + row0) * a.q_row_stride + c0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int64_t r = (int64_t)nb * kScaleBlock + row0 + 16 * i;
-    if (r >= a.rows) break;
-    uint8_t *to = a.q + e * a.q_batch_stride + r * a.q_row_stride + c0;
-    uint2 q;
-    q.x = e4m3x4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv);
-    q.y = e4m3x4(x[i][4] * inv, x[i][5] * inv, x[i][6] * inv, x[i][7] * inv);
+  for (int i = 0; i < 8; ++i, to += 16 * a.q_row_stride) {
+    if (16 * i >= rows) break;
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = value_of<T>(v[i], j) * inv;
+    const uint2 q = make_uint2(e4m3x4(x[0], x[1], x[2], x[3]), e4m3x4(x[4], x[5], x[6], x[7]));
     if (wide_q && left >= 8) {
       *reinterpret_cast<uint2 *>(to) = q;
     } else {
@@ -221,10 +282,12 @@ int enqueue_quantize_rows(const Rows &r, cudaStream_t stream) {
   if (blocks == 0) return RESHARD_OK;
   const dim3 grid((unsigned)((blocks + kQThreads / 8 - 1) / (kQThreads / 8)));
   const bool wide = aligned16(r.x, r.stride, element_bytes(r.dtype)), wide_q = aligned16(r.q, r.q_stride, 1);
-  cudaError_t e;
-  if (r.dtype == RESHARD_F32) e = launch(reshard_quantize_rows_kernel<float>, grid, kQThreads, 0, 1, stream, r, blocks, kb, wide, wide_q);
-  else if (r.dtype == RESHARD_BF16) e = launch(reshard_quantize_rows_kernel<__nv_bfloat16>, grid, kQThreads, 0, 1, stream, r, blocks, kb, wide, wide_q);
-  else e = launch(reshard_quantize_rows_kernel<__half>, grid, kQThreads, 0, 1, stream, r, blocks, kb, wide, wide_q);
+  auto go = [&](auto t) {
+    using T = decltype(t);
+    return wide ? launch(reshard_quantize_rows_kernel<T, true>, grid, kQThreads, 0, 1, stream, r, blocks, kb, wide_q)
+                : launch(reshard_quantize_rows_kernel<T, false>, grid, kQThreads, 0, 1, stream, r, blocks, kb, wide_q);
+  };
+  const cudaError_t e = r.dtype == RESHARD_F32 ? go(float()) : r.dtype == RESHARD_BF16 ? go(__nv_bfloat16()) : go(__half());
   return e == cudaSuccess ? RESHARD_OK : cuda_error(e, "launching reshard_quantize_rows_kernel");
 }
 
