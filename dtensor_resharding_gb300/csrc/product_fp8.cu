@@ -9,7 +9,7 @@
 // Two kernels, by which operand sits on the tensor cores' 128 rows:
 //  - wide: 128 rows of `a` x 256 rows of `w`, persistent, for many rows a group. A thread of the eight epilogue warps
 //    owns one row and 128 columns, so that one scale a block serves all of them. Bound by the tensor cores.
-//  - narrow: 128 rows of `w` x 16 .. 128 rows of `a`, for few rows a group: the tile's narrow side fits the
+//  - narrow: 128 rows of `w` x 16 .. 64 rows of `a`, for few rows a group: the tile's narrow side fits the
 //    rows at hand instead of padding them to 128. Bound by the read of the weights. Where the tiles alone do not fill
 //    the GPU, a cluster of CTAs splits K and adds its partial tiles through distributed shared memory, in rank order.
 // Both can end in silu(gate) * up, quantized by rows (the expert layer's first product): a tile then holds the 128
@@ -824,7 +824,8 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<NT, Gated>::kPerSm)
 
 // ----------------------------------------------------------------------------------------------------------- few --
 
-constexpr int kFewRows = 8;              // rows of a: the columns of one warp-wide product
+constexpr int kFewRows = 8;              // columns of one warp-wide product: rows of a
+constexpr int kFewMost = 4;              // rows that are worth it: every CTA quantizes them (8 rows, 4096 x 4096: 11.9 us, narrow 7.5)
 constexpr int kFewN = 16;                // rows of w a CTA
 constexpr int kFewWarps = 8;             // of a CTA: each has a share of K
 
@@ -1065,6 +1066,11 @@ int enqueue_wide(const Product &p, Args a, int sms, cudaStream_t stream) {
   return e == cudaSuccess ? RESHARD_OK : cuda_error(e, "launching reshard_product_wide_kernel");
 }
 
+// K is split where the tiles leave places on the GPU empty, as far as each share keeps four blocks.
+int narrow_split(int64_t tiles, int64_t places, int kblocks) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>({kMostSplit, places / tiles, kblocks / 4}));
+}
+
 template <int NT, bool Gated>
 int enqueue_narrow(const Product &p, const Args &a, int sms, cudaStream_t stream) {
   using C = Narrow<NT, Gated>;
@@ -1075,9 +1081,8 @@ int enqueue_narrow(const Product &p, const Args &a, int sms, cudaStream_t stream
   if (rc) return rc;
   const int64_t tiles = (p.offsets ? p.m / NT + std::min<int64_t>(p.groups, p.m) : (p.m + NT - 1) / NT) * ((p.n + kNarrowM - 1) / kNarrowM);
   if (tiles > INT32_MAX) return fail(RESHARD_ERR_UNSUPPORTED, "too many tiles for one launch");
-  // K is split where the tiles leave places on the GPU empty, as far as each share keeps four blocks
   const int64_t places = (int64_t)sms * C::kPerSm;
-  const int split = (int)std::max<int64_t>(1, std::min<int64_t>({kMostSplit, places / tiles, a.kblocks / 4}));
+  const int split = narrow_split(tiles, places, a.kblocks);
   const unsigned grid = (unsigned)(split > 1 ? tiles * split : std::min(tiles, places));
   const cudaError_t e = launch(reshard_product_narrow_kernel<NT, Gated>, dim3(grid), kNarrowThreads, C::kSmem, split, stream, ma, mw, a, split, p.early);
   return e == cudaSuccess ? RESHARD_OK : cuda_error(e, "launching reshard_product_narrow_kernel");
@@ -1085,7 +1090,19 @@ int enqueue_narrow(const Product &p, const Args &a, int sms, cudaStream_t stream
 
 // Rows a group, on average: by them a product takes the narrow kernel or the wide one.
 int64_t rows_a_group(int64_t m, int groups) { return (m + groups - 1) / groups; }
-constexpr int64_t kMostNarrow = 64, kMostNarrowDense = 128;
+constexpr int64_t kMostNarrow = 64;
+
+// Whether a dense product of more than 64 rows is narrow's (in tiles of 64, K split) or wide's. Wide fills the GPU only from
+// 152 tiles of 128 x 256 on; below that narrow has more and shorter pieces. Both times are of this form, in ns, as
+// measured: 256 x 1024 x 4096 narrow 10.7 us, wide 17.7; 300 x 300 x 14336 15.3 and 46.8; but 400 x 4096 x 4096 24.7 and 19.1,
+// 128 x 14336 x 1024 12.0 and 9.1.
+bool narrow_is_shorter(int64_t m, int64_t n, int kblocks, int sms) {
+  const int64_t tiles = (m + 63) / 64 * ((n + kNarrowM - 1) / kNarrowM), places = 2 * sms, split = narrow_split(tiles, places, kblocks);
+  const int64_t ctas = tiles * split, rounds = (ctas + places - 1) / places, share = (kblocks + split - 1) / split;
+  const int64_t narrow = 7000 + share * rounds * (ctas <= sms ? 550 : 900);
+  const int64_t wide_tiles = (m + kWideM - 1) / kWideM * ((n + kWideN - 1) / kWideN);
+  return narrow < 5000 + 390 * kblocks * ((wide_tiles + sms - 1) / sms);
+}
 
 template <bool Gated>
 int enqueue_by_rows(const Product &p, const Args &a, cudaStream_t stream) {
@@ -1095,10 +1112,7 @@ int enqueue_by_rows(const Product &p, const Args &a, cudaStream_t stream) {
   const int64_t per = rows_a_group(p.m, p.groups);
   if (per <= 16) return enqueue_narrow<16, Gated>(p, a, sms, stream);
   if (per <= 32) return enqueue_narrow<32, Gated>(p, a, sms, stream);
-  if (per <= kMostNarrow) return enqueue_narrow<64, Gated>(p, a, sms, stream);
-  if constexpr (!Gated) {
-    if (!p.offsets && per <= kMostNarrowDense) return enqueue_narrow<128, Gated>(p, a, sms, stream);
-  }
+  if (per <= kMostNarrow || (!p.offsets && narrow_is_shorter(p.m, p.n, a.kblocks, sms))) return enqueue_narrow<64, Gated>(p, a, sms, stream);
   return enqueue_wide<Gated>(p, a, sms, stream);
 }
 
@@ -1113,7 +1127,7 @@ int enqueue_few(const Product &p, const Args &a, cudaStream_t stream) {
 
 }  // namespace
 
-bool product_quantizes(int64_t m, int64_t k) { return m <= kFewRows && m * ((k + kBlockK - 1) / kBlockK * kBlockK) <= kFewBytes; }
+bool product_quantizes(int64_t m, int64_t k) { return m <= kFewMost && m * ((k + kBlockK - 1) / kBlockK * kBlockK) <= kFewBytes; }
 bool product_gathers(int64_t m, int groups) { return rows_a_group(m, groups) <= kMostNarrow; }
 
 int enqueue_product(const Product &p, cudaStream_t stream) {
