@@ -59,8 +59,9 @@ inline int element_bytes(int dtype) { return dtype == RESHARD_F32 ? 4 : dtype ==
 
 int device_sms(int *sms);   // multiprocessors of the current device
 
-// Every operator kernel begins with griddepcontrol.wait, so its CTAs may be scheduled while the grid before it on
-// the stream drains: of a chain of short kernels only the work itself is left, not the launches between them.
+// Every operator kernel begins with griddepcontrol.wait (or has it after reads of what the grid before cannot have written),
+// so its CTAs may be scheduled while that grid drains: of a chain of short kernels only the work itself is left, not the
+// launches between them.
 template <typename... KArgs, typename... Args>
 cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, int block, size_t smem, int cluster, cudaStream_t stream, Args &&...args) {
   cudaLaunchConfig_t cfg{};

@@ -6,16 +6,14 @@
 // scaled and added in registers: out = fma(sa sw, inner, out) per block. Tensor memory holds two such partial tiles, so
 // that the tensor cores work on one while the epilogue warps read the other.
 //
-// Two kernels, by which operand sits on the tensor cores' 128 rows:
-//  - wide: 128 rows of `a` x 256 rows of `w`, persistent, for many rows a group. A thread of the eight epilogue warps
-//    owns one row and 128 columns, so that one scale a block serves all of them. Bound by the tensor cores.
-//  - narrow: 128 rows of `w` x 16 .. 64 rows of `a`, for few rows a group: the tile's narrow side fits the
-//    rows at hand instead of padding them to 128. Bound by the read of the weights. Where the tiles alone do not fill
-//    the GPU, a cluster of CTAs splits K and adds its partial tiles through distributed shared memory, in rank order.
-// Both can end in silu(gate) * up, quantized by rows (the expert layer's first product): a tile then holds the 128
-// columns of one quantization block and their gate and up rows.
+// Three kernels, by the rows of `a` (their sides of the choice, measured, stand at the rules below):
+//  - wide: 128 rows of `a` x 256 rows of `w`, persistent, for many rows a group.
+//  - narrow: 128 rows of `w` x 16 .. 64 rows of `a`: the tile's narrow side fits the rows at hand.
+//  - few: up to four rows, dense: streams `w` through registers.
+// Wide and narrow can end in silu(gate) * up, quantized by rows (the expert layer's first product): a tile then holds the
+// 128 columns of one quantization block and their gate and up rows.
 //
-// Operands come by TMA (128-byte swizzle, K along the row), rows beyond a tensor as zeros. Rows of a tile beyond its
+// Their operands come by TMA (128-byte swizzle, K along the row), rows beyond a tensor as zeros. Rows of a tile beyond its
 // group's end belong to the next group: they are computed and not stored.
 #include <cudaTypedefs.h>
 
@@ -101,6 +99,13 @@ __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
 
 // ---------------------------------------------------------------------------------------------------------- wide --
 
+// A CTA an SM walks over tiles: one warp loads, one issues the products, one fetches the scales, eight take the partial
+// tiles out of tensor memory. A thread of those owns one row and 128 columns, so that one scale a block serves all of
+// them, and adds pairs of columns with one instruction. A block's products take 512 cycles of the tensor cores; taking its
+// 128 x 256 partial sums out, with the handshake, takes about 740, and that is what bounds the kernel: 650 are left
+// where the products take no time at all. 8192 x 14336 x 4096 takes 346 us, 2.8 PFLOP/s, tensor cores 60% busy.
+// Measured and not kept: 16 epilogue warps of 64 columns each (4% slower), products of 128 columns that signal the halves
+// apart (6% slower), 32 columns a load (spills, 25% slower).
 constexpr int kWideM = 128, kWideN = 256, kWideStages = 3;
 constexpr int kWideStageBytes = (kWideM + kWideN) * kBlockK;
 constexpr int kWideEpi = 8;              // epilogue warps: 4 row quarters x 2 column halves
@@ -108,7 +113,7 @@ constexpr int kWideThreads = (kWideEpi + 4) * 32;        // behind a warpgroup: 
 constexpr int kWideCols = kWideN / 2;    // columns of a thread
 constexpr int kScaleSlots = 2 * kWideStages;
 constexpr int kOutBox = 32 * 128;        // an epilogue warp's rows on their way out, 128 bytes of each; two of them a warp
-constexpr int kTileSlots = 8;            // tiles whose place the loader has written down: it is 6 blocks ahead at most
+constexpr int kTileSlots = 8;            // tiles whose place the loader has written down: it is 5 blocks ahead at most, see the scales
 // Registers a thread: at launch, of the epilogue's two warpgroups and of the other. The epilogue holds 128 sums and two loads
 // of 16 columns.
 constexpr int kWideRegs = 168, kWideRegsEpi = 200, kWideRegsRest = 104;
@@ -313,7 +318,6 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       __syncwarp();
     } else if (warp == 0) {
       // ---- issuer: the first warp, which the scheduler prefers
-
       // The loop is kept to a few dependent steps: they, not the products, are what a block would wait for.
       if (elect_one()) {
         const uint32_t idesc = instruction(kWideN), full = smem_addr(s.full), empty = smem_addr(s.empty);
@@ -345,7 +349,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       __syncwarp();
     } else if (warp == 2) {
       // ---- scales of a stage's block, arriving with its operands. Two slots a stage: when a stage is free for block i,
-      // the products of block i - 4 are done, which began after the epilogue had taken block i - 6, so slot i % 8 is free too.
+      // the products of block i - 3 are done, which began after the epilogue had taken block i - 5, so slot i % 6 is free too.
       uint32_t st = 0, phase = 1, slot = 0;
       bool ok = true;
       for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
@@ -491,6 +495,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 
 // -------------------------------------------------------------------------------------------------------- narrow --
 
+// Few rows a group: bound by the read of the weights, so that what counts is how much of them is on the way at any time:
+// two CTAs an SM with some 100 KB of stages each, or one with 200 where the sums need the registers. The weights sit on
+// the tensor cores' 128 rows, and a product is as wide as the rows at hand, to 16. Where the tiles alone do not fill the
+// GPU, a cluster of CTAs splits K and adds its partial tiles through distributed shared memory, in rank order: the
+// same order on every run. 128 experts of 2048 x 768, one row each or two: both products 60 us, 6.6 TB/s;
+// 77 x 2867 x 4096: 8.4 us, bound by latency (launch, first loads, the cluster's sum).
 constexpr int kNarrowM = 128;            // rows of w (of gate and of up, when gated)
 constexpr int kNarrowThreads = 192;      // 4 epilogue warps, the loader, the issuer
 constexpr int kMostSplit = 8;            // CTAs of a cluster that share a tile's K
@@ -828,7 +838,6 @@ constexpr int kFewRows = 8;              // columns of one warp-wide product: ro
 constexpr int kFewMost = 4;              // rows that are worth it: every CTA quantizes them (8 rows, 4096 x 4096: 11.9 us, narrow 7.5)
 constexpr int kFewN = 16;                // rows of w a CTA
 constexpr int kFewWarps = 8;             // of a CTA: each has a share of K
-
 constexpr int kFewAhead = 2;             // blocks of w on their way to a warp
 constexpr int64_t kFewBytes = 64 << 10;  // of the rows of a, quantized, in shared memory
 
@@ -886,7 +895,8 @@ __device__ __forceinline__ void unpack(uint4 v, float *x) {
 // and row g of a at columns 32 t .. 32 t + 31 of a block: which columns a product takes from a lane is the same for both
 // operands, so that a lane's bytes can be neighbours. The CTA quantizes its rows of a into shared memory (X: their type, or
 // uint8_t where they come quantized) while the first loads of w are on their way: one launch for the whole call. The K
-// shares of a CTA's warps are added in order.
+// shares of a CTA's warps are added in order. 1 x 14336 x 4096: 12.6 us, 4.7 TB/s (as narrow: 16.5); of that the read
+// alone would take 8.7, the start and the end the rest. Three blocks ahead spill, one leaves it at 13.8.
 template <typename X>
 __global__ void __launch_bounds__(kFewWarps * 32, 3) reshard_product_few_kernel(const __grid_constant__ Args p, const uint8_t *wq, int64_t w_stride) {
   constexpr bool kGiven = std::is_same_v<X, uint8_t>;
@@ -1089,8 +1099,8 @@ int enqueue_narrow(const Product &p, const Args &a, int sms, cudaStream_t stream
 }
 
 // Whether a grouped product is narrow's, by the rows a group has on average, as far as the host knows them (m is an
-// upper bound). 128 experts of 2048 x 768, the whole layer: 8 rows each narrow 109 us, wide 115; 16 rows 129 and 120; 64 rows
-// 307 and 138.
+// upper bound). 128 experts of 2048 x 768, the whole layer: 8 rows each narrow 109 us, wide 115; 16 rows 129 and 120; 64
+// rows 307 and 138.
 bool few_a_group(int64_t m, int groups) { return m <= 8 * (int64_t)groups; }
 
 // Whether a dense product of more than 64 rows is narrow's (in tiles of 64, K split) or wide's. Wide fills the GPU only from
