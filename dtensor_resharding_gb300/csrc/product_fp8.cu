@@ -84,6 +84,15 @@ __device__ __forceinline__ void row_tiles(const int *off, int *tiles, int groups
   if (lane == 0) tiles[groups] = base;
 }
 
+// The last group whose first tile is at most t, by a whole warp: two looks at 32 groups each. (Halving 128 groups took a
+// loader some 1,000 cycles a tile, in which its stages ran dry.)
+static_assert(RESHARD_MAX_GROUPS <= 32 * 32, "two looks");
+__device__ __forceinline__ int group_of(const int *tiles, int groups, uint32_t ntiles, uint32_t t, int lane) {
+  auto at_most = [&](int g) { return 31 - __clz(__ballot_sync(kFull, g < groups && tiles[min(g, groups)] * ntiles <= t)); };
+  const int lo = groups > 32 ? 32 * at_most(32 * lane) : 0;
+  return lo + at_most(lo + lane);
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b);
 template <>
@@ -137,13 +146,8 @@ constexpr size_t kWideOut = (size_t)kWideEpi * 2 * kOutBox;
 constexpr size_t kWideSmem = (size_t)kWideStages * kWideStageBytes + kWideOut + sizeof(WideShared);
 static_assert(kWideSmem <= 232448, "shared memory of a CTA");
 
-__device__ __forceinline__ WideTile wide_tile(const WideShared &s, int groups, uint32_t ntiles, uint32_t t) {
-  int lo = 0, hi = groups - 1;          // the last group whose first tile is <= t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (s.tiles[mid] * ntiles <= t) lo = mid;
-    else hi = mid - 1;
-  }
+__device__ __forceinline__ WideTile wide_tile(const WideShared &s, int groups, uint32_t ntiles, uint32_t t, int lane) {
+  const int lo = group_of(s.tiles, groups, ntiles, t, lane);
   const uint32_t here = s.tiles[lo + 1] - s.tiles[lo], l = t - s.tiles[lo] * ntiles;
   const uint32_t n = l / here, m = l - n * here;     // row tiles first: neighbours share w's tile
   WideTile r;
@@ -284,7 +288,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       uint32_t it = 0, st = 0, phase = 1, tile_no = 0;
       bool ok = true;
       for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x, ++tile_no) {
-        const WideTile w = wide_tile(s, p.groups, ntiles, t);
+        const WideTile w = wide_tile(s, p.groups, ntiles, t, lane);
         for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
           const uint32_t bar = smem_addr(s.full) + st * 8;
           ok = bar_wait(smem_addr(s.empty) + st * 8, phase, stop);
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       uint32_t st = 0, phase = 1, slot = 0;
       bool ok = true;
       for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
-        const WideTile w = wide_tile(s, p.groups, ntiles, t);
+        const WideTile w = wide_tile(s, p.groups, ntiles, t, lane);
         const float *sa[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) sa[i] = p.a_scale + (int64_t)(w.row + min(lane + 32 * i, w.rows - 1)) * p.as_row;
@@ -530,13 +534,8 @@ struct NarrowTile {
   int g, row, rows, n;     // group, first row, rows, column tile
 };
 template <int NT>
-__device__ __forceinline__ NarrowTile narrow_tile(const int *off, const int *tiles, int groups, uint32_t ntiles, uint32_t t) {
-  int lo = 0, hi = groups - 1;          // the last group whose first tile is <= t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (tiles[mid] * ntiles <= t) lo = mid;
-    else hi = mid - 1;
-  }
+__device__ __forceinline__ NarrowTile narrow_tile(const int *off, const int *tiles, int groups, uint32_t ntiles, uint32_t t, int lane) {
+  const int lo = group_of(tiles, groups, ntiles, t, lane);
   const uint32_t l = t - tiles[lo] * ntiles, m = l / ntiles;      // column tiles first: w is read in order
   NarrowTile r;
   r.g = lo;
@@ -591,7 +590,7 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<NT, Gated>::kPerSm)
   const int kb0 = (int)((int64_t)p.kblocks * rank / split), kb1 = (int)((int64_t)p.kblocks * (rank + 1) / split);
   float acc[kParts][NT];
   bool ok = true;
-  auto tile = [&](uint32_t t) { return narrow_tile<NT>(s.off, s.tiles, p.groups, ntiles, t); };
+  auto tile = [&](uint32_t t) { return narrow_tile<NT>(s.off, s.tiles, p.groups, ntiles, t, lane); };
 
   if (warp == 4) {
     // ---- loader: one lane; where rows are gathered, four rows a lane
@@ -642,12 +641,13 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<NT, Gated>::kPerSm)
     __syncwarp();
   } else if (warp == 5) {
     // ---- issuer
-    if (elect_one()) {
-      uint32_t st = 0, phase = 0, half = 0, free_phase = 1;
-      const uint64_t a0 = operand(smem_addr(stages));
-      for (uint32_t t = first; ok && t < total; t += step) {
-        const uint32_t idesc = instruction((tile(t).rows + 15) & ~15);
-        for (int kb = kb0; kb < kb1; ++kb) {
+    uint32_t st = 0, phase = 0, half = 0, free_phase = 1;
+    const uint64_t a0 = operand(smem_addr(stages));
+    const bool one = elect_one();      // the warp's other lanes help to find the tiles, and wait for nothing
+    for (uint32_t t = first; t < total; t += step) {
+      const uint32_t idesc = instruction((tile(t).rows + 15) & ~15);
+      if (one) {
+        for (int kb = kb0; ok && kb < kb1; ++kb) {
           if (!(ok = bar_wait(smem_addr(s.full) + st * 8, phase, stop))) break;
           if (!(ok = bar_wait(smem_addr(s.taken) + half * 8, free_phase, stop))) break;
           tc_after_sync();
@@ -664,10 +664,10 @@ __global__ void __launch_bounds__(kNarrowThreads, Narrow<NT, Gated>::kPerSm)
           half ^= 1;
         }
       }
-      if (!ok) {
-        mma_commit(smem_addr(&s.last));
-        bar_drain(smem_addr(&s.last), 0);
-      }
+    }
+    if (!ok) {
+      mma_commit(smem_addr(&s.last));
+      bar_drain(smem_addr(&s.last), 0);
     }
     __syncwarp();
   } else {
