@@ -110,19 +110,20 @@ __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
 
 // A CTA an SM walks over tiles: one warp loads, one issues the products, one fetches the scales, eight take the partial
 // tiles out of tensor memory. A thread of those owns one row and 128 columns, so that one scale a block serves all of
-// them, and adds pairs of columns with one instruction. A block's products take 512 cycles of the tensor cores; taking its
-// 128 x 256 partial sums out, with the handshake, takes about 740, and that is what bounds the kernel: 650 are left
-// where the products take no time at all. 8192 x 14336 x 4096 takes 346 us, 2.8 PFLOP/s, tensor cores 60% busy.
+// them, and adds pairs of columns with one instruction. A block's products take 512 cycles of the tensor cores and a block
+// about 750: a half of tensor memory is handed from the products to the epilogue and back (two barriers each way and the
+// completion of the products, 400 cycles with no work in between), and there is room for two only. 8192 x 14336 x 4096
+// takes 348 us, 2.8 PFLOP/s, tensor cores 60% busy; a tile's end, 2,000 to 3,400 cycles, weighs more where K is short:
+// 65,536 rows of 128 experts, 2048 x 768 without a gate 125 us, 1.6 PFLOP/s.
 // Measured and not kept: 16 epilogue warps of 64 columns each (4% slower), products of 128 columns that signal the halves
-// apart (6% slower), 32 columns a load (spills, 25% slower).
-constexpr int kWideM = 128, kWideN = 256, kWideStages = 3;
+// apart (6% slower), 32 columns a load (the same), w's blocks prefetched into L2 (15% slower), the next block's barrier
+// looked at early (1% slower), one reciprocal for two or four gates (the same).
+constexpr int kWideM = 128, kWideN = 256;
 constexpr int kWideStageBytes = (kWideM + kWideN) * kBlockK;
 constexpr int kWideEpi = 8;              // epilogue warps: 4 row quarters x 2 column halves
 constexpr int kWideThreads = (kWideEpi + 4) * 32;        // behind a warpgroup: the issuer, the loader, the scales' loader, one idle
 constexpr int kWideCols = kWideN / 2;    // columns of a thread
-constexpr int kScaleSlots = 2 * kWideStages;
-constexpr int kOutBox = 32 * 128;        // an epilogue warp's rows on their way out, 128 bytes of each; two of them a warp
-constexpr int kTileSlots = 8;            // tiles whose place the loader has written down: it is 5 blocks ahead at most, see the scales
+constexpr int kTileSlots = 8;            // tiles whose place the loader has written down: it is 6 blocks ahead at most, see the scales
 // Registers a thread: at launch, of the epilogue's two warpgroups and of the other. The epilogue holds 128 sums and two loads
 // of 16 columns.
 constexpr int kWideRegs = 168, kWideRegsEpi = 200, kWideRegsRest = 104;
@@ -131,29 +132,38 @@ static_assert(kWideThreads * kWideRegs >= kWideEpi * 32 * kWideRegsEpi + 128 * k
 struct WideTile {
   int g, row, rows, n;     // group, first row, rows of the group from there (can exceed the tile), column tile
 };
-struct WideShared {
-  alignas(16) uint64_t done[2];        // 16-byte pairs: the address of the other is this one's ^ 8
-  alignas(16) uint64_t taken[2];
-  uint64_t full[kWideStages], empty[kWideStages], paired[2], last;
-  uint32_t tmem;
-  int stop;
-  uint32_t amax[2][2][kWideM];
-  alignas(16) WideTile tile[kTileSlots];
-  float a_scale[kScaleSlots][kWideM], w_scale[kScaleSlots][2];     // w: the column halves', or gate's and up's
-  int off[RESHARD_MAX_GROUPS + 1], tiles[RESHARD_MAX_GROUPS + 1];   // row offsets; tiles of rows before each group
+template <bool Gated>
+struct Wide {
+  static constexpr int kStages = Gated ? 4 : 3;
+  static constexpr int kScaleSlots = 2 * kStages;
+  // An epilogue warp's 32 rows on their way out: boxes of so many bytes of each row. The gated product's, 64 bytes, leave
+  // room for a fourth stage (65,536 x 768 x 2048: 212 us with three). Without a gate a fourth stage would leave 64 bytes,
+  // too, of 256: 8192 x 14336 x 4096 2% faster, 65,536 x 2048 x 768 6% slower.
+  static constexpr int kBox = Gated ? 64 : 128, kBoxes = Gated ? 1 : 2;
+  struct Shared {
+    alignas(16) uint64_t done[2];        // 16-byte pairs: the address of the other is this one's ^ 8
+    alignas(16) uint64_t taken[2];
+    uint64_t full[kStages], empty[kStages], paired[2], last;
+    uint32_t tmem;
+    int stop;
+    uint32_t amax[2][2][kWideM];
+    alignas(16) WideTile tile[kTileSlots];
+    float a_scale[kScaleSlots][kWideM], w_scale[kScaleSlots][2];     // w: the column halves', or gate's and up's
+    int off[RESHARD_MAX_GROUPS + 1], tiles[RESHARD_MAX_GROUPS + 1];   // row offsets; tiles of rows before each group
+  };
+  static constexpr size_t kOut = (size_t)kWideEpi * kBoxes * 32 * kBox;
+  static constexpr size_t kSmem = (size_t)kStages * kWideStageBytes + kOut + sizeof(Shared);
+  static_assert(kSmem <= 232448, "shared memory of a CTA");
 };
-constexpr size_t kWideOut = (size_t)kWideEpi * 2 * kOutBox;
-constexpr size_t kWideSmem = (size_t)kWideStages * kWideStageBytes + kWideOut + sizeof(WideShared);
-static_assert(kWideSmem <= 232448, "shared memory of a CTA");
 
-__device__ __forceinline__ WideTile wide_tile(const WideShared &s, int groups, uint32_t ntiles, uint32_t t, int lane) {
-  const int lo = group_of(s.tiles, groups, ntiles, t, lane);
-  const uint32_t here = s.tiles[lo + 1] - s.tiles[lo], l = t - s.tiles[lo] * ntiles;
+__device__ __forceinline__ WideTile wide_tile(const int *off, const int *tiles, int groups, uint32_t ntiles, uint32_t t, int lane) {
+  const int lo = group_of(tiles, groups, ntiles, t, lane);
+  const uint32_t here = tiles[lo + 1] - tiles[lo], l = t - tiles[lo] * ntiles;
   const uint32_t n = l / here, m = l - n * here;     // row tiles first: neighbours share w's tile
   WideTile r;
   r.g = lo;
-  r.row = s.off[lo] + m * kWideM;
-  r.rows = s.off[lo + 1] - r.row;
+  r.row = off[lo] + m * kWideM;
+  r.rows = off[lo + 1] - r.row;
   r.n = n;
   return r;
 }
@@ -177,7 +187,7 @@ __device__ __forceinline__ void box_out(const CUtensorMap *map, const uint8_t *b
     if (lane == 0) {
 #pragma unroll
       for (int i = 0; i < Boxes; ++i)
-        if (i * Bytes < bytes) tma_store_2d(map, smem_addr(box + i * kOutBox), (int)x + i * Bytes, (int)row);
+        if (i * Bytes < bytes) tma_store_2d(map, smem_addr(box + i * 32 * Bytes), (int)x + i * Bytes, (int)row);
       bulk_commit();
     }
   } else {                       // a group's last rows
@@ -185,7 +195,7 @@ __device__ __forceinline__ void box_out(const CUtensorMap *map, const uint8_t *b
     for (int i = lane; i < rows * (Boxes * Bytes / 16); i += 32) {
       const int r = i / (Boxes * Bytes / 16), c = i % (Boxes * Bytes / 16), b = c / (Bytes / 16), piece = c % (Bytes / 16);
       const int at = Bytes == 128 ? piece ^ (r & 7) : piece ^ (r >> 1 & 3);
-      const uint4 v = *reinterpret_cast<const uint4 *>(box + b * kOutBox + r * Bytes + at * 16);
+      const uint4 v = *reinterpret_cast<const uint4 *>(box + b * 32 * Bytes + r * Bytes + at * 16);
       uint8_t *to = out + (row + r) * pitch + x + c * 16;
       if (c * 16 + 16 <= bytes) {
         *reinterpret_cast<uint4 *>(to) = v;
@@ -205,26 +215,26 @@ __device__ __forceinline__ void box_free(int lane) {
 
 // A warp's 32 rows of 128 columns in T. boxed: out's rows start on 16 bytes (a tensor map describes it); otherwise the warp
 // writes a row at a time from the boxes, an element a lane (rows from the registers, one a lane, took three times as long).
-template <typename T>
+template <typename T, int Bytes, int Boxes>
 __device__ __forceinline__ void store_tile(const CUtensorMap *map, bool boxed, uint8_t *box, int lane, const float2 (&sum)[kWideCols / 2], void *out, int64_t stride,
                                            int64_t n0, int64_t row, int rows, int cols) {
-  constexpr int per = 256 / sizeof(T), piece = 16 / sizeof(T);       // columns of two boxes, of 16 bytes
+  constexpr int per = Boxes * Bytes / sizeof(T), piece = 16 / sizeof(T), pieces = Bytes / 16;       // columns of the boxes, of 16 bytes; those of a row of a box
 #pragma unroll
   for (int c = 0; c < kWideCols; c += per) {
     if (c >= cols) break;
     box_free(lane);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
+    for (int j = 0; j < Boxes * pieces; ++j) {
       uint32_t v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if constexpr (sizeof(T) == 4) v[i] = __float_as_uint(i & 1 ? sum[(c + 4 * j + i) / 2].y : sum[(c + 4 * j + i) / 2].x);
         else v[i] = pack2<T>(sum[c / 2 + 4 * j + i].x, sum[c / 2 + 4 * j + i].y);
       }
-      box_put<128>(box + j / 8 * kOutBox, lane, j % 8, make_uint4(v[0], v[1], v[2], v[3]));
+      box_put<Bytes>(box + j / pieces * 32 * Bytes, lane, j % pieces, make_uint4(v[0], v[1], v[2], v[3]));
     }
     if (boxed) {
-      box_out<128, 2>(map, box, lane, static_cast<uint8_t *>(out), stride * (int64_t)sizeof(T), (n0 + c) * (int64_t)sizeof(T), row, rows,
+      box_out<Bytes, Boxes>(map, box, lane, static_cast<uint8_t *>(out), stride * (int64_t)sizeof(T), (n0 + c) * (int64_t)sizeof(T), row, rows,
                       min(per, cols - c) * (int)sizeof(T));
     } else {
       __syncwarp();
@@ -233,7 +243,7 @@ __device__ __forceinline__ void store_tile(const CUtensorMap *map, bool boxed, u
       for (int r = 0; r < min(rows, 32); ++r, to += stride) {
 #pragma unroll
         for (int u = 0; u < per / 32; ++u) {
-          const int e = u * 32 + lane, at = e / (8 * piece) * kOutBox + r * 128 + ((e / piece % 8) ^ (r & 7)) * 16;
+          const int e = u * 32 + lane, at = e / (pieces * piece) * 32 * Bytes + r * Bytes + ((e / piece % pieces) ^ (Bytes == 128 ? r & 7 : r >> 1 & 3)) * 16;
           if (c + e < cols) to[e] = reinterpret_cast<const T *>(box + at)[e % piece];
         }
       }
@@ -246,8 +256,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     reshard_product_wide_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mo,
                                 const __grid_constant__ Args p) {
   extern __shared__ __align__(1024) uint8_t stages[];
-  uint8_t *const out_boxes = stages + (size_t)kWideStages * kWideStageBytes;
-  WideShared &s = *reinterpret_cast<WideShared *>(out_boxes + kWideOut);
+  using C = Wide<Gated>;
+  using Shared = typename C::Shared;
+  constexpr int kStages = C::kStages;
+  uint8_t *const out_boxes = stages + (size_t)kStages * kWideStageBytes;
+  Shared &s = *reinterpret_cast<Shared *>(out_boxes + C::kOut);
   if (smem_addr(stages) & 1023) {      // not seen: the swizzle needs it
     atomicOr(&g_ops_status, 1);
     return;
@@ -255,7 +268,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Stop stop{&s.stop, &g_ops_status};
   if (tid == 0) {
-    for (int i = 0; i < kWideStages; ++i) {
+    for (int i = 0; i < kStages; ++i) {
       bar_init(smem_addr(&s.full[i]), 33);       // the loader, and a lane's copies of scales each
       bar_init(smem_addr(&s.empty[i]), 1);
     }
@@ -288,7 +301,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       uint32_t it = 0, st = 0, phase = 1, tile_no = 0;
       bool ok = true;
       for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x, ++tile_no) {
-        const WideTile w = wide_tile(s, p.groups, ntiles, t, lane);
+        const WideTile w = wide_tile(s.off, s.tiles, p.groups, ntiles, t, lane);
         for (int kb = 0; kb < p.kblocks; ++kb, ++it) {
           const uint32_t bar = smem_addr(s.full) + st * 8;
           ok = bar_wait(smem_addr(s.empty) + st * 8, phase, stop);
@@ -313,12 +326,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
               tma_3d(tw + 16384, &mw, kb * kBlockK, w.n * kCols + 128, w.g, bar);
             }
           }
-          if (++st == kWideStages) st = 0, phase ^= 1;
+          if (++st == kStages) st = 0, phase ^= 1;
         }
       }
       if (!ok && lane == 0)            // stopped: what is on its way still lands in this CTA's memory
-        for (uint32_t i = it > kWideStages ? it - kWideStages : 0; i < it; ++i)
-          bar_drain(smem_addr(&s.full[i % kWideStages]), i / kWideStages & 1);
+        for (uint32_t i = it > kStages ? it - kStages : 0; i < it; ++i)
+          bar_drain(smem_addr(&s.full[i % kStages]), i / kStages & 1);
       __syncwarp();
     } else if (warp == 0) {
       // ---- issuer: the first warp, which the scheduler prefers
@@ -338,7 +351,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           for (int k = 0; k < kBlockK / 32; ++k) mma_e4m3(d, a + 2 * k, b + 2 * k, idesc, k > 0);
           mma_commit(done);
           mma_commit(empty + st * 8);
-          if (++st == kWideStages) st = 0, phase ^= 1;
+          if (++st == kStages) st = 0, phase ^= 1;
           free_phase ^= second;
           second ^= 1;
           d ^= kWideN;
@@ -353,11 +366,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       __syncwarp();
     } else if (warp == 2) {
       // ---- scales of a stage's block, arriving with its operands. Two slots a stage: when a stage is free for block i,
-      // the products of block i - 3 are done, which began after the epilogue had taken block i - 5, so slot i % 6 is free too.
+      // the products of block i - kStages are done, which began after the epilogue had taken the block two before that one, so
+      // the slot is free too.
       uint32_t st = 0, phase = 1, slot = 0;
       bool ok = true;
       for (uint32_t t = blockIdx.x; ok && t < total; t += gridDim.x) {
-        const WideTile w = wide_tile(s, p.groups, ntiles, t, lane);
+        const WideTile w = wide_tile(s.off, s.tiles, p.groups, ntiles, t, lane);
         const float *sa[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) sa[i] = p.a_scale + (int64_t)(w.row + min(lane + 32 * i, w.rows - 1)) * p.as_row;
@@ -377,8 +391,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           }
           if (lane < 2) copy4(smem_addr(&s.w_scale[slot][lane]), sw + kb);
           bar_arrive_copied(smem_addr(s.full) + st * 8);
-          if (++st == kWideStages) st = 0, phase ^= 1;
-          if (++slot == kScaleSlots) slot = 0;
+          if (++st == kStages) st = 0, phase ^= 1;
+          if (++slot == C::kScaleSlots) slot = 0;
         }
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
@@ -387,12 +401,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     // ---- epilogue: a row and half of the columns a thread
     registers_up<kWideRegsEpi>();
     const int side = (warp >> 2) - 1, r = (warp & 3) * 32 + lane;
-    uint8_t *const box = out_boxes + (warp - 4) * 2 * kOutBox;
+    uint8_t *const box = out_boxes + (warp - 4) * C::kBoxes * 32 * C::kBox;
     // the next block's: tensor memory, barrier, parity, scales. tries: 1 once a wait gave up, so that the others pass
     uint32_t from = tmem + ((uint32_t)((warp & 3) * 32) << 16) + side * kWideCols, done = smem_addr(s.done), phase = 0, second = 0;
     uint32_t sa = smem_addr(&s.a_scale[0][r]), sw = smem_addr(&s.w_scale[0][Gated ? 0 : side]), tries = kTries;
     const uint32_t sa_end = sa + sizeof s.a_scale;
-    constexpr uint32_t kToTaken = offsetof(WideShared, taken) - offsetof(WideShared, done);
+    constexpr uint32_t kToTaken = offsetof(Shared, taken) - offsetof(Shared, done);
     for (uint32_t t = blockIdx.x, tile_no = 0; t < total; t += gridDim.x, ++tile_no) {
       float2 sum[kWideCols / 2];       // pairs of columns
 #pragma unroll
@@ -446,9 +460,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (!Gated) {
         const int n0 = w.n * kCols + side * kWideCols, cols = min(kWideCols, p.n - n0);
         if (rows > 0 && cols > 0) {
-          if (p.out_dtype == RESHARD_BF16) store_tile<__nv_bfloat16>(&mo, p.boxed, box, lane, sum, p.out, p.out_stride, n0, row0, rows, cols);
-          else if (p.out_dtype == RESHARD_F16) store_tile<__half>(&mo, p.boxed, box, lane, sum, p.out, p.out_stride, n0, row0, rows, cols);
-          else store_tile<float>(&mo, p.boxed, box, lane, sum, p.out, p.out_stride, n0, row0, rows, cols);
+          if (p.out_dtype == RESHARD_BF16) store_tile<__nv_bfloat16, C::kBox, C::kBoxes>(&mo, p.boxed, box, lane, sum, p.out, p.out_stride, n0, row0, rows, cols);
+          else if (p.out_dtype == RESHARD_F16) store_tile<__half, C::kBox, C::kBoxes>(&mo, p.boxed, box, lane, sum, p.out, p.out_stride, n0, row0, rows, cols);
+          else store_tile<float, C::kBox, C::kBoxes>(&mo, p.boxed, box, lane, sum, p.out, p.out_stride, n0, row0, rows, cols);
         }
       } else {
         // of the sums the first half is gate, the second up: this thread's 64 of the row's 128 values
@@ -1065,13 +1079,13 @@ int enqueue_wide(const Product &p, Args a, int sms, cudaStream_t stream) {
   if (!rc) rc = encode(&mw, p.w, p.k, Gated ? 2 * p.n : p.n, p.w_stride, p.groups, p.w_batch, Gated ? 64 : 128);
   const int64_t es = Gated ? 1 : element_bytes(p.out_dtype), pitch = p.out_stride * es;
   a.boxed = Gated || ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)pitch) & 15) == 0;
-  if (!rc && a.boxed) rc = encode(&mo, p.out, p.n * es, p.m, pitch, 0, 0, 32, Gated ? 64 : 128);
-  if (!rc) rc = allow_smem<&reshard_product_wide_kernel<Gated>>(kWideSmem, kWideRegs);
+  if (!rc && a.boxed) rc = encode(&mo, p.out, p.n * es, p.m, pitch, 0, 0, 32, Wide<Gated>::kBox);
+  if (!rc) rc = allow_smem<&reshard_product_wide_kernel<Gated>>(Wide<Gated>::kSmem, kWideRegs);
   if (rc) return rc;
   const int64_t cols = Gated ? kWideN / 2 : kWideN;
   const int64_t most = (p.m / kWideM + std::min<int64_t>(p.groups, p.m)) * ((p.n + cols - 1) / cols);
   if (most > INT32_MAX) return fail(RESHARD_ERR_UNSUPPORTED, "too many tiles for one launch");
-  const cudaError_t e = launch(reshard_product_wide_kernel<Gated>, dim3((unsigned)std::min<int64_t>(sms, most)), kWideThreads, kWideSmem, 1,
+  const cudaError_t e = launch(reshard_product_wide_kernel<Gated>, dim3((unsigned)std::min<int64_t>(sms, most)), kWideThreads, Wide<Gated>::kSmem, 1,
                                stream, ma, mw, mo, a);
   return e == cudaSuccess ? RESHARD_OK : cuda_error(e, "launching reshard_product_wide_kernel");
 }
