@@ -517,8 +517,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 // two CTAs an SM with some 100 KB of stages each, or one with 200 where the sums need the registers. The weights sit on
 // the tensor cores' 128 rows, and a product is as wide as the rows at hand, to 16. Where the tiles alone do not fill the
 // GPU, a cluster of CTAs splits K and adds its partial tiles through distributed shared memory, in rank order: the
-// same order on every run. 128 experts of 2048 x 768, one row each or two: both products 60 us, 6.6 TB/s;
-// 77 x 2867 x 4096: 8.4 us, bound by latency (launch, first loads, the cluster's sum).
+// same order on every run. 16 tokens to 8 of 128 experts of 2048 x 768 each: 41 and 24 us, 389 MB, 6.0
+// TB/s; 77 x 2867 x 4096 with the rows' quantization before it: 11.1 us, bound by latency (launch, first loads, the
+// cluster's sum).
 constexpr int kNarrowM = 128;            // rows of w (of gate and of up, when gated)
 constexpr int kNarrowThreads = 192;      // 4 epilogue warps, the loader, the issuer
 constexpr int kMostSplit = 8;            // CTAs of a cluster that share a tile's K
@@ -909,8 +910,8 @@ __device__ __forceinline__ void unpack(uint4 v, float *x) {
 // and row g of a at columns 32 t .. 32 t + 31 of a block: which columns a product takes from a lane is the same for both
 // operands, so that a lane's bytes can be neighbours. The CTA quantizes its rows of a into shared memory (X: their type, or
 // uint8_t where they come quantized) while the first loads of w are on their way: one launch for the whole call. The K
-// shares of a CTA's warps are added in order. 1 x 14336 x 4096: 12.6 us, 4.7 TB/s (as narrow: 16.5); of that the read
-// alone would take 8.7, the start and the end the rest. Three blocks ahead spill, one leaves it at 13.8.
+// shares of a CTA's warps are added in order. 1 x 14336 x 4096: 12.5 us, 4.7 TB/s (quantization and narrow: 14.9); of that the read
+// alone would take 8.7, the start and the end the rest. Three blocks ahead spill, one takes 13.8.
 template <typename X>
 __global__ void __launch_bounds__(kFewWarps * 32, 3) reshard_product_few_kernel(const __grid_constant__ Args p, const uint8_t *wq, int64_t w_stride) {
   constexpr bool kGiven = std::is_same_v<X, uint8_t>;

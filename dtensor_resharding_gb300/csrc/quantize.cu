@@ -80,6 +80,7 @@ __device__ __forceinline__ const uint8_t *first_word(const void *p) {
 }
 
 // 8 lanes a block of 128 values, 16 each: two or four 16-byte loads, three shuffles and one 16-byte store a lane.
+// 16,384 x 4096 bf16: 38.2 us, 5.3 TB/s, where a plain copy reaches 6.8 (4 lanes a block, 32 values each: the same).
 template <typename T, bool Wide>
 __global__ void __launch_bounds__(kQThreads) reshard_quantize_rows_kernel(Rows a, int64_t blocks, int per_row_blocks, bool wide_q) {
   grid_enter();
@@ -130,6 +131,7 @@ __global__ void __launch_bounds__(kQThreads) reshard_quantize_rows_kernel(Rows a
 }
 
 // One CTA a 128 x 128 block: 16 lanes a row, 8 values a lane in each of 8 passes, all loads in flight before the amax.
+// 128 matrices of 768 x 2048 bf16: 107 us, 5.6 TB/s (values widened to 32 bits as they came: 265 us).
 struct Blocks {
   const void *w;
   int64_t batch_stride, row_stride;
@@ -233,7 +235,8 @@ __global__ void __launch_bounds__(kQThreads) reshard_quantize_blocks_kernel(Bloc
 }
 
 // out[t] = sum_j weights[t, j] * y[position[t, j]] in the order of j, slots without a place skipped; 32-bit sums, one
-// rounding. One thread 8 columns of a token; bound by the read of y.
+// rounding. One thread 8 columns of a token; bound by the read of y: 8 slots a token, 8,192 x 2048 bf16, 54 us, 5.6 TB/s (loads of
+// all eight slots before the sums: three times as long).
 template <typename T>
 __global__ void __launch_bounds__(kQThreads)
     reshard_combine_kernel(const T *y, int64_t y_stride, const int32_t *position, const float *weights, int64_t tokens, int k, int64_t cols,

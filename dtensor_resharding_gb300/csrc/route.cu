@@ -10,7 +10,8 @@
 // One warp holds a row in registers (E / 32 values a lane), so that a row is read once and selection is k rounds of a
 // warp-wide integer maximum: keys are mapped to unsigned integers of the same order, removed ones to 0, and
 // redux.sync gives the maximum and then the lowest index that has it. Bound by instruction issue (about k rounds of
-// E / 32 compares and two redux), not by HBM, for the usual 128 to 256 experts.
+// E / 32 compares and two redux), not by HBM, for the usual 128 to 256 experts: 16,384 x 256 fp32 in 8 groups, 8 chosen,
+// takes 22.5 us for some 1,270 instructions a row, where the read alone would take 2.6; 24 x 128 takes 3.1, a launch.
 #include <algorithm>
 #include <climits>
 
@@ -115,7 +116,7 @@ __device__ __forceinline__ void keep_groups(const RouteArgs &a, int lane, const 
   const int size = a.experts / a.groups;
   if (W == 4 && size >= 4 && size <= 128 && (size & (size - 1)) == 0) {
     // A vector's four experts are of one group, and `lanes` neighbouring lanes hold all of it: their two best meet by
-    // shuffles, for all groups of a vector index at once. 16,384 x 256 in 8 groups: 36 us without this path, 15 with it.
+    // shuffles, for all groups of a vector index at once. 16,384 x 256 in 8 groups: 36 us without this path, 22 with it.
     const int lanes = size / 4, shift = 31 - __clz(size), per = 128 >> shift;      // groups a vector index
     uint32_t total = 0;
 #pragma unroll
@@ -271,7 +272,9 @@ __global__ void __launch_bounds__(kRouteWarps * 32) reshard_route_kernel(RouteAr
 //   sigmoid:               d z_{i_j} = g_j s_j (1 - s_j)
 //   sigmoid, renormalised: r_j = s_j / sum s;  d z_{i_j} = (g_j - sum g r) r_j (1 - s_j)
 // 1 - s is computed as sigmoid(-z). The bias only selects and has no gradient. Written whole, one warp a row; bound by
-// the write of the rows (and, for the whole softmax, the read of the logits).
+// the write of the rows (and, for the whole softmax, the read of the logits) and by a row's chain of dependent loads
+// (ids, then the chosen logits): 32,768 x 128 fp32, sigmoid, 9.5 us, 2.1 TB/s. Where no id repeats, zeros are written and
+// the k values over them: comparing every value's expert with every id took 11.0 us there.
 template <typename T, int V, int W>
 __global__ void __launch_bounds__(kRouteWarps * 32)
     reshard_route_backward_kernel(RouteArgs a, const float *grad, const int32_t *ids, T *out, int64_t out_stride) {
@@ -363,8 +366,8 @@ __global__ void __launch_bounds__(kRouteWarps * 32)
 // a cluster of eight that shares its counts through distributed shared memory, in one launch without workspace: every
 // warp counts the experts of a run of slots of its own; the counts of the warps and CTAs before it give each warp its
 // first place of each expert; a second walk of the run places 32 slots at a time, equal ones ranked by lane
-// (match.any). Counts are integers, so their atomics change nothing: the order is the same on every run. 65,536 slots
-// over 128 experts: 9 us (one CTA an expert, each reading all ids: 117 us).
+// (match.any). Counts are integers, so their atomics change nothing: the order is the same on every run. Bound by
+// latency: 65,536 slots over 128 experts 14 us, 32,760 over 16 of them 8 (one CTA an expert, each reading all ids: 117).
 constexpr int kDispatchWarps = 32, kDispatchCluster = 8;
 
 __global__ void __launch_bounds__(kDispatchWarps * 32)

@@ -318,7 +318,8 @@ def test_product_whole_grid(M, N, K):
         assert torch.equal(first, R.reshard_linear_fp8(x, wq, ws))
 
 
-@pytest.mark.parametrize("counts", [[0, 0, 0], [1, 0, 2], [5, 17, 0, 1], [130, 0, 1, 255, 64], [300, 129], [1] * 40, [0, 700, 3]])
+@pytest.mark.parametrize("counts", [[0, 0, 0], [1, 0, 2], [5, 17, 0, 1], [130, 0, 1, 255, 64], [300, 129], [1] * 40, [0, 700, 3],
+                                    [0] * 60 + [400, 3], [17] * 40 + [0], [i % 3 for i in range(512)]])
 @pytest.mark.parametrize("N,K", [(130, 300), (256, 1024)])
 def test_grouped_product(counts, N, K):
     """Empty groups, groups of one row, groups that end inside a tile, rows beyond the last group untouched."""
