@@ -8,19 +8,18 @@ namespace reshard {
 namespace ops {
 
 void Checks::pointer(const void *p, const char *name, uintptr_t align) {
-  if (!p) return add(true, RESHARD_ERR_INVALID_ARG, std::string(name) + " is NULL");
+  if (!p) return violation(RESHARD_ERR_INVALID_ARG, std::string(name) + " is NULL");
   if (reinterpret_cast<uintptr_t>(p) % align)
-    return add(true, RESHARD_ERR_INVALID_ARG, std::string(name) + " is not aligned to " + std::to_string(align) + " bytes");
+    return violation(RESHARD_ERR_INVALID_ARG, std::string(name) + " is not aligned to " + std::to_string(align) + " bytes");
   cudaPointerAttributes a{};
   if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
     (void)cudaGetLastError();
-    return add(true, RESHARD_ERR_INVALID_ARG, std::string(name) + " is not a pointer the device can dereference");
+    return violation(RESHARD_ERR_INVALID_ARG, std::string(name) + " is not a pointer the device can dereference");
   }
-  if (a.type == cudaMemoryTypeUnregistered) return add(true, RESHARD_ERR_INVALID_ARG, std::string(name) + " is pageable host memory");
+  if (a.type == cudaMemoryTypeUnregistered) return violation(RESHARD_ERR_INVALID_ARG, std::string(name) + " is pageable host memory");
   if (a.type == cudaMemoryTypeDevice) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) == cudaSuccess && a.device != dev)
-      add(true, RESHARD_ERR_INVALID_ARG, std::string(name) + " is memory of device " + std::to_string(a.device));
+    if (device_ < 0 && cudaGetDevice(&device_) != cudaSuccess) device_ = -1;
+    if (device_ >= 0 && a.device != device_) violation(RESHARD_ERR_INVALID_ARG, std::string(name) + " is memory of device " + std::to_string(a.device));
   }
 }
 
@@ -85,7 +84,7 @@ using namespace reshard::ops;
 extern "C" int reshard_matmul_fp8(const void *a, int64_t a_stride, const float *a_scale, int64_t a_scale_row, int64_t a_scale_block,
                                   const void *w, int64_t w_batch_stride, int64_t w_stride, const float *w_scale, const int32_t *offsets,
                                   int groups, int64_t m, int64_t n, int64_t k, void *out, int out_dtype, int64_t out_stride,
-                                  reshard_stream_t stream) {
+                                  reshard_stream_t stream) try {
   Checks c("reshard_matmul_fp8");
   c.invalid(m < 0 || n < 0 || k < 1, "m and n must be >= 0 and k >= 1");
   c.unsupported(m > RESHARD_MAX_EXTENT || n > RESHARD_MAX_EXTENT || k > RESHARD_MAX_EXTENT, "m, n or k above 2^30");
@@ -111,7 +110,7 @@ extern "C" int reshard_matmul_fp8(const void *a, int64_t a_stride, const float *
   p.offsets = offsets, p.groups = groups, p.m = m, p.n = n, p.k = k;
   p.out = out, p.out_dtype = out_dtype, p.out_stride = out_stride;
   return enqueue_product(p, reinterpret_cast<cudaStream_t>(stream));
-}
+} OPS_CATCH
 
 extern "C" int64_t reshard_linear_fp8_workspace(int64_t m, int64_t k) {
   return m < 0 || k < 0 || product_quantizes(m, k) ? 0 : QuantizedRows(m, k).bytes();
@@ -119,7 +118,7 @@ extern "C" int64_t reshard_linear_fp8_workspace(int64_t m, int64_t k) {
 
 extern "C" int reshard_linear_fp8(const void *x, int dtype, int64_t m, int64_t k, int64_t row_stride, const void *w, int64_t w_stride,
                                   const float *w_scale, int64_t n, void *out, int64_t out_stride, void *workspace, int64_t workspace_bytes,
-                                  reshard_stream_t stream_) {
+                                  reshard_stream_t stream_) try {
   Checks c("reshard_linear_fp8");
   c.invalid(m < 0 || n < 0 || k < 1, "m and n must be >= 0 and k >= 1");
   c.unsupported(m > RESHARD_MAX_EXTENT || n > RESHARD_MAX_EXTENT || k > RESHARD_MAX_EXTENT, "m, n or k above 2^30");
@@ -152,7 +151,7 @@ extern "C" int reshard_linear_fp8(const void *x, int dtype, int64_t m, int64_t k
   p.m = m, p.n = n, p.k = k;
   p.out = out, p.out_dtype = dtype, p.out_stride = out_stride;
   return enqueue_product(p, stream);
-}
+} OPS_CATCH
 
 extern "C" int64_t reshard_experts_fp8_workspace(int64_t tokens, int k, int experts, int64_t hidden, int64_t ffn, int dtype) {
   if (tokens < 0 || k < 1 || experts < 1 || hidden < 0 || ffn < 0 || !element_bytes(dtype)) return 0;
@@ -163,7 +162,7 @@ extern "C" int reshard_experts_fp8(const void *x, int dtype, int64_t tokens, int
                                    const float *weights, int k, int first_expert, int experts, int64_t ffn, const void *w13,
                                    int64_t w13_batch_stride, int64_t w13_stride, const float *w13_scale, const void *w2,
                                    int64_t w2_batch_stride, int64_t w2_stride, const float *w2_scale, void *out, int64_t out_stride,
-                                   void *workspace, int64_t workspace_bytes, reshard_stream_t stream_) {
+                                   void *workspace, int64_t workspace_bytes, reshard_stream_t stream_) try {
   Checks c("reshard_experts_fp8");
   c.invalid(tokens < 0 || hidden < 1 || ffn < 1 || k < 1, "tokens must be >= 0, hidden, ffn and k >= 1");
   c.invalid(first_expert < 0 || experts < 1, "first_expert must be >= 0 and experts >= 1");
@@ -225,9 +224,9 @@ extern "C" int reshard_experts_fp8(const void *x, int dtype, int64_t tokens, int
   p2.out = y, p2.out_dtype = dtype, p2.out_stride = up(hidden, 16);
   if ((rc = enqueue_product(p2, stream))) return rc;
   return enqueue_combine(y, dtype, up(hidden, 16), position, weights, tokens, k, hidden, out, out_stride, stream);
-}
+} OPS_CATCH
 
-extern "C" int reshard_ops_call(int op, const reshard_word_t *a) {
+extern "C" int reshard_ops_call(int op, const reshard_word_t *a) try {
   if (!a) return fail(RESHARD_ERR_INVALID_ARG, "args is NULL");
   switch (op) {
     case RESHARD_OP_ROUTE:
@@ -274,4 +273,4 @@ extern "C" int reshard_ops_call(int op, const reshard_word_t *a) {
     default:
       return fail(RESHARD_ERR_INVALID_ARG, "unknown operator number");
   }
-}
+} OPS_CATCH

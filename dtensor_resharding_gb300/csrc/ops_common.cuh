@@ -27,6 +27,16 @@ inline int cuda_error(cudaError_t e, const char *what) {
               std::string(what) + ": " + cudaGetErrorString(e));
 }
 
+// Closes the body of a C entry that is a function try block: no exception leaves the library.
+inline int out_of_memory() noexcept {
+  try {
+    return fail(RESHARD_ERR_OOM, "out of host memory");
+  } catch (...) {
+    return RESHARD_ERR_OOM;
+  }
+}
+#define OPS_CATCH catch (...) { return ::reshard::ops::out_of_memory(); }
+
 #define OPS_CUDA(call)                                            \
   do {                                                            \
     cudaError_t e_ = (call);                                      \
@@ -45,13 +55,15 @@ class Checks {
   bool ok() const { return n_ == 0; }
 
  private:
-  void add(bool bad, int code, const std::string &why) {
-    if (!bad) return;
+  void add(bool bad, int code, const char *why) {
+    if (bad) violation(code, why);
+  }
+  void violation(int code, const std::string &why) {
     if (n_++ == 0 || code == RESHARD_ERR_INVALID_ARG) code_ = code;
     lines_ += "\n  " + why;
   }
   const char *call_;
-  int n_ = 0, code_ = RESHARD_OK;
+  int n_ = 0, code_ = RESHARD_OK, device_ = -1;
   std::string lines_;
 };
 

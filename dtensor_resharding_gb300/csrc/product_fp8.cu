@@ -1197,7 +1197,7 @@ int enqueue_product(const Product &p, cudaStream_t stream) {
 using namespace reshard;
 using namespace reshard::ops;
 
-extern "C" int reshard_ops_status(int32_t *status, int reset) {
+extern "C" int reshard_ops_status(int32_t *status, int reset) try {
   if (!status) return fail(RESHARD_ERR_INVALID_ARG, "status is NULL");
   OPS_CUDA(cudaDeviceSynchronize());
   int v = 0;
@@ -1208,4 +1208,4 @@ extern "C" int reshard_ops_status(int32_t *status, int reset) {
   }
   *status = v;
   return RESHARD_OK;
-}
+} OPS_CATCH

@@ -321,7 +321,7 @@ using namespace reshard::ops;
 
 extern "C" int reshard_quantize_rows(const void *x, int dtype, int64_t rows, int64_t cols, int64_t row_stride, void *q,
                                      int64_t q_stride, float *scale, int64_t scale_row_stride, int64_t scale_block_stride,
-                                     reshard_stream_t stream) {
+                                     reshard_stream_t stream) try {
   Checks c("reshard_quantize_rows");
   c.invalid(rows < 0 || cols < 0, "rows or cols < 0");
   c.invalid(!element_bytes(dtype), "dtype must be BF16, F16 or F32");
@@ -337,11 +337,11 @@ extern "C" int reshard_quantize_rows(const void *x, int dtype, int64_t rows, int
   if (!c.ok()) return c.report();
   const Rows r{x, dtype, rows, cols, row_stride, static_cast<uint8_t *>(q), q_stride, scale, scale_row_stride, scale_block_stride};
   return enqueue_quantize_rows(r, reinterpret_cast<cudaStream_t>(stream));
-}
+} OPS_CATCH
 
 extern "C" int reshard_quantize_blocks(const void *w, int dtype, int64_t batch, int64_t rows, int64_t cols, int64_t batch_stride,
                                        int64_t row_stride, void *q, int64_t q_batch_stride, int64_t q_row_stride, float *scale,
-                                       reshard_stream_t stream) {
+                                       reshard_stream_t stream) try {
   Checks c("reshard_quantize_blocks");
   c.invalid(batch < 0 || rows < 0 || cols < 0, "batch, rows or cols < 0");
   c.invalid(!element_bytes(dtype), "dtype must be BF16, F16 or F32");
@@ -368,4 +368,4 @@ extern "C" int reshard_quantize_blocks(const void *w, int dtype, int64_t batch, 
   else if (dtype == RESHARD_BF16) e = launch(reshard_quantize_blocks_kernel<__nv_bfloat16>, grid, kQThreads, 0, 1, s, a, wide, wide_q);
   else e = launch(reshard_quantize_blocks_kernel<__half>, grid, kQThreads, 0, 1, s, a, wide, wide_q);
   return e == cudaSuccess ? RESHARD_OK : cuda_error(e, "launching reshard_quantize_blocks_kernel");
-}
+} OPS_CATCH

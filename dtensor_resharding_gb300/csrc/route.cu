@@ -528,7 +528,7 @@ using namespace reshard::ops;
 
 extern "C" int reshard_route(const void *logits, int dtype, int64_t tokens, int experts, int64_t row_stride, const float *bias,
                              int score, int groups, int groups_kept, int group_top, int k, int renormalize, float scale,
-                             float *weights, int32_t *ids, reshard_stream_t stream) {
+                             float *weights, int32_t *ids, reshard_stream_t stream) try {
   Checks c("reshard_route");
   check_route(c, tokens, experts, row_stride, dtype, k, score);
   c.invalid(groups < 1 || (groups >= 1 && experts >= 1 && experts % groups), "groups must divide experts");
@@ -557,11 +557,11 @@ extern "C" int reshard_route(const void *logits, int dtype, int64_t tokens, int 
     });
   });
   return e == cudaSuccess ? RESHARD_OK : cuda_error(e, "launching reshard_route_kernel");
-}
+} OPS_CATCH
 
 extern "C" int reshard_route_backward(const float *grad_weights, const void *logits, int dtype, int64_t tokens, int experts,
                                       int64_t row_stride, const int32_t *ids, int k, int score, int renormalize, float scale,
-                                      void *grad_logits, int64_t grad_stride, reshard_stream_t stream) {
+                                      void *grad_logits, int64_t grad_stride, reshard_stream_t stream) try {
   Checks c("reshard_route_backward");
   check_route(c, tokens, experts, row_stride, dtype, k, score);
   c.invalid(grad_stride < experts, "a row stride is shorter than the row");
@@ -585,10 +585,10 @@ extern "C" int reshard_route_backward(const float *grad_weights, const void *log
     });
   });
   return e == cudaSuccess ? RESHARD_OK : cuda_error(e, "launching reshard_route_backward_kernel");
-}
+} OPS_CATCH
 
 extern "C" int reshard_dispatch(const int32_t *ids, int64_t slots, int first_expert, int experts, int32_t *offsets, int32_t *order,
-                                int32_t *position, reshard_stream_t stream) {
+                                int32_t *position, reshard_stream_t stream) try {
   Checks c("reshard_dispatch");
   c.invalid(slots < 0, "slots < 0");
   c.unsupported(slots > RESHARD_MAX_SLOTS, "more than 2^30 slots");
@@ -604,4 +604,4 @@ extern "C" int reshard_dispatch(const int32_t *ids, int64_t slots, int first_exp
   }
   if (!c.ok()) return c.report();
   return enqueue_dispatch(ids, slots, first_expert, experts, offsets, order, position, reinterpret_cast<cudaStream_t>(stream));
-}
+} OPS_CATCH
