@@ -64,6 +64,24 @@ def test_route_orders_and_weighs(E, k, dtype, score):
         check_route(z, k, score=score, renormalize=renormalize, scale=2.5 if renormalize else 1.0)
 
 
+@pytest.mark.parametrize("E,k", [(32, 32), (60, 20), (128, 32), (256, 8), (300, 32), (1024, 32)])
+def test_route_ties_and_neighbours(E, k):
+    """Rows of few different logits, and rows whose largest are neighbours (held by one lane) or lie far apart."""
+    g = gen(E * k)
+    z = torch.randint(0, 3, (40, E), generator=g, device="cuda").float()
+    z[0] = 1.0
+    for i in range(1, 13):
+        at = int(torch.randint(0, max(1, E - 16), (1,), generator=g, device="cuda"))
+        z[i] = randn(g, E) - 20
+        z[i, at:at + 16] += 20
+        z[i + 13, ::(i * 11) % 37 + 1] += 3.0
+    z[30, : E - k] = float("-inf")
+    z[31, k:] = float("-inf")
+    z[32, k // 2:] = float("nan")
+    for dtype in (torch.float32, torch.bfloat16):
+        check_route(z.to(dtype), k)
+
+
 def separated(g, T, E, score):
     """f32 logits and a bias whose keys (score + bias) lie far apart against fp32 roundings: a permuted grid for each row."""
     bias = (torch.rand(E, generator=g, device="cuda") - 0.5) * 0.2
