@@ -113,7 +113,8 @@ extern "C" int reshard_matmul_fp8(const void *a, int64_t a_stride, const float *
 } OPS_CATCH
 
 extern "C" int64_t reshard_linear_fp8_workspace(int64_t m, int64_t k) {
-  return m < 0 || k < 0 || product_quantizes(m, k) ? 0 : QuantizedRows(m, k).bytes();
+  if (m < 0 || k < 0 || m > RESHARD_MAX_EXTENT || k > RESHARD_MAX_EXTENT || product_quantizes(m, k)) return 0;
+  return QuantizedRows(m, k).bytes();
 }
 
 extern "C" int reshard_linear_fp8(const void *x, int dtype, int64_t m, int64_t k, int64_t row_stride, const void *w, int64_t w_stride,
@@ -155,6 +156,8 @@ extern "C" int reshard_linear_fp8(const void *x, int dtype, int64_t m, int64_t k
 
 extern "C" int64_t reshard_experts_fp8_workspace(int64_t tokens, int k, int experts, int64_t hidden, int64_t ffn, int dtype) {
   if (tokens < 0 || k < 1 || experts < 1 || hidden < 0 || ffn < 0 || !element_bytes(dtype)) return 0;
+  // what the call refuses has no size, and none of the sums below passes 63 bits
+  if (experts > RESHARD_MAX_GROUPS || tokens > RESHARD_MAX_SLOTS / k || hidden > RESHARD_MAX_EXTENT / 2 || ffn > RESHARD_MAX_EXTENT / 2) return 0;
   return ExpertLayout(tokens, k, experts, hidden, ffn, dtype).bytes();
 }
 

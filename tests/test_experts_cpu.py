@@ -67,6 +67,7 @@ def test_every_violation_is_listed():
 
 def test_workspace_sizes():
     L = B.LIB
+    assert L.reshard_linear_fp8_workspace(1 << 62, 1 << 62) == 0 and L.reshard_experts_fp8_workspace(1 << 62, 8, 4, 256, 128, 1) == 0
     assert L.reshard_linear_fp8_workspace(-1, 4) == 0 and L.reshard_experts_fp8_workspace(4, 0, 4, 256, 128, 1) == 0
     # values at a 16-byte pitch and one fp32 scale for each 128, each part rounded up to 256 bytes
     assert L.reshard_linear_fp8_workspace(30, 300) == 30 * 304 // 256 * 256 + 256 + 512 and L.reshard_linear_fp8_workspace(3, 300) == 0
