@@ -52,9 +52,9 @@ struct QuantizedRows {
 struct ExpertLayout {
   int64_t slots, offsets, order, position, y;
   QuantizedRows x, h;
-  ExpertLayout(int64_t tokens, int k, int experts, int64_t hidden, int64_t ffn, int dtype)
+  ExpertLayout(int64_t tokens, int k, int experts, int64_t hidden, int64_t ffn)
       : slots(tokens * k), offsets(up(4 * (experts + 1), kAlign)), order(up(4 * slots, kAlign)), position(order),
-        y(up(slots * up(hidden, 16) * element_bytes(dtype), kAlign)), x(product_gathers(slots, experts) ? tokens : slots, hidden), h(slots, ffn) {}
+        y(up(slots * up(hidden, 16) * 4, kAlign)), x(product_gathers(slots, experts) ? tokens : slots, hidden), h(slots, ffn) {}
   int64_t bytes() const { return offsets + order + position + y + x.bytes() + h.bytes(); }
 };
 
@@ -158,7 +158,7 @@ extern "C" int64_t reshard_experts_fp8_workspace(int64_t tokens, int k, int expe
   if (tokens < 0 || k < 1 || experts < 1 || hidden < 0 || ffn < 0 || !element_bytes(dtype)) return 0;
   // what the call refuses has no size, and none of the sums below passes 63 bits
   if (experts > RESHARD_MAX_GROUPS || tokens > RESHARD_MAX_SLOTS / k || hidden > RESHARD_MAX_EXTENT / 2 || ffn > RESHARD_MAX_EXTENT / 2) return 0;
-  return ExpertLayout(tokens, k, experts, hidden, ffn, dtype).bytes();
+  return ExpertLayout(tokens, k, experts, hidden, ffn).bytes();
 }
 
 extern "C" int reshard_experts_fp8(const void *x, int dtype, int64_t tokens, int64_t hidden, int64_t row_stride, const int32_t *ids,
@@ -191,13 +191,13 @@ extern "C" int reshard_experts_fp8(const void *x, int dtype, int64_t tokens, int
   if (!c.ok()) return c.report();
   if (tokens == 0) return RESHARD_OK;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  const ExpertLayout l(tokens, k, experts, hidden, ffn, dtype);
+  const ExpertLayout l(tokens, k, experts, hidden, ffn);
   uint8_t *at = static_cast<uint8_t *>(workspace);
   auto take = [&](int64_t bytes) { uint8_t *p = at; at += bytes; return p; };
   int32_t *offsets = reinterpret_cast<int32_t *>(take(l.offsets));
   int32_t *order = reinterpret_cast<int32_t *>(take(l.order));
   int32_t *position = reinterpret_cast<int32_t *>(take(l.position));
-  uint8_t *y = take(l.y);
+  float *y = reinterpret_cast<float *>(take(l.y));
   uint8_t *xq = take(l.x.values);
   float *xs = reinterpret_cast<float *>(take(l.x.scales));
   uint8_t *hq = take(l.h.values);
@@ -224,9 +224,11 @@ extern "C" int reshard_experts_fp8(const void *x, int dtype, int64_t tokens, int
   p2.w = static_cast<const uint8_t *>(w2), p2.w_batch = map_batch(experts, w2_batch_stride, hidden, w2_stride), p2.w_stride = w2_stride;
   p2.w_scale = w2_scale, p2.offsets = offsets, p2.groups = experts, p2.m = l.slots, p2.n = hidden, p2.k = ffn;
   p2.early = true;
-  p2.out = y, p2.out_dtype = dtype, p2.out_stride = up(hidden, 16);
+  // fp32 until the weighted sum: an expert's output can be beyond float16 where its share of the sum is not, and outputs that
+  // cancel would leave their roundings. (16 bits there: 424 us instead of 509 for 8,192 tokens to 8 of 128 experts of 2048 x 768.)
+  p2.out = y, p2.out_dtype = RESHARD_F32, p2.out_stride = up(hidden, 16);
   if ((rc = enqueue_product(p2, stream))) return rc;
-  return enqueue_combine(y, dtype, up(hidden, 16), position, weights, tokens, k, hidden, out, out_stride, stream);
+  return enqueue_combine(y, up(hidden, 16), position, weights, tokens, k, hidden, out, dtype, out_stride, stream);
 } OPS_CATCH
 
 extern "C" int reshard_ops_call(int op, const reshard_word_t *a) try {

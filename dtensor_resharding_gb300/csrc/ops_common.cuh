@@ -132,8 +132,8 @@ struct Rows {                 // a quantization by rows
 int enqueue_quantize_rows(const Rows &r, cudaStream_t stream);
 int enqueue_dispatch(const int32_t *ids, int64_t slots, int first, int experts, int32_t *offsets, int32_t *order,
                      int32_t *position, cudaStream_t stream);
-int enqueue_combine(const void *y, int dtype, int64_t y_stride, const int32_t *position, const float *weights, int64_t tokens,
-                    int k, int64_t cols, void *out, int64_t out_stride, cudaStream_t stream);
+int enqueue_combine(const float *y, int64_t y_stride, const int32_t *position, const float *weights, int64_t tokens, int k, int64_t cols,
+                    void *out, int dtype, int64_t out_stride, cudaStream_t stream);
 
 struct Product {              // out[m, n] = sum_k a[m, k] w[n, k], both as 8-bit values times block scales
   const uint8_t *a;

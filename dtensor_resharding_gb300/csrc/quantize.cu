@@ -234,12 +234,12 @@ __global__ void __launch_bounds__(kQThreads) reshard_quantize_blocks_kernel(Bloc
   }
 }
 
-// out[t] = sum_j weights[t, j] * y[position[t, j]] in the order of j, slots without a place skipped; 32-bit sums, one
-// rounding. One thread 8 columns of a token; bound by the read of y: 8 slots a token, 8,192 x 2048 bf16, 54 us, 5.6 TB/s (loads of
+// out[t] = sum_j weights[t, j] * y[position[t, j]] in the order of j, slots without a place skipped; terms and sums of 32
+// bits, one rounding. One thread 8 columns of a token; bound by the read of y: 8 slots a token, 8,192 x 2048, 83 us, 6.9 TB/s (loads of
 // all eight slots before the sums: three times as long).
 template <typename T>
 __global__ void __launch_bounds__(kQThreads)
-    reshard_combine_kernel(const T *y, int64_t y_stride, const int32_t *position, const float *weights, int64_t tokens, int k, int64_t cols,
+    reshard_combine_kernel(const float *y, int64_t y_stride, const int32_t *position, const float *weights, int64_t tokens, int k, int64_t cols,
                            T *out, int64_t out_stride, int chunks, bool wide) {
   grid_enter();
   const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(kQThreads)
     if (p < 0) continue;
     const float w = weights[t * k + j];
     float x[8];
-    load_values<T, 8>(y + (int64_t)p * y_stride + c, left, wide, x);
+    load_values<float, 8>(y + (int64_t)p * y_stride + c, left, wide, x);
 #pragma unroll
     for (int u = 0; u < 8; ++u) sum[u] = fmaf(w, x[u], sum[u]);
   }
@@ -294,18 +294,18 @@ int enqueue_quantize_rows(const Rows &r, cudaStream_t stream) {
   return e == cudaSuccess ? RESHARD_OK : cuda_error(e, "launching reshard_quantize_rows_kernel");
 }
 
-int enqueue_combine(const void *y, int dtype, int64_t y_stride, const int32_t *position, const float *weights, int64_t tokens,
-                    int k, int64_t cols, void *out, int64_t out_stride, cudaStream_t stream) {
+int enqueue_combine(const float *y, int64_t y_stride, const int32_t *position, const float *weights, int64_t tokens, int k, int64_t cols,
+                    void *out, int dtype, int64_t out_stride, cudaStream_t stream) {
   if (tokens == 0 || cols == 0) return RESHARD_OK;
   const int chunks = (int)((cols + 7) / 8), es = element_bytes(dtype);
   const int block = tokens * chunks <= 32768 ? 64 : kQThreads;      // a few tokens' columns spread over the SMs
   const dim3 grid((unsigned)((tokens * chunks + block - 1) / block));
-  const bool wide = aligned16(y, y_stride, es) && aligned16(out, out_stride, es);
+  const bool wide = aligned16(y, y_stride, 4) && aligned16(out, out_stride, es);
   cudaError_t e;
   auto go = [&](auto t) {
     using T = decltype(t);
-    return launch(reshard_combine_kernel<T>, grid, block, 0, 1, stream, static_cast<const T *>(y), y_stride, position, weights,
-                  tokens, k, cols, static_cast<T *>(out), out_stride, chunks, wide);
+    return launch(reshard_combine_kernel<T>, grid, block, 0, 1, stream, y, y_stride, position, weights, tokens, k, cols,
+                  static_cast<T *>(out), out_stride, chunks, wide);
   };
   if (dtype == RESHARD_F32) e = go(float());
   else if (dtype == RESHARD_BF16) e = go(__nv_bfloat16());

@@ -113,8 +113,8 @@ int reshard_linear_fp8(const void *x, int dtype, int64_t m, int64_t k, int64_t r
  * over the choices with 0 <= e < experts (other ids, -1 among them, add nothing: another rank's, or no choice).
  * x, out [tokens, hidden] in dtype; ids, weights [tokens, k]; w13 [experts, 2 ffn, hidden] (gate rows, then up rows)
  * and w2 [experts, hidden, ffn] E4M3 with block scales, 16-byte aligned, row and batch strides multiples of 16.
- * ffn must be a multiple of 128, so that no block holds gate and up rows. silu(g) * u stays in fp32 until it is quantized;
- * each expert's output is rounded to dtype before the weighted fp32 sum.
+ * ffn must be a multiple of 128, so that no block holds gate and up rows. silu(g) * u stays in fp32 until it is quantized,
+ * each expert's output until the weighted sum, which is rounded to dtype once.
  * workspace: reshard_experts_fp8_workspace(...) bytes, 256-byte aligned.
  */
 int64_t reshard_experts_fp8_workspace(int64_t tokens, int k, int experts, int64_t hidden, int64_t ffn, int dtype);
