@@ -93,7 +93,7 @@ extern "C" int reshard_matmul_fp8(const void *a, int64_t a_stride, const float *
   c.invalid(!element_bytes(out_dtype), "out_dtype must be BF16, F16 or F32");
   c.invalid(a_stride < k || out_stride < n, "a row stride is shorter than the row");
   c.unsupported(a_stride % 16 != 0, "a's row stride is not a multiple of 16 bytes");
-  c.invalid(a_scale_row < 1 || a_scale_block < 1, "scale strides must be positive");
+  c.invalid(a_scale_row < 0 || a_scale_block < 0, "scale strides must not be negative");
   if (m > 0 && n > 0 && c.ok()) {
     c.pointer(a, "a", 16);
     c.pointer(a_scale, "a_scale", 4);

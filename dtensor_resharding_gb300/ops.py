@@ -287,7 +287,7 @@ def reshard_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, 
 
     ``w`` is [n, k], or [groups, n, k] with ``offsets`` [groups + 1] int32 (on the device): rows offsets[g]:offsets[g + 1] of
     ``a`` meet w[g], rows beyond the last offset are left as they are in ``out``. float8 values may also come as the
-    uint8 bytes that a reshard moved."""
+    uint8 bytes that a reshard moved. ``a_scale`` may have any strides: one scale a row or one in all may come expanded."""
     here = _here(a, stream)
     if here is None:
         with _on(a, stream):
@@ -304,9 +304,8 @@ def reshard_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, 
     if a_scale.dtype is not torch.float32 or a_scale.shape != (M, -(-K // 128)) or a_scale.device != a.device:
         _bad(f"a_scale must be float32 of shape {(M, -(-K // 128))} on {a.device}, not {a_scale.dtype} of shape {tuple(a_scale.shape)}")
     out, to_step = _output(out, M, N, out_dtype if out is None else out.dtype, a)
-    _call(5, _MATMUL_FP8(a.data_ptr(), step if M > 1 else -(-step // 16) * 16, a_scale.data_ptr(), max(1, a_scale.stride(0)),
-                         max(1, a_scale.stride(1)), at_w, batch, pitch, at_ws, at_offsets, groups, M, N, K, out.data_ptr(), _code(out, "out"),
-                         to_step, here))
+    _call(5, _MATMUL_FP8(a.data_ptr(), step if M > 1 else -(-step // 16) * 16, a_scale.data_ptr(), *a_scale.stride(), at_w, batch, pitch, at_ws,
+                         at_offsets, groups, M, N, K, out.data_ptr(), _code(out, "out"), to_step, here))
     return out
 
 

@@ -76,3 +76,29 @@ def test_experts_outputs_that_cancel(T):
     want = X.experts(x, ids, ones, w13, s13, w2, s2)
     err = R.reshard_experts_fp8(x, ids, ones, w13, s13, w2, s2).to(F64) - want
     assert float(err.norm()) <= 7e-3 * float(want.norm()), float(err.norm() / want.norm())
+
+
+# ------------------------------------------------------------------------------------------ strides of the rows' scales
+
+@pytest.mark.parametrize("M,groups", [(1, 0), (3, 0), (40, 0), (300, 0), (2000, 0), (20, 4), (700, 4)])
+@pytest.mark.parametrize("K", [128, 1000])
+def test_product_scales_of_any_strides(M, groups, K):
+    """Scales stored row by row, block by block, one a row, one a block and one in all, through each product kernel: what
+    their copies give."""
+    g = gen(M + K)
+    kb, N = -(-K // 128), 200
+    q, s = R.reshard_quantize_rows(randn(g, M, K).bfloat16())
+    wq, ws = weights(g, groups, N, K) if groups else weights(g, N, K)
+    kw = {"offsets": torch.tensor([M * i // groups for i in range(groups + 1)], dtype=torch.int32, device="cuda")} if groups else {}
+    rows = torch.rand(M, 2 * kb + 3, generator=g, device="cuda") + 0.5
+    for scale in (rows[:, :kb], rows[:, 1:2 * kb + 1:2], rows[:, :1].expand(M, kb), rows[:1, :kb].expand(M, kb), rows[0, 0].expand(M, kb),
+                  rows[:, :kb].t().contiguous().t()):
+        got = R.reshard_matmul_fp8(q, scale, wq, ws, out_dtype=torch.float32, **kw)
+        copy = torch.empty_strided((M, kb), (1, M), device="cuda").copy_(scale)       # as the quantization stores them
+        assert torch.equal(got, R.reshard_matmul_fp8(q, copy, wq, ws, out_dtype=torch.float32, **kw))
+        a, w = X.dequantize(X.values(q), scale.contiguous(), 1), X.dequantize(X.values(wq), ws, 128)
+        for e in range(groups or 1):
+            r = slice(M * e // groups, M * (e + 1) // groups) if groups else slice(None)
+            we = w[e] if groups else w
+            tol = (min(K, 128) + 3 * kb) * 2.0 ** -23 * (a[r].abs() @ we.abs().t()) + 2.0 ** -24 * (a[r] @ we.t()).abs()
+            assert bool(((got[r].to(F64) - a[r] @ we.t()).abs() <= tol).all())
