@@ -1079,7 +1079,8 @@ int enqueue_wide(const Product &p, Args a, int sms, cudaStream_t stream) {
   int rc = encode(&ma, p.a, p.k, p.m, p.a_stride, 0, 0, kWideM);
   if (!rc) rc = encode(&mw, p.w, p.k, Gated ? 2 * p.n : p.n, p.w_stride, p.groups, p.w_batch, Gated ? 64 : 128);
   const int64_t es = Gated ? 1 : element_bytes(p.out_dtype), pitch = p.out_stride * es;
-  a.boxed = Gated || ((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)pitch) & 15) == 0;
+  // a box's column is a 32-bit number of bytes: rows of 2^31 and more are written without
+  a.boxed = Gated || (((reinterpret_cast<uintptr_t>(p.out) | (uintptr_t)pitch) & 15) == 0 && p.n * es <= INT32_MAX);
   if (!rc && a.boxed) rc = encode(&mo, p.out, p.n * es, p.m, pitch, 0, 0, 32, Wide<Gated>::kBox);
   if (!rc) rc = allow_smem<&reshard_product_wide_kernel<Gated>>(Wide<Gated>::kSmem, kWideRegs);
   if (rc) return rc;

@@ -102,3 +102,31 @@ def test_product_scales_of_any_strides(M, groups, K):
             we = w[e] if groups else w
             tol = (min(K, 128) + 3 * kb) * 2.0 ** -23 * (a[r].abs() @ we.abs().t()) + 2.0 ** -24 * (a[r] @ we.t()).abs()
             assert bool(((got[r].to(F64) - a[r] @ we.t()).abs() <= tol).all())
+
+
+# --------------------------------------------------------------------------------------------------- rows of 2^31 bytes
+
+def test_product_columns_beyond_2_31_bytes():
+    """fp32 rows of 2^29 + 300 columns, whole quarters of a tile's rows: the first, the last and those around byte 2^31 are written."""
+    N, K, M = 2 ** 29 + 300, 16, 32
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 100 * 2 ** 30:
+        pytest.skip("needs 100 GiB of device memory")
+    g = gen(29)
+    q, s = R.reshard_quantize_rows(randn(g, M, K).bfloat16())
+    w = torch.zeros(1, N, K, dtype=torch.uint8, device="cuda")
+    ws = torch.ones(1, -(-N // 128), 1, device="cuda")
+    at = [0, 2 ** 28, 2 ** 29 - 256, N - 300]
+    for c in at:
+        w[0, c:c + 300] = (randn(g, 300, K) * 100).to(torch.float8_e4m3fn).view(torch.uint8)
+    out = torch.empty(M, -(-N // 4) * 4, device="cuda")[:, :N]
+    for c in at:
+        out[:, c:c + 300] = float("nan")
+    R.reshard_matmul_fp8(q, s, w, ws, offsets=torch.tensor([0, M], dtype=torch.int32, device="cuda"), out=out)
+    a = X.dequantize(X.values(q), s, 1)
+    for c in at:
+        v = X.values(w[0, c:c + 300])
+        tol = (K + 3) * 2.0 ** -23 * (a.abs() @ v.abs().t()) + 2.0 ** -24 * (a @ v.t()).abs()
+        assert bool(((out[:, c:c + 300].to(F64) - a @ v.t()).abs() <= tol).all()), c
+    del out, w, ws
+    torch.cuda.empty_cache()
