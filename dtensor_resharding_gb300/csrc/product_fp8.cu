@@ -66,13 +66,29 @@ __device__ __forceinline__ int source_row(const Args &p, int r) {
 
 __device__ __forceinline__ float silu_times(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
+// Offsets that descend are raised to the largest before them, so that no row is of two groups and the tiles are as many as
+// the host counted at most. One warp.
+__device__ __forceinline__ void ascending(int *off, int groups, int lane) {
+  int most = 0;
+  for (int g0 = 0; g0 <= groups; g0 += 32) {
+    int v = g0 + lane <= groups ? off[g0 + lane] : 0;
+    for (int o = 1; o < 32; o <<= 1) v = max(v, __shfl_up_sync(kFull, v, o));
+    v = max(v, most);
+    if (g0 + lane <= groups) off[g0 + lane] = v;
+    most = __shfl_sync(kFull, v, 31);
+  }
+  __syncwarp();
+}
+
 // tiles[g] = tiles of M rows before group g. One warp.
 template <int M>
-__device__ __forceinline__ void row_tiles(const int *off, int *tiles, int groups, int lane) {
-  int base = 0;
+__device__ __forceinline__ void row_tiles(int *off, int *tiles, int groups, int lane) {
+  int base = 0, down = 0;
+  for (int g = lane; g < groups; g += 32) down |= off[g + 1] - off[g];
+  if (__any_sync(kFull, down < 0)) ascending(off, groups, lane);
   for (int g0 = 0; g0 < groups; g0 += 32) {
     const int g = g0 + lane;
-    const int own = g < groups ? max(0, off[g + 1] - off[g] + M - 1) / M : 0;
+    const int own = g < groups ? (off[g + 1] - off[g] + M - 1) / M : 0;
     int sum = own;
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(kFull, sum, o);

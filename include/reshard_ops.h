@@ -86,7 +86,8 @@ int reshard_quantize_blocks(const void *w, int dtype, int64_t batch, int64_t row
 /*
  * reshard_matmul_fp8 -- out[m, n] = sum over blocks b of a_scale[m, b] w_scale[n / 128, b] (sum over k in b of
  * a[m, k] w[n, k]): a [m, k] quantized by rows, w [groups, n, k] by blocks.
- * offsets NULL: groups must be 1. Otherwise offsets [groups + 1] int32 on the device, ascending from 0 to at most m: rows
+ * offsets NULL: groups must be 1. Otherwise offsets [groups + 1] int32 on the device, ascending from 0 to at most m (one that is not
+ * counts as the nearest that is: within 0 .. m and not below those before it): rows
  * offsets[g] .. offsets[g + 1] - 1 meet w[g]; rows from offsets[groups] on are not written.
  * a_scale's strides are 0 where it is broadcast (one scale a row, or one in all).
  * a, w: 16-byte aligned, row strides (and w's batch stride) multiples of 16. out [m, n] BF16, F16 or F32.

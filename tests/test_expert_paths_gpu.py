@@ -130,3 +130,28 @@ def test_product_columns_beyond_2_31_bytes():
         assert bool(((out[:, c:c + 300].to(F64) - a @ v.t()).abs() <= tol).all()), c
     del out, w, ws
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------------------------------ offsets that are not ascending
+
+@pytest.mark.parametrize("offsets", [[0, 40, 10, 40], [0, 30, 5, 20, 35, 12, 40], [40, 0, 40], [-3, 25, 90, 7, 31], [0] + [33, 1] * 80 + [40]])
+@pytest.mark.parametrize("K", [256, 2048])
+@pytest.mark.parametrize("times", [1, 20])
+def test_grouped_product_of_descending_offsets(offsets, K, times):
+    """Offsets below one before them count as that one: no row is of two groups, and a repeated call gives the same."""
+    g = gen(len(offsets) + K)
+    E, M, N = len(offsets) - 1, 40 * times, 130
+    q, s = R.reshard_quantize_rows(randn(g, M, K).bfloat16())
+    wq, ws = weights(g, E, N, K)
+    given = torch.tensor(offsets, dtype=torch.int32, device="cuda") * times
+    raised = given.clamp(0, M).cummax(0).values.int()
+    out = torch.full((M, N), 7.0, device="cuda")
+    R.reshard_matmul_fp8(q, s, wq, ws, offsets=given, out=out)
+    want = torch.full((M, N), 7.0, device="cuda")
+    R.reshard_matmul_fp8(q, s, wq, ws, offsets=raised, out=want)
+    assert torch.equal(out, want)
+    a, w = X.dequantize(X.values(q), s, 1), X.dequantize(X.values(wq), ws, 128)
+    for e in range(E):
+        r = slice(int(raised[e]), int(raised[e + 1]))
+        tol = (128 + 3 * (K // 128)) * 2.0 ** -23 * (a[r].abs() @ w[e].abs().t()) + 2.0 ** -24 * (a[r] @ w[e].t()).abs()
+        assert bool(((out[r].to(F64) - a[r] @ w[e].t()).abs() <= tol).all())
