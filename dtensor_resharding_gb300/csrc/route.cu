@@ -13,6 +13,7 @@
 // rounds), not by HBM, for the usual 128 to 256 experts: 16,384 x 256 fp32 in 8 groups, 8 chosen, takes 19.7 us, where the
 // read alone would take 2.6; 24 x 128 takes 3.4, a launch.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 
 #include "ops_common.cuh"
@@ -95,7 +96,7 @@ __device__ __forceinline__ float row_max(const float (&z)[V]) {
 }
 
 __device__ __forceinline__ uint32_t group_key(uint32_t best, uint32_t next) {
-  return next ? order_key(__fadd_rn(key_value(best), key_value(next))) : best;
+  return next ? order_key(fmaxf(__fadd_rn(key_value(best), key_value(next)), -FLT_MAX)) : best;      // biases of the lowest value: not -inf
 }
 
 // Bit g: group g is one of the `kept` best; total: lane g's group's key (0: nothing to choose).

@@ -155,3 +155,22 @@ def test_grouped_product_of_descending_offsets(offsets, K, times):
         r = slice(int(raised[e]), int(raised[e + 1]))
         tol = (128 + 3 * (K // 128)) * 2.0 ** -23 * (a[r].abs() @ w[e].abs().t()) + 2.0 ** -24 * (a[r] @ w[e].t()).abs()
         assert bool(((out[r].to(F64) - a[r] @ w[e].t()).abs() <= tol).all())
+
+
+# ------------------------------------------------------------------------------------ experts switched off by their bias
+
+@pytest.mark.parametrize("E,groups,kept,k", [(32, 4, 2, 12), (256, 32, 6, 32), (60, 4, 3, 20)])
+@pytest.mark.parametrize("top", [1, 2])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_bias_of_the_lowest_value(E, groups, kept, k, top, score):
+    """Biases of fp32's lowest value put experts behind all others and switch no group off: a sum of two of them is below
+    every fp32 number, and its group still comes before none."""
+    size = E // groups
+    z = torch.arange(E, device="cuda").float()[torch.randperm(E, generator=gen(E), device="cuda")][None].repeat(3, 1) * (4.0 / E)
+    bias = torch.full((E,), torch.finfo(torch.float32).min, device="cuda")
+    bias[size:2 * size] = 0.0
+    for renormalize in (True, False):
+        w, ids = R.reshard_route(z, k, score=score, bias=bias, groups=groups, groups_kept=kept, group_top=top, renormalize=renormalize)
+        ww, want = X.route(z, k, score=score, bias=bias, groups=groups, groups_kept=kept, group_top=top, renormalize=renormalize)
+        assert bool((want >= 0).all()) and torch.equal(ids.cpu().long(), want)
+        assert bool(((w.cpu().to(F64) - ww).abs() <= 64 * 2.0 ** -24 * ww.abs() + 1e-38).all())
