@@ -9,6 +9,10 @@ Argument marshalling only, as in ``binding``: the checks on values are the libra
 Outputs are allocated unless given (``out``). Work is enqueued on ``stream`` (a cudaStream_t as int, or a
 ``torch.cuda.Stream``; the current stream if None) and is asynchronous. What a call allocates belongs to that stream; an
 input made on another stream must be ready there (an event), as for any torch operation.
+
+Gradients: ``reshard_route``'s weights carry the gradient to its logits (``reshard_route_backward``). ``reshard_linear_fp8`` and
+``reshard_experts_fp8`` have none: of an input that requires one, their result raises when a gradient is asked of it. Codes and
+scales (the quantizations, ``reshard_matmul_fp8`` over them) carry none.
 """
 from __future__ import annotations
 
@@ -19,7 +23,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from .binding import LIB, ReshardError, RESHARD_ERR_INVALID_ARG, _check, reshard_last_error
+from .binding import LIB, ReshardError, RESHARD_ERR_INVALID_ARG, RESHARD_ERR_UNSUPPORTED, _check, reshard_last_error
 
 RESHARD_SCORE_SOFTMAX = 0
 RESHARD_SCORE_SIGMOID = 1
@@ -162,12 +166,15 @@ def reshard_route(logits: torch.Tensor, k: int, *, score="softmax", bias: Option
     Experts are ordered by score (softmax or sigmoid of the logits) + ``bias``, the lowest index first among equals; with
     ``groups`` only the ``groups_kept`` groups whose ``group_top`` best experts have the largest sum take part. The weights are
     the chosen scores without the bias, divided by their sum if ``renormalize``, times ``scale``. A logit of -inf or NaN
-    is never chosen: missing choices have id -1 and weight 0."""
+    is never chosen: missing choices have id -1 and weight 0. The weights are differentiable in the logits, the choice and
+    the bias that makes it are not."""
     here = _here(logits, stream)
     if here is None:
         with _on(logits, stream):
             return reshard_route(logits, k, score=score, bias=bias, groups=groups, groups_kept=groups_kept, group_top=group_top,
                                  renormalize=renormalize, scale=scale)
+    if logits.requires_grad and torch.is_grad_enabled():
+        return _Route.apply(logits, k, score, bias, groups, groups_kept, group_top, renormalize, scale)
     T, E, step = _matrix(logits, "logits")
     code = _code(logits, "logits")
     at_bias = 0 if bias is None else _dense(bias, "bias", torch.float32, (E,), logits)
@@ -177,6 +184,36 @@ def reshard_route(logits: torch.Tensor, k: int, *, score="softmax", bias: Option
     _call(0, _ROUTE(logits.data_ptr(), code, T, E, step, at_bias, _score(score), groups, groups_kept, group_top, k,
                     renormalize, scale, weights.data_ptr(), ids.data_ptr(), here))
     return weights, ids
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, k, score, bias, groups, groups_kept, group_top, renormalize, scale):
+        weights, ids = reshard_route(logits.detach(), k, score=score, bias=bias, groups=groups, groups_kept=groups_kept,
+                                     group_top=group_top, renormalize=renormalize, scale=scale)
+        ctx.save_for_backward(logits, ids)
+        ctx.how = dict(score=score, renormalize=renormalize, scale=scale)
+        ctx.mark_non_differentiable(ids)
+        return weights, ids
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad_weights, _):
+        logits, ids = ctx.saved_tensors
+        return (reshard_route_backward(grad_weights, logits, ids, **ctx.how), *[None] * 8)
+
+
+class _Undifferentiable(torch.autograd.Function):
+    """A call's result that depends on inputs that require a gradient, where the call has none."""
+
+    @staticmethod
+    def forward(ctx, name, out, *inputs):
+        ctx.name = name
+        return out.view_as(out)
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise ReshardError(RESHARD_ERR_UNSUPPORTED, f"{ctx.name} has no gradient: call it under torch.no_grad(), or detach its inputs")
 
 
 def reshard_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, *, score="softmax",
@@ -327,6 +364,8 @@ def reshard_linear_fp8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, 
     space = torch.empty(need, dtype=torch.uint8, device=x.device) if need else None
     _call(6, _LINEAR_FP8(x.data_ptr(), code, M, K, step, at_w, pitch, at_ws, N, out.data_ptr(), to_step,
                          space.data_ptr() if need else 0, need, here))
+    if x.requires_grad and torch.is_grad_enabled():
+        return _Undifferentiable.apply("reshard_linear_fp8", out, x)
     return out
 
 
@@ -358,6 +397,8 @@ def reshard_experts_fp8(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tenso
     space = torch.empty(need, dtype=torch.uint8, device=x.device)
     _call(7, _EXPERTS_FP8(x.data_ptr(), code, T, H, step, at_ids, at_weights, k, first_expert, E, I, at_w13, batch13, pitch13,
                           at_s13, at_w2, batch2, pitch2, at_s2, out.data_ptr(), to_step, space.data_ptr(), need, here))
+    if (x.requires_grad or weights.requires_grad) and torch.is_grad_enabled():
+        return _Undifferentiable.apply("reshard_experts_fp8", out, x, weights)
     return out
 
 

@@ -174,3 +174,67 @@ def test_route_bias_of_the_lowest_value(E, groups, kept, k, top, score):
         ww, want = X.route(z, k, score=score, bias=bias, groups=groups, groups_kept=kept, group_top=top, renormalize=renormalize)
         assert bool((want >= 0).all()) and torch.equal(ids.cpu().long(), want)
         assert bool(((w.cpu().to(F64) - ww).abs() <= 64 * 2.0 ** -24 * ww.abs() + 1e-38).all())
+
+
+# --------------------------------------------------------------------------------------------------------- autograd
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_route_weights_carry_their_gradient(score, renormalize, dtype):
+    """A loss of the routing weights reaches the logits and what made them, as reshard_route_backward gives it."""
+    g = gen(21)
+    x, router = randn(g, 37, 64).to(DT[dtype]), randn(g, 64, 24).to(DT[dtype]).requires_grad_()
+    logits = x @ router
+    logits.retain_grad()
+    grad = randn(g, 37, 4)
+    w, ids = R.reshard_route(logits, 4, score=score, renormalize=renormalize, scale=2.5)
+    plain, plain_ids = R.reshard_route(logits.detach(), 4, score=score, renormalize=renormalize, scale=2.5)
+    assert torch.equal(w, plain) and torch.equal(ids, plain_ids) and w.requires_grad and not ids.requires_grad and not plain.requires_grad
+    (w * grad).sum().backward()
+    want = R.reshard_route_backward(grad, logits.detach(), ids, score=score, renormalize=renormalize, scale=2.5)
+    assert torch.equal(logits.grad, want)
+    assert torch.equal(router.grad, x.t() @ want)
+    with torch.no_grad():
+        assert not R.reshard_route(logits, 4)[0].requires_grad
+
+
+def test_route_gradient_of_groups_bias_streams_and_broadcasts():
+    g = gen(22)
+    z, bias = randn(g, 9, 32), randn(g, 32) * 0.1
+    kw = dict(score="sigmoid", bias=bias, groups=4, groups_kept=2, group_top=2, renormalize=True, scale=1.5)
+    a = z.clone().requires_grad_()
+    w, ids = R.reshard_route(a, 5, **kw)
+    (w[:, :1].expand(9, 5) * 2.0).sum().backward()
+    grad = torch.zeros(9, 5, device="cuda")
+    grad[:, 0] = 10.0
+    assert torch.equal(a.grad, R.reshard_route_backward(grad, z, ids, score="sigmoid", scale=1.5))
+    side, b = torch.cuda.Stream(), z.clone().requires_grad_()
+    side.wait_stream(torch.cuda.current_stream())
+    w2, ids2 = R.reshard_route(b, 5, stream=side, **kw)
+    torch.cuda.current_stream().wait_stream(side)
+    w2[:, 0].sum().backward()
+    torch.cuda.synchronize()
+    grad[:, 0] = 1.0
+    assert torch.equal(ids, ids2) and torch.equal(b.grad, R.reshard_route_backward(grad, z, ids, score="sigmoid", scale=1.5))
+
+
+def test_gradients_that_do_not_exist_are_refused():
+    g = gen(23)
+    x = randn(g, 6, 256).bfloat16().requires_grad_()
+    w13, s13 = weights(g, 4, 256, 256)
+    w2, s2 = weights(g, 4, 256, 128)
+    y = R.reshard_linear_fp8(x, w13[0], s13[0])
+    assert torch.equal(y.detach(), R.reshard_linear_fp8(x.detach(), w13[0], s13[0]))
+    with pytest.raises(R.ReshardError, match="no gradient") as e:
+        y.sum().backward()
+    assert e.value.code == R.RESHARD_ERR_UNSUPPORTED
+    z = randn(g, 6, 4).requires_grad_()
+    for xs, zs in ((x.detach(), z), (x, z.detach())):
+        shares, ids = R.reshard_route(zs, 2)
+        y = R.reshard_experts_fp8(xs, ids, shares, w13, s13, w2, s2)
+        assert torch.equal(y.detach(), R.reshard_experts_fp8(x.detach(), ids, shares.detach(), w13, s13, w2, s2))
+        with pytest.raises(R.ReshardError, match="no gradient"):
+            y.float().sum().backward()
+    with torch.no_grad():
+        assert not R.reshard_linear_fp8(x, w13[0], s13[0]).requires_grad
