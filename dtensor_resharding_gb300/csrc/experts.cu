@@ -63,7 +63,7 @@ void check_weight(Checks &c, const void *w, int64_t batch, int64_t batch_stride,
   c.invalid(stride < cols, "a weight row stride is shorter than the row");
   c.unsupported(stride % 16 != 0, "a weight row stride is not a multiple of 16 bytes (lay the rows out with a padded pitch)");
   if (batch > 1) {
-    c.invalid(batch_stride < (rows - 1) * stride + cols, "weight matrices overlap");
+    c.unsupported(batch_stride < (rows - 1) * stride + cols, "weight matrices interleave or overlap (lay them out one after another)");
     c.unsupported(batch_stride % 16 != 0, "a weight batch stride is not a multiple of 16 bytes");
   }
 }

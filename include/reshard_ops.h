@@ -90,7 +90,7 @@ int reshard_quantize_blocks(const void *w, int dtype, int64_t batch, int64_t row
  * counts as the nearest that is: within 0 .. m and not below those before it): rows
  * offsets[g] .. offsets[g + 1] - 1 meet w[g]; rows from offsets[groups] on are not written.
  * a_scale's strides are 0 where it is broadcast (one scale a row, or one in all).
- * a, w: 16-byte aligned, row strides (and w's batch stride) multiples of 16. out [m, n] BF16, F16 or F32.
+ * a, w: 16-byte aligned, row strides (and w's batch stride) multiples of 16, w's matrices one after another. out [m, n] BF16, F16 or F32.
  * Each 128-block's products are summed by the tensor cores in fp32 and scaled and added in fp32 registers.
  * A gradient to the rows is the same product with w transposed (its blocks transpose with it).
  */

@@ -47,3 +47,13 @@ def test_matmul_takes_broadcast_scales_and_no_negative_strides():
         assert call(row, block) == B.RESHARD_ERR_INVALID_ARG and "stride" not in R.reshard_last_error()      # only the missing buffers
     for row, block in ((-1, 1), (1, -1)):
         assert call(row, block) == B.RESHARD_ERR_INVALID_ARG and "scale strides" in R.reshard_last_error()
+
+
+def test_interleaved_weight_matrices_are_named():
+    """[rows, experts, cols] seen as [experts, rows, cols]: such matrices do not overlap, and the refusal does not say so."""
+    E, N, K = 4, 128, 256
+    rc = B.LIB.reshard_matmul_fp8(None, K, None, 1, 1, None, K, E * K, None, 16, E, 8, N, K, None, 1, N, None)
+    text = R.reshard_last_error()
+    assert rc != 0 and "interleave" in text and "one after another" in text
+    rc = B.LIB.reshard_matmul_fp8(None, K, None, 1, 1, None, N * K, K, None, 16, E, 8, N, K, None, 1, N, None)
+    assert rc != 0 and "interleave" not in R.reshard_last_error()
