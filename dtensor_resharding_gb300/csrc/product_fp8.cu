@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 // -------------------------------------------------------------------------------------------------------- narrow --
 
 // Few rows a group: bound by the read of the weights, so that what counts is how much of them is on the way at any time:
-// two CTAs an SM with some 100 KB of stages each, or one with 200 where the sums need the registers. The weights sit on
+// two CTAs an SM with some 100 KB of stages each. The weights sit on
 // the tensor cores' 128 rows, and a product is as wide as the rows at hand, to 16. Where the tiles alone do not fill the
 // GPU, a cluster of CTAs splits K and adds its partial tiles through distributed shared memory, in rank order: the
 // same order on every run. 16 tokens to 8 of 128 experts of 2048 x 768 each: 41 and 24 us, 389 MB, 6.0
@@ -539,13 +539,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 constexpr int kNarrowM = 128;            // rows of w (of gate and of up, when gated)
 constexpr int kNarrowThreads = 192;      // 4 epilogue warps, the loader, the issuer
 constexpr int kMostSplit = 8;            // CTAs of a cluster that share a tile's K
+constexpr int kNarrowPerSm = 2;          // CTAs an SM
 
 template <int NT, bool Gated>
 struct Narrow {
   static constexpr int kParts = Gated ? 2 : 1;
   static constexpr int kStageBytes = (kParts * kNarrowM + NT) * kBlockK;
-  static constexpr int kPerSm = NT * kParts <= 64 ? 2 : 1;       // CTAs an SM: as many as the sums' registers allow
-  static constexpr int kStages = (kPerSm == 2 ? 107520 : 215040) / kStageBytes;
+  static_assert(NT * kParts <= 64, "sums in the registers of a thread");
+  static constexpr int kStages = 107520 / kStageBytes;
   static constexpr int kPartial = NT * kNarrowM * 4 * kParts;   // a CTA's sums, in stage memory, for the cluster
   static constexpr int kColumns = 2 * NT * kParts < 32 ? 32 : 2 * NT * kParts;
   static_assert(kStages >= 2 && kPartial <= kStages * kStageBytes, "stages");
@@ -558,7 +559,7 @@ struct Narrow {
     int off[RESHARD_MAX_GROUPS + 1], tiles[RESHARD_MAX_GROUPS + 1];   // row offsets; tiles of rows before each group
   };
   static constexpr size_t kSmem = (size_t)kStages * kStageBytes + sizeof(Shared);
-  static_assert(kSmem <= (kPerSm == 2 ? 115712 : 232448), "shared memory of a CTA");
+  static_assert(kSmem <= 115712, "shared memory of a CTA");
 };
 
 struct NarrowTile {
@@ -579,7 +580,7 @@ __device__ __forceinline__ NarrowTile narrow_tile(const int *off, const int *til
 // early: the kernel before this one on the stream wrote neither weights nor offsets nor order, and had itself waited for
 // what did: their reads need not wait for its end, and the first weights are on their way while it runs.
 template <int NT, bool Gated>
-__global__ void __launch_bounds__(kNarrowThreads, Narrow<NT, Gated>::kPerSm)
+__global__ void __launch_bounds__(kNarrowThreads, kNarrowPerSm)
     reshard_product_narrow_kernel(const __grid_constant__ CUtensorMap ma, const __grid_constant__ CUtensorMap mw, const __grid_constant__ Args p,
                                   const int split, const bool early) {
   using C = Narrow<NT, Gated>;
@@ -1123,7 +1124,7 @@ int enqueue_narrow(const Product &p, const Args &a, int sms, cudaStream_t stream
   if (rc) return rc;
   const int64_t tiles = (p.offsets ? p.m / NT + std::min<int64_t>(p.groups, p.m) : (p.m + NT - 1) / NT) * ((p.n + kNarrowM - 1) / kNarrowM);
   if (tiles > INT32_MAX) return fail(RESHARD_ERR_UNSUPPORTED, "too many tiles for one launch");
-  const int64_t places = (int64_t)sms * C::kPerSm;
+  const int64_t places = (int64_t)sms * kNarrowPerSm;
   const int split = narrow_split(tiles, places, a.kblocks);
   const unsigned grid = (unsigned)(split > 1 ? tiles * split : std::min(tiles, places));
   const cudaError_t e = launch(reshard_product_narrow_kernel<NT, Gated>, dim3(grid), kNarrowThreads, C::kSmem, split, stream, ma, mw, a, split, p.early);
@@ -1140,7 +1141,7 @@ bool few_a_group(int64_t m, int groups) { return m <= 8 * (int64_t)groups; }
 // measured: 256 x 1024 x 4096 narrow 10.7 us, wide 17.7; 300 x 300 x 14336 15.3 and 46.8; but 400 x 4096 x 4096 24.7 and 19.1,
 // 128 x 14336 x 1024 12.0 and 9.1.
 bool narrow_is_shorter(int64_t m, int64_t n, int kblocks, int sms) {
-  const int64_t tiles = (m + 63) / 64 * ((n + kNarrowM - 1) / kNarrowM), places = 2 * sms, split = narrow_split(tiles, places, kblocks);
+  const int64_t tiles = (m + 63) / 64 * ((n + kNarrowM - 1) / kNarrowM), places = (int64_t)kNarrowPerSm * sms, split = narrow_split(tiles, places, kblocks);
   const int64_t ctas = tiles * split, rounds = (ctas + places - 1) / places, share = (kblocks + split - 1) / split;
   const int64_t narrow = 7000 + share * rounds * (ctas <= sms ? 550 : 900);
   const int64_t wide_tiles = (m + kWideM - 1) / kWideM * ((n + kWideN - 1) / kWideN);
