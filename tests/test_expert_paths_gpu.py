@@ -238,3 +238,93 @@ def test_gradients_that_do_not_exist_are_refused():
             y.float().sum().backward()
     with torch.no_grad():
         assert not R.reshard_linear_fp8(x, w13[0], s13[0]).requires_grad
+
+
+# ------------------------------------------------------------------------------- the gated products' splits and many tiles
+
+def layer(g, T, E, k, H, I, local=None, dtype=torch.bfloat16):
+    n = E if local is None else local
+    x = randn(g, T, H).to(dtype)
+    w, ids = R.reshard_route(randn(g, T, E), k)
+    return (x, ids, w, *weights(g, n, 2 * I, H), *weights(g, n, H, I))
+
+
+def check_layer(args, first=0):
+    got = R.reshard_experts_fp8(*args, first_expert=first)
+    want = X.experts(*args, first=first)
+    tol = 5e-3 if got.dtype == torch.bfloat16 else 2.5e-3
+    err = got.to(F64) - want
+    assert float(err.norm()) <= tol * float(want.norm()) * (6 if len(got) < 7 else 1), float(err.norm() / want.norm())
+    assert bool((err.norm(dim=1) <= 6 * tol * want.norm(dim=1) + 1e-30).all())
+    for _ in range(3):
+        assert torch.equal(got, R.reshard_experts_fp8(*args, first_expert=first))
+    return got
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 16, 2, 1024, 256), (3, 16, 2, 1024, 256), (1, 16, 2, 2048, 256), (3, 16, 2, 2048, 256),
+                                       (3, 4, 4, 4096, 384), (1, 2, 1, 4224, 128), (9, 16, 2, 1920, 128), (30, 4, 1, 2048, 128), (1, 128, 8, 2048, 768)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_experts_gated_product_split_over_a_cluster(T, E, k, H, I, dtype):
+    """Few tiles and a long row: the gated product's K is shared by 2 to 8 CTAs (H / 512 at most), which add gate and up
+    before silu and meet for the row's amax."""
+    check_layer(layer(gen(T + H + I), T, E, k, H, I, dtype=DT[dtype]))
+
+
+@pytest.mark.parametrize("T", [1, 16, 17, 64])
+def test_experts_a_share_of_a_decode_step(T):
+    """16 of 128 experts: most choices are another rank's, and some calls have none here."""
+    x, ids, w, w13, s13, w2, s2 = layer(gen(T), T, 128, 8, 2048, 256, local=16)
+    for first in (0, 48, 112):
+        args = (x, ids, w, w13, s13, w2, s2)
+        here = bool(((ids >= first) & (ids < first + 16)).any())
+        if here:
+            check_layer(args, first)
+        else:
+            assert not R.reshard_experts_fp8(*args, first_expert=first).any()
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(100, 128, 8, 256, 1280), (2000, 16, 8, 256, 768)])
+def test_experts_many_gated_tiles_a_cta(T, E, k, H, I):
+    """Four tiles and more for each CTA of the narrow and of the wide gated product: the amax buffers, their barriers' parity
+    and the boxes on their way out are used again."""
+    check_layer(layer(gen(T), T, E, k, H, I))
+
+
+# ------------------------------------------------------------------------------------------------- the linear's types
+
+@pytest.mark.parametrize("M", [1, 3, 4, 5, 130])
+@pytest.mark.parametrize("K", [16, 300, 1000, 1024])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_linear_types_and_rows(M, K, dtype):
+    """Every type through the few-row kernel and through quantization and product, rows aligned and not."""
+    g = gen(M * K)
+    big = randn(g, M, K + 24).to(DT[dtype])
+    wq, ws = weights(g, 140, K)
+    w = X.dequantize(X.values(wq), ws, 128)
+    for off in (0, 8, 1, 3):
+        x = big[:, off:off + K]
+        got = R.reshard_linear_fp8(x, wq, ws)
+        q, s = X.quantize(x, 1)
+        a = X.dequantize(q, s, 1)
+        want = a @ w.t()
+        tol = (min(K, 128) + 3 * s.shape[1]) * 2.0 ** -23 * (a.abs() @ w.abs().t()) + torch.finfo(x.dtype).eps / 2 * want.abs() * (1 + 1e-3)
+        assert got.dtype == x.dtype and bool(((got.to(F64) - want).abs() <= tol).all())
+        assert torch.equal(got, R.reshard_linear_fp8(x.contiguous(), wq, ws))
+
+
+@pytest.mark.parametrize("M", [2, 48, 300])
+def test_linear_replayed_from_a_graph(M):
+    """A captured linear computes with what its input holds at each replay."""
+    g = gen(M)
+    x, (wq, ws) = randn(g, M, 512).bfloat16(), weights(g, 384, 512)
+    inp, side = x.clone(), torch.cuda.Stream()
+    R.reshard_linear_fp8(inp, wq, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = R.reshard_linear_fp8(inp, wq, ws)
+    for scale in (1.0, -0.5, 3.0):
+        inp.copy_(x * scale)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, R.reshard_linear_fp8(inp, wq, ws)) and float(out.float().norm()) > 0
