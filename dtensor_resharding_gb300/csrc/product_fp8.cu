@@ -1132,9 +1132,12 @@ int enqueue_narrow(const Product &p, const Args &a, int sms, cudaStream_t stream
 }
 
 // Whether a grouped product is narrow's, by the rows a group has on average, as far as the host knows them (m is an
-// upper bound). 128 experts of 2048 x 768, the whole layer: 8 rows each narrow 109 us, wide 115; 16 rows 129 and 120; 64
-// rows 307 and 138.
-bool few_a_group(int64_t m, int groups) { return m <= 8 * (int64_t)groups; }
+// upper bound). The whole layer, narrow and wide: 128 experts of 2048 x 768, 8 rows each 115 us and 129, 12 rows 119 and 133,
+// 20 rows 138 and 138, 32 rows 175 and 144; 16 experts of 4096 x 1536, 12 rows 64 and 80, 20 rows 85 and 82; 32 experts of 1024 x 512, 12
+// rows 25 and 26, 32 rows 36 and 30. Their products alone into bf16: 12 rows 41 and 46, 19 and 22, 71 and 72, 40 and 38; 16 rows 41
+// and 46, 23 and 22, 76 and 72, 46 and 38. Where ids range over more experts than are here the bound counts the others' slots, too: 16
+// of 128 experts of 4096 x 1536, 64 tokens to 8 (4 rows each) take wide's 77 us instead of 63; from 512 tokens on wide is right (84; 91).
+bool few_a_group(int64_t m, int groups) { return m <= 12 * (int64_t)groups; }
 
 // Whether a dense product of more than 64 rows is narrow's (in tiles of 64, K split) or wide's. Wide fills the GPU only from
 // 152 tiles of 128 x 256 on; below that narrow has more and shorter pieces. Both times are of this form, in ns, as

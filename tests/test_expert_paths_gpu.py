@@ -328,3 +328,25 @@ def test_linear_replayed_from_a_graph(M):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, R.reshard_linear_fp8(inp, wq, ws)) and float(out.float().norm()) > 0
+
+
+@pytest.mark.parametrize("T", [23, 24, 25, 36, 37])
+def test_experts_where_the_product_changes(T):
+    """8 experts, 2 choices, so 6 to 9 rows each, and with 4 experts 12 and 13: both sides of the choice between kernels that
+    gather tokens and kernels that read copies of them, by the same oracle."""
+    for E in (4, 8):
+        check_layer(layer(gen(T + E), T, E, 2, 1024, 384))
+
+
+@pytest.mark.parametrize("rows", [12, 13])
+def test_grouped_product_where_the_kernel_changes(rows):
+    g = gen(rows)
+    E, N, K = 16, 300, 1024
+    q, s = R.reshard_quantize_rows(randn(g, rows * E, K).bfloat16())
+    wq, ws = weights(g, E, N, K)
+    offsets = torch.arange(0, rows * E + 1, rows, dtype=torch.int32, device="cuda")
+    got = R.reshard_matmul_fp8(q, s, wq, ws, offsets=offsets, out_dtype=torch.float32).to(F64).view(E, rows, N)
+    a, w = X.dequantize(X.values(q), s, 1).view(E, rows, K), X.dequantize(X.values(wq), ws, 128)
+    want = a @ w.transpose(1, 2)
+    tol = (128 + 3 * 8) * 2.0 ** -23 * (a.abs() @ w.abs().transpose(1, 2)) + 2.0 ** -24 * want.abs()
+    assert bool(((got - want).abs() <= tol).all())
