@@ -64,6 +64,9 @@ __device__ __forceinline__ int source_row(const Args &p, int r) {
   return p.order ? min(max(p.order[r], 0) / p.per_row, p.a_rows - 1) : r;
 }
 
+// The fast exponential and division: their error (some ulp, and 1.2 |g| ulp of the exponential for negative g) is far below
+// the step of the 8-bit code that the product becomes. With expf and a rounded division the layer of 8,192 tokens takes 75 us more
+// and is as far from 64 bits (0.0129 of the norm).
 __device__ __forceinline__ float silu_times(float g, float u) { return __fdividef(g, 1.0f + __expf(-g)) * u; }
 
 // Offsets that descend are raised to the largest before them, so that no row is of two groups and the tiles are as many as
@@ -129,8 +132,8 @@ __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
 // them, and adds pairs of columns with one instruction. A block's products take 512 cycles of the tensor cores and a block
 // about 750: a half of tensor memory is handed from the products to the epilogue and back (two barriers each way and the
 // completion of the products, 400 cycles with no work in between), and there is room for two only. 8192 x 14336 x 4096
-// takes 348 us, 2.8 PFLOP/s, tensor cores 60% busy; a tile's end, 2,000 to 3,400 cycles, weighs more where K is short:
-// 65,536 rows of 128 experts, 2048 x 768 without a gate 125 us, 1.6 PFLOP/s.
+// takes 349 us, 2.8 PFLOP/s, tensor cores 60% busy; a tile's end, 2,000 to 3,400 cycles, weighs more where K is short:
+// 65,536 rows of 128 experts, 2048 x 768 without a gate 119 us into bf16, 1.7 PFLOP/s, and 150 into fp32, which the layer takes.
 // Measured and not kept: 16 epilogue warps of 64 columns each (4% slower), products of 128 columns that signal the halves
 // apart (6% slower), 32 columns a load (the same), w's blocks prefetched into L2 (15% slower), the next block's barrier
 // looked at early (1% slower), one reciprocal for two or four gates (the same).
@@ -530,11 +533,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 // -------------------------------------------------------------------------------------------------------- narrow --
 
 // Few rows a group: bound by the read of the weights, so that what counts is how much of them is on the way at any time:
-// two CTAs an SM with some 100 KB of stages each. The weights sit on
-// the tensor cores' 128 rows, and a product is as wide as the rows at hand, to 16. Where the tiles alone do not fill the
+// two CTAs an SM with some 100 KB of stages each. The weights sit on the tensor cores' 128 rows, and a product is as wide as
+// the rows at hand, to 16. Where the tiles alone do not fill the
 // GPU, a cluster of CTAs splits K and adds its partial tiles through distributed shared memory, in rank order: the
 // same order on every run. 16 tokens to 8 of 128 experts of 2048 x 768 each: 41 and 24 us, 389 MB, 6.0
-// TB/s; 77 x 2867 x 4096 with the rows' quantization before it: 11.1 us, bound by latency (launch, first loads, the
+// TB/s; 77 x 2867 x 4096 with the rows' quantization before it: 11.2 us, bound by latency (launch, first loads, the
 // cluster's sum).
 constexpr int kNarrowM = 128;            // rows of w (of gate and of up, when gated)
 constexpr int kNarrowThreads = 192;      // 4 epilogue warps, the loader, the issuer
@@ -1141,8 +1144,8 @@ bool few_a_group(int64_t m, int groups) { return m <= 12 * (int64_t)groups; }
 
 // Whether a dense product of more than 64 rows is narrow's (in tiles of 64, K split) or wide's. Wide fills the GPU only from
 // 152 tiles of 128 x 256 on; below that narrow has more and shorter pieces. Both times are of this form, in ns, as
-// measured: 256 x 1024 x 4096 narrow 10.7 us, wide 17.7; 300 x 300 x 14336 15.3 and 46.8; but 400 x 4096 x 4096 24.7 and 19.1,
-// 128 x 14336 x 1024 12.0 and 9.1.
+// measured. With the rows' quantization before them: 256 x 1024 x 4096 narrow 10.9 us, wide 17.6; 300 x 300 x 14336 14.4 and 49.0;
+// but 400 x 4096 x 4096 24.8 and 22.2, 128 x 14336 x 1024 12.2 and 10.3.
 bool narrow_is_shorter(int64_t m, int64_t n, int kblocks, int sms) {
   const int64_t tiles = (m + 63) / 64 * ((n + kNarrowM - 1) / kNarrowM), places = (int64_t)kNarrowPerSm * sms, split = narrow_split(tiles, places, kblocks);
   const int64_t ctas = tiles * split, rounds = (ctas + places - 1) / places, share = (kblocks + split - 1) / split;

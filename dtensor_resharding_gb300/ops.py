@@ -10,6 +10,9 @@ Outputs are allocated unless given (``out``). Work is enqueued on ``stream`` (a 
 ``torch.cuda.Stream``; the current stream if None) and is asynchronous. What a call allocates belongs to that stream; an
 input made on another stream must be ready there (an event), as for any torch operation.
 
+A wait inside a product kernel that gives up (it does not on a working GPU) leaves an incomplete output and a status that no call
+looks at: ``reshard_ops_status`` reads it.
+
 Gradients: ``reshard_route``'s weights carry the gradient to its logits (``reshard_route_backward``). ``reshard_linear_fp8`` and
 ``reshard_experts_fp8`` have none: of an input that requires one, their result raises when a gradient is asked of it. Codes and
 scales (the quantizations, ``reshard_matmul_fp8`` over them) carry none.

@@ -47,7 +47,8 @@ extern "C" {
  * experts have the largest sum of s + bias take part; equal sums go to the lowest group.
  * weights [tokens, k] fp32 = scale * s of the chosen (without the bias), divided by their sum where renormalize is
  * set (0 where that sum is 0); ids [tokens, k] int32, in order. A logit of -inf or NaN is never chosen and has score 0;
- * where fewer than k experts are left the id is -1 and the weight 0. A logit of +inf makes a softmax row's weights NaN.
+ * neither is an expert whose bias makes its key one of these; where fewer than k experts are left the id is -1 and the
+ * weight 0. Scores are fp32: those that round or underflow to the same number are equal. A logit of +inf makes a softmax row's weights NaN.
  */
 int reshard_route(const void *logits, int dtype, int64_t tokens, int experts, int64_t row_stride, const float *bias,
                   int score, int groups, int groups_kept, int group_top, int k, int renormalize, float scale,
@@ -117,7 +118,8 @@ int reshard_linear_fp8(const void *x, int dtype, int64_t m, int64_t k, int64_t r
  * and w2 [experts, hidden, ffn] E4M3 with block scales, 16-byte aligned, row and batch strides multiples of 16.
  * ffn must be a multiple of 128, so that no block holds gate and up rows. silu(g) * u stays in fp32 until it is quantized,
  * each expert's output until the weighted sum, which is rounded to dtype once.
- * workspace: reshard_experts_fp8_workspace(...) bytes, 256-byte aligned.
+ * workspace: reshard_experts_fp8_workspace(...) bytes, 256-byte aligned; it has room for all tokens * k choices, since how
+ * many are of this rank's experts is known on the device only.
  */
 int64_t reshard_experts_fp8_workspace(int64_t tokens, int k, int experts, int64_t hidden, int64_t ffn, int dtype);
 int reshard_experts_fp8(const void *x, int dtype, int64_t tokens, int64_t hidden, int64_t row_stride, const int32_t *ids,
