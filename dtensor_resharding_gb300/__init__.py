@@ -9,7 +9,9 @@ package loads libreshard.so and raises if it is not built.
 
 The expert layer over resharded weights (``ops``, include/reshard_ops.h) takes torch tensors: ``reshard_route`` /
 ``reshard_route_backward``, ``reshard_dispatch``, ``reshard_quantize_rows`` / ``reshard_quantize_blocks``,
-``reshard_matmul_fp8``, ``reshard_linear_fp8``, ``reshard_experts_fp8``, ``reshard_ops_status``. It is imported (and torch
+``reshard_matmul_fp8``, ``reshard_linear_fp8``, ``reshard_experts_fp8``, ``reshard_ops_status``; around it, for training,
+``reshard_permute`` / ``reshard_combine`` (tokens to their experts and back), ``reshard_embedding`` (a vocabulary's shard), their
+``_backward`` calls, and ``reshard_grad_norm`` / ``reshard_clip_grads`` over a ``reshard_tensor_list``. It is imported (and torch
 with it) at the first use of one of its names.
 """
 from .binding import (  # noqa: F401
@@ -25,7 +27,9 @@ from .binding import (  # noqa: F401
 from .workload import plan_workload, workload_pointers  # noqa: F401
 
 _OPS = ("reshard_route", "reshard_route_backward", "reshard_dispatch", "reshard_quantize_rows", "reshard_quantize_blocks",
-        "reshard_matmul_fp8", "reshard_linear_fp8", "reshard_experts_fp8", "reshard_ops_status",
+        "reshard_matmul_fp8", "reshard_linear_fp8", "reshard_experts_fp8", "reshard_permute", "reshard_permute_backward", "reshard_combine",
+        "reshard_combine_backward", "reshard_embedding", "reshard_embedding_backward", "reshard_tensor_list", "TensorList",
+        "reshard_grad_norm", "reshard_clip_grads", "reshard_ops_status",
         "RESHARD_SCORE_SOFTMAX", "RESHARD_SCORE_SIGMOID")
 
 

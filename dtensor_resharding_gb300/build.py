@@ -11,7 +11,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB_PATH = os.path.join(HERE, "libreshard.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-UNITS = ("execute", "route", "quantize", "product_fp8", "experts")   # CUDA translation units, compiled side by side
+UNITS = ("execute", "route", "quantize", "rows", "embedding", "gradients", "product_fp8", "experts")   # CUDA translation units, compiled side by side
 
 
 def _nvcc() -> str:

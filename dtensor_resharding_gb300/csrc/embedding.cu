@@ -1,0 +1,382 @@
+// The gradient of an embedding: grad_table[r] = scale * sum of grad[t] over the tokens t whose id is row r of this shard.
+//
+// Four launches. *Zero* writes the table's zeros while *sort* (one cluster) sorts the tokens by row beside it: a radix sort
+// of the pairs (row, token), at most ten bits a pass, stable, so that a row's tokens ascend. *Sum* takes runs of the sorted
+// tokens, one thread eight columns: rows that begin and end inside a run are written from there, the pieces of one
+// that does not are left in the workspace, and *join* adds them in the order of the runs. A token that is half of the
+// text is so spread over as many CTAs as it has runs, without atomics: the order of every sum follows from the ids alone.
+// Sums are fp32, rounded once. Bound by the write of the table (and the read of the gradients).
+#include <algorithm>
+
+#include "ops_common.cuh"
+#include "values.cuh"
+
+namespace reshard {
+namespace ops {
+
+namespace {
+
+constexpr int64_t kAlign = 256;
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+int launched(cudaError_t e, const char *what) { return e == cudaSuccess ? RESHARD_OK : cuda_error(e, what); }
+
+// ------------------------------------------------------------------------------------------------------------- zero --
+
+constexpr int kZeroThreads = 512;
+constexpr int64_t kZeroPiece = 16384;      // bytes a warp writes at a time
+
+// Zeros in `rows` rows of `bytes` bytes, `stride` apart, all a multiple of `unit` (2 or 4) bytes.
+__global__ void __launch_bounds__(kZeroThreads) reshard_zero_kernel(uint8_t *base, int64_t rows, int64_t bytes, int64_t stride, int unit) {
+  grid_enter();
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * (kZeroThreads / 32);
+  const int64_t pieces = (bytes + kZeroPiece - 1) / kZeroPiece;
+  for (int64_t w = (int64_t)blockIdx.x * (kZeroThreads / 32) + (threadIdx.x >> 5); w < rows * pieces; w += warps) {
+    const int64_t r = w / pieces, at = (w - r * pieces) * kZeroPiece;
+    uint8_t *p = base + r * stride + at;
+    int64_t n = min(kZeroPiece, bytes - at);
+    const int head = (int)min((int64_t)(-reinterpret_cast<uintptr_t>(p) & 15), n);
+    for (int i = lane * unit; i < head; i += 32 * unit) unit == 4 ? (void)(*reinterpret_cast<uint32_t *>(p + i) = 0) : (void)(*reinterpret_cast<uint16_t *>(p + i) = 0);
+    p += head, n -= head;
+#pragma unroll 4
+    for (int64_t i = lane; i < n / 16; i += 32) reinterpret_cast<uint4 *>(p)[i] = make_uint4(0, 0, 0, 0);
+    for (int64_t i = n / 16 * 16 + lane * unit; i < n; i += 32 * unit)
+      unit == 4 ? (void)(*reinterpret_cast<uint32_t *>(p + i) = 0) : (void)(*reinterpret_cast<uint16_t *>(p + i) = 0);
+  }
+}
+
+// ------------------------------------------------------------------------------------------------------------- sort --
+
+constexpr int kSortWarps = 16, kSortCluster = 8, kSortBits = 10;
+
+struct Sort {
+  const void *ids;
+  bool wide_ids;
+  int64_t tokens, first, rows;
+  uint2 *sorted, *other;             // (row, token) pairs; the last pass writes `sorted`
+  int32_t *held;                     // how many tokens are of this shard
+  int passes, bits;                  // bits a pass
+};
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Every warp has a run of the pairs in each pass: it counts their digits, the counts of the warps and CTAs before it give
+// its first place of each digit, and a second walk places 32 pairs at a time, equal digits ranked by lane (match.any).
+// Integer counts: the order is the same on every run. Bound by latency (two walks and three barriers a pass).
+__global__ void __launch_bounds__(kSortWarps * 32) reshard_sort_rows_kernel(Sort a) {
+  extern __shared__ int32_t count[];             // [warp][digit], then this CTA's sums [digit], then its first places [digit]
+  __shared__ int32_t warp_sum[kSortWarps];
+  const int bins = 1 << a.bits;
+  int32_t *const sum = count + kSortWarps * bins, *const base = sum + bins;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = (int)blockIdx.x;
+  int32_t *const mine = count + warp * bins;
+  int64_t n = a.tokens;
+  for (int pass = 0; pass < a.passes; ++pass) {
+    const uint2 *const from = (a.passes - pass) & 1 ? a.other : a.sorted;
+    uint2 *const to = (a.passes - pass) & 1 ? a.sorted : a.other;
+    const int64_t run = (n + kSortCluster * kSortWarps * 32 - 1) / (kSortCluster * kSortWarps * 32) * 32;
+    const int64_t lo = (cta * kSortWarps + warp) * run, hi = min(lo + run, n);
+    auto pair = [&](int64_t i) {                 // row 2^32 - 1: none
+      uint2 p = make_uint2(~0u, 0);
+      if (i < hi) {
+        if (pass == 0) {
+          const int64_t id = a.wide_ids ? __ldg(static_cast<const long long *>(a.ids) + i) : __ldg(static_cast<const int32_t *>(a.ids) + i);
+          if (id >= a.first && id - a.first < a.rows) p = make_uint2((uint32_t)(id - a.first), (uint32_t)i);
+        } else {
+          p = __ldcg(from + i);
+        }
+      }
+      return p;
+    };
+    const int shift = pass * a.bits;
+    for (int i = tid; i < kSortWarps * bins; i += kSortWarps * 32) count[i] = 0;
+    __syncthreads();
+    for (int64_t i0 = lo + lane; i0 < hi; i0 += 4 * 32) {
+      uint2 p[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) p[u] = pair(i0 + 32 * u);
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (p[u].x != ~0u) atomicAdd(&mine[p[u].x >> shift & (bins - 1)], 1);
+    }
+    __syncthreads();
+    for (int d = tid; d < bins; d += kSortWarps * 32) {
+      int s = 0;
+#pragma unroll
+      for (int w = 0; w < kSortWarps; ++w) {
+        const int c = count[w * bins + d];
+        count[w * bins + d] = s;
+        s += c;
+      }
+      sum[d] = s;
+    }
+    cluster_barrier();
+    // the digits' first places: a running sum of the cluster's counts, and this CTA's share of each
+    int done = 0;
+    for (int d0 = 0; d0 < bins; d0 += kSortWarps * 32) {
+      const int d = d0 + tid;
+      int all = 0, before = 0;
+      if (d < bins) {
+#pragma unroll
+        for (int c = 0; c < kSortCluster; ++c) {
+          uint32_t at;
+          int v;
+          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(&sum[d])), "r"(c));
+          asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at));
+          if (c < cta) before += v;
+          all += v;
+        }
+      }
+      int upto = all;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(kFull, upto, o);
+        if (lane >= o) upto += x;
+      }
+      __syncthreads();                           // the round before has read warp_sum
+      if (lane == 31) warp_sum[warp] = upto;
+      __syncthreads();
+      int here = 0;
+      for (int w = 0; w < kSortWarps; ++w) {
+        if (w < warp) upto += warp_sum[w];
+        here += warp_sum[w];
+      }
+      if (d < bins) base[d] = done + upto - all + before;
+      done += here;
+    }
+    __syncthreads();
+    for (int64_t i0 = lo; i0 < hi; i0 += 4 * 32) {
+      uint2 p[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) p[u] = pair(i0 + 32 * u + lane);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool in = p[u].x != ~0u;
+        const int d = in ? (int)(p[u].x >> shift & (bins - 1)) : bins;
+        const uint32_t same = __match_any_sync(kFull, d);
+        if (in) to[base[d] + mine[d] + __popc(same & ((1u << lane) - 1))] = p[u];
+        __syncwarp();
+        if (in && (same >> lane) == 1) mine[d] += __popc(same);      // the last of each digit's lanes
+        __syncwarp();
+      }
+    }
+    n = done;
+    cluster_barrier();                           // the pairs are in place, and nobody reads `sum` any more
+  }
+  if (cta == 0 && tid == 0) *a.held = (int32_t)n;
+  // The grid before (the zeros) may still be running: this one began when all of its CTAs had, behind everything that
+  // came earlier on the stream. The grid behind this one has to find both done.
+  grid_wait();
+}
+
+// -------------------------------------------------------------------------------------------------------------- sum --
+
+constexpr int kSumThreads = 128;
+constexpr int kJoinThreads = 256;
+
+struct Sum {
+  const uint2 *sorted;
+  const int32_t *held;
+  const void *grad;
+  int64_t cols, grad_stride;
+  float scale;
+  void *table;
+  int64_t table_stride;
+  bool accumulate, wide, wide_table;
+  float *part;                       // [run][2][pitch]: of the row that a run begins inside, and of the one that it ends inside
+  int64_t pitch;
+  int run;                           // sorted tokens of a CTA
+  int slices;                        // CTAs a run
+};
+
+// Eight of a row's sums, scaled, into the table (its other values are another thread's).
+template <typename T>
+__device__ __forceinline__ void write_sums(const Sum &a, uint32_t row, int64_t c, const float (&sum)[8]) {
+  T *const to = static_cast<T *>(a.table) + (int64_t)row * a.table_stride + c;
+  float x[8];
+  const bool whole = a.wide_table && c + 8 <= a.cols;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = sum[e] * a.scale;
+  if (a.accumulate) {
+    float old[8];
+    load_values<T, 8>(to, (int)min((int64_t)8, a.cols - c), whole, old);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] += old[e];
+  }
+  if (whole) {
+    store_eight(to, x);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e < a.cols) to[e] = from_f32<T>(x[e]);
+  }
+}
+
+template <typename TG, typename T, bool Wide>
+__global__ void __launch_bounds__(kSumThreads) reshard_sum_rows_kernel(Sum a) {
+  grid_enter();
+  const int64_t run = blockIdx.x / (uint32_t)a.slices;
+  const int64_t c = ((int64_t)(blockIdx.x % (uint32_t)a.slices) * kSumThreads + threadIdx.x) * 8;
+  const int64_t held = *a.held, lo = run * a.run, hi = min(lo + a.run, held);
+  if (lo >= held || c >= a.cols) return;
+  const TG *const grad = static_cast<const TG *>(a.grad) + c;
+  const int left = (int)min((int64_t)8, a.cols - c);
+  uint32_t row = a.sorted[lo].x;
+  bool head = lo > 0 && a.sorted[lo - 1].x == row;
+  float *const part = a.part + 2 * run * a.pitch + c;
+  float sum[8] = {};
+  auto keep = [&](float *to) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) *reinterpret_cast<float4 *>(to + e) = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
+  };
+  constexpr int kRows = sizeof(TG) == 4 ? 4 : 8;       // rows in flight
+  for (int64_t i = lo; i < hi; i += kRows) {
+    uint2 p[kRows];
+    Eight<TG, Wide> v[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) p[u] = i + u < hi ? __ldg(a.sorted + i + u) : make_uint2(~0u, 0);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+      if (left == 8 && i + u < hi) v[u].ask(grad + p[u].y * a.grad_stride);
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+      if (i + u >= hi) break;
+      if (p[u].x != row) {
+        if (head) keep(part);
+        else write_sums<T>(a, row, c, sum);
+        head = false, row = p[u].x;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+      }
+      const TG *const from = grad + p[u].y * a.grad_stride;
+      float x[8];
+      if (left == 8) v[u].take(from, x);
+      else load_values<TG, 8>(from, left, false, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += x[e];
+    }
+  }
+  if (head) keep(part);
+  else if (hi < held && a.sorted[hi].x == row) keep(part + a.pitch);
+  else write_sums<T>(a, row, c, sum);
+}
+
+// The rows that end in another run than they begin in: one CTA each run that such a row begins in.
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads) reshard_join_rows_kernel(Sum a) {
+  grid_enter();
+  const int64_t run = blockIdx.x, held = *a.held, lo = run * a.run, hi = lo + a.run;
+  if (hi >= held) return;
+  const uint32_t row = a.sorted[hi - 1].x;
+  if (a.sorted[hi].x != row || (lo > 0 && a.sorted[lo - 1].x == row)) return;
+  int64_t in = hi, out = held;                   // the last of the row's tokens is sorted[in]
+  while (out - in > 1) {
+    const int64_t mid = (in + out) / 2;
+    if (a.sorted[mid].x == row) in = mid;
+    else out = mid;
+  }
+  const int64_t last = in / a.run;
+  for (int64_t c = threadIdx.x * 8; c < a.cols; c += kJoinThreads * 8) {
+    float sum[8];
+    load_values<float, 8>(a.part + (2 * run + 1) * a.pitch + c, 8, true, sum);
+#pragma unroll 4
+    for (int64_t r = run + 1; r <= last; ++r) {
+      float x[8];
+      load_values<float, 8>(a.part + 2 * r * a.pitch + c, 8, true, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += x[e];
+    }
+    write_sums<T>(a, row, c, sum);
+  }
+}
+
+// Sorted tokens of a CTA: few, so that a row's tokens are read by many CTAs, but at most 2,048 runs, whose pieces of rows
+// (two each) the workspace holds.
+int64_t run_of(int64_t tokens) { return std::max<int64_t>(16, (tokens + 2047) / 2048); }
+
+struct Layout {
+  int64_t sorted, held, runs, pitch, part;
+  Layout(int64_t tokens, int64_t cols)
+      : sorted(up(8 * tokens, kAlign)), held(kAlign), runs((tokens + run_of(tokens) - 1) / run_of(tokens)), pitch(up(cols, 8)),
+        part(up(2 * runs * pitch * 4, kAlign)) {}
+  int64_t bytes() const { return 2 * sorted + held + part; }
+};
+
+}  // namespace
+}  // namespace ops
+}  // namespace reshard
+
+using namespace reshard;
+using namespace reshard::ops;
+
+extern "C" int64_t reshard_embedding_backward_workspace(int64_t tokens, int64_t cols) {
+  if (tokens < 1 || cols < 1 || tokens > RESHARD_MAX_SLOTS || cols > RESHARD_MAX_EXTENT) return 0;
+  return Layout(tokens, cols).bytes();
+}
+
+extern "C" int reshard_embedding_backward(const void *grad, int grad_dtype, int64_t tokens, int64_t cols, int64_t grad_stride,
+                                          const void *ids, int id_bits, int64_t first_row, int64_t rows, float scale, void *grad_table,
+                                          int table_dtype, int64_t table_stride, int accumulate, void *workspace, int64_t workspace_bytes,
+                                          reshard_stream_t stream_) try {
+  Checks c("reshard_embedding_backward");
+  c.invalid(tokens < 0 || rows < 0 || cols < 0 || first_row < 0, "tokens, rows, cols and first_row must be >= 0");
+  c.unsupported(tokens > RESHARD_MAX_SLOTS || rows > RESHARD_MAX_EXTENT || cols > RESHARD_MAX_EXTENT, "tokens, rows or cols above 2^30");
+  c.invalid(id_bits != 32 && id_bits != 64, "id_bits must be 32 or 64");
+  c.invalid(!element_bytes(grad_dtype) || !element_bytes(table_dtype), "grad_dtype and table_dtype must be BF16, F16 or F32");
+  c.invalid(grad_stride < cols || table_stride < cols, "a row stride is shorter than the row");
+  if (c.ok() && tokens > 0)
+    c.unsupported(Layout(tokens, cols).runs * ((cols + kSumThreads * 8 - 1) / (kSumThreads * 8)) > INT32_MAX, "too many columns for one launch");
+  const bool work = rows > 0 && cols > 0 && (tokens > 0 || !accumulate);
+  if (work && c.ok()) {
+    c.pointer(grad_table, "grad_table", (uintptr_t)element_bytes(table_dtype));
+    if (tokens > 0) {
+      c.pointer(grad, "grad", (uintptr_t)element_bytes(grad_dtype));
+      c.pointer(ids, "ids", (uintptr_t)(id_bits / 8));
+      c.pointer(workspace, "workspace", kAlign);
+      c.invalid(workspace_bytes < reshard_embedding_backward_workspace(tokens, cols), "the workspace is smaller than reshard_embedding_backward_workspace");
+    }
+  }
+  if (!c.ok()) return c.report();
+  if (!work) return RESHARD_OK;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  const int es = element_bytes(table_dtype);
+  int sms = 0, rc = device_sms(&sms);
+  if (rc) return rc;
+  // Without zeros to write the same kernel, with no rows, stands before the sort: what the sort begins behind.
+  const bool dense = table_stride == cols;
+  const int64_t zero_rows = accumulate ? 0 : dense ? 1 : rows, zero_bytes = (dense ? rows : 1) * cols * es;
+  if ((rc = launched(launch(reshard_zero_kernel, dim3(accumulate ? 1u : (unsigned)sms), kZeroThreads, 0, 1, stream, static_cast<uint8_t *>(grad_table),
+                            zero_rows, zero_bytes, table_stride * es, es), "launching reshard_zero_kernel")))
+    return rc;
+  if (tokens == 0) return RESHARD_OK;
+  const Layout l(tokens, cols);
+  uint8_t *const at = static_cast<uint8_t *>(workspace);
+  Sort s{ids, id_bits == 64, tokens, first_row, rows, reinterpret_cast<uint2 *>(at), reinterpret_cast<uint2 *>(at + l.sorted),
+         reinterpret_cast<int32_t *>(at + 2 * l.sorted), 1, 1};
+  int need = 1;
+  while (need < 30 && (rows - 1) >> need) ++need;
+  s.passes = (need + kSortBits - 1) / kSortBits;
+  s.bits = (need + s.passes - 1) / s.passes;
+  const size_t smem = (size_t)(kSortWarps + 2) * 4 << s.bits;
+  if ((rc = allow_smem<reshard_sort_rows_kernel>((size_t)(kSortWarps + 2) * 4 << kSortBits))) return rc;
+  if ((rc = launched(launch(reshard_sort_rows_kernel, dim3(kSortCluster), kSortWarps * 32, smem, kSortCluster, stream, s), "launching reshard_sort_rows_kernel"))) return rc;
+  Sum a{s.sorted, s.held, grad, cols, grad_stride, scale, grad_table, table_stride, accumulate != 0, false, false, nullptr, l.pitch, (int)run_of(tokens), 0};
+  a.part = reinterpret_cast<float *>(at + 2 * l.sorted + l.held);
+  a.wide = aligned16(grad, grad_stride, element_bytes(grad_dtype));
+  a.wide_table = aligned16(grad_table, table_stride, es);
+  a.slices = (int)((cols + kSumThreads * 8 - 1) / (kSumThreads * 8));
+  rc = launched(by_type(grad_dtype, [&](auto g) {
+    using TG = decltype(g);
+    return by_type(table_dtype, [&](auto t) {
+      using T = decltype(t);
+      return launch(a.wide ? reshard_sum_rows_kernel<TG, T, true> : reshard_sum_rows_kernel<TG, T, false>, dim3((unsigned)(l.runs * a.slices)), kSumThreads, 0,
+                    1, stream, a);
+    });
+  }), "launching reshard_sum_rows_kernel");
+  if (rc || l.runs == 1) return rc;
+  return launched(by_type(table_dtype, [&](auto t) {
+    return launch(reshard_join_rows_kernel<decltype(t)>, dim3((unsigned)(l.runs - 1)), kJoinThreads, 0, 1, stream, a);
+  }), "launching reshard_join_rows_kernel");
+} OPS_CATCH

@@ -228,7 +228,7 @@ extern "C" int reshard_experts_fp8(const void *x, int dtype, int64_t tokens, int
   // cancel would leave their roundings. (16 bits there: 424 us instead of 506 for 8,192 tokens to 8 of 128 experts of 2048 x 768.)
   p2.out = y, p2.out_dtype = RESHARD_F32, p2.out_stride = up(hidden, 16);
   if ((rc = enqueue_product(p2, stream))) return rc;
-  return enqueue_combine(y, up(hidden, 16), position, weights, tokens, k, hidden, out, dtype, out_stride, stream);
+  return enqueue_combine(Combine{y, RESHARD_F32, l.slots, up(hidden, 16), position, weights, tokens, k, hidden, out, dtype, out_stride}, stream);
 } OPS_CATCH
 
 extern "C" int reshard_ops_call(int op, const reshard_word_t *a) try {
@@ -275,6 +275,38 @@ extern "C" int reshard_ops_call(int op, const reshard_word_t *a) try {
                                  reinterpret_cast<const void *>(a[15].i), a[16].i, a[17].i,
                                  reinterpret_cast<const float *>(a[18].i), reinterpret_cast<void *>(a[19].i), a[20].i,
                                  reinterpret_cast<void *>(a[21].i), a[22].i, reinterpret_cast<reshard_stream_t>(a[23].i));
+    case RESHARD_OP_PERMUTE:
+      return reshard_permute(reinterpret_cast<const void *>(a[0].i), as_int(a[1].i), a[2].i, a[3].i, a[4].i,
+                             reinterpret_cast<const int32_t *>(a[5].i), reinterpret_cast<const int32_t *>(a[6].i), as_int(a[7].i),
+                             reinterpret_cast<void *>(a[8].i), a[9].i, a[10].i, reinterpret_cast<reshard_stream_t>(a[11].i));
+    case RESHARD_OP_COMBINE:
+      return reshard_combine(reinterpret_cast<const void *>(a[0].i), as_int(a[1].i), a[2].i, a[3].i, a[4].i,
+                             reinterpret_cast<const int32_t *>(a[5].i), reinterpret_cast<const float *>(a[6].i), a[7].i,
+                             as_int(a[8].i), reinterpret_cast<void *>(a[9].i), as_int(a[10].i), a[11].i,
+                             reinterpret_cast<reshard_stream_t>(a[12].i));
+    case RESHARD_OP_COMBINE_BACKWARD:
+      return reshard_combine_backward(reinterpret_cast<const void *>(a[0].i), as_int(a[1].i), a[2].i,
+                                      reinterpret_cast<const void *>(a[3].i), as_int(a[4].i), a[5].i, a[6].i, a[7].i,
+                                      reinterpret_cast<const int32_t *>(a[8].i), reinterpret_cast<const int32_t *>(a[9].i),
+                                      reinterpret_cast<const float *>(a[10].i), a[11].i, as_int(a[12].i),
+                                      reinterpret_cast<void *>(a[13].i), a[14].i, reinterpret_cast<float *>(a[15].i),
+                                      reinterpret_cast<reshard_stream_t>(a[16].i));
+    case RESHARD_OP_EMBEDDING:
+      return reshard_embedding(reinterpret_cast<const void *>(a[0].i), as_int(a[1].i), a[2].i, reinterpret_cast<const void *>(a[3].i),
+                               as_int(a[4].i), a[5].i, a[6].i, a[7].i, a[8].i, (float)a[9].f, reinterpret_cast<void *>(a[10].i),
+                               a[11].i, reinterpret_cast<reshard_stream_t>(a[12].i));
+    case RESHARD_OP_EMBEDDING_BACKWARD:
+      return reshard_embedding_backward(reinterpret_cast<const void *>(a[0].i), as_int(a[1].i), a[2].i, a[3].i, a[4].i,
+                                        reinterpret_cast<const void *>(a[5].i), as_int(a[6].i), a[7].i, a[8].i, (float)a[9].f,
+                                        reinterpret_cast<void *>(a[10].i), as_int(a[11].i), a[12].i, as_int(a[13].i),
+                                        reinterpret_cast<void *>(a[14].i), a[15].i, reinterpret_cast<reshard_stream_t>(a[16].i));
+    case RESHARD_OP_GRAD_NORM:
+      return reshard_grad_norm(reinterpret_cast<const reshard_tensors_t *>(a[0].i), reinterpret_cast<float *>(a[1].i),
+                               reinterpret_cast<void *>(a[2].i), a[3].i, reinterpret_cast<reshard_stream_t>(a[4].i));
+    case RESHARD_OP_CLIP_GRADS:
+      return reshard_clip_grads(reinterpret_cast<const reshard_tensors_t *>(a[0].i), reinterpret_cast<const reshard_tensors_t *>(a[1].i),
+                                a[2].f, reinterpret_cast<const float *>(a[3].i), reinterpret_cast<float *>(a[4].i),
+                                reinterpret_cast<void *>(a[5].i), a[6].i, reinterpret_cast<reshard_stream_t>(a[7].i));
     default:
       return fail(RESHARD_ERR_INVALID_ARG, "unknown operator number");
   }

@@ -132,8 +132,21 @@ struct Rows {                 // a quantization by rows
 int enqueue_quantize_rows(const Rows &r, cudaStream_t stream);
 int enqueue_dispatch(const int32_t *ids, int64_t slots, int first, int experts, int32_t *offsets, int32_t *order,
                      int32_t *position, cudaStream_t stream);
-int enqueue_combine(const float *y, int64_t y_stride, const int32_t *position, const float *weights, int64_t tokens, int k, int64_t cols,
-                    void *out, int dtype, int64_t out_stride, cudaStream_t stream);
+
+struct Combine {              // out[t] = sum_j weights[t, j] * y[position[t, j]]
+  const void *y;
+  int dtype;
+  int64_t rows, y_stride;
+  const int32_t *position;    // one outside the rows adds nothing
+  const float *weights;       // NULL: 1
+  int64_t tokens;
+  int k;
+  int64_t cols;
+  void *out;
+  int out_dtype;
+  int64_t out_stride;
+};
+int enqueue_combine(const Combine &a, cudaStream_t stream);
 
 struct Product {              // out[m, n] = sum_k a[m, k] w[n, k], both as 8-bit values times block scales
   const uint8_t *a;

@@ -1,83 +1,21 @@
 // Values to e4m3 with one fp32 scale for each block of 128 (rows: 1 x 128; weights: 128 x 128, the layout whose scale
-// tensors reshard_plan_blockwise_fp8 derives), and the weighted sum that ends the expert layer.
+// tensors reshard_plan_blockwise_fp8 derives).
 //
 // A block's amax a = max |x| (at least 2^-100) gives the scale a * (1 / 448) and the values e4m3(x * ((1 / a) * 448)),
 // rounded to nearest even. One reciprocal a block instead of a division a value; the product differs from x / scale by a
 // few roundings of 32 bits, far below the 2^-4 of an e4m3 step. A block holding an infinity or NaN gets scale and values NaN.
 // Both kernels read each value once, keep it in registers between the amax and the rounding, and are bound by HBM.
 #include <algorithm>
-#include <type_traits>
 
 #include "ops_common.cuh"
+#include "values.cuh"
 
 namespace reshard {
 namespace ops {
 
 namespace {
 
-constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kQThreads = 256;
-
-template <typename T, int N>
-struct alignas(sizeof(T) * N <= 16 ? sizeof(T) * N : 16) Pack {
-  T v[N];
-};
-
-// N values at p (elements from `left` on are 0); `wide`: p is aligned to 16 bytes (or to N values, if fewer) and all are in.
-template <typename T, int N>
-__device__ __forceinline__ void load_values(const T *p, int left, bool wide, float (&x)[N]) {
-  if (wide && left >= N) {
-    const Pack<T, N> r = *reinterpret_cast<const Pack<T, N> *>(p);
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = to_f32(r.v[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = i < left ? to_f32(p[i]) : 0.0f;
-  }
-}
-
-// The 16-byte words that hold N values at p, wherever p is: ask() reads them (words that hold none of the `left` values
-// are not read, `any` is in their place), take() shifts the values into place and clears those from `left` on. Rows that
-// start anywhere are read as fast as aligned ones this way; value by value they took three times as long.
-template <typename T, int N>
-struct Shifted {
-  static constexpr int kWords = N * (int)sizeof(T) / 4;
-  static_assert(kWords % 4 == 0, "16-byte words");
-  uint32_t w[kWords + 4];
-  __device__ __forceinline__ void ask(const T *p, int left, const uint8_t *any) {
-    const uintptr_t skip = reinterpret_cast<uintptr_t>(p) & 15;
-    const uint8_t *from = reinterpret_cast<const uint8_t *>(p) - skip;
-    const int end = left > 0 ? (int)skip + min(left, N) * (int)sizeof(T) : 0;        // bytes from there to the last value
-#pragma unroll
-    for (int i = 0; i < kWords + 4; i += 4) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(4 * i < end ? from + 4 * i : any));
-      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
-    }
-  }
-  __device__ __forceinline__ void take(const T *p, int left, uint32_t (&v)[kWords]) {
-    const uint32_t skip = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
-#pragma unroll
-    for (int i = 0; i < kWords + 3; ++i) w[i] = skip & 4 ? w[i + 1] : w[i];
-#pragma unroll
-    for (int i = 0; i < kWords + 2; ++i) w[i] = skip & 8 ? w[i + 2] : w[i];
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      const uint32_t x = sizeof(T) < 4 ? __funnelshift_r(w[i], w[i + 1], 8 * (skip & 3)) : w[i];
-      const int have = left - i * (4 / (int)sizeof(T));          // values from this word on
-      v[i] = have >= 4 / (int)sizeof(T) ? x : have > 0 ? x & 0xffffu : 0;
-    }
-  }
-};
-template <typename T>
-__device__ __forceinline__ float value_of(const uint32_t *v, int i) {
-  if constexpr (sizeof(T) == 4) return __uint_as_float(v[i]);
-  else if constexpr (std::is_same_v<T, __nv_bfloat16>) return __uint_as_float(i & 1 ? v[i / 2] & 0xffff0000u : v[i / 2] << 16);
-  else return __half2float(__ushort_as_half((uint16_t)(v[i / 2] >> (16 * (i & 1)))));
-}
-// A 16-byte word that holds a tensor's first value.
-__device__ __forceinline__ const uint8_t *first_word(const void *p) {
-  return reinterpret_cast<const uint8_t *>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15);
-}
 
 // 8 lanes a block of 128 values, 16 each: two or four 16-byte loads, three shuffles and one 16-byte store a lane.
 // 16,384 x 4096 bf16: 38.2 us, 5.3 TB/s, where a plain copy reaches 6.8 (4 lanes a block, 32 values each: the same).
@@ -234,49 +172,6 @@ __global__ void __launch_bounds__(kQThreads) reshard_quantize_blocks_kernel(Bloc
   }
 }
 
-// out[t] = sum_j weights[t, j] * y[position[t, j]] in the order of j, slots without a place skipped; terms and sums of 32
-// bits, one rounding. One thread 8 columns of a token; bound by the read of y: 8 slots a token, 8,192 x 2048, 83 us, 6.9 TB/s (loads of
-// all eight slots before the sums: three times as long).
-template <typename T>
-__global__ void __launch_bounds__(kQThreads)
-    reshard_combine_kernel(const float *y, int64_t y_stride, const int32_t *position, const float *weights, int64_t tokens, int k, int64_t cols,
-                           T *out, int64_t out_stride, int chunks, bool wide) {
-  grid_enter();
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= tokens * chunks) return;
-  const int64_t t = tokens * chunks <= 0xffffffffll ? (uint32_t)i / (uint32_t)chunks : i / chunks;
-  const int64_t c = (i - t * chunks) * 8;
-  const int left = (int)min((int64_t)8, cols - c);
-  float sum[8];
-#pragma unroll
-  for (int u = 0; u < 8; ++u) sum[u] = 0.0f;
-#pragma unroll 4
-  for (int j = 0; j < k; ++j) {
-    const int p = position[t * k + j];
-    if (p < 0) continue;
-    const float w = weights[t * k + j];
-    float x[8];
-    load_values<float, 8>(y + (int64_t)p * y_stride + c, left, wide, x);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) sum[u] = fmaf(w, x[u], sum[u]);
-  }
-  T *to = out + t * out_stride + c;
-  if (wide && left >= 8) {
-    Pack<T, 8> r;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) r.v[u] = from_f32<T>(sum[u]);
-    *reinterpret_cast<Pack<T, 8> *>(to) = r;
-  } else {
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (u < left) to[u] = from_f32<T>(sum[u]);
-  }
-}
-
-bool aligned16(const void *p, int64_t stride, int bytes) {
-  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (stride * bytes) % 16 == 0;
-}
-
 }  // namespace
 
 int enqueue_quantize_rows(const Rows &r, cudaStream_t stream) {
@@ -292,25 +187,6 @@ int enqueue_quantize_rows(const Rows &r, cudaStream_t stream) {
   };
   const cudaError_t e = r.dtype == RESHARD_F32 ? go(float()) : r.dtype == RESHARD_BF16 ? go(__nv_bfloat16()) : go(__half());
   return e == cudaSuccess ? RESHARD_OK : cuda_error(e, "launching reshard_quantize_rows_kernel");
-}
-
-int enqueue_combine(const float *y, int64_t y_stride, const int32_t *position, const float *weights, int64_t tokens, int k, int64_t cols,
-                    void *out, int dtype, int64_t out_stride, cudaStream_t stream) {
-  if (tokens == 0 || cols == 0) return RESHARD_OK;
-  const int chunks = (int)((cols + 7) / 8), es = element_bytes(dtype);
-  const int block = tokens * chunks <= 32768 ? 64 : kQThreads;      // a few tokens' columns spread over the SMs
-  const dim3 grid((unsigned)((tokens * chunks + block - 1) / block));
-  const bool wide = aligned16(y, y_stride, 4) && aligned16(out, out_stride, es);
-  cudaError_t e;
-  auto go = [&](auto t) {
-    using T = decltype(t);
-    return launch(reshard_combine_kernel<T>, grid, block, 0, 1, stream, y, y_stride, position, weights, tokens, k, cols,
-                  static_cast<T *>(out), out_stride, chunks, wide);
-  };
-  if (dtype == RESHARD_F32) e = go(float());
-  else if (dtype == RESHARD_BF16) e = go(__nv_bfloat16());
-  else e = go(__half());
-  return e == cudaSuccess ? RESHARD_OK : cuda_error(e, "launching reshard_combine_kernel");
 }
 
 }  // namespace ops

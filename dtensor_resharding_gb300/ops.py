@@ -1,7 +1,8 @@
 """The expert layer over resharded weights: the calls of include/reshard_ops.h on torch tensors.
 
 Routing to experts and its gradient, quantization to 8-bit floating point in blocks of 128, the matrix product over
-such blocks, and the routed expert feed-forward. A refit leaves a generation rank with FP8 weights and their fp32 block
+such blocks, and the routed expert feed-forward; tokens to their experts and back and the rows of a vocabulary's shard, with
+their gradients, and the norm and clipping of many gradients. A refit leaves a generation rank with FP8 weights and their fp32 block
 scales (``reshard_plan_blockwise_fp8``), or with BF16 weights that ``reshard_quantize_blocks`` brings to that form;
 these calls compute with them.
 
@@ -13,7 +14,8 @@ input made on another stream must be ready there (an event), as for any torch op
 A wait inside a product kernel that gives up (it does not on a working GPU) leaves an incomplete output and a status that no call
 looks at: ``reshard_ops_status`` reads it.
 
-Gradients: ``reshard_route``'s weights carry the gradient to its logits (``reshard_route_backward``). ``reshard_linear_fp8`` and
+Gradients: ``reshard_route``'s weights carry the gradient to its logits (``reshard_route_backward``); ``reshard_permute``,
+``reshard_combine`` and ``reshard_embedding`` carry theirs, which are also calls of their own. ``reshard_linear_fp8`` and
 ``reshard_experts_fp8`` have none: of an input that requires one, their result raises when a gradient is asked of it. Codes and
 scales (the quantizations, ``reshard_matmul_fp8`` over them) carry none.
 """
@@ -22,7 +24,7 @@ from __future__ import annotations
 import ctypes
 from functools import lru_cache
 from struct import Struct
-from typing import Optional, Tuple
+from typing import Iterable, Optional, Tuple, Union
 
 import torch
 
@@ -33,11 +35,13 @@ RESHARD_SCORE_SIGMOID = 1
 SCORES = {"softmax": RESHARD_SCORE_SOFTMAX, "sigmoid": RESHARD_SCORE_SIGMOID}
 OPS_EXPORTED = ("reshard_route", "reshard_route_backward", "reshard_dispatch", "reshard_quantize_rows", "reshard_quantize_blocks",
                 "reshard_matmul_fp8", "reshard_linear_fp8_workspace", "reshard_linear_fp8", "reshard_experts_fp8_workspace",
-                "reshard_experts_fp8", "reshard_ops_call", "reshard_ops_status")
+                "reshard_experts_fp8", "reshard_permute", "reshard_combine", "reshard_combine_backward", "reshard_embedding",
+                "reshard_embedding_backward_workspace", "reshard_embedding_backward", "reshard_tensors_create", "reshard_tensors_destroy",
+                "reshard_grad_norm_workspace", "reshard_grad_norm", "reshard_clip_grads", "reshard_ops_call", "reshard_ops_status")
 _CODES = {torch.bfloat16: 1, torch.float16: 2, torch.float32: 3}   # RESHARD_BF16, RESHARD_F16, RESHARD_F32
 _FP8 = torch.float8_e4m3fn
 
-_i, _l, _p, _f = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
+_i, _l, _p, _f, _d = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float, ctypes.c_double
 _SIGNATURES = {
     "reshard_route": [_p, _i, _l, _i, _l, _p, _i, _i, _i, _i, _i, _i, _f, _p, _p, _p],
     "reshard_route_backward": [_p, _p, _i, _l, _i, _l, _p, _i, _i, _i, _f, _p, _l, _p],
@@ -49,6 +53,17 @@ _SIGNATURES = {
     "reshard_linear_fp8": [_p, _i, _l, _l, _l, _p, _l, _p, _l, _p, _l, _p, _l, _p],
     "reshard_experts_fp8_workspace": [_l, _i, _i, _l, _l, _i],
     "reshard_experts_fp8": [_p, _i, _l, _l, _l, _p, _p, _i, _i, _i, _l, _p, _l, _l, _p, _p, _l, _l, _p, _p, _l, _p, _l, _p],
+    "reshard_permute": [_p, _i, _l, _l, _l, _p, _p, _i, _p, _l, _l, _p],
+    "reshard_combine": [_p, _i, _l, _l, _l, _p, _p, _l, _i, _p, _i, _l, _p],
+    "reshard_combine_backward": [_p, _i, _l, _p, _i, _l, _l, _l, _p, _p, _p, _l, _i, _p, _l, _p, _p],
+    "reshard_embedding": [_p, _i, _l, _p, _i, _l, _l, _l, _l, _f, _p, _l, _p],
+    "reshard_embedding_backward_workspace": [_l, _l],
+    "reshard_embedding_backward": [_p, _i, _l, _l, _l, _p, _i, _l, _l, _f, _p, _i, _l, _i, _p, _l, _p],
+    "reshard_tensors_create": [_p, _p, _p, _l, _p],
+    "reshard_tensors_destroy": [_p],
+    "reshard_grad_norm_workspace": [],
+    "reshard_grad_norm": [_p, _p, _p, _l, _p],
+    "reshard_clip_grads": [_p, _p, _d, _p, _p, _p, _l, _p],
     "reshard_ops_call": [_i, ctypes.c_char_p],
     "reshard_ops_status": [_p, _i],
 }
@@ -66,6 +81,13 @@ _QUANTIZE_BLOCKS = Struct("=12q").pack
 _MATMUL_FP8 = Struct("=18q").pack
 _LINEAR_FP8 = Struct("=14q").pack
 _EXPERTS_FP8 = Struct("=24q").pack
+_PERMUTE = Struct("=12q").pack
+_COMBINE = Struct("=13q").pack
+_COMBINE_BACKWARD = Struct("=17q").pack
+_EMBEDDING = Struct("=9qd3q").pack
+_EMBEDDING_BACKWARD = Struct("=9qd7q").pack
+_GRAD_NORM = Struct("=5q").pack
+_CLIP_GRADS = Struct("=2qd5q").pack
 
 
 def _call(op: int, words: bytes) -> None:
@@ -120,6 +142,8 @@ def _output(out: Optional[torch.Tensor], rows: int, cols: int, dtype: torch.dtyp
 # Workspace sizes by sizes: asking the library each time costs a call.
 _linear_space = lru_cache(maxsize=4096)(LIB.reshard_linear_fp8_workspace)
 _experts_space = lru_cache(maxsize=4096)(LIB.reshard_experts_fp8_workspace)
+_embedding_space = lru_cache(maxsize=4096)(LIB.reshard_embedding_backward_workspace)
+_norm_space = LIB.reshard_grad_norm_workspace()
 
 
 def _here(t: torch.Tensor, stream) -> Optional[int]:
@@ -403,6 +427,354 @@ def reshard_experts_fp8(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tenso
     if (x.requires_grad or weights.requires_grad) and torch.is_grad_enabled():
         return _Undifferentiable.apply("reshard_experts_fp8", out, x, weights)
     return out
+
+
+# ------------------------------------------------------------------------------- tokens to their experts and back
+
+Sort = Tuple[torch.Tensor, torch.Tensor, torch.Tensor]
+
+
+def _sorted(sort: Sort, like: torch.Tensor) -> Tuple[int, int, int, int]:
+    """(address of order, its length, address of position, its length) of what reshard_dispatch gave."""
+    _, order, position = sort
+    return (_dense(order, "the sort's order", torch.int32, order.shape, like), order.numel(),
+            _dense(position, "the sort's position", torch.int32, position.shape, like), position.numel())
+
+
+def _choices(slots: int, tokens: int) -> int:
+    """k of a sort of so many slots, of so many tokens."""
+    if tokens == 0 and slots == 0:
+        return 1
+    if tokens == 0 or slots == 0 or slots % tokens:
+        _bad(f"a sort of {slots} slots does not fit {tokens} tokens")
+    return slots // tokens
+
+
+def _tokens(sort: Sort, weights: Optional[torch.Tensor], k: Optional[int]) -> Tuple[int, int]:
+    """(tokens, k) of a sort, from its weights [tokens, k] or a k given."""
+    slots = sort[2].numel()
+    if weights is not None:
+        tokens, choices, _ = _matrix(weights, "weights")
+        if k is not None and k != choices:
+            _bad(f"k is {k}, the weights have {choices} columns")
+        if tokens * choices != slots:
+            _bad(f"weights {tuple(weights.shape)} do not fit a sort of {slots} slots")
+        return tokens, max(choices, 1)
+    if k is None or k < 1 or slots % k:
+        _bad(f"without weights k must be given and divide the sort's {slots} slots")
+    return slots // k, k
+
+
+def _rows(t: torch.Tensor) -> torch.Tensor:
+    """A gradient as autograd brings it (expanded, transposed): copied if its rows are not rows of a matrix."""
+    return t if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= t.shape[1] else t.contiguous()
+
+
+def _no_out(out, *inputs) -> None:
+    if out is not None and torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in inputs):
+        raise ReshardError(RESHARD_ERR_UNSUPPORTED, "a result that carries a gradient cannot be written to out: call under torch.no_grad(), or without out")
+
+
+def reshard_permute(x: torch.Tensor, sort: Sort, *, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y [slots, cols] with y[position[t * k + j]] = x[t]: each token's row at the places of its experts.
+
+    ``sort`` is what ``reshard_dispatch`` gave for these tokens' ids. Rows of no slot (from offsets[-1] on: other ranks' experts') are
+    left as they are in ``out``, which may have more or fewer rows than slots, and undefined in a new tensor. Values
+    are copied bit for bit; differentiable in ``x``."""
+    here = _here(x, stream)
+    if here is None:
+        with _on(x, stream):
+            return reshard_permute(x, sort, out=out)
+    if x.requires_grad and torch.is_grad_enabled():
+        _no_out(out, x)
+        return _Permute.apply(x, *sort)
+    T, H, step = _matrix(x, "x")
+    code = _code(x, "x")
+    at_order, places, at_position, slots = _sorted(sort, x)
+    k = _choices(slots, T)
+    rows = places if out is None else out.shape[0]
+    out, to_step = _output(out, rows, H, x.dtype, x)
+    if rows > places:      # places that the sort does not have are nobody's
+        rows = places
+    _call(8, _PERMUTE(x.data_ptr(), code, T, H, step, at_order, at_position, k, out.data_ptr(), rows, to_step, here))
+    return out
+
+
+def reshard_permute_backward(grad: torch.Tensor, sort: Sort, k: int, *, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The gradient to ``x`` of ``reshard_permute``: each token's sum over its k places, in ``grad``'s type."""
+    return reshard_combine(grad.detach(), sort, k=k, out=out, stream=stream)
+
+
+class _Permute(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, *sort):
+        ctx.save_for_backward(*sort)
+        ctx.k = _choices(sort[2].numel(), x.shape[0])
+        return reshard_permute(x.detach(), sort)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        return (reshard_permute_backward(_rows(grad), ctx.saved_tensors, ctx.k), None, None, None)
+
+
+def reshard_combine(y: torch.Tensor, sort: Sort, weights: Optional[torch.Tensor] = None, *, k: Optional[int] = None,
+                    out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out[t] = sum_j weights[t, j] * y[position[t * k + j]]: experts' rows back to their tokens.
+
+    ``weights`` [tokens, k] float32 (``reshard_route``), or None with ``k`` given: plain sums. Slots without a place add nothing.
+    The sum is fp32 and rounded once, to ``out_dtype`` (y's type if None). Differentiable in ``y`` and ``weights``."""
+    here = _here(y, stream)
+    if here is None:
+        with _on(y, stream):
+            return reshard_combine(y, sort, weights, k=k, out_dtype=out_dtype, out=out)
+    if torch.is_grad_enabled() and (y.requires_grad or (weights is not None and weights.requires_grad)):
+        _no_out(out, y, weights)
+        return _Combine.apply(y, weights, k, out_dtype, *sort)
+    rows, H, step = _matrix(y, "y")
+    code = _code(y, "y")
+    T, k = _tokens(sort, weights, k)
+    _, _, at_position, _ = _sorted(sort, y)
+    at_weights = 0 if weights is None else _dense(weights, "weights", torch.float32, (T, k), y)
+    out, to_step = _output(out, T, H, (out_dtype or y.dtype) if out is None else out.dtype, y)
+    _call(9, _COMBINE(y.data_ptr(), code, rows, H, step, at_position, at_weights, T, k, out.data_ptr(), _code(out, "out"), to_step, here))
+    return out
+
+
+def reshard_combine_backward(grad: torch.Tensor, y: torch.Tensor, sort: Sort, weights: Optional[torch.Tensor] = None, *,
+                             k: Optional[int] = None, needs: Tuple[bool, bool] = (True, True),
+                             stream=None) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """(grad_y in y's type, grad_weights float32) of ``reshard_combine`` for ``grad`` [tokens, cols].
+
+    Rows of ``y`` that belong to no slot have gradient 0, and so have weights of slots without a place. ``needs``: which of the two
+    are wanted (the other is None). Without ``weights`` there is no gradient to them."""
+    here = _here(grad, stream)
+    if here is None:
+        with _on(grad, stream):
+            return reshard_combine_backward(grad, y, sort, weights, k=k, needs=needs)
+    grad = _rows(grad)
+    T, k = _tokens(sort, weights, k)
+    G, H, grad_step = _matrix(grad, "grad")
+    rows, cols, step = _matrix(y, "y")
+    if (G, H) != (T, cols):
+        _bad(f"grad {tuple(grad.shape)} does not fit {T} tokens and y {tuple(y.shape)}")
+    if y.get_device() != grad.get_device():
+        _bad(f"y is on {y.device}, not on {grad.device}")
+    at_order, places, at_position, _ = _sorted(sort, grad)
+    if places < rows:
+        _bad(f"y has {rows} rows, the sort {places} places")
+    at_weights = 0 if weights is None else _dense(weights, "weights", torch.float32, (T, k), grad)
+    grad_y = torch.empty((rows, H), dtype=y.dtype, device=y.device) if needs[0] else None
+    grad_weights = torch.empty((T, k), dtype=torch.float32, device=y.device) if needs[1] and weights is not None else None
+    _call(10, _COMBINE_BACKWARD(grad.data_ptr(), _code(grad, "grad"), grad_step, y.data_ptr(), _code(y, "y"), rows, H, step, at_order, at_position,
+                                at_weights, T, k, 0 if grad_y is None else grad_y.data_ptr(), H,
+                                0 if grad_weights is None else grad_weights.data_ptr(), here))
+    return grad_y, grad_weights
+
+
+class _Combine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y, weights, k, out_dtype, *sort):
+        ctx.save_for_backward(y, weights, *sort)
+        ctx.k = k
+        return reshard_combine(y.detach(), sort, None if weights is None else weights.detach(), k=k, out_dtype=out_dtype)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        y, weights, *sort = ctx.saved_tensors
+        grad_y, grad_weights = reshard_combine_backward(grad, y, tuple(sort), weights, k=ctx.k, needs=ctx.needs_input_grad[:2])
+        return (grad_y, grad_weights, *[None] * 5)
+
+
+# ----------------------------------------------------------------------------------------- a shard of a vocabulary
+
+def _id_bits(ids: torch.Tensor, like: torch.Tensor) -> int:
+    if ids.dtype is not torch.int64 and ids.dtype is not torch.int32:
+        _bad(f"ids must be int64 or int32, not {ids.dtype}")
+    if ids.get_device() != like.get_device():
+        _bad(f"ids are on {ids.device}, not on {like.device}")
+    return 64 if ids.dtype is torch.int64 else 32
+
+
+def reshard_embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0, first_row: int = 0,
+                      out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """out [*ids.shape, cols] = scale * table[ids - first_row], 0 where the id's row is not in ``table`` (another rank's shard).
+
+    ``ids`` int64 or int32 of any shape (copied where not contiguous), ``table`` [rows, cols] the rows first_row .. first_row +
+    rows - 1 of the vocabulary: the shards' results sum to the whole lookup. Differentiable in ``table``."""
+    here = _here(table, stream)
+    if here is None:
+        with _on(table, stream):
+            return reshard_embedding(ids, table, scale=scale, first_row=first_row, out=out)
+    if table.requires_grad and torch.is_grad_enabled():
+        _no_out(out, table)
+        return _Embedding.apply(ids, table, scale, first_row)
+    rows, H, step = _matrix(table, "table")
+    code, bits = _code(table, "table"), _id_bits(ids, table)
+    ids = ids.contiguous()
+    T, shape = ids.numel(), ids.shape
+    if out is None:
+        out = torch.empty((*shape, H), dtype=table.dtype, device=table.device)
+        to, to_step = out, H
+    else:
+        if out.shape != (*shape, H):
+            _bad(f"out must be of shape {(*shape, H)}, not {tuple(out.shape)}")
+        if len(shape) != 1 and not out.is_contiguous():
+            _bad("out must be contiguous for ids of more than one dimension")
+        to, to_step = _output(out if len(shape) == 1 else out.view(T, H), T, H, table.dtype, table)
+    _call(11, _EMBEDDING(ids.data_ptr(), bits, T, table.data_ptr(), code, first_row, rows, H, step, scale, to.data_ptr(), to_step, here))
+    return out
+
+
+def reshard_embedding_backward(grad: torch.Tensor, ids: torch.Tensor, rows: int, *, scale: float = 1.0, first_row: int = 0,
+                               dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None, accumulate: bool = False,
+                               stream=None) -> torch.Tensor:
+    """The gradient [rows, cols] to ``reshard_embedding``'s table: scale * the sum of ``grad`` over each row's tokens.
+
+    Sums are fp32 in the order of the tokens, rounded once to ``dtype`` (``grad``'s if None). Rows without a token get 0; with
+    ``accumulate`` the sums are added to ``out`` instead (a main gradient of a training step), and other rows not touched."""
+    here = _here(grad, stream)
+    if here is None:
+        with _on(grad, stream):
+            return reshard_embedding_backward(grad, ids, rows, scale=scale, first_row=first_row, dtype=dtype, out=out, accumulate=accumulate)
+    if grad.shape[:-1] != ids.shape:
+        _bad(f"grad {tuple(grad.shape)} does not fit ids {tuple(ids.shape)}")
+    bits = _id_bits(ids, grad)
+    grad, ids = _rows(grad if grad.dim() == 2 else grad.reshape(ids.numel(), grad.shape[-1])), ids.contiguous()
+    T, H, step = _matrix(grad, "grad")
+    if accumulate and out is None:
+        _bad("accumulate needs out")
+    out, to_step = _output(out, max(0, rows), H, (dtype or grad.dtype) if out is None else out.dtype, grad)
+    need = _embedding_space(T, H)
+    space = torch.empty(need, dtype=torch.uint8, device=grad.device) if need else None
+    _call(12, _EMBEDDING_BACKWARD(grad.data_ptr(), _code(grad, "grad"), T, H, step, ids.data_ptr(), bits, first_row, rows, scale, out.data_ptr(),
+                                  _code(out, "out"), to_step, accumulate, space.data_ptr() if need else 0, need, here))
+    return out
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, ids, table, scale, first_row):
+        ctx.save_for_backward(ids)
+        ctx.how = dict(rows=table.shape[0], scale=scale, first_row=first_row, dtype=table.dtype)
+        return reshard_embedding(ids, table.detach(), scale=scale, first_row=first_row)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, grad):
+        return (None, reshard_embedding_backward(grad, ctx.saved_tensors[0], **ctx.how), None, None)
+
+
+# ------------------------------------------------------------------------------------------ many tensors' norm and clipping
+
+def _packed(t: torch.Tensor) -> bool:
+    """Whether the tensor's elements fill its storage from the first to the last, in some order of its dimensions."""
+    expect = 1
+    for step, size in sorted(zip(t.stride(), t.shape)):
+        if size > 1:
+            if step != expect:
+                return False
+            expect *= size
+    return True
+
+
+class TensorList:
+    """Dense tensors of one device for ``reshard_grad_norm`` and ``reshard_clip_grads``, looked over once: for tensors that
+    stay where they are from step to step (the list keeps them alive; one whose storage is replaced needs a new list)."""
+
+    is_cuda = True
+
+    def __init__(self, tensors: Iterable[torch.Tensor]):
+        self._handle = None
+        self.tensors = tensors = list(tensors)
+        at, sizes, types, self._order = [], [], [], {}
+        self.device = device = tensors[0].device if tensors else torch.device("cuda", torch.cuda.current_device())
+        if device.type != "cuda":
+            _bad(f"tensors must be on a CUDA device, not on {device}")
+        for i, t in enumerate(tensors):
+            if t.layout is not torch.strided:
+                _bad(f"tensor {i} is not strided but {t.layout}")
+            if t.device != device:
+                _bad(f"tensor {i} is on {t.device}, the first on {device}")
+            if not t.is_contiguous():
+                if not _packed(t):
+                    _bad(f"tensor {i} of shape {tuple(t.shape)}, strides {t.stride()} is not dense")
+                self._order[i] = (t.shape, t.stride())
+            at.append(t.data_ptr())
+            sizes.append(t.numel())
+            types.append(_code(t, "a tensor"))
+        n, handle = len(tensors), ctypes.c_void_p()
+        with torch.cuda.device(device):
+            _check(LIB.reshard_tensors_create((ctypes.c_void_p * n)(*at), (ctypes.c_int64 * n)(*sizes), (ctypes.c_int32 * n)(*types), n, ctypes.byref(handle)))
+        self._handle = handle.value
+
+    def get_device(self) -> int:
+        return self.device.index
+
+    def __len__(self) -> int:
+        return len(self.tensors)
+
+    def __del__(self):
+        if getattr(self, "_handle", None) is not None:
+            LIB.reshard_tensors_destroy(self._handle)
+
+
+def reshard_tensor_list(tensors: Iterable[torch.Tensor]) -> TensorList:
+    """A list of tensors for the calls below (bfloat16, float16 and float32, mixed as they come; dense in any order of dimensions)."""
+    return TensorList(tensors)
+
+
+Tensors = Union[TensorList, Iterable[torch.Tensor]]
+
+
+def reshard_grad_norm(tensors: Tensors, *, stream=None) -> torch.Tensor:
+    """The norm sqrt(sum x^2) over all elements of ``tensors`` (a ``TensorList`` or tensors), a float32 scalar on their device.
+
+    Other ranks' shards: the root of the sum of their norms' squares is the whole norm."""
+    if not isinstance(tensors, TensorList):
+        tensors = TensorList(tensors)
+    here = _here(tensors, stream)
+    if here is None:
+        with _on(tensors, stream):
+            return reshard_grad_norm(tensors)
+    norm = torch.empty((), dtype=torch.float32, device=tensors.device)
+    space = torch.empty(_norm_space, dtype=torch.uint8, device=tensors.device)
+    _call(13, _GRAD_NORM(tensors._handle, norm.data_ptr(), space.data_ptr(), _norm_space, here))
+    return norm
+
+
+def reshard_clip_grads(tensors: Tensors, limit: float, *, norm: Optional[torch.Tensor] = None, out: Optional[Tensors] = None,
+                       stream=None) -> torch.Tensor:
+    """Scales ``tensors`` by min(1, limit / (norm + 1e-6)), in place or into ``out`` (other types are fine); returns the norm.
+
+    ``norm``: a float32 scalar on the device (the norm over all ranks), or None: ``reshard_grad_norm`` of the tensors. Nothing is
+    read back: a step with a NaN norm makes every value NaN, one with an infinite norm 0 (see include/reshard_ops.h). As with
+    any write through a pointer, autograd is not told."""
+    if not isinstance(tensors, TensorList):
+        tensors = TensorList(tensors)
+    if out is not None and not isinstance(out, TensorList):
+        out = TensorList(out)
+    here = _here(tensors, stream)
+    if here is None:
+        with _on(tensors, stream):
+            return reshard_clip_grads(tensors, limit, norm=norm, out=out)
+    into = 0
+    if out is not None:
+        if len(out) != len(tensors) or out.device != tensors.device:
+            _bad(f"out has {len(out)} tensors on {out.device}, not {len(tensors)} on {tensors.device}")
+        if out._order != tensors._order:
+            _bad("a tensor of out has another order of dimensions than its source")
+        into = out._handle
+    if norm is None:
+        norm = torch.empty((), dtype=torch.float32, device=tensors.device)
+        space = torch.empty(_norm_space, dtype=torch.uint8, device=tensors.device)
+        _call(14, _CLIP_GRADS(tensors._handle, into, limit, 0, norm.data_ptr(), space.data_ptr(), _norm_space, here))
+    else:
+        if norm.dtype is not torch.float32 or norm.numel() != 1 or norm.device != tensors.device:
+            _bad(f"norm must be one float32 on {tensors.device}, not {norm.dtype} of shape {tuple(norm.shape)} on {norm.device}")
+        _call(14, _CLIP_GRADS(tensors._handle, into, limit, norm.data_ptr(), 0, 0, 0, here))
+    return norm
 
 
 def reshard_ops_status(reset: bool = False) -> int:

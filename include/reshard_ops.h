@@ -1,7 +1,8 @@
 /*
  * reshard_ops.h -- the expert layer over resharded weights (libreshard.so): routing to experts and its gradient,
  * quantization to 8-bit floating point in blocks of 128, the matrix product over such blocks, and the routed expert
- * feed-forward that uses them.
+ * feed-forward that uses them; and what a training step moves around it: tokens to their experts and back, the rows of a
+ * vocabulary's shard, all with their gradients, and the norm and clipping of many gradients.
  *
  * A refit (reshard.h) leaves a generation rank with FP8 expert weights and their fp32 block scales
  * (reshard_plan_blockwise_fp8, 128 x 128 blocks) or with BF16 weights (reshard_quantize_blocks gives them that form);
@@ -129,6 +130,84 @@ int reshard_experts_fp8(const void *x, int dtype, int64_t tokens, int64_t hidden
                         void *workspace, int64_t workspace_bytes, reshard_stream_t stream);
 
 /*
+ * reshard_permute -- tokens' rows to their experts' places: out[position[s]] = x[t] for the slots s = t * k + j.
+ * x [tokens, cols] in dtype, out [rows, cols] in the same; order [rows] and position [tokens * k] as reshard_dispatch gave
+ * them (the places and slots of one another): a slot whose position is negative, beyond the rows, or another's (order
+ * names another slot there) writes nothing. Rows that no slot writes stay as they were: those behind the last expert.
+ * Values are copied bit for bit. The gradient to x is reshard_combine without weights.
+ */
+int reshard_permute(const void *x, int dtype, int64_t tokens, int64_t cols, int64_t row_stride, const int32_t *order,
+                    const int32_t *position, int k, void *out, int64_t rows, int64_t out_stride, reshard_stream_t stream);
+
+/*
+ * reshard_combine -- experts' rows back to their tokens: out[t] = sum over j of weights[t, j] * y[position[t * k + j]].
+ * y [rows, cols] in dtype, weights [tokens, k] fp32 (NULL: 1), out [tokens, cols] in out_dtype. Slots without a place (a
+ * position that is negative or beyond the rows) add nothing, whatever their weight. Summed in fp32 in the order of j and rounded once.
+ */
+int reshard_combine(const void *y, int dtype, int64_t rows, int64_t cols, int64_t row_stride, const int32_t *position,
+                    const float *weights, int64_t tokens, int k, void *out, int out_dtype, int64_t out_stride,
+                    reshard_stream_t stream);
+
+/*
+ * reshard_combine_backward -- the gradients of reshard_combine, from grad [tokens, cols] in grad_dtype:
+ *   grad_y[position[s]] = weights[s] * grad[t], in y's type, one rounding; rows that no slot owns (see reshard_permute) 0
+ *   grad_weights[s] = <grad[t], y[position[s]]>, 0 for a slot without a place
+ * Either may be NULL: it is not computed (y is not read without grad_weights).
+ */
+int reshard_combine_backward(const void *grad, int grad_dtype, int64_t grad_stride, const void *y, int dtype, int64_t rows,
+                             int64_t cols, int64_t row_stride, const int32_t *order, const int32_t *position,
+                             const float *weights, int64_t tokens, int k, void *grad_y, int64_t grad_y_stride,
+                             float *grad_weights, reshard_stream_t stream);
+
+/*
+ * reshard_embedding -- rows of a vocabulary's shard: out[t] = scale * table[ids[t] - first_row], 0 where the id is not
+ * one of first_row .. first_row + rows - 1 (another shard's, or padding).
+ * ids [tokens] of id_bits 32 or 64, table [rows, cols] and out [tokens, cols] in dtype. scale 1 copies bit for bit;
+ * otherwise the product in fp32 is rounded once.
+ */
+int reshard_embedding(const void *ids, int id_bits, int64_t tokens, const void *table, int dtype, int64_t first_row, int64_t rows,
+                      int64_t cols, int64_t row_stride, float scale, void *out, int64_t out_stride, reshard_stream_t stream);
+
+/*
+ * reshard_embedding_backward -- the gradient to the table: grad_table[r] = scale * (sum of grad[t] over the tokens with
+ * ids[t] = first_row + r), fp32 sums rounded once to table_dtype. Written whole, 0 for rows without a token; or, with
+ * accumulate, added to the rows that have one, the others not touched.
+ * workspace: reshard_embedding_backward_workspace(tokens, cols) bytes, 256-byte aligned.
+ */
+int64_t reshard_embedding_backward_workspace(int64_t tokens, int64_t cols);
+int reshard_embedding_backward(const void *grad, int grad_dtype, int64_t tokens, int64_t cols, int64_t grad_stride, const void *ids,
+                               int id_bits, int64_t first_row, int64_t rows, float scale, void *grad_table, int table_dtype,
+                               int64_t table_stride, int accumulate, void *workspace, int64_t workspace_bytes,
+                               reshard_stream_t stream);
+
+/*
+ * reshard_tensors_create -- a list of `count` dense tensors on the current device, for the calls below: their addresses,
+ * numbers of elements (0 is fine) and types (BF16, F16, F32, mixed as they come). Host memory only; made once for tensors
+ * that stay where they are, and valid while they do. reshard_tensors_destroy frees it (NULL is fine); a call or a captured graph
+ * that used it does not need it any more.
+ */
+typedef struct reshard_tensors reshard_tensors_t;
+int reshard_tensors_create(const void *const *at, const int64_t *elements, const int32_t *dtypes, int64_t count, reshard_tensors_t **list);
+int reshard_tensors_destroy(reshard_tensors_t *list);
+
+/*
+ * reshard_grad_norm -- norm[0] (fp32, on the device) = sqrt(sum of x^2 over every element of the list), 0 for an empty one. Neither
+ * the squares nor their sum leave the range: the norm is infinite only if it is beyond fp32 or an element is, and NaN if one is.
+ * Norms of parts (other ranks' shards) combine as the root of their squares' sum.
+ * workspace: reshard_grad_norm_workspace() bytes, 8-byte aligned.
+ *
+ * reshard_clip_grads -- every tensor x of the list times min(1, limit / (norm + 1e-6)) into the tensor of `into` in the same
+ * place (as many elements, any of the types; NULL: in place), product in fp32, rounded once. norm_in: the norm on the device
+ * (several ranks' combined), or NULL: it is computed as above and written to norm_out. In place, a norm under the
+ * limit leaves the tensors unread and unwritten. A NaN norm makes every value NaN and an infinite one 0 (NaN where it is infinite),
+ * but an infinite limit leaves all as it is. limit >= 0. Tensors that are written must not overlap one another, nor others that are read.
+ */
+int64_t reshard_grad_norm_workspace(void);
+int reshard_grad_norm(const reshard_tensors_t *list, float *norm, void *workspace, int64_t workspace_bytes, reshard_stream_t stream);
+int reshard_clip_grads(const reshard_tensors_t *list, const reshard_tensors_t *into, double limit, const float *norm_in,
+                       float *norm_out, void *workspace, int64_t workspace_bytes, reshard_stream_t stream);
+
+/*
  * reshard_ops_call -- one of the calls above with its arguments, in order, as 64-bit words (integers and pointers in `i`,
  * floats in `f`): for bindings in which marshalling each argument costs more than the call. op is a RESHARD_OP_* number;
  * another one is INVALID_ARG.
@@ -141,6 +220,13 @@ int reshard_experts_fp8(const void *x, int dtype, int64_t tokens, int64_t hidden
 #define RESHARD_OP_MATMUL_FP8 5
 #define RESHARD_OP_LINEAR_FP8 6
 #define RESHARD_OP_EXPERTS_FP8 7
+#define RESHARD_OP_PERMUTE 8
+#define RESHARD_OP_COMBINE 9
+#define RESHARD_OP_COMBINE_BACKWARD 10
+#define RESHARD_OP_EMBEDDING 11
+#define RESHARD_OP_EMBEDDING_BACKWARD 12
+#define RESHARD_OP_GRAD_NORM 13
+#define RESHARD_OP_CLIP_GRADS 14
 typedef union {
   int64_t i;
   double f;
