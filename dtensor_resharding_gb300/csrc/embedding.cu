@@ -1,11 +1,11 @@
 // The gradient of an embedding: grad_table[r] = scale * sum of grad[t] over the tokens t whose id is row r of this shard.
 //
-// Four launches. *Zero* writes the table's zeros while *sort* (one cluster) sorts the tokens by row beside it: a radix sort
-// of the pairs (row, token), at most ten bits a pass, stable, so that a row's tokens ascend. *Sum* takes runs of the sorted
-// tokens, one thread eight columns: rows that begin and end inside a run are written from there, the pieces of one
+// Four launches. *Sort* (one cluster) sorts the tokens by row: a radix sort of the pairs (row, token), at most ten bits a pass,
+// stable, so that a row's tokens ascend. *Zero* writes the table's zeros beside it. *Sum* takes runs of the sorted
+// tokens, one thread a piece of the columns: rows that begin and end inside a run are written from there, the parts of one
 // that does not are left in the workspace, and *join* adds them in the order of the runs. A token that is half of the
 // text is so spread over as many CTAs as it has runs, without atomics: the order of every sum follows from the ids alone.
-// Sums are fp32, rounded once. Bound by the write of the table (and the read of the gradients).
+// Sums are fp32, rounded once. Bound by the write of the table and the read of the gradients.
 #include <algorithm>
 
 #include "ops_common.cuh"
@@ -20,31 +20,6 @@ constexpr int64_t kAlign = 256;
 int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
 int launched(cudaError_t e, const char *what) { return e == cudaSuccess ? RESHARD_OK : cuda_error(e, what); }
-
-// ------------------------------------------------------------------------------------------------------------- zero --
-
-constexpr int kZeroThreads = 512;
-constexpr int64_t kZeroPiece = 16384;      // bytes a warp writes at a time
-
-// Zeros in `rows` rows of `bytes` bytes, `stride` apart, all a multiple of `unit` (2 or 4) bytes.
-__global__ void __launch_bounds__(kZeroThreads) reshard_zero_kernel(uint8_t *base, int64_t rows, int64_t bytes, int64_t stride, int unit) {
-  grid_enter();
-  const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (kZeroThreads / 32);
-  const int64_t pieces = (bytes + kZeroPiece - 1) / kZeroPiece;
-  for (int64_t w = (int64_t)blockIdx.x * (kZeroThreads / 32) + (threadIdx.x >> 5); w < rows * pieces; w += warps) {
-    const int64_t r = w / pieces, at = (w - r * pieces) * kZeroPiece;
-    uint8_t *p = base + r * stride + at;
-    int64_t n = min(kZeroPiece, bytes - at);
-    const int head = (int)min((int64_t)(-reinterpret_cast<uintptr_t>(p) & 15), n);
-    for (int i = lane * unit; i < head; i += 32 * unit) unit == 4 ? (void)(*reinterpret_cast<uint32_t *>(p + i) = 0) : (void)(*reinterpret_cast<uint16_t *>(p + i) = 0);
-    p += head, n -= head;
-#pragma unroll 4
-    for (int64_t i = lane; i < n / 16; i += 32) reinterpret_cast<uint4 *>(p)[i] = make_uint4(0, 0, 0, 0);
-    for (int64_t i = n / 16 * 16 + lane * unit; i < n; i += 32 * unit)
-      unit == 4 ? (void)(*reinterpret_cast<uint32_t *>(p + i) = 0) : (void)(*reinterpret_cast<uint16_t *>(p + i) = 0);
-  }
-}
 
 // ------------------------------------------------------------------------------------------------------------- sort --
 
@@ -67,6 +42,7 @@ __device__ __forceinline__ void cluster_barrier() {
 // its first place of each digit, and a second walk places 32 pairs at a time, equal digits ranked by lane (match.any).
 // Integer counts: the order is the same on every run. Bound by latency (two walks and three barriers a pass).
 __global__ void __launch_bounds__(kSortWarps * 32) reshard_sort_rows_kernel(Sort a) {
+  grid_enter();
   extern __shared__ int32_t count[];             // [warp][digit], then this CTA's sums [digit], then its first places [digit]
   __shared__ int32_t warp_sum[kSortWarps];
   const int bins = 1 << a.bits;
@@ -83,7 +59,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) reshard_sort_rows_kernel(Sort
       uint2 p = make_uint2(~0u, 0);
       if (i < hi) {
         if (pass == 0) {
-          const int64_t id = a.wide_ids ? __ldg(static_cast<const long long *>(a.ids) + i) : __ldg(static_cast<const int32_t *>(a.ids) + i);
+          const int64_t id = a.wide_ids ? static_cast<const int64_t *>(a.ids)[i] : static_cast<const int32_t *>(a.ids)[i];
           if (id >= a.first && id - a.first < a.rows) p = make_uint2((uint32_t)(id - a.first), (uint32_t)i);
         } else {
           p = __ldcg(from + i);
@@ -166,135 +142,181 @@ __global__ void __launch_bounds__(kSortWarps * 32) reshard_sort_rows_kernel(Sort
     cluster_barrier();                           // the pairs are in place, and nobody reads `sum` any more
   }
   if (cta == 0 && tid == 0) *a.held = (int32_t)n;
-  // The grid before (the zeros) may still be running: this one began when all of its CTAs had, behind everything that
-  // came earlier on the stream. The grid behind this one has to find both done.
-  grid_wait();
+}
+
+// ------------------------------------------------------------------------------------------------------------- zero --
+
+constexpr int kZeroThreads = 256;
+constexpr int64_t kZeroPiece = 32768;      // bytes of a CTA
+
+// Zeros in `rows` rows of `bytes` bytes, `stride` apart, all a multiple of `unit` (2 or 4) bytes. Behind a sort it begins
+// when that has begun, and so behind everything that came earlier on the stream; only its last CTA waits for the sort, so that the
+// grid behind this one finds both done.
+__global__ void __launch_bounds__(kZeroThreads) reshard_zero_kernel(uint8_t *base, int64_t rows, int64_t bytes, int64_t stride, int unit, bool behind_sort) {
+  if (!behind_sort) grid_wait();
+  grid_release();
+  const int64_t pieces = (bytes + kZeroPiece - 1) / kZeroPiece;
+  for (int64_t w = blockIdx.x; w < rows * pieces; w += gridDim.x) {
+    const int64_t r = w / pieces, at = (w - r * pieces) * kZeroPiece;
+    uint8_t *p = base + r * stride + at;
+    int n = (int)min(kZeroPiece, bytes - at);
+    auto small = [&](int i) {
+      if (unit == 4) *reinterpret_cast<uint32_t *>(p + i) = 0;
+      else *reinterpret_cast<uint16_t *>(p + i) = 0;
+    };
+    const int head = min(n, (int)(-reinterpret_cast<uintptr_t>(p) & 15));
+    if ((int)threadIdx.x * unit < head) small((int)threadIdx.x * unit);
+    p += head, n -= head;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < n / 16; i += kZeroThreads) reinterpret_cast<uint4 *>(p)[i] = make_uint4(0, 0, 0, 0);
+    const int tail = (n & ~15) + (int)threadIdx.x * unit;
+    if (tail < n) small(tail);
+  }
+  if (behind_sort && blockIdx.x == gridDim.x - 1) grid_wait();
 }
 
 // -------------------------------------------------------------------------------------------------------------- sum --
 
 constexpr int kSumThreads = 128;
-constexpr int kJoinThreads = 256;
+constexpr int kJoinColumns = kSumThreads * 4;
 
 struct Sum {
   const uint2 *sorted;
   const int32_t *held;
   const void *grad;
-  int64_t cols, grad_stride;
+  int64_t tokens, cols, grad_stride;
   float scale;
   void *table;
   int64_t table_stride;
-  bool accumulate, wide, wide_table;
+  bool accumulate, wide_table;
   float *part;                       // [run][2][pitch]: of the row that a run begins inside, and of the one that it ends inside
   int64_t pitch;
   int run;                           // sorted tokens of a CTA
   int slices;                        // CTAs a run
 };
 
-// Eight of a row's sums, scaled, into the table (its other values are another thread's).
-template <typename T>
-__device__ __forceinline__ void write_sums(const Sum &a, uint32_t row, int64_t c, const float (&sum)[8]) {
+// N of a row's sums, scaled, into the table.
+template <typename T, int N>
+__device__ __forceinline__ void write_sums(const Sum &a, uint32_t row, int64_t c, const float (&sum)[N]) {
   T *const to = static_cast<T *>(a.table) + (int64_t)row * a.table_stride + c;
-  float x[8];
-  const bool whole = a.wide_table && c + 8 <= a.cols;
+  float x[N];
+  const bool whole = a.wide_table && c + N <= a.cols;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = sum[e] * a.scale;
+  for (int e = 0; e < N; ++e) x[e] = sum[e] * a.scale;
   if (a.accumulate) {
-    float old[8];
-    load_values<T, 8>(to, (int)min((int64_t)8, a.cols - c), whole, old);
+    float old[N];
+    load_values<T, N>(to, (int)min((int64_t)N, a.cols - c), whole, old);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] += old[e];
+    for (int e = 0; e < N; ++e) x[e] += old[e];
   }
   if (whole) {
-    store_eight(to, x);
+    store_piece(to, x);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
+    for (int e = 0; e < N; ++e)
       if (c + e < a.cols) to[e] = from_f32<T>(x[e]);
   }
 }
 
 template <typename TG, typename T, bool Wide>
 __global__ void __launch_bounds__(kSumThreads) reshard_sum_rows_kernel(Sum a) {
+  constexpr int kN = kPieceOf<TG, T>, kRows = 8;       // rows in flight
   grid_enter();
+  const int lane = threadIdx.x & 31;
   const int64_t run = blockIdx.x / (uint32_t)a.slices;
-  const int64_t c = ((int64_t)(blockIdx.x % (uint32_t)a.slices) * kSumThreads + threadIdx.x) * 8;
-  const int64_t held = *a.held, lo = run * a.run, hi = min(lo + a.run, held);
-  if (lo >= held || c >= a.cols) return;
+  const int64_t c = ((int64_t)(blockIdx.x % (uint32_t)a.slices) * kSumThreads + threadIdx.x) * kN;
+  const int64_t lo = run * a.run;
+  // what lies behind the last pair is read as well, and not used: nothing here waits for how many there are
+  uint2 mine = lo + lane < a.tokens ? a.sorted[lo + lane] : make_uint2(0, 0);
+  const uint32_t before = lo > 0 ? a.sorted[lo - 1].x : ~0u;
+  const uint32_t after = lo + a.run < a.tokens ? a.sorted[lo + a.run].x : ~0u;
+  const int64_t held = *a.held, hi = min(lo + a.run, held);
+  if (lo >= held || c - lane * kN >= a.cols) return;       // whole warps
   const TG *const grad = static_cast<const TG *>(a.grad) + c;
-  const int left = (int)min((int64_t)8, a.cols - c);
-  uint32_t row = a.sorted[lo].x;
-  bool head = lo > 0 && a.sorted[lo - 1].x == row;
+  const int left = (int)max((int64_t)0, min((int64_t)kN, a.cols - c));
+  uint32_t row = __shfl_sync(kFull, mine.x, 0);
+  bool head = before == row;
   float *const part = a.part + 2 * run * a.pitch + c;
-  float sum[8] = {};
+  float sum[kN] = {};
   auto keep = [&](float *to) {
+    if (left == 0) return;
 #pragma unroll
-    for (int e = 0; e < 8; e += 4) *reinterpret_cast<float4 *>(to + e) = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
+    for (int e = 0; e < kN; e += 4) *reinterpret_cast<float4 *>(to + e) = make_float4(sum[e], sum[e + 1], sum[e + 2], sum[e + 3]);
   };
-  constexpr int kRows = sizeof(TG) == 4 ? 4 : 8;       // rows in flight
-  for (int64_t i = lo; i < hi; i += kRows) {
-    uint2 p[kRows];
-    Eight<TG, Wide> v[kRows];
+  for (int64_t base = lo; base < hi; base += 32) {
+    if (base > lo) mine = base + lane < hi ? a.sorted[base + lane] : make_uint2(0, 0);
+    const int n = (int)min((int64_t)32, hi - base);
+    for (int i = 0; i < n; i += kRows) {
+      Piece<TG, kN, Wide> v[kRows];
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) p[u] = i + u < hi ? __ldg(a.sorted + i + u) : make_uint2(~0u, 0);
-#pragma unroll
-    for (int u = 0; u < kRows; ++u)
-      if (left == 8 && i + u < hi) v[u].ask(grad + p[u].y * a.grad_stride);
-#pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      if (i + u >= hi) break;
-      if (p[u].x != row) {
-        if (head) keep(part);
-        else write_sums<T>(a, row, c, sum);
-        head = false, row = p[u].x;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+      for (int u = 0; u < kRows; ++u) {
+        const uint32_t t = __shfl_sync(kFull, mine.y, i + u);      // i is a multiple of kRows: below 32
+        if (left == kN && i + u < n) v[u].ask(grad + t * a.grad_stride);
       }
-      const TG *const from = grad + p[u].y * a.grad_stride;
-      float x[8];
-      if (left == 8) v[u].take(from, x);
-      else load_values<TG, 8>(from, left, false, x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += x[e];
+      for (int u = 0; u < kRows; ++u) {
+        if (i + u >= n) break;
+        const uint32_t r = __shfl_sync(kFull, mine.x, i + u), t = __shfl_sync(kFull, mine.y, i + u);
+        if (r != row) {
+          if (head) keep(part);
+          else if (left) write_sums<T, kN>(a, row, c, sum);
+          head = false, row = r;
+#pragma unroll
+          for (int e = 0; e < kN; ++e) sum[e] = 0.0f;
+        }
+        const TG *const from = grad + t * a.grad_stride;
+        float x[kN];
+        if (left == kN) v[u].take(from, x);
+        else load_values<TG, kN>(from, left, false, x);
+#pragma unroll
+        for (int e = 0; e < kN; ++e) sum[e] += x[e];
+      }
     }
   }
   if (head) keep(part);
-  else if (hi < held && a.sorted[hi].x == row) keep(part + a.pitch);
-  else write_sums<T>(a, row, c, sum);
+  else if (hi < held && after == row) keep(part + a.pitch);
+  else if (left) write_sums<T, kN>(a, row, c, sum);
 }
 
-// The rows that end in another run than they begin in: one CTA each run that such a row begins in.
+// The rows that end in another run than they begin in: the CTAs of the run that such a row begins in.
 template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) reshard_join_rows_kernel(Sum a) {
+__global__ void __launch_bounds__(kSumThreads) reshard_join_rows_kernel(Sum a) {
   grid_enter();
-  const int64_t run = blockIdx.x, held = *a.held, lo = run * a.run, hi = lo + a.run;
-  if (hi >= held) return;
-  const uint32_t row = a.sorted[hi - 1].x;
-  if (a.sorted[hi].x != row || (lo > 0 && a.sorted[lo - 1].x == row)) return;
-  int64_t in = hi, out = held;                   // the last of the row's tokens is sorted[in]
-  while (out - in > 1) {
-    const int64_t mid = (in + out) / 2;
-    if (a.sorted[mid].x == row) in = mid;
-    else out = mid;
-  }
-  const int64_t last = in / a.run;
-  for (int64_t c = threadIdx.x * 8; c < a.cols; c += kJoinThreads * 8) {
-    float sum[8];
-    load_values<float, 8>(a.part + (2 * run + 1) * a.pitch + c, 8, true, sum);
-#pragma unroll 4
-    for (int64_t r = run + 1; r <= last; ++r) {
-      float x[8];
-      load_values<float, 8>(a.part + 2 * r * a.pitch + c, 8, true, x);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += x[e];
+  const int lane = threadIdx.x & 31;
+  const int64_t run = blockIdx.x / (uint32_t)a.slices;
+  const int64_t c = (int64_t)(blockIdx.x % (uint32_t)a.slices) * kJoinColumns + threadIdx.x * 4;
+  const int64_t lo = run * a.run, hi = lo + a.run;       // hi < tokens: no CTA has the last run
+  const uint32_t row = a.sorted[hi - 1].x, after = a.sorted[hi].x, before = lo > 0 ? a.sorted[lo - 1].x : ~0u;
+  const int64_t held = *a.held;
+  if (hi >= held || after != row || before == row) return;
+  // the run that the row ends in: the first whose next run begins with another row, or that is the last
+  int64_t last = run + 1;
+  for (;; last += 32) {
+    const int64_t next = (last + lane + 1) * a.run;
+    const uint32_t ends = __ballot_sync(kFull, next >= held || a.sorted[min(next, held - 1)].x != row);
+    if (ends) {
+      last += __ffs(ends) - 1;
+      break;
     }
-    write_sums<T>(a, row, c, sum);
   }
+  if (c >= a.cols) return;
+  float sum[4];
+  load_values<float, 4>(a.part + (2 * run + 1) * a.pitch + c, 4, true, sum);
+  const float *from = a.part + 2 * (run + 1) * a.pitch + c;
+#pragma unroll 8
+  for (int64_t r = run + 1; r <= last; ++r, from += 2 * a.pitch) {
+    float x[4];
+    load_values<float, 4>(from, 4, true, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum[e] += x[e];
+  }
+  write_sums<T, 4>(a, row, c, sum);
 }
 
+constexpr int64_t kMinRun = 16, kRuns = 256;
 // Sorted tokens of a CTA: few, so that a row's tokens are read by many CTAs, but at most 2,048 runs, whose pieces of rows
 // (two each) the workspace holds.
-int64_t run_of(int64_t tokens) { return std::max<int64_t>(16, (tokens + 2047) / 2048); }
+int64_t run_of(int64_t tokens) { return std::max<int64_t>(kMinRun, (tokens + kRuns - 1) / kRuns); }
 
 struct Layout {
   int64_t sorted, held, runs, pitch, part;
@@ -327,7 +349,7 @@ extern "C" int reshard_embedding_backward(const void *grad, int grad_dtype, int6
   c.invalid(!element_bytes(grad_dtype) || !element_bytes(table_dtype), "grad_dtype and table_dtype must be BF16, F16 or F32");
   c.invalid(grad_stride < cols || table_stride < cols, "a row stride is shorter than the row");
   if (c.ok() && tokens > 0)
-    c.unsupported(Layout(tokens, cols).runs * ((cols + kSumThreads * 8 - 1) / (kSumThreads * 8)) > INT32_MAX, "too many columns for one launch");
+    c.unsupported(Layout(tokens, cols).runs * ((cols + kJoinColumns - 1) / kJoinColumns) > INT32_MAX, "too many columns for one launch");
   const bool work = rows > 0 && cols > 0 && (tokens > 0 || !accumulate);
   if (work && c.ok()) {
     c.pointer(grad_table, "grad_table", (uintptr_t)element_bytes(table_dtype));
@@ -342,41 +364,46 @@ extern "C" int reshard_embedding_backward(const void *grad, int grad_dtype, int6
   if (!work) return RESHARD_OK;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   const int es = element_bytes(table_dtype);
-  int sms = 0, rc = device_sms(&sms);
-  if (rc) return rc;
-  // Without zeros to write the same kernel, with no rows, stands before the sort: what the sort begins behind.
-  const bool dense = table_stride == cols;
-  const int64_t zero_rows = accumulate ? 0 : dense ? 1 : rows, zero_bytes = (dense ? rows : 1) * cols * es;
-  if ((rc = launched(launch(reshard_zero_kernel, dim3(accumulate ? 1u : (unsigned)sms), kZeroThreads, 0, 1, stream, static_cast<uint8_t *>(grad_table),
-                            zero_rows, zero_bytes, table_stride * es, es), "launching reshard_zero_kernel")))
-    return rc;
-  if (tokens == 0) return RESHARD_OK;
   const Layout l(tokens, cols);
   uint8_t *const at = static_cast<uint8_t *>(workspace);
-  Sort s{ids, id_bits == 64, tokens, first_row, rows, reinterpret_cast<uint2 *>(at), reinterpret_cast<uint2 *>(at + l.sorted),
-         reinterpret_cast<int32_t *>(at + 2 * l.sorted), 1, 1};
-  int need = 1;
-  while (need < 30 && (rows - 1) >> need) ++need;
-  s.passes = (need + kSortBits - 1) / kSortBits;
-  s.bits = (need + s.passes - 1) / s.passes;
-  const size_t smem = (size_t)(kSortWarps + 2) * 4 << s.bits;
-  if ((rc = allow_smem<reshard_sort_rows_kernel>((size_t)(kSortWarps + 2) * 4 << kSortBits))) return rc;
-  if ((rc = launched(launch(reshard_sort_rows_kernel, dim3(kSortCluster), kSortWarps * 32, smem, kSortCluster, stream, s), "launching reshard_sort_rows_kernel"))) return rc;
-  Sum a{s.sorted, s.held, grad, cols, grad_stride, scale, grad_table, table_stride, accumulate != 0, false, false, nullptr, l.pitch, (int)run_of(tokens), 0};
-  a.part = reinterpret_cast<float *>(at + 2 * l.sorted + l.held);
-  a.wide = aligned16(grad, grad_stride, element_bytes(grad_dtype));
-  a.wide_table = aligned16(grad_table, table_stride, es);
-  a.slices = (int)((cols + kSumThreads * 8 - 1) / (kSumThreads * 8));
+  int rc = RESHARD_OK;
+  uint2 *const sorted = reinterpret_cast<uint2 *>(at);
+  int32_t *const held = reinterpret_cast<int32_t *>(at + 2 * l.sorted);
+  if (tokens > 0) {
+    Sort s{ids, id_bits == 64, tokens, first_row, rows, sorted, reinterpret_cast<uint2 *>(at + l.sorted), held, 1, 1};
+    int need = 1;
+    while (need < 30 && (rows - 1) >> need) ++need;
+    s.passes = (need + kSortBits - 1) / kSortBits;
+    s.bits = (need + s.passes - 1) / s.passes;
+    if ((rc = allow_smem<reshard_sort_rows_kernel>((size_t)(kSortWarps + 2) * 4 << kSortBits))) return rc;
+    if ((rc = launched(launch(reshard_sort_rows_kernel, dim3(kSortCluster), kSortWarps * 32, (size_t)(kSortWarps + 2) * 4 << s.bits, kSortCluster, stream, s),
+                       "launching reshard_sort_rows_kernel")))
+      return rc;
+  }
+  if (!accumulate) {
+    const bool dense = table_stride == cols;
+    const int64_t zero_rows = dense ? 1 : rows, bytes = (dense ? rows : 1) * cols * es;
+    const int64_t ctas = std::min<int64_t>(RESHARD_MAX_EXTENT, zero_rows * ((bytes + kZeroPiece - 1) / kZeroPiece));
+    if ((rc = launched(launch(reshard_zero_kernel, dim3((unsigned)ctas), kZeroThreads, 0, 1, stream, static_cast<uint8_t *>(grad_table), zero_rows, bytes,
+                              table_stride * es, es, tokens > 0), "launching reshard_zero_kernel")))
+      return rc;
+  }
+  if (tokens == 0) return RESHARD_OK;
+  Sum a{sorted, held, grad, tokens, cols, grad_stride, scale, grad_table, table_stride, accumulate != 0, aligned16(grad_table, table_stride, es),
+        reinterpret_cast<float *>(at + 2 * l.sorted + l.held), l.pitch, (int)run_of(tokens), 0};
+  const bool wide = aligned16(grad, grad_stride, element_bytes(grad_dtype));
   rc = launched(by_type(grad_dtype, [&](auto g) {
     using TG = decltype(g);
     return by_type(table_dtype, [&](auto t) {
       using T = decltype(t);
-      return launch(a.wide ? reshard_sum_rows_kernel<TG, T, true> : reshard_sum_rows_kernel<TG, T, false>, dim3((unsigned)(l.runs * a.slices)), kSumThreads, 0,
+      a.slices = (int)((cols + kSumThreads * kPieceOf<TG, T> - 1) / (kSumThreads * kPieceOf<TG, T>));
+      return launch(wide ? reshard_sum_rows_kernel<TG, T, true> : reshard_sum_rows_kernel<TG, T, false>, dim3((unsigned)(l.runs * a.slices)), kSumThreads, 0,
                     1, stream, a);
     });
   }), "launching reshard_sum_rows_kernel");
   if (rc || l.runs == 1) return rc;
+  a.slices = (int)((cols + kJoinColumns - 1) / kJoinColumns);
   return launched(by_type(table_dtype, [&](auto t) {
-    return launch(reshard_join_rows_kernel<decltype(t)>, dim3((unsigned)(l.runs - 1)), kJoinThreads, 0, 1, stream, a);
+    return launch(reshard_join_rows_kernel<decltype(t)>, dim3((unsigned)((l.runs - 1) * a.slices)), kSumThreads, 0, 1, stream, a);
   }), "launching reshard_join_rows_kernel");
 } OPS_CATCH

@@ -1,6 +1,6 @@
 // The global norm of many tensors, and their clipping: norm = sqrt(sum x^2), x * min(1, limit / (norm + 1e-6)).
 //
-// A list (reshard_tensors_create) keeps the tensors' places on the host. A launch takes up to kBatch of them as its argument,
+// A list (reshard_tensors_create) keeps the tensors' places on the host. A launch takes some of them as its argument,
 // so that a call copies nothing to the device and allocates nothing there, and a captured one holds its list. A tensor is
 // cut into units of one size (its head before the first 16-byte boundary belongs to the first); the CTAs of a launch share
 // the units of all its tensors evenly, whatever the tensors' sizes, and look their first one up by bisection.
@@ -28,6 +28,7 @@ struct reshard_tensors {
   bool overlap = false;              // some elements are in two tensors
   uintptr_t low = UINTPTR_MAX, high = 0;
   int64_t unit = 0;                  // elements
+  int64_t units = 0;                 // of all tensors
 };
 
 namespace reshard {
@@ -36,31 +37,47 @@ namespace ops {
 namespace {
 
 constexpr int kNormThreads = 256;
-constexpr int kBatch = 1024;                      // tensors a launch
 constexpr int kMaxCtas = 1024;                    // whose sums the workspace holds
 constexpr int kUnitStep = kNormThreads * 8;       // a unit is a multiple of it
 constexpr int kCtasPerSm = 4;
+constexpr int kFillCtas = 608;                    // of 152 SMs
 constexpr double kEps = 1e-6;
 
-// Up to kBatch tensors: 28 KB of the 32 that a kernel's arguments may have.
+// The tensors of a launch, as one of its arguments: those have 32,764 bytes. A tensor is its address and one word: the units of
+// the tensors before it (32 bits), the elements of its last unit (16), its type (2).
+template <int N>
+struct Places {
+  uint64_t at[N];
+};
+struct InPlace {};
+template <bool Moved>                // with places of their own for the clipped values
 struct Batch {
-  uint64_t at[kBatch];
-  uint64_t to[kBatch];               // where the clipped values go
-  uint64_t n[kBatch];                // elements << 4 | type of `to` << 2 | type of `at`
-  uint32_t first[kBatch + 1];        // units before the tensor's
+  static constexpr int kMost = Moved ? 1300 : 2000;
+  uint64_t at[kMost];
+  uint64_t word[kMost + 1];          // the last: all units
+  std::conditional_t<Moved, Places<kMost>, InPlace> to;
   int count;
   int unit;
+  __host__ __device__ uint32_t first(int t) const { return (uint32_t)word[t]; }
+  __host__ __device__ uint32_t units() const { return first(count); }
+  __device__ __forceinline__ int type(int t) const { return (int)(word[t] >> 48); }
+  __device__ __forceinline__ int64_t elements(int t) const { return (int64_t)(first(t + 1) - first(t) - 1) * unit + (int64_t)(word[t] >> 32 & 0xffff); }
+  __device__ __forceinline__ uint64_t target(int t) const {
+    if constexpr (Moved) return to.at[t];
+    else return at[t];
+  }
 };
-static_assert(sizeof(Batch) + 64 <= 32764, "a kernel's arguments");
+static_assert(sizeof(Batch<true>) + 64 <= 32764 && sizeof(Batch<false>) + 64 <= 32764, "a kernel's arguments");
 
 int launched(cudaError_t e, const char *what) { return e == cudaSuccess ? RESHARD_OK : cuda_error(e, what); }
 
 // The tensor that holds unit u.
-__device__ __forceinline__ int find(const Batch &b, uint32_t u) {
+template <typename B>
+__device__ __forceinline__ int find(const B &b, uint32_t u) {
   int in = 0, out = b.count;
   while (out - in > 1) {
     const int mid = (in + out) / 2;
-    if (b.first[mid] <= u) in = mid;
+    if (b.first(mid) <= u) in = mid;
     else out = mid;
   }
   return in;
@@ -70,22 +87,26 @@ __device__ __forceinline__ int find(const Batch &b, uint32_t u) {
 struct Squares {
   float s = 0.0f, r = 0.0f;
   double d = 0.0;
-  // x: up to 64 bytes' values, sq: the fp32 sum of their squares
+  // Adds an fp32 sum of squares; false where fp32 may not hold it: its values are to be added by add_far.
+  __device__ __forceinline__ bool add(float sq) {
+    if (!(sq > 0x1p-80f && sq < 0x1p100f)) return false;
+    const float t = s + sq, z = t - s;
+    r += (s - (t - z)) + (sq - z);
+    s = t;
+    return true;
+  }
   template <int N>
-  __device__ __forceinline__ void add(float sq, const float (&x)[N]) {
-    if (sq > 0x1p-80f && sq < 0x1p100f) {
-      const float t = s + sq, z = t - s;
-      r += (s - (t - z)) + (sq - z);
-      s = t;
-    } else {
-      bool any = false;
+  __device__ __forceinline__ void add_far(const float (&x)[N]) {
+    bool any = false;
 #pragma unroll
-      for (int i = 0; i < N; ++i) any |= x[i] != 0.0f;      // NaN too
-      if (any) {
+    for (int i = 0; i < N; ++i) any |= x[i] != 0.0f;      // NaN too
+    if (!any) return;
 #pragma unroll
-        for (int i = 0; i < N; ++i) d += (double)x[i] * (double)x[i];
-      }
-    }
+    for (int i = 0; i < N; ++i) d += (double)x[i] * (double)x[i];
+  }
+  __device__ __forceinline__ void add_one(float v) {
+    const float x[1] = {v};
+    if (!add(v * v)) add_far(x);
   }
   __device__ __forceinline__ double total() const { return (double)s + (double)r + d; }
 };
@@ -112,56 +133,51 @@ __device__ __forceinline__ void add_unit(const T *p, int64_t n, int64_t unit, in
   constexpr int kPer = 16 / sizeof(T), kAhead = 4;
   const int tid = threadIdx.x;
   const int64_t head = head_of(p, n);
-  if (unit == 0 && tid < head) {
-    const float x[1] = {to_f32(p[tid])};
-    sum.add(x[0] * x[0], x);
-  }
+  if (unit == 0 && tid < head) sum.add_one(to_f32(p[tid]));
   const T *const body = p + head + unit * step;
   const int m = (int)max((int64_t)0, min((int64_t)step, n - head - unit * step));
   const int words = m / kPer;
   for (int w0 = tid; w0 < words; w0 += kNormThreads * kAhead) {
-    Pack<T, kPer> v[kAhead];
+    Words<T, kPer> v[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int w = w0 + kNormThreads * u;
-      v[u] = w < words ? *reinterpret_cast<const Pack<T, kPer> *>(body + w * kPer) : Pack<T, kPer>{};
+      v[u] = Words<T, kPer>{};
+      if (w < words) v[u].load(body + w * kPer);
     }
-    float x[kPer * kAhead], sq[kAhead];
+    float sq[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
+      float x[kPer];
+      v[u].values(x);
       sq[u] = 0.0f;
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        x[u * kPer + i] = to_f32(v[u].v[i]);
-        sq[u] = fmaf(x[u * kPer + i], x[u * kPer + i], sq[u]);
+      for (int i = 0; i < kPer; ++i) sq[u] = fmaf(x[i], x[i], sq[u]);
+    }
+    if (!sum.add((sq[0] + sq[1]) + (sq[2] + sq[3]))) {
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        float x[kPer];
+        v[u].values(x);
+        sum.add_far(x);
       }
     }
-    sum.add((sq[0] + sq[1]) + (sq[2] + sq[3]), x);
   }
-  if (tid < m - words * kPer) {
-    const float x[1] = {to_f32(body[words * kPer + tid])};
-    sum.add(x[0] * x[0], x);
-  }
+  if (tid < m - words * kPer) sum.add_one(to_f32(body[words * kPer + tid]));
 }
 
-// Each CTA's sum of squares over its share of the launch's units; later launches of a call add to it.
-__global__ void __launch_bounds__(kNormThreads, kCtasPerSm) reshard_squares_kernel(const __grid_constant__ Batch b, double *part, bool fresh) {
+// Each CTA's sum of squares over its units of the launch, every gridDim-th; later launches of a call add to it.
+__global__ void __launch_bounds__(kNormThreads, kCtasPerSm) reshard_squares_kernel(const __grid_constant__ Batch<false> b, double *part, bool fresh) {
   grid_enter();
   __shared__ double warps[kNormThreads / 32];
-  const uint32_t units = b.first[b.count];
-  uint32_t u = (uint32_t)((uint64_t)units * blockIdx.x / gridDim.x);
-  const uint32_t end = (uint32_t)((uint64_t)units * (blockIdx.x + 1) / gridDim.x);
+  const uint32_t units = b.units();
   Squares sum;
-  if (u < end) {
-    int t = find(b, u);
-    for (; u < end; ++u) {
-      while (b.first[t + 1] <= u) ++t;
-      const int64_t n = (int64_t)(b.n[t] >> 4), unit = u - b.first[t];
-      const int type = (int)(b.n[t] & 3);
-      if (type == RESHARD_F32) add_unit(reinterpret_cast<const float *>(b.at[t]), n, unit, b.unit, sum);
-      else if (type == RESHARD_BF16) add_unit(reinterpret_cast<const __nv_bfloat16 *>(b.at[t]), n, unit, b.unit, sum);
-      else add_unit(reinterpret_cast<const __half *>(b.at[t]), n, unit, b.unit, sum);
-    }
+  for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int t = find(b, u), type = b.type(t);
+    const int64_t n = b.elements(t), unit = u - b.first(t);
+    if (type == RESHARD_F32) add_unit(reinterpret_cast<const float *>(b.at[t]), n, unit, b.unit, sum);
+    else if (type == RESHARD_BF16) add_unit(reinterpret_cast<const __nv_bfloat16 *>(b.at[t]), n, unit, b.unit, sum);
+    else add_unit(reinterpret_cast<const __half *>(b.at[t]), n, unit, b.unit, sum);
   }
   const double v = cta_sum(sum.total(), warps);
   if (threadIdx.x == 0) part[blockIdx.x] = fresh ? v : part[blockIdx.x] + v;
@@ -183,7 +199,7 @@ __global__ void __launch_bounds__(kNormThreads) reshard_norm_kernel(const double
 
 template <typename T, typename TO>
 __device__ __forceinline__ void clip_unit(const T *p, TO *to, int64_t n, int64_t unit, int step, float factor) {
-  constexpr int kAhead = 4;
+  constexpr int kN = kPieceOf<T, TO>, kAhead = 4;
   const int tid = threadIdx.x;
   const int64_t head = head_of(to, n);
   if (unit == 0 && tid < head) to[tid] = from_f32<TO>(to_f32(p[tid]) * factor);
@@ -192,97 +208,85 @@ __device__ __forceinline__ void clip_unit(const T *p, TO *to, int64_t n, int64_t
   const int m = (int)max((int64_t)0, min((int64_t)step, n - head - unit * step));
   auto body = [&](auto wide) {
     constexpr bool kWide = decltype(wide)::value;
-    for (int w0 = tid * 8; w0 + 8 <= m; w0 += kNormThreads * 8 * kAhead) {
-      Eight<T, kWide> v[kAhead];
+    for (int w0 = tid * kN; w0 + kN <= m; w0 += kNormThreads * kN * kAhead) {
+      Piece<T, kN, kWide> v[kAhead];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        const int w = w0 + kNormThreads * 8 * u;
-        if (w + 8 <= m) v[u].ask(from + w);
+        const int w = w0 + kNormThreads * kN * u;
+        if (w + kN <= m) v[u].ask(from + w);
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        const int w = w0 + kNormThreads * 8 * u;
-        if (w + 8 > m) break;
-        float x[8];
+        const int w = w0 + kNormThreads * kN * u;
+        if (w + kN > m) break;
+        float x[kN];
         v[u].take(from + w, x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= factor;
-        store_eight(into + w, x);
+        for (int e = 0; e < kN; ++e) x[e] *= factor;
+        store_piece(into + w, x);
       }
     }
   };
   if ((reinterpret_cast<uintptr_t>(from) & 15) == 0) body(std::true_type());
   else body(std::false_type());
-  const int rest = m & ~7;
+  const int rest = m / kN * kN;
   if (tid < m - rest) into[rest + tid] = from_f32<TO>(to_f32(from[rest + tid]) * factor);
 }
 
 // Every value times the factor. Under the limit in place there is nothing to do. norm: given, or NULL and found from the
 // CTAs' sums, by each CTA for itself; `out` gets it. The units are taken from the last to the first, since what the sums
-// read last is still in L2.
-__global__ void __launch_bounds__(kNormThreads, kCtasPerSm)
-    reshard_clip_kernel(const __grid_constant__ Batch b, const float *given, const double *part, int ctas, double limit, bool here, float *out) {
+// read last is still in L2: a batch has its tensors from the last to the first. A launch has tensors of one pair of types: all nine pairs in one kernel spilled its registers.
+template <typename T, typename TO, bool Moved>
+__global__ void __launch_bounds__(kNormThreads, (sizeof(TO) > sizeof(T) ? 6 : kCtasPerSm))
+    reshard_clip_kernel(const __grid_constant__ Batch<Moved> b, const float *given, const double *part, int ctas, double limit, float *out) {
   grid_enter();
   __shared__ double warps[kNormThreads / 32];
   const float norm = given ? *given : norm_of(part, ctas, warps);
   if (out && blockIdx.x == 0 && threadIdx.x == 0) *out = norm;
   const double f = limit / ((double)norm + kEps);
   const float factor = f >= 1.0 || isinf(limit) ? 1.0f : (float)f;      // NaN stays
-  if (here && factor == 1.0f) return;
-  const uint32_t units = b.first[b.count];
-  const uint32_t lo = (uint32_t)((uint64_t)units * blockIdx.x / gridDim.x);
-  uint32_t u = (uint32_t)((uint64_t)units * (blockIdx.x + 1) / gridDim.x);
-  if (u == lo) return;
-  int t = find(b, u - 1);
-  while (u-- > lo) {
-    while (b.first[t] > u) --t;
-    const int64_t n = (int64_t)(b.n[t] >> 4), unit = u - b.first[t];
-    const int type = (int)(b.n[t] & 3), to = (int)(b.n[t] >> 2 & 3);
-    auto go = [&](auto from_type, auto to_type) {
-      clip_unit(reinterpret_cast<const decltype(from_type) *>(b.at[t]), reinterpret_cast<decltype(to_type) *>(b.to[t]), n, unit, b.unit, factor);
-    };
-    auto by_to = [&](auto from_type) {
-      if (to == RESHARD_F32) go(from_type, float());
-      else if (to == RESHARD_BF16) go(from_type, __nv_bfloat16());
-      else go(from_type, __half());
-    };
-    if (type == RESHARD_F32) by_to(float());
-    else if (type == RESHARD_BF16) by_to(__nv_bfloat16());
-    else by_to(__half());
+  if (!Moved && factor == 1.0f) return;
+  const uint32_t units = b.units();
+  for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
+    const int t = find(b, u);
+    const uint32_t back = b.first(t + 1) - 1 - u;        // a tensor's units, too, from the last to the first
+    clip_unit(reinterpret_cast<const T *>(b.at[t]), reinterpret_cast<TO *>(b.target(t)), b.elements(t), back, b.unit, factor);
   }
 }
 
-// Calls f with each batch of the list that has something to do, from the last to the first where `back`.
-template <typename F>
-int batches(const reshard_tensors &list, const reshard_tensors *into, bool back, F &&f) {
-  const int64_t count = (int64_t)list.tensors.size(), pieces = (count + kBatch - 1) / kBatch;
-  Batch b;
-  for (int64_t i = 0; i < pieces; ++i) {
-    const int64_t at = (back ? pieces - 1 - i : i) * kBatch, end = std::min(count, at + kBatch);
-    b.count = 0, b.first[0] = 0, b.unit = (int)list.unit;
-    for (int64_t j = at; j < end; ++j) {
-      const auto &t = list.tensors[(size_t)j];
-      if (t.n == 0) continue;
-      const auto &o = into ? into->tensors[(size_t)j] : t;
+// Calls f with each batch of the list that has something to do, from the last to the first where `back`: of all its tensors,
+// or of those of one type whose targets in `into` have one type.
+template <bool Moved, typename F>
+int batches(const reshard_tensors &list, const reshard_tensors *into, int dtype, int to, bool back, F &&f) {
+  const int64_t count = (int64_t)list.tensors.size();
+  Batch<Moved> b;
+  b.unit = (int)list.unit, b.count = 0, b.word[0] = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const size_t j = (size_t)(back ? count - 1 - i : i);
+    const auto &t = list.tensors[j];
+    if (t.n > 0 && (!into || (t.dtype == dtype && into->tensors[j].dtype == to))) {
       const int k = b.count++;
-      b.at[k] = t.at, b.to[k] = o.at, b.n[k] = (uint64_t)t.n << 4 | (uint64_t)o.dtype << 2 | (uint64_t)t.dtype;
-      b.first[k + 1] = b.first[k] + (uint32_t)((t.n + list.unit - 1) / list.unit);
+      const uint64_t units = (uint64_t)((t.n + list.unit - 1) / list.unit);
+      b.at[k] = t.at;
+      if constexpr (Moved) b.to.at[k] = into->tensors[j].at;
+      b.word[k] |= (uint64_t)(t.n - (int64_t)(units - 1) * list.unit) << 32 | (uint64_t)t.dtype << 48;
+      b.word[k + 1] = (uint32_t)b.word[k] + units;
     }
-    if (b.count == 0) continue;
-    const int rc = f(b);
-    if (rc) return rc;
+    if (b.count == Batch<Moved>::kMost || (i == count - 1 && b.count > 0)) {
+      const int rc = f(b);
+      if (rc) return rc;
+      b.count = 0, b.word[0] = 0;
+    }
   }
   return RESHARD_OK;
 }
 
-// The CTAs of every launch of a call on this list: as many as it has units, up to what the GPU holds at a time.
+// The CTAs of the launches that sum squares: as many as the list has units, up to what the GPU holds at a time.
 int ctas_of(const reshard_tensors &list, int *ctas) {
   int sms = 0;
   const int rc = device_sms(&sms);
   if (rc) return rc;
-  int64_t units = 0;
-  for (const auto &t : list.tensors) units += (t.n + list.unit - 1) / list.unit;
-  *ctas = (int)std::max<int64_t>(1, std::min<int64_t>(units, std::min(kMaxCtas, sms * kCtasPerSm)));
+  *ctas = (int)std::max<int64_t>(1, std::min<int64_t>(list.units, std::min(kMaxCtas, sms * kCtasPerSm)));
   return RESHARD_OK;
 }
 
@@ -321,15 +325,15 @@ bool entangled(const reshard_tensors &a, const reshard_tensors &b) {
 
 int enqueue_squares(const reshard_tensors &list, double *part, int ctas, cudaStream_t stream) {
   bool fresh = true;
-  return batches(list, nullptr, false, [&](const Batch &b) {
+  return batches<false>(list, nullptr, 0, 0, false, [&](const Batch<false> &b) {
     const int rc = launched(launch(reshard_squares_kernel, dim3((unsigned)ctas), kNormThreads, 0, 1, stream, b, part, fresh), "launching reshard_squares_kernel");
     fresh = false;
     return rc;
   });
 }
 
-bool empty(const reshard_tensors &list) {
-  return std::all_of(list.tensors.begin(), list.tensors.end(), [](const reshard_tensors::Tensor &t) { return t.n == 0; });
+int enqueue_norm(const double *part, int ctas, float *norm, cudaStream_t stream) {
+  return launched(launch(reshard_norm_kernel, dim3(1), kNormThreads, 0, 1, stream, part, ctas, norm), "launching reshard_norm_kernel");
 }
 
 }  // namespace
@@ -361,8 +365,9 @@ extern "C" int reshard_tensors_create(const void *const *at, const int64_t *elem
     l.tensors.push_back({reinterpret_cast<uintptr_t>(at[i]), elements[i], dtypes[i]});
   }
   if (!c.ok()) return c.report();
-  // Units that give every CTA some, up to 16,384 elements: 8 pieces of 16 bytes a thread and more.
-  l.unit = std::max<int64_t>(kUnitStep, std::min<int64_t>(8 * kUnitStep, total / (2 * kMaxCtas) / kUnitStep * kUnitStep));
+  // Units of up to 16,384 elements (8 pieces of 16 bytes a thread, or 16), smaller where there would not be one for each CTA.
+  l.unit = std::max<int64_t>(kUnitStep, std::min<int64_t>(8 * kUnitStep, total / kFillCtas / kUnitStep * kUnitStep));
+  for (const auto &t : l.tensors) l.units += (t.n + l.unit - 1) / l.unit;
   std::vector<std::pair<uintptr_t, uintptr_t>> spans;
   for (const auto &t : l.tensors)
     if (t.n) spans.push_back({t.at, t.at + (uintptr_t)(t.n * element_bytes(t.dtype))});
@@ -394,9 +399,9 @@ extern "C" int reshard_grad_norm(const reshard_tensors_t *list, float *norm, voi
   if (!c.ok()) return c.report();
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   double *const part = static_cast<double *>(workspace);
-  int ctas = 0, rc = empty(*list) ? RESHARD_OK : ctas_of(*list, &ctas);
+  int ctas = 0, rc = list->units ? ctas_of(*list, &ctas) : RESHARD_OK;
   if (rc || (rc = enqueue_squares(*list, part, ctas, stream))) return rc;
-  return launched(launch(reshard_norm_kernel, dim3(1), kNormThreads, 0, 1, stream, static_cast<const double *>(part), ctas, norm), "launching reshard_norm_kernel");
+  return enqueue_norm(part, ctas, norm, stream);
 } OPS_CATCH
 
 extern "C" int reshard_clip_grads(const reshard_tensors_t *list, const reshard_tensors_t *into, double limit, const float *norm_in, float *norm_out,
@@ -423,8 +428,7 @@ extern "C" int reshard_clip_grads(const reshard_tensors_t *list, const reshard_t
   if (!c.ok()) return c.report();
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   double *const part = static_cast<double *>(workspace);
-  if (empty(*list))
-    return norm_in ? RESHARD_OK : launched(launch(reshard_norm_kernel, dim3(1), kNormThreads, 0, 1, stream, static_cast<const double *>(part), 0, norm_out), "launching reshard_norm_kernel");
+  if (list->units == 0) return norm_in ? RESHARD_OK : enqueue_norm(part, 0, norm_out, stream);
   int ctas = 0, rc = ctas_of(*list, &ctas);
   if (rc || (!norm_in && (rc = enqueue_squares(*list, part, ctas, stream)))) return rc;
   // in place only if every tensor is its own target
@@ -433,10 +437,36 @@ extern "C" int reshard_clip_grads(const reshard_tensors_t *list, const reshard_t
     const auto &x = list->tensors[i], &y = into->tensors[i];
     here = x.n == 0 || (x.at == y.at && x.dtype == y.dtype);
   }
-  return batches(*list, into, true, [&](const Batch &b) {
-    const int rc = launched(launch(reshard_clip_kernel, dim3((unsigned)ctas), kNormThreads, 0, 1, stream, b, norm_in, static_cast<const double *>(part), ctas, limit,
-                                   here, norm_out), "launching reshard_clip_kernel");
-    norm_out = nullptr;
-    return rc;
-  });
+  // Where every unit has a CTA on the GPU at once, each of them adds up the norm for itself; more CTAs find it added up.
+  if (!norm_in && list->units > ctas) {
+    if ((rc = enqueue_norm(part, ctas, norm_out, stream))) return rc;
+    norm_in = norm_out, norm_out = nullptr;
+  }
+  bool present[4][4] = {};
+  const reshard_tensors &to = into ? *into : *list;
+  for (size_t i = 0; i < to.tensors.size(); ++i)
+    if (to.tensors[i].n) present[list->tensors[i].dtype][to.tensors[i].dtype] = true;
+  auto clip = [&](auto moved, int x, int y) {
+    constexpr bool kMoved = decltype(moved)::value;
+    return batches<kMoved>(*list, &to, x, y, true, [&](const Batch<kMoved> &b) {
+      // One CTA a unit, which writes faster than CTAs that stay; in place those, since most often they have nothing to do.
+      const unsigned grid = kMoved ? b.units() : std::min((unsigned)ctas, b.units());
+      const int rc = launched(by_type(x, [&](auto from_type) {
+        return by_type(y, [&](auto to_type) {
+          using T = decltype(from_type);
+          using TO = decltype(to_type);
+          if constexpr (kMoved || std::is_same_v<T, TO>)
+            return launch(reshard_clip_kernel<T, TO, kMoved>, dim3(grid), kNormThreads, 0, 1, stream, b, norm_in, static_cast<const double *>(part), ctas, limit, norm_out);
+          else
+            return cudaErrorInvalidValue;        // in place the types are the same
+        });
+      }), "launching reshard_clip_kernel");
+      norm_out = nullptr;
+      return rc;
+    });
+  };
+  for (int x = 3; x > 0; --x)
+    for (int y = 3; y > 0; --y)
+      if (present[x][y] && (rc = here ? clip(std::false_type(), x, y) : clip(std::true_type(), x, y))) return rc;
+  return RESHARD_OK;
 } OPS_CATCH

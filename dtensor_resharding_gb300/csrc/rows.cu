@@ -22,6 +22,7 @@ namespace ops {
 namespace {
 
 constexpr int kRowThreads = 256;
+constexpr int kFewThreads = 64;                  // of a CTA where warps are few: spread over the SMs
 constexpr int kAhead = 4;                        // pieces of a lane in flight together
 constexpr int kSpan = 32 * kAhead;               // pieces of a row that a warp moves
 
@@ -30,6 +31,16 @@ __device__ __forceinline__ int place_of(const int32_t *position, int64_t s, int6
   const int p = position[s];
   return p >= 0 && p < rows ? p : -1;
 }
+
+// The warp's row and span where every row has `spans` warps.
+struct Where {
+  int64_t row, span;
+  __device__ __forceinline__ explicit Where(int spans) {
+    const int64_t w = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+    row = w <= 0xffffffffll ? (uint32_t)w / (uint32_t)spans : w / spans;
+    span = w - row * spans;
+  }
+};
 
 // ---------------------------------------------------------------------------------------------------------- permute --
 
@@ -43,19 +54,20 @@ struct Permute {
   int spans;                         // warps a row (a slot's row, where rows start anywhere)
 };
 
-// Rows of whole 16-byte pieces: a warp reads 2 KB of a token's row once and writes it to each of its places.
+// Rows of whole 16-byte pieces: a warp reads 2 KB of a token's row once and writes it to each of its places. Bound by the writes:
+// 8,192 x 2048 bf16 to 8 places each, 47 us, 6.4 TB/s.
 __global__ void __launch_bounds__(kRowThreads) reshard_permute_kernel(Permute a) {
   grid_enter();
   const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = w / a.spans;
+  const Where at(a.spans);
+  const int64_t t = at.row;
   if (t >= a.tokens) return;
-  const int64_t c0 = (w - t * a.spans) * kSpan + lane;
+  const int64_t c0 = at.span * kSpan + lane;
   const uint4 *const from = static_cast<const uint4 *>(a.x) + t * a.stride;
   uint4 v[kAhead];
 #pragma unroll
   for (int u = 0; u < kAhead; ++u)
-    if (c0 + 32 * u < a.cols) v[u] = __ldg(from + c0 + 32 * u);
+    if (c0 + 32 * u < a.cols) v[u] = from[c0 + 32 * u];
   for (int j0 = 0; j0 < a.k; j0 += 32) {
     int mine = -1;
     if (j0 + lane < a.k) {
@@ -63,11 +75,8 @@ __global__ void __launch_bounds__(kRowThreads) reshard_permute_kernel(Permute a)
       mine = place_of(a.position, s, a.rows);
       if (mine >= 0 && a.order[mine] != s) mine = -1;
     }
-    const int n = min(32, a.k - j0);
-    for (int j = 0; j < n; ++j) {
-      const int p = __shfl_sync(kFull, mine, j);
-      if (p < 0) continue;
-      uint4 *const to = static_cast<uint4 *>(a.out) + (int64_t)p * a.out_stride;
+    for (uint32_t live = __ballot_sync(kFull, mine >= 0); live; live &= live - 1) {
+      uint4 *const to = static_cast<uint4 *>(a.out) + (int64_t)__shfl_sync(kFull, mine, __ffs(live) - 1) * a.out_stride;
 #pragma unroll
       for (int u = 0; u < kAhead; ++u)
         if (c0 + 32 * u < a.cols) to[c0 + 32 * u] = v[u];
@@ -78,46 +87,49 @@ __global__ void __launch_bounds__(kRowThreads) reshard_permute_kernel(Permute a)
 // Pieces [first, first + kSpan) of a row, copied (times `scale`, where scaled) or, without a source, zeroed.
 template <typename T, bool Wide, bool Scaled>
 __device__ __forceinline__ void move_span(const T *from, T *to, int64_t cols, int64_t first, int lane, float scale) {
-  Eight<T, Wide> v[kAhead];
+  constexpr int kN = kPieceOf<T, T>;
+  Piece<T, kN, Wide> v[kAhead];
   int64_t c[kAhead];
   bool whole[kAhead];
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) {
-    c[u] = piece_start<T, Wide>(first + lane + 32 * u, to);
-    whole[u] = c[u] >= 0 && c[u] + 8 <= cols;
+    c[u] = piece_start<T, kN, Wide>(first + lane + 32 * u, to);
+    whole[u] = c[u] >= 0 && c[u] + kN <= cols;
     if (from && whole[u]) v[u].ask(from + c[u]);
   }
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) {
     if (whole[u]) {
       if (Scaled && from) {
-        float x[8];
+        float x[kN];
         v[u].take(from + c[u], x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= scale;
-        store_eight(to + c[u], x);
+        for (int i = 0; i < kN; ++i) x[i] *= scale;
+        store_piece(to + c[u], x);
       } else {
-        *reinterpret_cast<Pack<T, 8> *>(to + c[u]) = from ? v[u].bits(from + c[u]) : Pack<T, 8>{};
+        Words<T, kN> r{};
+        if (from) r = v[u].words(from + c[u]);
+        r.store(to + c[u]);
       }
     } else if (c[u] < cols) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < kN; ++i)
         if (c[u] + i >= 0 && c[u] + i < cols) to[c[u] + i] = from ? (Scaled ? from_f32<T>(to_f32(from[c[u] + i]) * scale) : from[c[u] + i]) : from_f32<T>(0.0f);
     }
   }
 }
 
-// Rows that start anywhere: a warp a piece of a slot's row, which starts elsewhere than the token's does.
+// Rows that start anywhere: a warp a span of a slot's row, which starts elsewhere than the token's does.
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) reshard_permute_any_kernel(Permute a) {
   grid_enter();
-  const int64_t w = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const int64_t s = w / a.spans;
+  const Where at(a.spans);
+  const int64_t s = at.row;
   if (s >= a.tokens * a.k) return;
   const int p = place_of(a.position, s, a.rows);
   if (p < 0 || a.order[p] != s) return;
-  move_span<T, false, false>(static_cast<const T *>(a.x) + s / a.k * a.stride, static_cast<T *>(a.out) + (int64_t)p * a.out_stride, a.cols,
-                             (w - s * a.spans) * kSpan, threadIdx.x & 31, 1.0f);
+  move_span<T, false, false>(static_cast<const T *>(a.x) + s / a.k * a.stride, static_cast<T *>(a.out) + (int64_t)p * a.out_stride, a.cols, at.span * kSpan,
+                             threadIdx.x & 31, 1.0f);
 }
 
 // -------------------------------------------------------------------------------------------------------- embedding --
@@ -134,59 +146,104 @@ struct Lookup {
   int spans;
 };
 
+// A warp 2 KB of a token's row. Bound by the writes, and the reads of the rows that are not in L2: 32,768 tokens on a quarter of a
+// vocabulary of 128,000 x 4096 bf16, 48 us, 6.1 TB/s.
 template <typename T, bool Wide, bool Scaled>
 __global__ void __launch_bounds__(kRowThreads) reshard_embedding_kernel(Lookup a) {
   grid_enter();
-  const int64_t w = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const int64_t t = w / a.spans;
+  const Where at(a.spans);
+  const int64_t t = at.row;
   if (t >= a.tokens) return;
   const int64_t id = a.wide_ids ? static_cast<const int64_t *>(a.ids)[t] : static_cast<const int32_t *>(a.ids)[t];
   const bool here = id >= a.first && id - a.first < a.rows;
-  move_span<T, Wide, Scaled>(here ? static_cast<const T *>(a.table) + (id - a.first) * a.stride : nullptr,
-                             static_cast<T *>(a.out) + t * a.out_stride, a.cols, (w - t * a.spans) * kSpan, threadIdx.x & 31, a.scale);
+  move_span<T, Wide, Scaled>(here ? static_cast<const T *>(a.table) + (id - a.first) * a.stride : nullptr, static_cast<T *>(a.out) + t * a.out_stride, a.cols,
+                             at.span * kSpan, threadIdx.x & 31, a.scale);
 }
 
 // ---------------------------------------------------------------------------------------------------------- combine --
 
-// One thread eight columns of a token; bound by the read of y: 8 slots a token, 8,192 x 2048 fp32, 83 us, 6.9 TB/s (loads of all
-// eight slots before the sums: three times as long).
+// A warp a span of a token's columns. Lanes look up the places of up to 32 slots at once; those that have one are taken in
+// order, kSlots rows in flight together.
+constexpr int kCombineCtas = 4;                  // of an SM
 template <typename TY, typename TO, bool Wide>
-__global__ void __launch_bounds__(kRowThreads)
-    reshard_combine_kernel(const TY *y, int64_t rows, int64_t y_stride, const int32_t *position, const float *weights, int64_t tokens, int k,
-                           int64_t cols, TO *out, int64_t out_stride, int pieces) {
+struct CombineShape {
+  static constexpr int kN = kPieceOf<TY, TO>;
+  static constexpr int kPieces = 16 / kN;        // 16 columns a lane
+  static constexpr int kSlots = Wide ? 2 : 1;    // rows in flight; rows that start anywhere need twice the registers
+};
+
+template <typename TY, typename TO, bool Wide>
+__global__ void __launch_bounds__(kRowThreads, kCombineCtas) reshard_combine_kernel(Combine a, int spans) {
+  using Shape = CombineShape<TY, TO, Wide>;
+  constexpr int kN = Shape::kN, kU = Shape::kPieces, kSlots = Shape::kSlots;
   grid_enter();
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= tokens * pieces) return;
-  const int64_t t = tokens * pieces <= 0xffffffffll ? (uint32_t)i / (uint32_t)pieces : i / pieces;
-  TO *const to = out + t * out_stride;
-  const int64_t c = piece_start<TO, Wide>(i - t * pieces, to);
-  if (c >= cols) return;
-  float sum[8] = {};
-  const bool whole = c >= 0 && c + 8 <= cols;
-#pragma unroll 4
-  for (int j = 0; j < k; ++j) {
-    const int p = place_of(position, t * k + j, rows);
-    if (p < 0) continue;
-    const float w = weights ? weights[t * k + j] : 1.0f;
-    const TY *const from = y + (int64_t)p * y_stride + c;
-    float x[8];
-    if (whole) {
-      Eight<TY, Wide> v;
-      v.ask(from);
-      v.take(from, x);
+  const int lane = threadIdx.x & 31;
+  const Where at(spans);
+  const int64_t t = at.row;
+  if (t >= a.tokens) return;
+  TO *const to = static_cast<TO *>(a.out) + t * a.out_stride;
+  int64_t c[kU];
+  bool whole[kU];
+  bool edge = false;
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    c[u] = piece_start<TO, kN, Wide>(at.span * 32 * kU + lane + 32 * u, to);
+    whole[u] = c[u] >= 0 && c[u] + kN <= a.cols;
+    edge |= !whole[u] && c[u] < a.cols;
+  }
+  float sum[kU][kN] = {};
+  for (int j0 = 0; j0 < a.k; j0 += 32) {
+    const int64_t s = t * a.k + j0 + lane;
+    const bool in = j0 + lane < a.k;
+    const int mine = in ? place_of(a.position, s, a.rows) : -1;
+    const float weight = in && a.weights ? a.weights[s] : 1.0f;
+    for (uint32_t live = __ballot_sync(kFull, mine >= 0); live;) {
+      const TY *from[kSlots];
+      float w[kSlots];
+      Piece<TY, kN, Wide> v[kSlots][kU];
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+        const int j = __ffs(live) - 1;           // -1: none left
+        const int p = __shfl_sync(kFull, mine, max(j, 0));
+        w[q] = __shfl_sync(kFull, weight, max(j, 0));
+        from[q] = j >= 0 ? static_cast<const TY *>(a.y) + (int64_t)p * a.y_stride : nullptr;
+        live &= live - 1;
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          if (from[q] && whole[u]) v[q][u].ask(from[q] + c[u]);
+      }
+#pragma unroll
+      for (int q = 0; q < kSlots; ++q) {
+        if (!from[q]) break;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          if (!whole[u]) continue;
+          float x[kN];
+          v[q][u].take(from[q] + c[u], x);
+#pragma unroll
+          for (int e = 0; e < kN; ++e) sum[u][e] = fmaf(w[q], x[e], sum[u][e]);
+        }
+        if (edge) {
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            if (whole[u]) continue;
+#pragma unroll
+            for (int e = 0; e < kN; ++e)
+              if (c[u] + e >= 0 && c[u] + e < a.cols) sum[u][e] = fmaf(w[q], to_f32(from[q][c[u] + e]), sum[u][e]);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kU; ++u) {
+    if (whole[u]) {
+      store_piece(to + c[u], sum[u]);
     } else {
 #pragma unroll
-      for (int u = 0; u < 8; ++u) x[u] = c + u >= 0 && c + u < cols ? to_f32(from[u]) : 0.0f;
+      for (int e = 0; e < kN; ++e)
+        if (c[u] + e >= 0 && c[u] + e < a.cols) to[c[u] + e] = from_f32<TO>(sum[u][e]);
     }
-#pragma unroll
-    for (int u = 0; u < 8; ++u) sum[u] = fmaf(w, x[u], sum[u]);
-  }
-  if (whole) {
-    store_eight(to + c, sum);
-  } else {
-#pragma unroll
-    for (int u = 0; u < 8; ++u)
-      if (c + u >= 0 && c + u < cols) to[c + u] = from_f32<TO>(sum[u]);
   }
 }
 
@@ -205,22 +262,127 @@ struct CombineBackward {
   int64_t grad_y_stride;
   float *grad_weights;               // NULL: not asked for
   int pieces;
+  int lanes;                         // threads a token, of the kernel of whole pieces
+  int token_ctas;                    // the CTAs behind them look for rows that no slot owns
 };
 
-// A warp a slot: the token's gradient (which the k warps of a token share in L1), its row of y, one row written, and the
-// dot product by shuffles. Warp i also zeroes row i of the gradient if no slot owns it.
-template <typename TG, typename TY, bool Wide>
-__global__ void __launch_bounds__(kRowThreads) reshard_combine_backward_kernel(CombineBackward a) {
+// Zeros in the rows of the gradient that no slot owns: a warp 32 rows, whose owners it looks up at once.
+template <typename TY, bool Wide>
+__device__ __forceinline__ void zero_unowned(const CombineBackward &a, int64_t first, int lane) {
+  const int64_t i = first + lane;
+  bool none = false;
+  if (i < a.rows) {
+    const int64_t s = a.order[i];      // not written behind the last place: whatever it holds there is no owner
+    none = s < 0 || s >= a.tokens * a.k || a.position[s] != i;
+  }
+  for (uint32_t left = __ballot_sync(kFull, none); left; left &= left - 1)
+    for (int c = 0; c < a.pieces; c += kSpan)
+      move_span<TY, Wide, false>(nullptr, static_cast<TY *>(a.grad_y) + (first + __ffs(left) - 1) * a.grad_y_stride, a.cols, c, lane, 1.0f);
+}
+
+// Whole pieces: `lanes` threads a token (a warp to a CTA, as many as have columns), which read its gradient once and keep the
+// rows of eight slots in flight; the dot products by shuffles, then over the token's warps through shared memory.
+constexpr int kBackSlots = 8, kBackCtas = 3;     // slots in flight, CTAs of an SM
+template <typename TG, typename TY>
+__global__ void __launch_bounds__(kRowThreads, kBackCtas) reshard_combine_backward_kernel(CombineBackward a) {
+  constexpr int kN = kPieceOf<TG, TY>;
+  grid_enter();
+  __shared__ float part[kRowThreads / 32][kBackSlots];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if ((int)blockIdx.x >= a.token_ctas) {
+    zero_unowned<TY, true>(a, ((int64_t)((int)blockIdx.x - a.token_ctas) * (kRowThreads / 32) + warp) * 32, lane);
+    return;
+  }
+  const int group = threadIdx.x / a.lanes, me = threadIdx.x - group * a.lanes, warps = a.lanes >> 5;
+  const int64_t t = (int64_t)blockIdx.x * (kRowThreads / a.lanes) + group;
+  const bool in = t < a.tokens;                    // of a whole warp
+  const TG *const g = static_cast<const TG *>(a.grad) + t * a.grad_stride;
+  for (int j0 = 0; j0 < a.k; j0 += kBackSlots) {
+    const int64_t s = t * a.k + j0 + lane;
+    const bool slot = in && lane < kBackSlots && j0 + lane < a.k;
+    const int mine = slot ? place_of(a.position, s, a.rows) : -1;
+    const bool own = mine >= 0 && a.grad_y && a.order[mine] == s;
+    const float weight = slot && a.weights ? a.weights[s] : 1.0f;
+    const uint32_t live = __ballot_sync(kFull, mine >= 0), owned = __ballot_sync(kFull, own);
+    int p[kBackSlots];
+    float w[kBackSlots], dot[kBackSlots];
+#pragma unroll
+    for (int q = 0; q < kBackSlots; ++q) {
+      p[q] = __shfl_sync(kFull, mine, q);
+      w[q] = __shfl_sync(kFull, weight, q);
+      dot[q] = 0.0f;
+    }
+    if (live) {
+      for (int64_t c = (int64_t)me * kN; c < a.cols; c += (int64_t)a.lanes * kN) {
+        Piece<TG, kN, true> gv;
+        Piece<TY, kN, true> v[kBackSlots];
+        gv.ask(g + c);
+        if (a.grad_weights) {
+#pragma unroll
+          for (int q = 0; q < kBackSlots; ++q)
+            if (live >> q & 1) v[q].ask(static_cast<const TY *>(a.y) + (int64_t)p[q] * a.y_stride + c);
+        }
+        float x[kN];
+        gv.take(g + c, x);
+#pragma unroll
+        for (int q = 0; q < kBackSlots; ++q) {
+          if (owned >> q & 1) {
+            float z[kN];
+#pragma unroll
+            for (int e = 0; e < kN; ++e) z[e] = x[e] * w[q];
+            store_piece(static_cast<TY *>(a.grad_y) + (int64_t)p[q] * a.grad_y_stride + c, z);
+          }
+        }
+        if (a.grad_weights) {
+#pragma unroll
+          for (int q = 0; q < kBackSlots; ++q) {
+            if (!(live >> q & 1)) continue;
+            float y[kN];
+            v[q].take(nullptr, y);
+#pragma unroll
+            for (int e = 0; e < kN; ++e) dot[q] = fmaf(x[e], y[e], dot[q]);
+          }
+        }
+      }
+    }
+    if (!a.grad_weights) continue;
+    // Eight sums over the lanes: halves are exchanged until a lane has one, of the slot that its upper three bits name.
+#pragma unroll
+    for (int o = 16, n = kBackSlots / 2; n; o >>= 1, n >>= 1)
+#pragma unroll
+      for (int q = 0; q < n; ++q) {
+        const float give = lane & o ? dot[q] : dot[q + n];
+        dot[q] = (lane & o ? dot[q + n] : dot[q]) + __shfl_xor_sync(kFull, give, o);
+      }
+    dot[0] += __shfl_xor_sync(kFull, dot[0], 2);
+    dot[0] += __shfl_xor_sync(kFull, dot[0], 1);
+    if (warps == 1) {
+      if (in && (lane & 3) == 0 && j0 + (lane >> 2) < a.k) a.grad_weights[t * a.k + j0 + (lane >> 2)] = dot[0];
+      continue;
+    }
+    if (j0) __syncthreads();                       // the slots before have been added
+    if ((lane & 3) == 0) part[warp][lane >> 2] = dot[0];
+    __syncthreads();
+    if (in && me < kBackSlots && j0 + me < a.k) {
+      float sum = 0.0f;
+      for (int i = 0; i < warps; ++i) sum += part[group * warps + i][me];
+      a.grad_weights[t * a.k + j0 + me] = sum;
+    }
+  }
+}
+
+// Rows that start anywhere: a warp a slot.
+template <typename TG, typename TY>
+__global__ void __launch_bounds__(kRowThreads) reshard_combine_backward_any_kernel(CombineBackward a) {
+  constexpr int kN = kPieceOf<TG, TY>, kU = 2;
   grid_enter();
   const int lane = threadIdx.x & 31;
-  const int64_t i = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
-  const int64_t slots = a.tokens * a.k;
-  if (a.grad_y && i < a.rows) {
-    const int64_t s = a.order[i];      // not written behind the last place: whatever it holds there is no owner
-    if (s < 0 || s >= slots || a.position[s] != i)
-      for (int c = 0; c < a.pieces; c += kSpan) move_span<TY, Wide, false>(nullptr, static_cast<TY *>(a.grad_y) + i * a.grad_y_stride, a.cols, c, lane, 1.0f);
+  if ((int)blockIdx.x >= a.token_ctas) {
+    zero_unowned<TY, false>(a, ((int64_t)((int)blockIdx.x - a.token_ctas) * (kRowThreads / 32) + (threadIdx.x >> 5)) * 32, lane);
+    return;
   }
-  if (i >= slots) return;
+  const int64_t i = (int64_t)blockIdx.x * (kRowThreads / 32) + (threadIdx.x >> 5);
+  if (i >= a.tokens * a.k) return;
   const int p = place_of(a.position, i, a.rows);
   float dot = 0.0f;
   if (p >= 0) {
@@ -228,48 +390,48 @@ __global__ void __launch_bounds__(kRowThreads) reshard_combine_backward_kernel(C
     const TY *const y = a.grad_weights ? static_cast<const TY *>(a.y) + (int64_t)p * a.y_stride : nullptr;
     TY *const to = a.grad_y && a.order[p] == i ? static_cast<TY *>(a.grad_y) + (int64_t)p * a.grad_y_stride : nullptr;
     const float w = a.weights ? a.weights[i] : 1.0f;
-    // Where rows start anywhere, the pieces are those of a dense gradient of y whether it is written or not, dense or not: they
-    // set the order of the dot product.
+    // The pieces are those of a dense gradient of y whether it is written or not, dense or not: they set the order of the dot
+    // product.
     const TY *const dense = reinterpret_cast<const TY *>(p * a.cols * (int64_t)sizeof(TY));
-    for (int c1 = lane; c1 < a.pieces; c1 += kSpan) {
-      Eight<TG, Wide> gv[kAhead];
-      Eight<TY, Wide> yv[kAhead];
-      int64_t c[kAhead];
-      bool whole[kAhead];
+    for (int c1 = lane; c1 < a.pieces; c1 += 32 * kU) {
+      Piece<TG, kN, false> gv[kU];
+      Piece<TY, kN, false> yv[kU];
+      int64_t c[kU];
+      bool whole[kU];
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        c[u] = piece_start<TY, Wide>(c1 + 32 * u, dense);
-        whole[u] = c[u] >= 0 && c[u] + 8 <= a.cols;
+      for (int u = 0; u < kU; ++u) {
+        c[u] = piece_start<TY, kN, false>(c1 + 32 * u, dense);
+        whole[u] = c[u] >= 0 && c[u] + kN <= a.cols;
         if (whole[u]) {
           gv[u].ask(g + c[u]);
           if (y) yv[u].ask(y + c[u]);
         }
       }
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        float x[8], z[8] = {};
+      for (int u = 0; u < kU; ++u) {
+        float x[kN], z[kN] = {};
         if (whole[u]) {
           gv[u].take(g + c[u], x);
           if (y) yv[u].take(y + c[u], z);
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
+          for (int e = 0; e < kN; ++e) {
             const bool in = c[u] + e >= 0 && c[u] + e < a.cols;
             x[e] = in ? to_f32(g[c[u] + e]) : 0.0f;
             z[e] = in && y ? to_f32(y[c[u] + e]) : 0.0f;
           }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < kN; ++e) {
           dot = fmaf(x[e], z[e], dot);
           x[e] *= w;
         }
         if (!to) continue;
-        if (whole[u] && (Wide || (reinterpret_cast<uintptr_t>(to + c[u]) & 15) == 0)) {
-          store_eight(to + c[u], x);
+        if (whole[u] && (reinterpret_cast<uintptr_t>(to + c[u]) & (kN * sizeof(TY) - 1)) == 0) {
+          store_piece(to + c[u], x);
         } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
+          for (int e = 0; e < kN; ++e)
             if (c[u] + e >= 0 && c[u] + e < a.cols) to[c[u] + e] = from_f32<TY>(x[e]);
         }
       }
@@ -281,12 +443,16 @@ __global__ void __launch_bounds__(kRowThreads) reshard_combine_backward_kernel(C
   if (lane == 0) a.grad_weights[i] = dot;
 }
 
-int64_t warps_grid(int64_t warps) { return (warps + kRowThreads / 32 - 1) / (kRowThreads / 32); }
-
-// Warps of a row of so many pieces.
-int spans_of(int64_t pieces) { return (int)((pieces + kSpan - 1) / kSpan); }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 int launched(cudaError_t e, const char *what) { return e == cudaSuccess ? RESHARD_OK : cuda_error(e, what); }
+
+// A launch of so many warps, in small CTAs where they would leave SMs without one.
+template <typename... K, typename... A>
+cudaError_t launch_warps(void (*kernel)(K...), int64_t warps, cudaStream_t stream, A &&...args) {
+  const int block = warps <= 2048 ? kFewThreads : kRowThreads;
+  return launch(kernel, dim3((unsigned)ceil_div(warps, block / 32)), block, 0, 1, stream, std::forward<A>(args)...);
+}
 
 }  // namespace
 
@@ -297,12 +463,9 @@ int enqueue_combine(const Combine &a, cudaStream_t stream) {
     using TY = decltype(y);
     return by_type(a.out_dtype, [&](auto o) {
       using TO = decltype(o);
-      const int64_t pieces = piece_count<TO>(a.cols, wide);
-      const int block = a.tokens * pieces <= 32768 ? 64 : kRowThreads;      // a few tokens' columns spread over the SMs
-      const dim3 grid((unsigned)((a.tokens * pieces + block - 1) / block));
-      return launch(wide ? reshard_combine_kernel<TY, TO, true> : reshard_combine_kernel<TY, TO, false>, grid, block, 0, 1, stream,
-                    static_cast<const TY *>(a.y), a.rows, a.y_stride, a.position, a.weights, a.tokens, a.k, a.cols, static_cast<TO *>(a.out),
-                    a.out_stride, (int)pieces);
+      using Shape = CombineShape<TY, TO, true>;
+      const int spans = (int)ceil_div(piece_count(a.cols, Shape::kN, wide), 32 * Shape::kPieces);
+      return launch_warps(wide ? reshard_combine_kernel<TY, TO, true> : reshard_combine_kernel<TY, TO, false>, a.tokens * spans, stream, a, spans);
     });
   }), "launching reshard_combine_kernel");
 }
@@ -315,7 +478,7 @@ void check_slots(Checks &c, int64_t tokens, int64_t cols, int k, int64_t rows) {
   c.unsupported(tokens > RESHARD_MAX_EXTENT || cols > RESHARD_MAX_EXTENT || rows > RESHARD_MAX_SLOTS, "tokens, cols or rows above 2^30");
   if (c.ok()) {
     c.unsupported(tokens * k > RESHARD_MAX_SLOTS, "more than 2^30 slots");
-    c.unsupported((double)std::max<int64_t>(tokens * k, rows) * (double)(cols / 256 + 1) > 8.0 * INT32_MAX, "too many rows and columns for one launch");
+    c.unsupported((double)std::max<int64_t>(tokens * k, rows) * (double)(cols / 256 + 1) > 2.0 * INT32_MAX, "too many rows and columns for one launch");
   }
 }
 
@@ -346,13 +509,13 @@ extern "C" int reshard_permute(const void *x, int dtype, int64_t tokens, int64_t
   Permute a{x, tokens, cols, row_stride, order, position, k, out, rows, out_stride, 0};
   if (aligned16(x, row_stride, es) && aligned16(out, out_stride, es) && cols * es % 16 == 0) {
     a.cols = cols * es / 16, a.stride = row_stride * es / 16, a.out_stride = out_stride * es / 16;
-    a.spans = spans_of(a.cols);
-    return launched(launch(reshard_permute_kernel, dim3((unsigned)warps_grid(tokens * a.spans)), kRowThreads, 0, 1, stream, a), "launching reshard_permute_kernel");
+    a.spans = (int)ceil_div(a.cols, kSpan);
+    return launched(launch_warps(reshard_permute_kernel, tokens * a.spans, stream, a), "launching reshard_permute_kernel");
   }
   // values are copied as they are: the types of a size share a kernel
-  a.spans = spans_of(es == 4 ? piece_count<float>(cols, false) : piece_count<__half>(cols, false));
-  return launched(launch(es == 4 ? reshard_permute_any_kernel<float> : reshard_permute_any_kernel<__half>,
-                         dim3((unsigned)warps_grid(tokens * k * a.spans)), kRowThreads, 0, 1, stream, a), "launching reshard_permute_any_kernel");
+  a.spans = (int)ceil_div(piece_count(cols, 16 / es, false), kSpan);
+  return launched(launch_warps(es == 4 ? reshard_permute_any_kernel<float> : reshard_permute_any_kernel<__half>, tokens * k * a.spans, stream, a),
+                  "launching reshard_permute_any_kernel");
 } OPS_CATCH
 
 extern "C" int reshard_combine(const void *y, int dtype, int64_t rows, int64_t cols, int64_t row_stride, const int32_t *position,
@@ -382,8 +545,8 @@ extern "C" int reshard_combine_backward(const void *grad, int grad_dtype, int64_
   c.invalid(!element_bytes(dtype) || !element_bytes(grad_dtype), "dtype and grad_dtype must be BF16, F16 or F32");
   c.invalid(grad_stride < cols || (grad_weights && row_stride < cols) || (grad_y && grad_y_stride < cols), "a row stride is shorter than the row");
   const int es = element_bytes(dtype);
-  const int64_t warps = !c.ok() ? 0 : std::max(grad_weights || grad_y ? tokens * k : 0, grad_y ? rows : 0);
-  if (warps > 0 && c.ok()) {
+  const bool work = c.ok() && ((tokens > 0 && (grad_weights || grad_y)) || (grad_y && rows > 0));
+  if (work) {
     if (tokens > 0) {
       if (cols > 0) c.pointer(grad, "grad", (uintptr_t)element_bytes(grad_dtype));
       if (cols > 0 && rows > 0 && grad_weights) c.pointer(y, "y", (uintptr_t)es);
@@ -397,17 +560,21 @@ extern "C" int reshard_combine_backward(const void *grad, int grad_dtype, int64_
     if (grad_weights && tokens > 0) c.pointer(grad_weights, "grad_weights", 4);
   }
   if (!c.ok()) return c.report();
-  if (warps == 0) return RESHARD_OK;
+  if (!work) return RESHARD_OK;
   const bool wide = aligned16(grad, grad_stride, element_bytes(grad_dtype)) && (!grad_weights || aligned16(y, row_stride, es)) &&
                     (!grad_y || aligned16(grad_y, grad_y_stride, es)) && cols * es % 16 == 0;
-  const CombineBackward a{grad, grad_stride, y, rows, cols, row_stride, order, position, weights, tokens, k, grad_y, grad_y_stride, grad_weights,
-                          (int)(es == 4 ? piece_count<float>(cols, wide) : piece_count<__half>(cols, wide))};
+  CombineBackward a{grad, grad_stride, y, rows, cols, row_stride, order, position, weights, tokens, k, grad_y, grad_y_stride, grad_weights, 0, 32, 0};
   return launched(by_type(grad_dtype, [&](auto g) {
     using TG = decltype(g);
     return by_type(dtype, [&](auto t) {
       using TY = decltype(t);
-      return launch(wide ? reshard_combine_backward_kernel<TG, TY, true> : reshard_combine_backward_kernel<TG, TY, false>,
-                    dim3((unsigned)warps_grid(warps)), kRowThreads, 0, 1, reinterpret_cast<cudaStream_t>(stream), a);
+      constexpr int kN = kPieceOf<TG, TY>;
+      while (a.lanes < kRowThreads && a.lanes * kN < cols) a.lanes *= 2;
+      a.token_ctas = (int)(wide ? ceil_div(tokens, kRowThreads / a.lanes) : ceil_div(tokens * k, kRowThreads / 32));
+      a.pieces = (int)std::max(piece_count(cols, kN, wide), piece_count(cols, kPieceOf<TY, TY>, wide));      // of a row, and of its zeros
+      const int64_t ctas = a.token_ctas + (grad_y ? ceil_div(rows, kRowThreads) : 0);
+      return launch(wide ? reshard_combine_backward_kernel<TG, TY> : reshard_combine_backward_any_kernel<TG, TY>, dim3((unsigned)ctas), kRowThreads, 0, 1,
+                    reinterpret_cast<cudaStream_t>(stream), a);
     });
   }), "launching reshard_combine_backward_kernel");
 } OPS_CATCH
@@ -422,7 +589,7 @@ extern "C" int reshard_embedding(const void *ids, int id_bits, int64_t tokens, c
   c.invalid(row_stride < cols || out_stride < cols, "a row stride is shorter than the row");
   const int es = element_bytes(dtype);
   const bool work = tokens > 0 && cols > 0;
-  if (c.ok()) c.unsupported((double)tokens * (double)(cols / 256 + 1) > 8.0 * INT32_MAX, "too many rows and columns for one launch");
+  if (c.ok()) c.unsupported((double)tokens * (double)(cols / 256 + 1) > 2.0 * INT32_MAX, "too many rows and columns for one launch");
   if (work && c.ok()) {
     c.pointer(ids, "ids", (uintptr_t)(id_bits / 8));
     if (rows > 0) c.pointer(table, "table", (uintptr_t)es);
@@ -434,9 +601,9 @@ extern "C" int reshard_embedding(const void *ids, int id_bits, int64_t tokens, c
   Lookup a{ids, id_bits == 64, tokens, table, first_row, rows, cols, row_stride, scale, out, out_stride, 0};
   return launched(by_type(dtype, [&](auto t) {
     using T = decltype(t);
-    a.spans = spans_of(piece_count<T>(cols, wide));
+    a.spans = (int)ceil_div(piece_count(cols, kPieceOf<T, T>, wide), kSpan);
     auto *kernel = wide ? scale == 1.0f ? reshard_embedding_kernel<T, true, false> : reshard_embedding_kernel<T, true, true>
                         : scale == 1.0f ? reshard_embedding_kernel<T, false, false> : reshard_embedding_kernel<T, false, true>;
-    return launch(kernel, dim3((unsigned)warps_grid(tokens * a.spans)), kRowThreads, 0, 1, reinterpret_cast<cudaStream_t>(stream), a);
+    return launch_warps(kernel, tokens * a.spans, reinterpret_cast<cudaStream_t>(stream), a);
   }), "launching reshard_embedding_kernel");
 } OPS_CATCH

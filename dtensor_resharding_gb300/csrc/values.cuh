@@ -40,30 +40,40 @@ __device__ __forceinline__ void load_values(const T *p, int left, bool wide, flo
   }
 }
 
-// The 16-byte words that hold N values at p, wherever p is: ask() reads them (words that hold none of the `left` values
-// are not read, `any` is in their place), take() shifts the values into place and clears those from `left` on. Rows that
-// start anywhere are read as fast as aligned ones this way; value by value they took three times as long.
+// The 16-byte words (8-byte ones for 8 bytes of values) that hold N values at p, wherever p is: ask() reads them (words that
+// hold none of the `left` values are not read, `any` is in their place), take() shifts the values into place and clears those from
+// `left` on. Rows that start anywhere are read as fast as aligned ones this way; value by value they took three times as long.
 template <typename T, int N>
 struct Shifted {
   static constexpr int kWords = N * (int)sizeof(T) / 4;
-  static_assert(kWords % 4 == 0, "16-byte words");
-  uint32_t w[kWords + 4];
+  static constexpr int kLoad = kWords % 4 == 0 ? 4 : 2;        // 32-bit words of a load
+  static_assert(kWords % kLoad == 0, "whole loads");
+  uint32_t w[kWords + kLoad];
+  static __device__ __forceinline__ uint32_t skip_of(const T *p) { return (uint32_t)(reinterpret_cast<uintptr_t>(p) & (4 * kLoad - 1)); }
   __device__ __forceinline__ void ask(const T *p, int left, const uint8_t *any) {
-    const uintptr_t skip = reinterpret_cast<uintptr_t>(p) & 15;
+    const uint32_t skip = skip_of(p);
     const uint8_t *from = reinterpret_cast<const uint8_t *>(p) - skip;
     const int end = left > 0 ? (int)skip + min(left, N) * (int)sizeof(T) : 0;        // bytes from there to the last value
 #pragma unroll
-    for (int i = 0; i < kWords + 4; i += 4) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4 *>(4 * i < end ? from + 4 * i : any));
-      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+    for (int i = 0; i < kWords + kLoad; i += kLoad) {
+      const uint8_t *const at = 4 * i < end ? from + 4 * i : any;
+      if constexpr (kLoad == 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(at);
+        w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+      } else {
+        const uint2 v = *reinterpret_cast<const uint2 *>(at);
+        w[i] = v.x, w[i + 1] = v.y;
+      }
     }
   }
   __device__ __forceinline__ void take(const T *p, int left, uint32_t (&v)[kWords]) {
-    const uint32_t skip = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+    const uint32_t skip = skip_of(p);
 #pragma unroll
-    for (int i = 0; i < kWords + 3; ++i) w[i] = skip & 4 ? w[i + 1] : w[i];
+    for (int i = 0; i < kWords + kLoad - 1; ++i) w[i] = skip & 4 ? w[i + 1] : w[i];
+    if constexpr (kLoad == 4) {
 #pragma unroll
-    for (int i = 0; i < kWords + 2; ++i) w[i] = skip & 8 ? w[i + 2] : w[i];
+      for (int i = 0; i < kWords + 2; ++i) w[i] = skip & 8 ? w[i + 2] : w[i];
+    }
 #pragma unroll
     for (int i = 0; i < kWords; ++i) {
       const uint32_t x = sizeof(T) < 4 ? __funnelshift_r(w[i], w[i + 1], 8 * (skip & 3)) : w[i];
@@ -83,56 +93,107 @@ __device__ __forceinline__ const uint8_t *first_word(const void *p) {
   return reinterpret_cast<const uint8_t *>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15);
 }
 
-// Eight neighbours of a row, all inside it: `Wide` rows start on 16 bytes, others anywhere. ask() starts the loads.
-template <typename T, bool Wide>
-struct Eight {
-  std::conditional_t<Wide, Pack<T, 8>, Shifted<T, 8>> w;
-  __device__ __forceinline__ void ask(const T *p) {
-    if constexpr (Wide) w = *reinterpret_cast<const Pack<T, 8> *>(p);
-    else w.ask(p, 8, first_word(p));
-  }
-  __device__ __forceinline__ Pack<T, 8> bits(const T *p) {
-    if constexpr (Wide) {
-      return w;
+// Rows are moved in pieces of as many neighbours as make 16 bytes of the wider of two types: a warp's loads and stores then
+// cover whole sectors. (Eight floats a thread in two stores of 16 bytes, half a sector each: 604M bf16 values to fp32 took 690 us instead
+// of 570.)
+template <typename A, typename B>
+constexpr int kPieceOf = sizeof(A) == 4 || sizeof(B) == 4 ? 4 : 8;
+
+// N values of type T as the 32-bit words that hold them, in loads and stores of 8 or 16 bytes. Values stay words until they are
+// computed with: taken apart as 16-bit registers, as they arrive, they spilled.
+template <typename T, int N>
+struct Words {
+  static constexpr int kCount = N * (int)sizeof(T) / 4;
+  static_assert(kCount == 2 || kCount % 4 == 0, "8 bytes, or 16-byte words");
+  uint32_t v[kCount];
+  __device__ __forceinline__ void load(const T *p) {
+    if constexpr (kCount == 2) {
+      const uint2 x = *reinterpret_cast<const uint2 *>(p);
+      v[0] = x.x, v[1] = x.y;
     } else {
-      uint32_t v[Shifted<T, 8>::kWords];
-      w.take(p, 8, v);
-      Pack<T, 8> r;
 #pragma unroll
-      for (int i = 0; i < Shifted<T, 8>::kWords; i += 4) reinterpret_cast<uint4 *>(&r)[i / 4] = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-      return r;
+      for (int i = 0; i < kCount; i += 4) {
+        const uint4 x = reinterpret_cast<const uint4 *>(p)[i / 4];
+        v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
+      }
     }
   }
-  __device__ __forceinline__ void take(const T *p, float (&x)[8]) {
-    const Pack<T, 8> r = bits(p);
+  __device__ __forceinline__ void store(T *p) const {
+    if constexpr (kCount == 2) {
+      *reinterpret_cast<uint2 *>(p) = make_uint2(v[0], v[1]);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = to_f32(r.v[i]);
+      for (int i = 0; i < kCount; i += 4) reinterpret_cast<uint4 *>(p)[i / 4] = make_uint4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    }
+  }
+  __device__ __forceinline__ void values(float (&x)[N]) const {
+    if constexpr (std::is_same_v<T, __half>) {
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v[i / 2]));
+        x[i] = f.x, x[i + 1] = f.y;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) x[i] = value_of<T>(v, i);
+    }
+  }
+  __device__ __forceinline__ void round(const float (&x)[N]) {
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) {
+      if constexpr (std::is_same_v<T, float>) {
+        v[i] = __float_as_uint(x[i]);
+      } else if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+        const __nv_bfloat162 r = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        v[i] = *reinterpret_cast<const uint32_t *>(&r);
+      } else {
+        const __half2 r = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+        v[i] = *reinterpret_cast<const uint32_t *>(&r);
+      }
+    }
   }
 };
 
-// Eight values rounded to T and stored at a 16-byte boundary.
-template <typename T>
-__device__ __forceinline__ void store_eight(T *p, const float (&x)[8]) {
-  Pack<T, 8> r;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) r.v[i] = from_f32<T>(x[i]);
-  *reinterpret_cast<Pack<T, 8> *>(p) = r;
+// N neighbours of a row, all inside it: `Wide` rows start on 16 bytes, others anywhere. ask() starts the loads.
+template <typename T, int N, bool Wide>
+struct Piece {
+  std::conditional_t<Wide, Words<T, N>, Shifted<T, N>> w;
+  __device__ __forceinline__ void ask(const T *p) {
+    if constexpr (Wide) w.load(p);
+    else w.ask(p, N, reinterpret_cast<const uint8_t *>(p) - Shifted<T, N>::skip_of(p));
+  }
+  __device__ __forceinline__ Words<T, N> words(const T *p) {
+    if constexpr (Wide) {
+      return w;
+    } else {
+      Words<T, N> r;
+      w.take(p, N, r.v);
+      return r;
+    }
+  }
+  __device__ __forceinline__ void take(const T *p, float (&x)[N]) { words(p).values(x); }
+};
+
+// N values rounded to T and stored at a boundary of as many.
+template <typename T, int N>
+__device__ __forceinline__ void store_piece(T *p, const float (&x)[N]) {
+  Words<T, N> r;
+  r.round(x);
+  r.store(p);
 }
 
-// A row's columns in pieces of eight whose places in the row that is written start on 16 bytes: where rows start anywhere
-// the first piece begins that much before the row, and it and the last are written value by value.
-template <typename T, bool Wide>
+// Where a row's piece begins, so that its place in the row that is written is a boundary of N values: where rows start
+// anywhere the first piece begins that much before the row, and it and the last are written value by value.
+template <typename T, int N, bool Wide>
 __device__ __forceinline__ int64_t piece_start(int64_t piece, const T *row) {
-  if constexpr (Wide) return piece * 8;
-  else return piece * 8 - (int64_t)((reinterpret_cast<uintptr_t>(row) & 15) / sizeof(T));
-}
-// The pieces that a row of so many columns can have.
-template <typename T>
-constexpr int64_t piece_count(int64_t cols, bool wide) {
-  return wide ? (cols + 7) / 8 : (cols + 7 + (16 / (int)sizeof(T) - 1)) / 8;
+  if constexpr (Wide) return piece * N;
+  else return piece * N - (int64_t)((reinterpret_cast<uintptr_t>(row) & (N * sizeof(T) - 1)) / sizeof(T));
 }
 
 #endif  // __CUDACC__
+
+// The pieces of so many values that a row of so many columns can have.
+inline int64_t piece_count(int64_t cols, int values, bool wide) { return wide ? (cols + values - 1) / values : (cols + 2 * (values - 1)) / values; }
 
 }  // namespace ops
 }  // namespace reshard
