@@ -23,7 +23,7 @@ int launched(cudaError_t e, const char *what) { return e == cudaSuccess ? RESHAR
 
 // ------------------------------------------------------------------------------------------------------------- sort --
 
-constexpr int kSortWarps = 16, kSortCluster = 8, kSortBits = 10;
+constexpr int kSortWarps = 32, kSortCluster = 8, kSortBits = 10;      // warps of a CTA at most
 
 struct Sort {
   const void *ids;
@@ -45,16 +45,16 @@ __global__ void __launch_bounds__(kSortWarps * 32) reshard_sort_rows_kernel(Sort
   grid_enter();
   extern __shared__ int32_t count[];             // [warp][digit], then this CTA's sums [digit], then its first places [digit]
   __shared__ int32_t warp_sum[kSortWarps];
-  const int bins = 1 << a.bits;
-  int32_t *const sum = count + kSortWarps * bins, *const base = sum + bins;
+  const int bins = 1 << a.bits, warps = blockDim.x >> 5;
+  int32_t *const sum = count + warps * bins, *const base = sum + bins;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = (int)blockIdx.x;
   int32_t *const mine = count + warp * bins;
   int64_t n = a.tokens;
   for (int pass = 0; pass < a.passes; ++pass) {
     const uint2 *const from = (a.passes - pass) & 1 ? a.other : a.sorted;
     uint2 *const to = (a.passes - pass) & 1 ? a.sorted : a.other;
-    const int64_t run = (n + kSortCluster * kSortWarps * 32 - 1) / (kSortCluster * kSortWarps * 32) * 32;
-    const int64_t lo = (cta * kSortWarps + warp) * run, hi = min(lo + run, n);
+    const int64_t run = (n + kSortCluster * (int)blockDim.x - 1) / (kSortCluster * (int)blockDim.x) * 32;
+    const int64_t lo = (cta * warps + warp) * run, hi = min(lo + run, n);
     auto pair = [&](int64_t i) {                 // row 2^32 - 1: none
       uint2 p = make_uint2(~0u, 0);
       if (i < hi) {
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) reshard_sort_rows_kernel(Sort
       return p;
     };
     const int shift = pass * a.bits;
-    for (int i = tid; i < kSortWarps * bins; i += kSortWarps * 32) count[i] = 0;
+    for (int i = tid; i < warps * bins; i += (int)blockDim.x) count[i] = 0;
     __syncthreads();
     for (int64_t i0 = lo + lane; i0 < hi; i0 += 4 * 32) {
       uint2 p[4];
@@ -79,10 +79,10 @@ __global__ void __launch_bounds__(kSortWarps * 32) reshard_sort_rows_kernel(Sort
         if (p[u].x != ~0u) atomicAdd(&mine[p[u].x >> shift & (bins - 1)], 1);
     }
     __syncthreads();
-    for (int d = tid; d < bins; d += kSortWarps * 32) {
+    for (int d = tid; d < bins; d += (int)blockDim.x) {
       int s = 0;
-#pragma unroll
-      for (int w = 0; w < kSortWarps; ++w) {
+#pragma unroll 16
+      for (int w = 0; w < warps; ++w) {
         const int c = count[w * bins + d];
         count[w * bins + d] = s;
         s += c;
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) reshard_sort_rows_kernel(Sort
     cluster_barrier();
     // the digits' first places: a running sum of the cluster's counts, and this CTA's share of each
     int done = 0;
-    for (int d0 = 0; d0 < bins; d0 += kSortWarps * 32) {
+    for (int d0 = 0; d0 < bins; d0 += (int)blockDim.x) {
       const int d = d0 + tid;
       int all = 0, before = 0;
       if (d < bins) {
@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) reshard_sort_rows_kernel(Sort
       if (lane == 31) warp_sum[warp] = upto;
       __syncthreads();
       int here = 0;
-      for (int w = 0; w < kSortWarps; ++w) {
+      for (int w = 0; w < warps; ++w) {
         if (w < warp) upto += warp_sum[w];
         here += warp_sum[w];
       }
@@ -178,21 +178,29 @@ __global__ void __launch_bounds__(kZeroThreads) reshard_zero_kernel(uint8_t *bas
 // -------------------------------------------------------------------------------------------------------------- sum --
 
 constexpr int kSumThreads = 128;
-constexpr int kJoinColumns = kSumThreads * 4;
+constexpr int kJoinThreads = 128, kJoinColumns = kJoinThreads * 4;
+
+// The sorted tokens go in runs, one to each CTA (of a slice of the columns): at least kMinRun tokens, and as many runs as give the
+// GPU one round of CTAs, kSumCtas of each of 152 SMs (a second round of a few CTAs took a third longer). How many tokens are of this
+// shard, the device knows. Each run leaves up to two rows in the workspace.
+constexpr int64_t kMinRun = 16, kMostRuns = 512;
+constexpr int kSumCtas = 6;
+int runs_of(int64_t slices) { return (int)std::max<int64_t>(64, std::min<int64_t>(kMostRuns, 152 * kSumCtas / slices)); }
 
 struct Sum {
   const uint2 *sorted;
   const int32_t *held;
   const void *grad;
-  int64_t tokens, cols, grad_stride;
+  int64_t cols, grad_stride;
   float scale;
   void *table;
   int64_t table_stride;
   bool accumulate, wide_table;
   float *part;                       // [run][2][pitch]: of the row that a run begins inside, and of the one that it ends inside
   int64_t pitch;
-  int run;                           // sorted tokens of a CTA
+  int runs;                          // at most
   int slices;                        // CTAs a run
+  __device__ __forceinline__ int64_t run_of(int64_t tokens) const { return tokens <= kMinRun * runs ? kMinRun : (tokens + runs - 1) / runs; }
 };
 
 // N of a row's sums, scaled, into the table.
@@ -219,24 +227,22 @@ __device__ __forceinline__ void write_sums(const Sum &a, uint32_t row, int64_t c
 }
 
 template <typename TG, typename T, bool Wide>
-__global__ void __launch_bounds__(kSumThreads) reshard_sum_rows_kernel(Sum a) {
-  constexpr int kN = kPieceOf<TG, T>, kRows = 8;       // rows in flight
+__global__ void __launch_bounds__(kSumThreads, Wide ? kSumCtas : 5) reshard_sum_rows_kernel(Sum a) {
+  constexpr int kN = kPieceOf<TG, T>, kRows = Wide ? 8 : 4;       // rows in flight
   grid_enter();
   const int lane = threadIdx.x & 31;
-  const int64_t run = blockIdx.x / (uint32_t)a.slices;
+  const int64_t number = blockIdx.x / (uint32_t)a.slices;
   const int64_t c = ((int64_t)(blockIdx.x % (uint32_t)a.slices) * kSumThreads + threadIdx.x) * kN;
-  const int64_t lo = run * a.run;
-  // what lies behind the last pair is read as well, and not used: nothing here waits for how many there are
-  uint2 mine = lo + lane < a.tokens ? a.sorted[lo + lane] : make_uint2(0, 0);
-  const uint32_t before = lo > 0 ? a.sorted[lo - 1].x : ~0u;
-  const uint32_t after = lo + a.run < a.tokens ? a.sorted[lo + a.run].x : ~0u;
-  const int64_t held = *a.held, hi = min(lo + a.run, held);
+  const int64_t held = *a.held, run = a.run_of(held), lo = number * run, hi = min(lo + run, held);
   if (lo >= held || c - lane * kN >= a.cols) return;       // whole warps
+  uint2 mine = lo + lane < hi ? a.sorted[lo + lane] : make_uint2(0, 0);
+  const uint32_t before = lo > 0 ? a.sorted[lo - 1].x : ~0u;
+  const uint32_t after = hi < held ? a.sorted[hi].x : ~0u;
   const TG *const grad = static_cast<const TG *>(a.grad) + c;
   const int left = (int)max((int64_t)0, min((int64_t)kN, a.cols - c));
   uint32_t row = __shfl_sync(kFull, mine.x, 0);
   bool head = before == row;
-  float *const part = a.part + 2 * run * a.pitch + c;
+  float *const part = a.part + 2 * number * a.pitch + c;
   float sum[kN] = {};
   auto keep = [&](float *to) {
     if (left == 0) return;
@@ -274,37 +280,37 @@ __global__ void __launch_bounds__(kSumThreads) reshard_sum_rows_kernel(Sum a) {
     }
   }
   if (head) keep(part);
-  else if (hi < held && after == row) keep(part + a.pitch);
+  else if (after == row) keep(part + a.pitch);
   else if (left) write_sums<T, kN>(a, row, c, sum);
 }
 
 // The rows that end in another run than they begin in: the CTAs of the run that such a row begins in.
 template <typename T>
-__global__ void __launch_bounds__(kSumThreads) reshard_join_rows_kernel(Sum a) {
+__global__ void __launch_bounds__(kJoinThreads) reshard_join_rows_kernel(Sum a) {
   grid_enter();
   const int lane = threadIdx.x & 31;
-  const int64_t run = blockIdx.x / (uint32_t)a.slices;
+  const int64_t number = blockIdx.x / (uint32_t)a.slices;
   const int64_t c = (int64_t)(blockIdx.x % (uint32_t)a.slices) * kJoinColumns + threadIdx.x * 4;
-  const int64_t lo = run * a.run, hi = lo + a.run;       // hi < tokens: no CTA has the last run
+  const int64_t held = *a.held, run = a.run_of(held), lo = number * run, hi = lo + run;
+  if (hi >= held) return;
   const uint32_t row = a.sorted[hi - 1].x, after = a.sorted[hi].x, before = lo > 0 ? a.sorted[lo - 1].x : ~0u;
-  const int64_t held = *a.held;
-  if (hi >= held || after != row || before == row) return;
   // the run that the row ends in: the first whose next run begins with another row, or that is the last
-  int64_t last = run + 1;
-  for (;; last += 32) {
-    const int64_t next = (last + lane + 1) * a.run;
-    const uint32_t ends = __ballot_sync(kFull, next >= held || a.sorted[min(next, held - 1)].x != row);
-    if (ends) {
-      last += __ffs(ends) - 1;
-      break;
-    }
+  int64_t last = number + 1;
+  const int64_t next = (last + lane + 1) * run;
+  uint32_t ends = __ballot_sync(kFull, next >= held || a.sorted[min(next, held - 1)].x != row);
+  if (after != row || before == row) return;
+  while (!ends) {
+    last += 32;
+    const int64_t more = (last + lane + 1) * run;
+    ends = __ballot_sync(kFull, more >= held || a.sorted[min(more, held - 1)].x != row);
   }
+  last += __ffs(ends) - 1;
   if (c >= a.cols) return;
   float sum[4];
-  load_values<float, 4>(a.part + (2 * run + 1) * a.pitch + c, 4, true, sum);
-  const float *from = a.part + 2 * (run + 1) * a.pitch + c;
-#pragma unroll 8
-  for (int64_t r = run + 1; r <= last; ++r, from += 2 * a.pitch) {
+  load_values<float, 4>(a.part + (2 * number + 1) * a.pitch + c, 4, true, sum);
+  const float *from = a.part + 2 * (number + 1) * a.pitch + c;
+#pragma unroll 16
+  for (int64_t r = number + 1; r <= last; ++r, from += 2 * a.pitch) {
     float x[4];
     load_values<float, 4>(from, 4, true, x);
 #pragma unroll
@@ -313,15 +319,10 @@ __global__ void __launch_bounds__(kSumThreads) reshard_join_rows_kernel(Sum a) {
   write_sums<T, 4>(a, row, c, sum);
 }
 
-constexpr int64_t kMinRun = 16, kRuns = 256;
-// Sorted tokens of a CTA: few, so that a row's tokens are read by many CTAs, but at most 2,048 runs, whose pieces of rows
-// (two each) the workspace holds.
-int64_t run_of(int64_t tokens) { return std::max<int64_t>(kMinRun, (tokens + kRuns - 1) / kRuns); }
-
 struct Layout {
   int64_t sorted, held, runs, pitch, part;
   Layout(int64_t tokens, int64_t cols)
-      : sorted(up(8 * tokens, kAlign)), held(kAlign), runs((tokens + run_of(tokens) - 1) / run_of(tokens)), pitch(up(cols, 8)),
+      : sorted(up(8 * tokens, kAlign)), held(kAlign), runs(std::min<int64_t>(kMostRuns, (tokens + kMinRun - 1) / kMinRun)), pitch(up(cols, 8)),
         part(up(2 * runs * pitch * 4, kAlign)) {}
   int64_t bytes() const { return 2 * sorted + held + part; }
 };
@@ -376,7 +377,9 @@ extern "C" int reshard_embedding_backward(const void *grad, int grad_dtype, int6
     s.passes = (need + kSortBits - 1) / kSortBits;
     s.bits = (need + s.passes - 1) / s.passes;
     if ((rc = allow_smem<reshard_sort_rows_kernel>((size_t)(kSortWarps + 2) * 4 << kSortBits))) return rc;
-    if ((rc = launched(launch(reshard_sort_rows_kernel, dim3(kSortCluster), kSortWarps * 32, (size_t)(kSortWarps + 2) * 4 << s.bits, kSortCluster, stream, s),
+    // Half the warps take a few microseconds less for a few tokens (4,095: 10 us), all of them for many (65,536: 20 instead of 28).
+    const int warps = tokens <= 16384 ? kSortWarps / 2 : kSortWarps;
+    if ((rc = launched(launch(reshard_sort_rows_kernel, dim3(kSortCluster), warps * 32, (size_t)(warps + 2) * 4 << s.bits, kSortCluster, stream, s),
                        "launching reshard_sort_rows_kernel")))
       return rc;
   }
@@ -389,21 +392,22 @@ extern "C" int reshard_embedding_backward(const void *grad, int grad_dtype, int6
       return rc;
   }
   if (tokens == 0) return RESHARD_OK;
-  Sum a{sorted, held, grad, tokens, cols, grad_stride, scale, grad_table, table_stride, accumulate != 0, aligned16(grad_table, table_stride, es),
-        reinterpret_cast<float *>(at + 2 * l.sorted + l.held), l.pitch, (int)run_of(tokens), 0};
+  Sum a{sorted, held, grad, cols, grad_stride, scale, grad_table, table_stride, accumulate != 0, aligned16(grad_table, table_stride, es),
+        reinterpret_cast<float *>(at + 2 * l.sorted + l.held), l.pitch, 0, 0};
   const bool wide = aligned16(grad, grad_stride, element_bytes(grad_dtype));
   rc = launched(by_type(grad_dtype, [&](auto g) {
     using TG = decltype(g);
     return by_type(table_dtype, [&](auto t) {
       using T = decltype(t);
       a.slices = (int)((cols + kSumThreads * kPieceOf<TG, T> - 1) / (kSumThreads * kPieceOf<TG, T>));
-      return launch(wide ? reshard_sum_rows_kernel<TG, T, true> : reshard_sum_rows_kernel<TG, T, false>, dim3((unsigned)(l.runs * a.slices)), kSumThreads, 0,
+      a.runs = (int)std::min<int64_t>(l.runs, runs_of(a.slices));
+      return launch(wide ? reshard_sum_rows_kernel<TG, T, true> : reshard_sum_rows_kernel<TG, T, false>, dim3((unsigned)(a.runs * a.slices)), kSumThreads, 0,
                     1, stream, a);
     });
   }), "launching reshard_sum_rows_kernel");
-  if (rc || l.runs == 1) return rc;
+  if (rc || a.runs == 1) return rc;
   a.slices = (int)((cols + kJoinColumns - 1) / kJoinColumns);
   return launched(by_type(table_dtype, [&](auto t) {
-    return launch(reshard_join_rows_kernel<decltype(t)>, dim3((unsigned)((l.runs - 1) * a.slices)), kSumThreads, 0, 1, stream, a);
+    return launch(reshard_join_rows_kernel<decltype(t)>, dim3((unsigned)((a.runs - 1) * a.slices)), kJoinThreads, 0, 1, stream, a);
   }), "launching reshard_join_rows_kernel");
 } OPS_CATCH

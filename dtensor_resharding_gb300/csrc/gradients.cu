@@ -39,8 +39,8 @@ namespace {
 constexpr int kNormThreads = 256;
 constexpr int kMaxCtas = 1024;                    // whose sums the workspace holds
 constexpr int kUnitStep = kNormThreads * 8;       // a unit is a multiple of it
-constexpr int kCtasPerSm = 4;
-constexpr int kFillCtas = 608;                    // of 152 SMs
+constexpr int kSquaresCtas = 6, kClipCtas = 4;   // of an SM
+constexpr int kFillCtas = 304;                    // two of each of 152 SMs
 constexpr double kEps = 1e-6;
 
 // The tensors of a launch, as one of its arguments: those have 32,764 bytes. A tensor is its address and one word: the units of
@@ -95,18 +95,9 @@ struct Squares {
     s = t;
     return true;
   }
-  template <int N>
-  __device__ __forceinline__ void add_far(const float (&x)[N]) {
-    bool any = false;
-#pragma unroll
-    for (int i = 0; i < N; ++i) any |= x[i] != 0.0f;      // NaN too
-    if (!any) return;
-#pragma unroll
-    for (int i = 0; i < N; ++i) d += (double)x[i] * (double)x[i];
-  }
+  __device__ __forceinline__ void add_far(float v) { d += (double)v * (double)v; }
   __device__ __forceinline__ void add_one(float v) {
-    const float x[1] = {v};
-    if (!add(v * v)) add_far(x);
+    if (!add(v * v)) add_far(v);
   }
   __device__ __forceinline__ double total() const { return (double)s + (double)r + d; }
 };
@@ -146,6 +137,7 @@ __device__ __forceinline__ void add_unit(const T *p, int64_t n, int64_t unit, in
       if (w < words) v[u].load(body + w * kPer);
     }
     float sq[kAhead];
+    uint32_t bits = 0;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       float x[kPer];
@@ -153,21 +145,22 @@ __device__ __forceinline__ void add_unit(const T *p, int64_t n, int64_t unit, in
       sq[u] = 0.0f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) sq[u] = fmaf(x[i], x[i], sq[u]);
-    }
-    if (!sum.add((sq[0] + sq[1]) + (sq[2] + sq[3]))) {
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        float x[kPer];
-        v[u].values(x);
-        sum.add_far(x);
-      }
+      for (int i = 0; i < 4; ++i) bits |= v[u].v[i];
+    }
+    if (sum.add((sq[0] + sq[1]) + (sq[2] + sq[3])) || (bits & (sizeof(T) == 4 ? 0x7fffffffu : 0x7fff7fffu)) == 0) continue;
+#pragma unroll 1
+    for (int u = 0; u < kAhead; ++u) {
+      const int w = w0 + kNormThreads * u;
+#pragma unroll 1
+      for (int i = 0; w < words && i < kPer; ++i) sum.add_far(to_f32(body[w * kPer + i]));
     }
   }
   if (tid < m - words * kPer) sum.add_one(to_f32(body[words * kPer + tid]));
 }
 
 // Each CTA's sum of squares over its units of the launch, every gridDim-th; later launches of a call add to it.
-__global__ void __launch_bounds__(kNormThreads, kCtasPerSm) reshard_squares_kernel(const __grid_constant__ Batch<false> b, double *part, bool fresh) {
+__global__ void __launch_bounds__(kNormThreads, kSquaresCtas) reshard_squares_kernel(const __grid_constant__ Batch<false> b, double *part, bool fresh) {
   grid_enter();
   __shared__ double warps[kNormThreads / 32];
   const uint32_t units = b.units();
@@ -237,7 +230,7 @@ __device__ __forceinline__ void clip_unit(const T *p, TO *to, int64_t n, int64_t
 // CTAs' sums, by each CTA for itself; `out` gets it. The units are taken from the last to the first, since what the sums
 // read last is still in L2: a batch has its tensors from the last to the first. A launch has tensors of one pair of types: all nine pairs in one kernel spilled its registers.
 template <typename T, typename TO, bool Moved>
-__global__ void __launch_bounds__(kNormThreads, (sizeof(TO) > sizeof(T) ? 6 : kCtasPerSm))
+__global__ void __launch_bounds__(kNormThreads, (sizeof(TO) > sizeof(T) ? 6 : kClipCtas))
     reshard_clip_kernel(const __grid_constant__ Batch<Moved> b, const float *given, const double *part, int ctas, double limit, float *out) {
   grid_enter();
   __shared__ double warps[kNormThreads / 32];
@@ -286,7 +279,7 @@ int ctas_of(const reshard_tensors &list, int *ctas) {
   int sms = 0;
   const int rc = device_sms(&sms);
   if (rc) return rc;
-  *ctas = (int)std::max<int64_t>(1, std::min<int64_t>(list.units, std::min(kMaxCtas, sms * kCtasPerSm)));
+  *ctas = (int)std::max<int64_t>(1, std::min<int64_t>(list.units, std::min(kMaxCtas, sms * kSquaresCtas)));
   return RESHARD_OK;
 }
 
@@ -365,8 +358,9 @@ extern "C" int reshard_tensors_create(const void *const *at, const int64_t *elem
     l.tensors.push_back({reinterpret_cast<uintptr_t>(at[i]), elements[i], dtypes[i]});
   }
   if (!c.ok()) return c.report();
-  // Units of up to 16,384 elements (8 pieces of 16 bytes a thread, or 16), smaller where there would not be one for each CTA.
-  l.unit = std::max<int64_t>(kUnitStep, std::min<int64_t>(8 * kUnitStep, total / kFillCtas / kUnitStep * kUnitStep));
+  // Units of up to 16,384 elements (8 pieces of 16 bytes a thread, or 16), halved while there is not one for each CTA.
+  l.unit = 8 * kUnitStep;
+  while (l.unit > kUnitStep && total / l.unit < kFillCtas) l.unit /= 2;
   for (const auto &t : l.tensors) l.units += (t.n + l.unit - 1) / l.unit;
   std::vector<std::pair<uintptr_t, uintptr_t>> spans;
   for (const auto &t : l.tensors)

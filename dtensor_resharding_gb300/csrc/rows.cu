@@ -163,88 +163,106 @@ __global__ void __launch_bounds__(kRowThreads) reshard_embedding_kernel(Lookup a
 // ---------------------------------------------------------------------------------------------------------- combine --
 
 // A warp a span of a token's columns. Lanes look up the places of up to 32 slots at once; those that have one are taken in
-// order, kSlots rows in flight together.
-constexpr int kCombineCtas = 4;                  // of an SM
+// order, kSlots rows in flight together. Bound by the read of y: 8 places a token, 8,192 x 2048 fp32, 85 us, 6.7 TB/s; where few
+// slots have a place by the chain places, rows, output of each span, so that warps stay and look up the next span's places
+// before this one's rows (16,383 tokens with one place of eight on average, 4096 fp32: 71 us; a warp a span: 78). Rows that start
+// anywhere need the registers for themselves, and more warps (61 us, with the look ahead 65, for 8,191 x 2867 fp16, four places each).
 template <typename TY, typename TO, bool Wide>
 struct CombineShape {
   static constexpr int kN = kPieceOf<TY, TO>;
   static constexpr int kPieces = 16 / kN;        // 16 columns a lane
-  static constexpr int kSlots = Wide ? 2 : 1;    // rows in flight; rows that start anywhere need twice the registers
+  static constexpr int kSlots = Wide ? 2 : 1;    // rows in flight
+  static constexpr int kCtas = (Wide ? 4 : 5) - (sizeof(TY) == 4 ? 1 : 0);      // of an SM
 };
 
 template <typename TY, typename TO, bool Wide>
-__global__ void __launch_bounds__(kRowThreads, kCombineCtas) reshard_combine_kernel(Combine a, int spans) {
+__global__ void __launch_bounds__(kRowThreads, CombineShape<TY, TO, Wide>::kCtas) reshard_combine_kernel(Combine a, int spans) {
   using Shape = CombineShape<TY, TO, Wide>;
   constexpr int kN = Shape::kN, kU = Shape::kPieces, kSlots = Shape::kSlots;
   grid_enter();
   const int lane = threadIdx.x & 31;
-  const Where at(spans);
-  const int64_t t = at.row;
-  if (t >= a.tokens) return;
-  TO *const to = static_cast<TO *>(a.out) + t * a.out_stride;
-  int64_t c[kU];
-  bool whole[kU];
-  bool edge = false;
-#pragma unroll
-  for (int u = 0; u < kU; ++u) {
-    c[u] = piece_start<TO, kN, Wide>(at.span * 32 * kU + lane + 32 * u, to);
-    whole[u] = c[u] >= 0 && c[u] + kN <= a.cols;
-    edge |= !whole[u] && c[u] < a.cols;
-  }
-  float sum[kU][kN] = {};
-  for (int j0 = 0; j0 < a.k; j0 += 32) {
+  const int64_t units = a.tokens * spans, step = (int64_t)gridDim.x * (blockDim.x >> 5);
+  int64_t unit = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  auto row_of = [&](int64_t w) { return w <= 0xffffffffll ? (int64_t)((uint32_t)w / (uint32_t)spans) : w / spans; };
+  // The lane's slot among 32 from j0 on: its place (-1: none) and weight. Those of the next unit are asked for before this one's rows.
+  auto look = [&](int64_t t, int j0, int &place, float &weight) {
     const int64_t s = t * a.k + j0 + lane;
     const bool in = j0 + lane < a.k;
-    const int mine = in ? place_of(a.position, s, a.rows) : -1;
-    const float weight = in && a.weights ? a.weights[s] : 1.0f;
-    for (uint32_t live = __ballot_sync(kFull, mine >= 0); live;) {
-      const TY *from[kSlots];
-      float w[kSlots];
-      Piece<TY, kN, Wide> v[kSlots][kU];
+    place = in ? a.position[s] : -1;
+    weight = in && a.weights ? a.weights[s] : 1.0f;
+  };
+  int next = -1;
+  float next_weight = 1.0f;
+  if (unit >= units) return;
+  look(row_of(unit), 0, next, next_weight);
+  do {
+    const int64_t t = row_of(unit), span = unit - t * spans;
+    int mine = next;
+    float weight = next_weight;
+    if (Wide && unit + step < units) look(row_of(unit + step), 0, next, next_weight);
+    TO *const to = static_cast<TO *>(a.out) + t * a.out_stride;
+    int64_t c[kU];
+    bool whole[kU];
+    bool edge = false;
 #pragma unroll
-      for (int q = 0; q < kSlots; ++q) {
-        const int j = __ffs(live) - 1;           // -1: none left
-        const int p = __shfl_sync(kFull, mine, max(j, 0));
-        w[q] = __shfl_sync(kFull, weight, max(j, 0));
-        from[q] = j >= 0 ? static_cast<const TY *>(a.y) + (int64_t)p * a.y_stride : nullptr;
-        live &= live - 1;
+    for (int u = 0; u < kU; ++u) {
+      c[u] = piece_start<TO, kN, Wide>(span * 32 * kU + lane + 32 * u, to);
+      whole[u] = c[u] >= 0 && c[u] + kN <= a.cols;
+      edge |= !whole[u] && c[u] < a.cols;
+    }
+    float sum[kU][kN] = {};
+    for (int j0 = 0;;) {
+      for (uint32_t live = __ballot_sync(kFull, mine >= 0 && mine < a.rows); live;) {
+        const TY *from[kSlots];
+        float w[kSlots];
+        Piece<TY, kN, Wide> v[kSlots][kU];
 #pragma unroll
-        for (int u = 0; u < kU; ++u)
-          if (from[q] && whole[u]) v[q][u].ask(from[q] + c[u]);
-      }
+        for (int q = 0; q < kSlots; ++q) {
+          const int j = __ffs(live) - 1;           // -1: none left
+          const int p = __shfl_sync(kFull, mine, max(j, 0));
+          w[q] = __shfl_sync(kFull, weight, max(j, 0));
+          from[q] = j >= 0 ? static_cast<const TY *>(a.y) + (int64_t)p * a.y_stride : nullptr;
+          live &= live - 1;
 #pragma unroll
-      for (int q = 0; q < kSlots; ++q) {
-        if (!from[q]) break;
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          if (!whole[u]) continue;
-          float x[kN];
-          v[q][u].take(from[q] + c[u], x);
-#pragma unroll
-          for (int e = 0; e < kN; ++e) sum[u][e] = fmaf(w[q], x[e], sum[u][e]);
+          for (int u = 0; u < kU; ++u)
+            if (from[q] && whole[u]) v[q][u].ask(from[q] + c[u]);
         }
-        if (edge) {
+#pragma unroll
+        for (int q = 0; q < kSlots; ++q) {
+          if (!from[q]) break;
 #pragma unroll
           for (int u = 0; u < kU; ++u) {
-            if (whole[u]) continue;
+            if (!whole[u]) continue;
+            float x[kN];
+            v[q][u].take(from[q] + c[u], x);
 #pragma unroll
-            for (int e = 0; e < kN; ++e)
-              if (c[u] + e >= 0 && c[u] + e < a.cols) sum[u][e] = fmaf(w[q], to_f32(from[q][c[u] + e]), sum[u][e]);
+            for (int e = 0; e < kN; ++e) sum[u][e] = fmaf(w[q], x[e], sum[u][e]);
+          }
+          if (edge) {
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+              if (whole[u]) continue;
+#pragma unroll
+              for (int e = 0; e < kN; ++e)
+                if (c[u] + e >= 0 && c[u] + e < a.cols) sum[u][e] = fmaf(w[q], to_f32(from[q][c[u] + e]), sum[u][e]);
+            }
           }
         }
       }
+      if ((j0 += 32) >= a.k) break;
+      look(t, j0, mine, weight);
     }
-  }
 #pragma unroll
-  for (int u = 0; u < kU; ++u) {
-    if (whole[u]) {
-      store_piece(to + c[u], sum[u]);
-    } else {
+    for (int u = 0; u < kU; ++u) {
+      if (whole[u]) {
+        store_piece(to + c[u], sum[u]);
+      } else {
 #pragma unroll
-      for (int e = 0; e < kN; ++e)
-        if (c[u] + e >= 0 && c[u] + e < a.cols) to[c[u] + e] = from_f32<TO>(sum[u][e]);
+        for (int e = 0; e < kN; ++e)
+          if (c[u] + e >= 0 && c[u] + e < a.cols) to[c[u] + e] = from_f32<TO>(sum[u][e]);
+      }
     }
-  }
+  } while (Wide && (unit += step) < units);
 }
 
 // ------------------------------------------------------------------------------------------------- combine backward --
@@ -458,6 +476,8 @@ cudaError_t launch_warps(void (*kernel)(K...), int64_t warps, cudaStream_t strea
 
 int enqueue_combine(const Combine &a, cudaStream_t stream) {
   if (a.tokens == 0 || a.cols == 0) return RESHARD_OK;
+  int sms = 0;
+  if (const int rc = device_sms(&sms)) return rc;
   const bool wide = aligned16(a.y, a.y_stride, element_bytes(a.dtype)) && aligned16(a.out, a.out_stride, element_bytes(a.out_dtype));
   return launched(by_type(a.dtype, [&](auto y) {
     using TY = decltype(y);
@@ -465,7 +485,11 @@ int enqueue_combine(const Combine &a, cudaStream_t stream) {
       using TO = decltype(o);
       using Shape = CombineShape<TY, TO, true>;
       const int spans = (int)ceil_div(piece_count(a.cols, Shape::kN, wide), 32 * Shape::kPieces);
-      return launch_warps(wide ? reshard_combine_kernel<TY, TO, true> : reshard_combine_kernel<TY, TO, false>, a.tokens * spans, stream, a, spans);
+      const int64_t warps = a.tokens * spans;
+      const int block = warps <= 2048 ? kFewThreads : kRowThreads;
+      const int64_t ctas = ceil_div(warps, block / 32), stay = (int64_t)sms * Shape::kCtas * (kRowThreads / block);
+      const unsigned grid = (unsigned)(wide ? std::min(ctas, stay) : ctas);      // rows that start anywhere: a warp has one span
+      return launch(wide ? reshard_combine_kernel<TY, TO, true> : reshard_combine_kernel<TY, TO, false>, dim3(grid), block, 0, 1, stream, a, spans);
     });
   }), "launching reshard_combine_kernel");
 }
