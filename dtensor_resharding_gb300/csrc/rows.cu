@@ -84,37 +84,44 @@ __global__ void __launch_bounds__(kRowThreads) reshard_permute_kernel(Permute a)
   }
 }
 
-// Pieces [first, first + kSpan) of a row, copied (times `scale`, where scaled) or, without a source, zeroed.
+// Pieces [first, first + kSpan) of a row, copied (times `scale`, where scaled) or, without a source, zeroed. All lanes call.
 template <typename T, bool Wide, bool Scaled>
 __device__ __forceinline__ void move_span(const T *from, T *to, int64_t cols, int64_t first, int lane, float scale) {
   constexpr int kN = kPieceOf<T, T>;
-  Piece<T, kN, Wide> v[kAhead];
-  int64_t c[kAhead];
-  bool whole[kAhead];
+  const int64_t c0 = piece_start<T, kN, Wide>(first, to);
+  std::conditional_t<Wide, Words<T, kN>[kAhead], Strip<T, kN, kAhead>> v;
+  if (from) {
+    if constexpr (Wide) {
 #pragma unroll
-  for (int u = 0; u < kAhead; ++u) {
-    c[u] = piece_start<T, kN, Wide>(first + lane + 32 * u, to);
-    whole[u] = c[u] >= 0 && c[u] + kN <= cols;
-    if (from && whole[u]) v[u].ask(from + c[u]);
+      for (int u = 0; u < kAhead; ++u)
+        if (c0 + (32 * u + lane + 1) * kN <= cols) v[u].load(from + c0 + (32 * u + lane) * kN);
+    } else {
+      v.ask(from, cols, c0, lane);
+    }
   }
 #pragma unroll
   for (int u = 0; u < kAhead; ++u) {
-    if (whole[u]) {
-      if (Scaled && from) {
-        float x[kN];
-        v[u].take(from + c[u], x);
+    const int64_t c = c0 + (32 * u + lane) * kN;
+    const bool whole = c >= 0 && c + kN <= cols;
+    Words<T, kN> r{};
+    if constexpr (Wide) {
+      if (from && whole) r = v[u];
+    } else {
+      if (from) r = v.words(u, lane);
+    }
+    if (Scaled && from) {
+      float x[kN];
+      r.values(x);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) x[i] *= scale;
-        store_piece(to + c[u], x);
-      } else {
-        Words<T, kN> r{};
-        if (from) r = v[u].words(from + c[u]);
-        r.store(to + c[u]);
-      }
-    } else if (c[u] < cols) {
+      for (int i = 0; i < kN; ++i) x[i] *= scale;
+      r.round(x);
+    }
+    if (whole) {
+      r.store(to + c);
+    } else if (c < cols) {           // the row's ends, value by value
 #pragma unroll
       for (int i = 0; i < kN; ++i)
-        if (c[u] + i >= 0 && c[u] + i < cols) to[c[u] + i] = from ? (Scaled ? from_f32<T>(to_f32(from[c[u] + i]) * scale) : from[c[u] + i]) : from_f32<T>(0.0f);
+        if (c + i >= 0 && c + i < cols) to[c + i] = !from ? from_f32<T>(0.0f) : Scaled ? from_f32<T>(to_f32(from[c + i]) * scale) : from[c + i];
     }
   }
 }
@@ -163,21 +170,22 @@ __global__ void __launch_bounds__(kRowThreads) reshard_embedding_kernel(Lookup a
 // ---------------------------------------------------------------------------------------------------------- combine --
 
 // A warp a span of a token's columns. Lanes look up the places of up to 32 slots at once; those that have one are taken in
-// order, kSlots rows in flight together. Bound by the read of y: 8 places a token, 8,192 x 2048 fp32, 85 us, 6.7 TB/s; where few
+// order, kSlots rows in flight together. Bound by the read of y: 8 places a token, 8,192 x 2048 fp32, 84 us, 6.8 TB/s; where few
 // slots have a place by the chain places, rows, output of each span, so that warps stay and look up the next span's places
 // before this one's rows (16,383 tokens with one place of eight on average, 4096 fp32: 71 us; a warp a span: 78). Rows that start
-// anywhere need the registers for themselves, and more warps (61 us, with the look ahead 65, for 8,191 x 2867 fp16, four places each).
-template <typename TY, typename TO, bool Wide>
+// anywhere are bound by instructions (8,191 x 2867 fp16, four places each: 48 us, where aligned ones would take 37; a word
+// before and one behind for each lane, without its neighbour's: 59).
+template <typename TY, typename TO>
 struct CombineShape {
   static constexpr int kN = kPieceOf<TY, TO>;
   static constexpr int kPieces = 16 / kN;        // 16 columns a lane
-  static constexpr int kSlots = Wide ? 2 : 1;    // rows in flight
-  static constexpr int kCtas = (Wide ? 4 : 5) - (sizeof(TY) == 4 ? 1 : 0);      // of an SM
+  static constexpr int kSlots = 2;
+  static constexpr int kCtas = sizeof(TY) == 4 ? 3 : 4;      // of an SM: what the registers allow
 };
 
 template <typename TY, typename TO, bool Wide>
-__global__ void __launch_bounds__(kRowThreads, CombineShape<TY, TO, Wide>::kCtas) reshard_combine_kernel(Combine a, int spans) {
-  using Shape = CombineShape<TY, TO, Wide>;
+__global__ void __launch_bounds__(kRowThreads, CombineShape<TY, TO>::kCtas) reshard_combine_kernel(Combine a, int spans) {
+  using Shape = CombineShape<TY, TO>;
   constexpr int kN = Shape::kN, kU = Shape::kPieces, kSlots = Shape::kSlots;
   grid_enter();
   const int lane = threadIdx.x & 31;
@@ -201,21 +209,15 @@ __global__ void __launch_bounds__(kRowThreads, CombineShape<TY, TO, Wide>::kCtas
     float weight = next_weight;
     if (Wide && unit + step < units) look(row_of(unit + step), 0, next, next_weight);
     TO *const to = static_cast<TO *>(a.out) + t * a.out_stride;
-    int64_t c[kU];
-    bool whole[kU];
-    bool edge = false;
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      c[u] = piece_start<TO, kN, Wide>(span * 32 * kU + lane + 32 * u, to);
-      whole[u] = c[u] >= 0 && c[u] + kN <= a.cols;
-      edge |= !whole[u] && c[u] < a.cols;
-    }
+    const int64_t c0 = piece_start<TO, kN, Wide>(span * 32 * kU, to);
+    auto column = [&](int u) { return c0 + (32 * u + lane) * kN; };
+    auto whole = [&](int u) { return column(u) >= 0 && column(u) + kN <= a.cols; };
     float sum[kU][kN] = {};
     for (int j0 = 0;;) {
       for (uint32_t live = __ballot_sync(kFull, mine >= 0 && mine < a.rows); live;) {
         const TY *from[kSlots];
         float w[kSlots];
-        Piece<TY, kN, Wide> v[kSlots][kU];
+        std::conditional_t<Wide, Words<TY, kN>[kU], Strip<TY, kN, kU>> v[kSlots];
 #pragma unroll
         for (int q = 0; q < kSlots; ++q) {
           const int j = __ffs(live) - 1;           // -1: none left
@@ -223,29 +225,33 @@ __global__ void __launch_bounds__(kRowThreads, CombineShape<TY, TO, Wide>::kCtas
           w[q] = __shfl_sync(kFull, weight, max(j, 0));
           from[q] = j >= 0 ? static_cast<const TY *>(a.y) + (int64_t)p * a.y_stride : nullptr;
           live &= live - 1;
+          if (!from[q]) continue;
+          if constexpr (Wide) {
 #pragma unroll
-          for (int u = 0; u < kU; ++u)
-            if (from[q] && whole[u]) v[q][u].ask(from[q] + c[u]);
+            for (int u = 0; u < kU; ++u)
+              if (whole(u)) v[q][u].load(from[q] + column(u));
+          } else {
+            v[q].ask(from[q], a.cols, c0, lane);
+          }
         }
 #pragma unroll
         for (int q = 0; q < kSlots; ++q) {
           if (!from[q]) break;
 #pragma unroll
           for (int u = 0; u < kU; ++u) {
-            if (!whole[u]) continue;
             float x[kN];
-            v[q][u].take(from[q] + c[u], x);
+            if constexpr (Wide) {
+              if (whole(u)) {
+                v[q][u].values(x);
+              } else {
+#pragma unroll
+                for (int e = 0; e < kN; ++e) x[e] = column(u) + e < a.cols ? to_f32(from[q][column(u) + e]) : 0.0f;
+              }
+            } else {
+              v[q].words(u, lane).values(x);
+            }
 #pragma unroll
             for (int e = 0; e < kN; ++e) sum[u][e] = fmaf(w[q], x[e], sum[u][e]);
-          }
-          if (edge) {
-#pragma unroll
-            for (int u = 0; u < kU; ++u) {
-              if (whole[u]) continue;
-#pragma unroll
-              for (int e = 0; e < kN; ++e)
-                if (c[u] + e >= 0 && c[u] + e < a.cols) sum[u][e] = fmaf(w[q], to_f32(from[q][c[u] + e]), sum[u][e]);
-            }
           }
         }
       }
@@ -254,12 +260,12 @@ __global__ void __launch_bounds__(kRowThreads, CombineShape<TY, TO, Wide>::kCtas
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      if (whole[u]) {
-        store_piece(to + c[u], sum[u]);
+      if (whole(u)) {
+        store_piece(to + column(u), sum[u]);
       } else {
 #pragma unroll
         for (int e = 0; e < kN; ++e)
-          if (c[u] + e >= 0 && c[u] + e < a.cols) to[c[u] + e] = from_f32<TO>(sum[u][e]);
+          if (column(u) + e >= 0 && column(u) + e < a.cols) to[column(u) + e] = from_f32<TO>(sum[u][e]);
       }
     }
   } while (Wide && (unit += step) < units);
@@ -483,7 +489,7 @@ int enqueue_combine(const Combine &a, cudaStream_t stream) {
     using TY = decltype(y);
     return by_type(a.out_dtype, [&](auto o) {
       using TO = decltype(o);
-      using Shape = CombineShape<TY, TO, true>;
+      using Shape = CombineShape<TY, TO>;
       const int spans = (int)ceil_div(piece_count(a.cols, Shape::kN, wide), 32 * Shape::kPieces);
       const int64_t warps = a.tokens * spans;
       const int block = warps <= 2048 ? kFewThreads : kRowThreads;

@@ -174,6 +174,53 @@ struct Piece {
   __device__ __forceinline__ void take(const T *p, float (&x)[N]) { words(p).values(x); }
 };
 
+// U pieces of N neighbours for each lane of a warp, which lie side by side in one row that starts anywhere: piece u of lane l
+// begins at p + (32 u + l) N. Every lane reads the word (of a piece's size) that its piece begins in, and has the rest from the lane
+// behind it; words without a value of the row are not read. Elements outside the row hold anything. All lanes call.
+template <typename T, int N, int U>
+struct Strip {
+  static constexpr int kCount = Words<T, N>::kCount;
+  static constexpr uint32_t kBytes = 4 * kCount;
+  Words<T, N> w[U], tail;
+  uint32_t skip;                     // bytes of the first piece's word before it; the same for all pieces
+  // row, cols: what may be read; first: lane 0's first piece
+  __device__ __forceinline__ void ask(const T *row, int64_t cols, int64_t first, int lane) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(row + first), lo = reinterpret_cast<uintptr_t>(row), hi = reinterpret_cast<uintptr_t>(row + cols);
+    skip = (uint32_t)(p & (kBytes - 1));
+    const uintptr_t base = p - skip;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uintptr_t at = base + (uintptr_t)(32 * u + lane) * kBytes;
+      if (at + kBytes > lo && at < hi) w[u].load(reinterpret_cast<const T *>(at));
+    }
+    const uintptr_t at = base + (uintptr_t)(32 * U) * kBytes;
+    if (lane == 0 && at + kBytes > lo && at < hi) tail.load(reinterpret_cast<const T *>(at));
+  }
+  __device__ __forceinline__ Words<T, N> words(int u, int lane) const {
+    uint32_t x[2 * kCount];
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) {
+      x[i] = w[u].v[i];
+      // lane 31's neighbour is lane 0 of the next piece
+      x[kCount + i] = __shfl_sync(kFull, lane == 0 ? (u + 1 < U ? w[u + 1 < U ? u + 1 : u].v[i] : tail.v[i]) : w[u].v[i], (lane + 1) & 31);
+    }
+    if constexpr (kCount == 4) {
+      if (skip & 8) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) x[i] = x[i + 2];
+      }
+    }
+    if (skip & 4) {
+#pragma unroll
+      for (int i = 0; i < kCount + 1; ++i) x[i] = x[i + 1];
+    }
+    Words<T, N> r;
+#pragma unroll
+    for (int i = 0; i < kCount; ++i) r.v[i] = sizeof(T) == 4 ? x[i] : __funnelshift_r(x[i], x[i + 1], 8 * (skip & 3));
+    return r;
+  }
+};
+
 // N values rounded to T and stored at a boundary of as many.
 template <typename T, int N>
 __device__ __forceinline__ void store_piece(T *p, const float (&x)[N]) {
