@@ -45,14 +45,16 @@ constexpr double kEps = 1e-6;
 
 // The tensors of a launch, as one of its arguments: those have 32,764 bytes. A tensor is its address and one word: the units of
 // the tensors before it (32 bits), the elements of its last unit (16), its type (2).
+// A list of a few tensors goes in an argument of its size: 28 KB of one cost the host some 3 us a launch.
+constexpr int kFewTensors = 96;
 template <int N>
 struct Places {
   uint64_t at[N];
 };
 struct InPlace {};
-template <bool Moved>                // with places of their own for the clipped values
+template <bool Moved, bool Few>      // Moved: with places of their own for the clipped values
 struct Batch {
-  static constexpr int kMost = Moved ? 1300 : 2000;
+  static constexpr int kMost = Few ? kFewTensors : Moved ? 1300 : 2000;
   uint64_t at[kMost];
   uint64_t word[kMost + 1];          // the last: all units
   std::conditional_t<Moved, Places<kMost>, InPlace> to;
@@ -67,7 +69,7 @@ struct Batch {
     else return at[t];
   }
 };
-static_assert(sizeof(Batch<true>) + 64 <= 32764 && sizeof(Batch<false>) + 64 <= 32764, "a kernel's arguments");
+static_assert(sizeof(Batch<true, false>) + 64 <= 32764 && sizeof(Batch<false, false>) + 64 <= 32764, "a kernel's arguments");
 
 int launched(cudaError_t e, const char *what) { return e == cudaSuccess ? RESHARD_OK : cuda_error(e, what); }
 
@@ -160,7 +162,8 @@ __device__ __forceinline__ void add_unit(const T *p, int64_t n, int64_t unit, in
 }
 
 // Each CTA's sum of squares over its units of the launch, every gridDim-th; later launches of a call add to it.
-__global__ void __launch_bounds__(kNormThreads, kSquaresCtas) reshard_squares_kernel(const __grid_constant__ Batch<false> b, double *part, bool fresh) {
+template <bool Few>
+__global__ void __launch_bounds__(kNormThreads, kSquaresCtas) reshard_squares_kernel(const __grid_constant__ Batch<false, Few> b, double *part, bool fresh) {
   grid_enter();
   __shared__ double warps[kNormThreads / 32];
   const uint32_t units = b.units();
@@ -229,9 +232,9 @@ __device__ __forceinline__ void clip_unit(const T *p, TO *to, int64_t n, int64_t
 // Every value times the factor. Under the limit in place there is nothing to do. norm: given, or NULL and found from the
 // CTAs' sums, by each CTA for itself; `out` gets it. The units are taken from the last to the first, since what the sums
 // read last is still in L2: a batch has its tensors from the last to the first. A launch has tensors of one pair of types: all nine pairs in one kernel spilled its registers.
-template <typename T, typename TO, bool Moved>
+template <typename T, typename TO, bool Moved, bool Few>
 __global__ void __launch_bounds__(kNormThreads, (sizeof(TO) > sizeof(T) ? 6 : kClipCtas))
-    reshard_clip_kernel(const __grid_constant__ Batch<Moved> b, const float *given, const double *part, int ctas, double limit, float *out) {
+    reshard_clip_kernel(const __grid_constant__ Batch<Moved, Few> b, const float *given, const double *part, int ctas, double limit, float *out) {
   grid_enter();
   __shared__ double warps[kNormThreads / 32];
   const float norm = given ? *given : norm_of(part, ctas, warps);
@@ -249,10 +252,10 @@ __global__ void __launch_bounds__(kNormThreads, (sizeof(TO) > sizeof(T) ? 6 : kC
 
 // Calls f with each batch of the list that has something to do, from the last to the first where `back`: of all its tensors,
 // or of those of one type whose targets in `into` have one type.
-template <bool Moved, typename F>
+template <bool Moved, bool Few, typename F>
 int batches(const reshard_tensors &list, const reshard_tensors *into, int dtype, int to, bool back, F &&f) {
   const int64_t count = (int64_t)list.tensors.size();
-  Batch<Moved> b;
+  Batch<Moved, Few> b;
   b.unit = (int)list.unit, b.count = 0, b.word[0] = 0;
   for (int64_t i = 0; i < count; ++i) {
     const size_t j = (size_t)(back ? count - 1 - i : i);
@@ -265,7 +268,7 @@ int batches(const reshard_tensors &list, const reshard_tensors *into, int dtype,
       b.word[k] |= (uint64_t)(t.n - (int64_t)(units - 1) * list.unit) << 32 | (uint64_t)t.dtype << 48;
       b.word[k + 1] = (uint32_t)b.word[k] + units;
     }
-    if (b.count == Batch<Moved>::kMost || (i == count - 1 && b.count > 0)) {
+    if (b.count == Batch<Moved, Few>::kMost || (i == count - 1 && b.count > 0)) {
       const int rc = f(b);
       if (rc) return rc;
       b.count = 0, b.word[0] = 0;
@@ -316,12 +319,20 @@ bool entangled(const reshard_tensors &a, const reshard_tensors &b) {
   return false;
 }
 
+template <typename F>
+int by_count(const reshard_tensors &list, F &&f) {
+  return list.tensors.size() <= kFewTensors ? f(std::true_type()) : f(std::false_type());
+}
+
 int enqueue_squares(const reshard_tensors &list, double *part, int ctas, cudaStream_t stream) {
   bool fresh = true;
-  return batches<false>(list, nullptr, 0, 0, false, [&](const Batch<false> &b) {
-    const int rc = launched(launch(reshard_squares_kernel, dim3((unsigned)ctas), kNormThreads, 0, 1, stream, b, part, fresh), "launching reshard_squares_kernel");
-    fresh = false;
-    return rc;
+  return by_count(list, [&](auto few) {
+    constexpr bool kFew = decltype(few)::value;
+    return batches<false, kFew>(list, nullptr, 0, 0, false, [&](const Batch<false, kFew> &b) {
+      const int rc = launched(launch(reshard_squares_kernel<kFew>, dim3((unsigned)ctas), kNormThreads, 0, 1, stream, b, part, fresh), "launching reshard_squares_kernel");
+      fresh = false;
+      return rc;
+    });
   });
 }
 
@@ -440,9 +451,9 @@ extern "C" int reshard_clip_grads(const reshard_tensors_t *list, const reshard_t
   const reshard_tensors &to = into ? *into : *list;
   for (size_t i = 0; i < to.tensors.size(); ++i)
     if (to.tensors[i].n) present[list->tensors[i].dtype][to.tensors[i].dtype] = true;
-  auto clip = [&](auto moved, int x, int y) {
-    constexpr bool kMoved = decltype(moved)::value;
-    return batches<kMoved>(*list, &to, x, y, true, [&](const Batch<kMoved> &b) {
+  auto clip = [&](auto moved, auto few, int x, int y) {
+    constexpr bool kMoved = decltype(moved)::value, kFew = decltype(few)::value;
+    return batches<kMoved, kFew>(*list, &to, x, y, true, [&](const Batch<kMoved, kFew> &b) {
       // One CTA a unit, which writes faster than CTAs that stay; in place those, since most often they have nothing to do.
       const unsigned grid = kMoved ? b.units() : std::min((unsigned)ctas, b.units());
       const int rc = launched(by_type(x, [&](auto from_type) {
@@ -450,7 +461,7 @@ extern "C" int reshard_clip_grads(const reshard_tensors_t *list, const reshard_t
           using T = decltype(from_type);
           using TO = decltype(to_type);
           if constexpr (kMoved || std::is_same_v<T, TO>)
-            return launch(reshard_clip_kernel<T, TO, kMoved>, dim3(grid), kNormThreads, 0, 1, stream, b, norm_in, static_cast<const double *>(part), ctas, limit, norm_out);
+            return launch(reshard_clip_kernel<T, TO, kMoved, kFew>, dim3(grid), kNormThreads, 0, 1, stream, b, norm_in, static_cast<const double *>(part), ctas, limit, norm_out);
           else
             return cudaErrorInvalidValue;        // in place the types are the same
         });
@@ -461,6 +472,6 @@ extern "C" int reshard_clip_grads(const reshard_tensors_t *list, const reshard_t
   };
   for (int x = 3; x > 0; --x)
     for (int y = 3; y > 0; --y)
-      if (present[x][y] && (rc = here ? clip(std::false_type(), x, y) : clip(std::true_type(), x, y))) return rc;
+      if (present[x][y] && (rc = by_count(*list, [&](auto few) { return here ? clip(std::false_type(), few, x, y) : clip(std::true_type(), few, x, y); }))) return rc;
   return RESHARD_OK;
 } OPS_CATCH

@@ -615,8 +615,8 @@ def reshard_embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 
     ids = ids.contiguous()
     T, shape = ids.numel(), ids.shape
     if out is None:
-        out = torch.empty((*shape, H), dtype=table.dtype, device=table.device)
-        to, to_step = out, H
+        out = to = torch.empty((*shape, H), dtype=table.dtype, device=table.device)
+        to_step = H
     else:
         if out.shape != (*shape, H):
             _bad(f"out must be of shape {(*shape, H)}, not {tuple(out.shape)}")
@@ -640,8 +640,8 @@ def reshard_embedding_backward(grad: torch.Tensor, ids: torch.Tensor, rows: int,
             return reshard_embedding_backward(grad, ids, rows, scale=scale, first_row=first_row, dtype=dtype, out=out, accumulate=accumulate)
     if grad.shape[:-1] != ids.shape:
         _bad(f"grad {tuple(grad.shape)} does not fit ids {tuple(ids.shape)}")
-    bits = _id_bits(ids, grad)
-    grad, ids = _rows(grad if grad.dim() == 2 else grad.reshape(ids.numel(), grad.shape[-1])), ids.contiguous()
+    bits, ids = _id_bits(ids, grad), ids.contiguous()
+    grad = _rows(grad if grad.dim() == 2 else grad.reshape(ids.numel(), grad.shape[-1]))
     T, H, step = _matrix(grad, "grad")
     if accumulate and out is None:
         _bad("accumulate needs out")
