@@ -4,7 +4,7 @@ The training side holds a mixture-of-experts layer's gate, up and down projectio
 quantized in blocks of 128 x 128 and moved to generation ranks that split the experts among fewer ranks and keep gate
 and up fused ([gate; up] rows of one buffer), values and scales in one reshard. Each generation rank then routes the same
 tokens and runs its own experts; the ranks' outputs sum to the whole layer's, which is checked against the layer run in
-one piece. All ranks are buffers on one GPU:
+one piece. A step of the router's training then goes through the layer's stages, with gradients. All ranks are buffers on one GPU:
 
   python examples/refit_experts.py [--tokens 256] [--experts 32] [--hidden 1024] [--ffn 512] [--train 8] [--gen 2]
 """
@@ -45,6 +45,16 @@ def refit(train, experts, hidden, ffn, n_train, n_gen):
     return [(r["w13"], r["s13"], r["w2"], r["s2"]) for r in ranks]
 
 
+@torch.no_grad()
+def experts(rows, offsets, weights):
+    """The experts' outputs, in 32 bits, for rows in the order of their experts."""
+    w13, s13, w2, s2 = weights
+    ffn = w13.shape[1] // 2
+    gu = R.reshard_matmul_fp8(*R.reshard_quantize_rows(rows), w13, s13, offsets=offsets, out_dtype=torch.float32)
+    h = torch.nn.functional.silu(gu[:, :ffn]) * gu[:, ffn:]
+    return R.reshard_matmul_fp8(*R.reshard_quantize_rows(h), w2, s2, offsets=offsets, out_dtype=torch.float32)
+
+
 def main(argv=None) -> float:
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     for name, value in (("tokens", 256), ("experts", 32), ("hidden", 1024), ("ffn", 512), ("train", 8), ("gen", 2), ("k", 4)):
@@ -80,9 +90,15 @@ def main(argv=None) -> float:
                                   *cat["down"])
     off = float((total - whole.float()).norm() / whole.float().norm())
 
-    # what a training step of the router needs of it: the gradient to its logits
-    grad = R.reshard_route_backward(torch.randn(a.tokens, a.k, generator=g, device="cuda"), x @ router, ids)
-    assert grad.shape == (a.tokens, a.experts) and R.reshard_ops_status() == 0
+    # a training step of the router through the same layer, its stages one by one: tokens to their experts' places, the experts
+    # in FP8, back with the weights. The gradient reaches the weights, the logits and the router; it is clipped before the update.
+    router = router.float().requires_grad_()
+    weights, ids = R.reshard_route(x.float() @ router, a.k)
+    sort = R.reshard_dispatch(ids, a.experts)
+    y = experts(R.reshard_permute(x, sort), sort[0], [torch.cat([r[i] for r in ranks]) for i in range(4)])
+    (R.reshard_combine(y, sort, weights, out_dtype=torch.bfloat16).float() - whole.float().roll(1, 0)).square().sum().backward()
+    norm = R.reshard_clip_grads([router.grad], 1.0)
+    assert float(norm) > 0 and abs(float(R.reshard_grad_norm([router.grad])) - min(1.0, float(norm))) < 1e-3 and R.reshard_ops_status() == 0
     print(f"{a.experts} experts from {a.train} training to {a.gen} generation ranks, {a.tokens} tokens: the ranks' sum is {off:.2e} from the whole layer")
     return off
 

@@ -91,6 +91,34 @@ def test_norm_and_clip(sizes, kinds, skip):
     assert all(torch.equal(a, b) for a, b in zip(ts, want))
 
 
+@pytest.mark.parametrize("count", [95, 96, 97, 1299, 1300, 1301, 1999, 2000, 2001, 4100])
+def test_lists_of_as_many_tensors_as_a_launch_takes(count):
+    kinds = ["bf16", "f32"] if count == 4100 else ["bf16"]
+    ts = tensors(count, [3, 17, 0, 40] * (count // 4) + [9] * (count % 4), kinds)
+    assert len(ts) == count
+    n = check_norm(ts)
+    out = [torch.zeros(t.shape, device="cuda") for t in ts]
+    R.reshard_clip_grads(ts, 0.5 * float(n), out=out)
+    check_clipped(out, ts, 0.5 * float(n), n)
+    keep = [t.clone() for t in ts]
+    R.reshard_clip_grads(ts, 0.5 * float(n))
+    check_clipped(ts, keep, 0.5 * float(n), n)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_units_of_every_size(kind):
+    """Totals for which a unit has 2,048, 4,096, 8,192 and 16,384 elements, tensors that end at its borders and beside them."""
+    for unit, total in ((2048, 300000), (4096, 1500000), (8192, 3000000), (16384, 6000000)):
+        ts = tensors(unit, [unit, unit - 1, unit + 1, 2 * unit + 7, 8, total], [kind], skip=1)
+        n = check_norm(ts)
+        out = [torch.zeros(t.shape, device="cuda") for t in ts]
+        R.reshard_clip_grads(ts, 0.1, out=out)
+        check_clipped(out, ts, 0.1, n)
+        keep = [t.clone() for t in ts]
+        R.reshard_clip_grads(ts, 0.1)
+        check_clipped(ts, keep, 0.1, n)
+
+
 def test_lists_made_once():
     ts = tensors(1, [300, 5000, 70000], ["bf16", "f32"])
     out = [torch.empty(t.shape, device="cuda") for t in ts]

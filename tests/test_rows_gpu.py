@@ -525,3 +525,91 @@ def test_refusals_name_what_is_wrong():
     host = torch.zeros(4, 16)
     rc = R.binding.LIB.reshard_permute(host.data_ptr(), 3, 4, 16, 16, order.data_ptr(), position.data_ptr(), 2, y.data_ptr(), 8, 16, None)
     assert rc == R.RESHARD_ERR_INVALID_ARG and "pageable" in R.reshard_last_error()
+
+
+# ------------------------------------------------------------------------- many rows: warps that stay, runs, several slices
+
+@pytest.mark.parametrize("T,k,E,H", [(6000, 3, 16, 72), (700, 2, 8, 8200), (5000, 40, 48, 24), (9000, 2, 8, 1000)])
+@pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "bf16"), ("f32", "f32")])
+@pytest.mark.parametrize("share", [False, True])
+def test_combine_of_many_tokens(T, k, E, H, types, share):
+    """More spans than the GPU holds warps: each warp takes several."""
+    g = gen(T + H)
+    ids = torch.rand(T, E, generator=g, device="cuda").argsort(1)[:, :k].int().contiguous()
+    sort = R.reshard_dispatch(ids, E // 4 if share else E, E // 4 if share else 0)
+    position = sort[2]
+    y, w = randn(g, T * k, H).to(DT[types[0]]), torch.rand(T, k, generator=g, device="cuda")
+    out = R.reshard_combine(y, sort, w, out_dtype=DT[types[1]])
+    close(out, X.combine(y, position, w, k), k * U * X.combine(y, position, w, k, True))
+    grad = randn(g, T, H).to(DT[types[1]])
+    dy, dw = R.reshard_combine_backward(grad, y, sort, w)
+    wy, ww = X.combine_backward(grad, y, position, w, k)
+    close(dy, wy, U * wy.abs())
+    close(dw, ww, (H / 32 + 32) * U * X.combine_backward(grad, y, position, w, k, True)[1])
+    x = randn(g, T, H).to(DT[types[0]])
+    to = torch.zeros_like(y)
+    assert torch.equal(R.reshard_permute(x, sort, out=to), X.permute(x, position, torch.zeros_like(y)))
+
+
+@pytest.mark.parametrize("T,V,H", [(9000, 40, 4100), (20000, 3, 1032), (5000, 6000, 4096), (16385, 100, 8), (16384, 100, 9)])
+@pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "f32")])
+def test_embedding_backward_of_many_columns_and_runs(T, V, H, types):
+    g = gen(T + H)
+    ids = (torch.rand(T, generator=g, device="cuda") ** 3 * V).long().clamp_max(V - 1)
+    check_embedding_backward(randn(g, T, H).to(DT[types[0]]), ids, V - V // 3, V // 3, dtype=DT[types[1]])
+
+
+def test_two_calls_at_once():
+    """Calls on two streams, workspaces of their own, give what they give alone."""
+    g = gen(31)
+    ids = [torch.randint(0, 300, (20000,), generator=g, device="cuda") for _ in range(2)]
+    grads = [randn(g, 20000, 256) for _ in range(2)]
+    want = [R.reshard_embedding_backward(a, i, 300) for a, i in zip(grads, ids)]
+    norms = [R.reshard_grad_norm([a]) for a in grads]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(5):
+        for s in range(2):
+            got[s].append((R.reshard_embedding_backward(grads[s], ids[s], 300, stream=streams[s]), R.reshard_grad_norm([grads[s]], stream=streams[s])))
+    torch.cuda.synchronize()
+    for s in range(2):
+        assert all(torch.equal(a, want[s]) and torch.equal(n, norms[s]) for a, n in got[s])
+
+
+def test_a_captured_training_step():
+    """Forward and backward by autograd, captured once and replayed with other inputs; the eager step's graph is gone by then."""
+    T, E, k, H, V = 64, 8, 2, 64, 50
+    g = gen(41)
+    tokens = torch.randint(0, V, (T,), generator=g, device="cuda")
+    table, router, experts = (randn(g, *s).requires_grad_() for s in ((V, H), (H, E), (E, H)))
+
+    def step():
+        x = R.reshard_embedding(tokens, table)
+        w, ids = R.reshard_route(x @ router, k)
+        sort = R.reshard_dispatch(ids, E)
+        scale = experts[torch.searchsorted(sort[0][1:].contiguous(), torch.arange(T * k, device="cuda", dtype=torch.int32), right=True)]
+        out = R.reshard_combine(R.reshard_permute(x, sort) * scale, sort, w)
+        grads = torch.autograd.grad(out.square().sum(), [table, router, experts])
+        R.reshard_clip_grads(list(grads), 1.0)
+        return grads
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        captured = step()
+    for i in range(3):
+        with torch.no_grad():
+            tokens.copy_(torch.randint(0, V, (T,), generator=g, device="cuda"))
+            table.mul_(0.9)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(captured, step()):
+            # torch's own indexing gradient adds in any order
+            assert float((a - b).abs().max()) <= 1e-5 * float(b.abs().max())
