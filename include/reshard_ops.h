@@ -172,7 +172,7 @@ int reshard_embedding(const void *ids, int id_bits, int64_t tokens, const void *
  * reshard_embedding_backward -- the gradient to the table: grad_table[r] = scale * (sum of grad[t] over the tokens with
  * ids[t] = first_row + r), fp32 sums rounded once to table_dtype. Written whole, 0 for rows without a token; or, with
  * accumulate, added to the rows that have one, the others not touched.
- * workspace: reshard_embedding_backward_workspace(tokens, cols) bytes, 256-byte aligned.
+ * workspace: reshard_embedding_backward_workspace(tokens, cols) bytes, 256-byte aligned; 0 bytes (NULL will do) for a few tokens.
  */
 int64_t reshard_embedding_backward_workspace(int64_t tokens, int64_t cols);
 int reshard_embedding_backward(const void *grad, int grad_dtype, int64_t tokens, int64_t cols, int64_t grad_stride, const void *ids,

@@ -52,8 +52,10 @@ def test_every_violation_is_listed():
     refused(L.reshard_embedding(4, 64, 2, 1, 1, 0, 9, 8, 8, 1.0, 1, 8, None), BAD, "ids is not aligned to 8", "table is not aligned", "out is not aligned")
     refused(L.reshard_embedding(None, 64, 1 << 31, None, 1, 0, 9, 8, 8, 1.0, None, 8, None), UNSUP, "2^30")
     refused(L.reshard_embedding_backward(None, 0, 2, 8, 4, None, 8, -1, 9, 1.0, None, 0, 4, 0, None, 0, None), BAD, "first_row", "id_bits", "grad_dtype", "row stride")
-    refused(L.reshard_embedding_backward(None, 1, 2, 8, 8, None, 64, 0, 9, 1.0, None, 1, 8, 0, None, 0, None), BAD, "grad_table is NULL", "grad is NULL",
+    refused(L.reshard_embedding_backward(None, 1, 300, 8, 8, None, 64, 0, 9, 1.0, None, 1, 8, 0, None, 0, None), BAD, "grad_table is NULL", "grad is NULL",
             "ids is NULL", "workspace is NULL", "workspace is smaller")
+    refused(L.reshard_embedding_backward(None, 1, 2, 8, 8, None, 64, 0, 9, 1.0, None, 1, 8, 0, None, 0, None), BAD, "grad is NULL", "ids is NULL")
+    assert "workspace" not in R.reshard_last_error()
     refused(L.reshard_grad_norm(None, None, None, 0, None), BAD, "list is NULL")
     refused(L.reshard_clip_grads(None, None, -1.0, 4, 4, None, 0, None), BAD, "list is NULL", "limit", "give one")
     refused(L.reshard_clip_grads(None, None, float("nan"), None, None, None, 0, None), BAD, "limit")
@@ -83,8 +85,9 @@ def test_workspace_sizes():
     assert L.reshard_embedding_backward_workspace(0, 8) == 0 and L.reshard_embedding_backward_workspace(-1, 8) == 0
     assert L.reshard_embedding_backward_workspace(1 << 31, 8) == 0 and L.reshard_embedding_backward_workspace(8, 1 << 31) == 0
     # pairs twice, their number, and two fp32 rows a run: everything that the tokens alone decide
-    small = L.reshard_embedding_backward_workspace(1, 1)
-    assert 0 < small <= 4096
+    assert L.reshard_embedding_backward_workspace(256, 64) == 0                # a few tokens need none
+    small = L.reshard_embedding_backward_workspace(257, 1)
+    assert 2 * 8 * 257 < small <= 16384
     assert L.reshard_embedding_backward_workspace(1 << 30, 1 << 30) > 1 << 34 and L.reshard_grad_norm_workspace() > 0
 
 

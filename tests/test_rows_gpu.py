@@ -230,7 +230,7 @@ def check_embedding_backward(grad, ids, rows, first=0, scale=1.0, **kw):
     return got
 
 
-@pytest.mark.parametrize("T,V,rows,H", [(0, 4, 4, 8), (1, 4, 4, 8), (1, 1, 1, 1), (15, 3, 3, 40), (16, 16, 16, 1024), (17, 30, 11, 33), (200, 7, 7, 2867), (1000, 5000, 1250, 64),
+@pytest.mark.parametrize("T,V,rows,H", [(0, 4, 4, 8), (1, 4, 4, 8), (1, 1, 1, 1), (15, 3, 3, 40), (16, 16, 16, 1024), (17, 30, 11, 33), (200, 7, 7, 2867), (255, 40, 30, 520), (256, 3, 3, 64), (257, 3, 3, 64), (1000, 5000, 1250, 64),
                                         (5000, 300, 300, 130), (40000, 70000, 70000, 24), (33000, 2000, 500, 256), (70000, 9, 9, 16)])
 @pytest.mark.parametrize("types", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("f16", "f16")])
 @pytest.mark.parametrize("skew", [False, True])
@@ -245,7 +245,7 @@ def test_embedding_backward(T, V, rows, H, types, skew):
     assert torch.equal(got, R.reshard_embedding_backward(grad, ids.int(), rows, first_row=first, scale=1.0 if skew else 0.3, dtype=DT[types[1]]))
 
 
-@pytest.mark.parametrize("T", [1, 31, 32, 33, 3000, 50000])
+@pytest.mark.parametrize("T", [1, 31, 32, 33, 255, 256, 257, 3000, 50000])
 @pytest.mark.parametrize("how", ["dense", "pitch", "odd"])
 def test_embedding_backward_one_row_takes_all(T, how):
     """All tokens of one id: the row's sum passes through every run and is joined from their pieces."""
