@@ -37,7 +37,7 @@ namespace ops {
 namespace {
 
 constexpr int kNormThreads = 256;
-constexpr int kMaxCtas = 1024;                    // whose sums the workspace holds
+constexpr int kMaxCtas = 1024;                    // whose sums the workspace holds, and the factor behind them
 constexpr int kUnitStep = kNormThreads * 8;       // a unit is a multiple of it
 constexpr int kSquaresCtas = 6, kClipCtas = 4;   // of an SM
 constexpr int kFillCtas = 304;                    // two of each of 152 SMs
@@ -104,14 +104,17 @@ struct Squares {
   __device__ __forceinline__ double total() const { return (double)s + (double)r + d; }
 };
 
-// The sum over the CTA's threads, in thread 0 (all threads call).
+// The sum over the CTA's threads, in its first warp (all threads call). 64-bit additions are slow here: few lanes make them.
 __device__ __forceinline__ double cta_sum(double v, double *part) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = 0.0;
-  for (int w = 0; w < kNormThreads / 32; ++w) v += part[w];
+  if (threadIdx.x < 32) {
+    v = threadIdx.x < kNormThreads / 32 ? part[threadIdx.x] : 0.0;
+#pragma unroll
+    for (int o = kNormThreads / 64; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  }
   return v;
 }
 
@@ -179,18 +182,29 @@ __global__ void __launch_bounds__(kNormThreads, kSquaresCtas) reshard_squares_ke
   if (threadIdx.x == 0) part[blockIdx.x] = fresh ? v : part[blockIdx.x] + v;
 }
 
-// The norm from the CTAs' sums (all threads call and have it).
+// The norm from the CTAs' sums, in thread 0 (all threads call).
 __device__ __forceinline__ float norm_of(const double *part, int ctas, double *warps) {
   double v = 0.0;
   for (int i = threadIdx.x; i < ctas; i += kNormThreads) v += part[i];
-  return (float)sqrt(cta_sum(v, warps));
+  v = cta_sum(v, warps);
+  return threadIdx.x == 0 ? (float)sqrt(v) : 0.0f;
 }
 
-__global__ void __launch_bounds__(kNormThreads) reshard_norm_kernel(const double *part, int ctas, float *norm) {
+// What values are multiplied by. One thread computes it: a 64-bit division in each of a launch's threads, nine million for 600M
+// values, took as long as the values.
+__device__ __forceinline__ float factor_of(float norm, double limit) {
+  const double f = limit / ((double)norm + kEps);
+  return f >= 1.0 || isinf(limit) ? 1.0f : (float)f;      // NaN stays
+}
+
+__global__ void __launch_bounds__(kNormThreads) reshard_norm_kernel(const double *part, int ctas, float *norm, double limit, float *factor) {
   grid_enter();
   __shared__ double warps[kNormThreads / 32];
   const float v = norm_of(part, ctas, warps);
-  if (threadIdx.x == 0) *norm = v;
+  if (threadIdx.x == 0) {
+    *norm = v;
+    if (factor) *factor = factor_of(v, limit);
+  }
 }
 
 template <typename T, typename TO>
@@ -229,18 +243,28 @@ __device__ __forceinline__ void clip_unit(const T *p, TO *to, int64_t n, int64_t
   if (tid < m - rest) into[rest + tid] = from_f32<TO>(to_f32(from[rest + tid]) * factor);
 }
 
-// Every value times the factor. Under the limit in place there is nothing to do. norm: given, or NULL and found from the
-// CTAs' sums, by each CTA for itself; `out` gets it. The units are taken from the last to the first, since what the sums
-// read last is still in L2: a batch has its tensors from the last to the first. A launch has tensors of one pair of types: all nine pairs in one kernel spilled its registers.
+// Every value times the factor: found already, or from a norm that was given, or from the CTAs' sums, by each CTA for itself (the
+// first writes the norm to `out`). Under the limit in place there is nothing to do. The units are taken from the last to the first, since
+// what the sums read last is still in L2: a batch has its tensors from the last to the first. A launch has tensors of one pair of
+// types: all nine pairs in one kernel spilled its registers.
 template <typename T, typename TO, bool Moved, bool Few>
 __global__ void __launch_bounds__(kNormThreads, (sizeof(TO) > sizeof(T) ? 6 : kClipCtas))
-    reshard_clip_kernel(const __grid_constant__ Batch<Moved, Few> b, const float *given, const double *part, int ctas, double limit, float *out) {
+    reshard_clip_kernel(const __grid_constant__ Batch<Moved, Few> b, const float *found, const float *given, const double *part, int ctas, double limit, float *out) {
   grid_enter();
   __shared__ double warps[kNormThreads / 32];
-  const float norm = given ? *given : norm_of(part, ctas, warps);
-  if (out && blockIdx.x == 0 && threadIdx.x == 0) *out = norm;
-  const double f = limit / ((double)norm + kEps);
-  const float factor = f >= 1.0 || isinf(limit) ? 1.0f : (float)f;      // NaN stays
+  __shared__ float shared;
+  float factor;
+  if (found) {
+    factor = *found;
+  } else {
+    const float norm = given ? *given : norm_of(part, ctas, warps);
+    if (threadIdx.x == 0) {
+      shared = factor_of(norm, limit);
+      if (out && blockIdx.x == 0) *out = norm;
+    }
+    __syncthreads();
+    factor = shared;
+  }
   if (!Moved && factor == 1.0f) return;
   const uint32_t units = b.units();
   for (uint32_t u = blockIdx.x; u < units; u += gridDim.x) {
@@ -336,8 +360,8 @@ int enqueue_squares(const reshard_tensors &list, double *part, int ctas, cudaStr
   });
 }
 
-int enqueue_norm(const double *part, int ctas, float *norm, cudaStream_t stream) {
-  return launched(launch(reshard_norm_kernel, dim3(1), kNormThreads, 0, 1, stream, part, ctas, norm), "launching reshard_norm_kernel");
+int enqueue_norm(const double *part, int ctas, float *norm, double limit, float *factor, cudaStream_t stream) {
+  return launched(launch(reshard_norm_kernel, dim3(1), kNormThreads, 0, 1, stream, part, ctas, norm, limit, factor), "launching reshard_norm_kernel");
 }
 
 }  // namespace
@@ -391,7 +415,7 @@ extern "C" int reshard_tensors_destroy(reshard_tensors_t *list) {
   return RESHARD_OK;
 }
 
-extern "C" int64_t reshard_grad_norm_workspace(void) { return kMaxCtas * (int64_t)sizeof(double); }
+extern "C" int64_t reshard_grad_norm_workspace(void) { return (kMaxCtas + 1) * (int64_t)sizeof(double); }
 
 extern "C" int reshard_grad_norm(const reshard_tensors_t *list, float *norm, void *workspace, int64_t workspace_bytes, reshard_stream_t stream_) try {
   Checks c("reshard_grad_norm");
@@ -406,7 +430,7 @@ extern "C" int reshard_grad_norm(const reshard_tensors_t *list, float *norm, voi
   double *const part = static_cast<double *>(workspace);
   int ctas = 0, rc = list->units ? ctas_of(*list, &ctas) : RESHARD_OK;
   if (rc || (rc = enqueue_squares(*list, part, ctas, stream))) return rc;
-  return enqueue_norm(part, ctas, norm, stream);
+  return enqueue_norm(part, ctas, norm, 0.0, nullptr, stream);
 } OPS_CATCH
 
 extern "C" int reshard_clip_grads(const reshard_tensors_t *list, const reshard_tensors_t *into, double limit, const float *norm_in, float *norm_out,
@@ -433,7 +457,7 @@ extern "C" int reshard_clip_grads(const reshard_tensors_t *list, const reshard_t
   if (!c.ok()) return c.report();
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   double *const part = static_cast<double *>(workspace);
-  if (list->units == 0) return norm_in ? RESHARD_OK : enqueue_norm(part, 0, norm_out, stream);
+  if (list->units == 0) return norm_in ? RESHARD_OK : enqueue_norm(part, 0, norm_out, limit, nullptr, stream);
   int ctas = 0, rc = ctas_of(*list, &ctas);
   if (rc || (!norm_in && (rc = enqueue_squares(*list, part, ctas, stream)))) return rc;
   // in place only if every tensor is its own target
@@ -442,10 +466,12 @@ extern "C" int reshard_clip_grads(const reshard_tensors_t *list, const reshard_t
     const auto &x = list->tensors[i], &y = into->tensors[i];
     here = x.n == 0 || (x.at == y.at && x.dtype == y.dtype);
   }
-  // Where every unit has a CTA on the GPU at once, each of them adds up the norm for itself; more CTAs find it added up.
+  // Where every unit has a CTA on the GPU at once, each of them adds up the norm for itself; more CTAs find the factor ready.
+  float *const factor = reinterpret_cast<float *>(part + kMaxCtas);
+  const float *found = nullptr;
   if (!norm_in && list->units > ctas) {
-    if ((rc = enqueue_norm(part, ctas, norm_out, stream))) return rc;
-    norm_in = norm_out, norm_out = nullptr;
+    if ((rc = enqueue_norm(part, ctas, norm_out, limit, factor, stream))) return rc;
+    found = factor;
   }
   bool present[4][4] = {};
   const reshard_tensors &to = into ? *into : *list;
@@ -461,7 +487,7 @@ extern "C" int reshard_clip_grads(const reshard_tensors_t *list, const reshard_t
           using T = decltype(from_type);
           using TO = decltype(to_type);
           if constexpr (kMoved || std::is_same_v<T, TO>)
-            return launch(reshard_clip_kernel<T, TO, kMoved, kFew>, dim3(grid), kNormThreads, 0, 1, stream, b, norm_in, static_cast<const double *>(part), ctas, limit, norm_out);
+            return launch(reshard_clip_kernel<T, TO, kMoved, kFew>, dim3(grid), kNormThreads, 0, 1, stream, b, found, norm_in, static_cast<const double *>(part), ctas, limit, norm_out);
           else
             return cudaErrorInvalidValue;        // in place the types are the same
         });
