@@ -3,11 +3,14 @@
 // A list (reshard_tensors_create) keeps the tensors' places on the host. A launch takes some of them as its argument,
 // so that a call copies nothing to the device and allocates nothing there, and a captured one holds its list. A tensor is
 // cut into units of one size (its head before the first 16-byte boundary belongs to the first); the CTAs of a launch share
-// the units of all its tensors evenly, whatever the tensors' sizes, and look their first one up by bisection.
+// the units of all its tensors evenly, whatever the tensors' sizes, and look each up by bisection.
 //
 // Squares are summed over 64 bytes a thread at most in fp32, those sums in fp32 with their roundings carried along
 // (two-sum), threads and CTAs in 64 bits in a fixed order: the norm is the correctly rounded one but for some 2^-24. Values
 // whose squares leave fp32's range (beyond 2^50, or all of them below 2^-40) are summed in 64 bits instead.
+//
+// Bound by HBM: 10,000 tensors of 150,000 bf16 values, norm only, 472 us, 6.4 TB/s; 384 of 1.57M clipped into fp32 720 us, of which the
+// second read is what a factor of all values costs.
 #include <algorithm>
 #include <cmath>
 #include <new>
@@ -43,15 +46,16 @@ constexpr int kSquaresCtas = 6, kClipCtas = 4;   // of an SM
 constexpr int kFillCtas = 304;                    // two of each of 152 SMs
 constexpr double kEps = 1e-6;
 
-// The tensors of a launch, as one of its arguments: those have 32,764 bytes. A tensor is its address and one word: the units of
-// the tensors before it (32 bits), the elements of its last unit (16), its type (2).
-// A list of a few tensors goes in an argument of its size: 28 KB of one cost the host some 3 us a launch.
+// A list of a few tensors goes in an argument of its size: 32 KB of one cost the host some 2 us a launch.
 constexpr int kFewTensors = 96;
 template <int N>
 struct Places {
   uint64_t at[N];
 };
 struct InPlace {};
+
+// The tensors of a launch, as one of its arguments: those have 32,764 bytes. A tensor is its address and one word: the units of
+// the tensors before it (32 bits), the elements of its last unit (16), its type (2).
 template <bool Moved, bool Few>      // Moved: with places of their own for the clipped values
 struct Batch {
   static constexpr int kMost = Few ? kFewTensors : Moved ? 1300 : 2000;

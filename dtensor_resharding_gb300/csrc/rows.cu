@@ -154,7 +154,7 @@ struct Lookup {
 };
 
 // A warp 2 KB of a token's row. Bound by the writes, and the reads of the rows that are not in L2: 32,768 tokens on a quarter of a
-// vocabulary of 128,000 x 4096 bf16, 48 us, 6.1 TB/s.
+// vocabulary of 128,000 x 4096 bf16, 46 us, 6.3 TB/s.
 template <typename T, bool Wide, bool Scaled>
 __global__ void __launch_bounds__(kRowThreads) reshard_embedding_kernel(Lookup a) {
   grid_enter();
@@ -172,9 +172,9 @@ __global__ void __launch_bounds__(kRowThreads) reshard_embedding_kernel(Lookup a
 // A warp a span of a token's columns. Lanes look up the places of up to 32 slots at once; those that have one are taken in
 // order, kSlots rows in flight together. Bound by the read of y: 8 places a token, 8,192 x 2048 fp32, 84 us, 6.8 TB/s; where few
 // slots have a place by the chain places, rows, output of each span, so that warps stay and look up the next span's places
-// before this one's rows (16,383 tokens with one place of eight on average, 4096 fp32: 71 us; a warp a span: 78). Rows that start
-// anywhere are bound by instructions (8,191 x 2867 fp16, four places each: 48 us, where aligned ones would take 37; a word
-// before and one behind for each lane, without its neighbour's: 59).
+// before this one's rows (16,383 tokens with one place of eight on average, 4096 fp32: 70 us; a warp a span: 78). Rows that start
+// anywhere are bound by instructions (8,191 x 2867 fp16, four places each: 48 us, of 2872 columns 43; with two words read by
+// each lane, without its neighbour's: 59).
 template <typename TY, typename TO>
 struct CombineShape {
   static constexpr int kN = kPieceOf<TY, TO>;
@@ -305,7 +305,8 @@ __device__ __forceinline__ void zero_unowned(const CombineBackward &a, int64_t f
 }
 
 // Whole pieces: `lanes` threads a token (a warp to a CTA, as many as have columns), which read its gradient once and keep the
-// rows of eight slots in flight; the dot products by shuffles, then over the token's warps through shared memory.
+// rows of eight slots in flight; the dot products by shuffles, then over the token's warps through shared memory. Bound by HBM:
+// 8,192 x 2048 bf16, 8 places each, 96 us, 5.9 TB/s (a warp a slot, its chain of loads after one another: 225).
 constexpr int kBackSlots = 8, kBackCtas = 3;     // slots in flight, CTAs of an SM
 template <typename TG, typename TY>
 __global__ void __launch_bounds__(kRowThreads, kBackCtas) reshard_combine_backward_kernel(CombineBackward a) {
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(kRowThreads, kBackCtas) reshard_combine_backwa
   }
 }
 
-// Rows that start anywhere: a warp a slot.
+// Rows that start anywhere: a warp a slot (8,191 x 2867 bf16, four places each: 103 us).
 template <typename TG, typename TY>
 __global__ void __launch_bounds__(kRowThreads) reshard_combine_backward_any_kernel(CombineBackward a) {
   constexpr int kN = kPieceOf<TG, TY>, kU = 2;

@@ -716,7 +716,7 @@ class TensorList:
         return len(self.tensors)
 
     def __del__(self):
-        if getattr(self, "_handle", None) is not None:
+        if getattr(self, "_handle", None) is not None and LIB is not None:      # (None while the interpreter ends)
             LIB.reshard_tensors_destroy(self._handle)
 
 
