@@ -278,7 +278,7 @@ extern "C" int reshard_ops_call(int op, const reshard_word_t *a) try {
     case RESHARD_OP_PERMUTE:
       return reshard_permute(reinterpret_cast<const void *>(a[0].i), as_int(a[1].i), a[2].i, a[3].i, a[4].i,
                              reinterpret_cast<const int32_t *>(a[5].i), reinterpret_cast<const int32_t *>(a[6].i), as_int(a[7].i),
-                             reinterpret_cast<void *>(a[8].i), a[9].i, a[10].i, reinterpret_cast<reshard_stream_t>(a[11].i));
+                             reinterpret_cast<void *>(a[8].i), a[9].i, a[10].i, as_int(a[11].i), reinterpret_cast<reshard_stream_t>(a[12].i));
     case RESHARD_OP_COMBINE:
       return reshard_combine(reinterpret_cast<const void *>(a[0].i), as_int(a[1].i), a[2].i, a[3].i, a[4].i,
                              reinterpret_cast<const int32_t *>(a[5].i), reinterpret_cast<const float *>(a[6].i), a[7].i,

@@ -51,8 +51,20 @@ struct Permute {
   int k;
   void *out;
   int64_t rows, out_stride;
-  int spans;                         // warps a row (a slot's row, where rows start anywhere)
+  int spans;                         // warps a row (a slot's row, where rows start anywhere); behind them, where `rest`,
+  bool rest;                         // a warp 32 rows to write zeros into those that no slot owns
 };
+
+// Of the 32 rows from `first` on those that no slot owns, as bits: each lane looks one up.
+__device__ __forceinline__ uint32_t unowned(const int32_t *order, const int32_t *position, int64_t slots, int64_t rows, int64_t first, int lane) {
+  const int64_t i = first + lane;
+  bool none = false;
+  if (i < rows) {
+    const int64_t s = order[i];        // not written behind the last place: whatever it holds there is no owner
+    none = s < 0 || s >= slots || position[s] != i;
+  }
+  return __ballot_sync(kFull, none);
+}
 
 // Rows of whole 16-byte pieces: a warp reads 2 KB of a token's row once and writes it to each of its places. Bound by the writes:
 // 8,192 x 2048 bf16 to 8 places each, 47 us, 6.4 TB/s.
@@ -61,7 +73,15 @@ __global__ void __launch_bounds__(kRowThreads) reshard_permute_kernel(Permute a)
   const int lane = threadIdx.x & 31;
   const Where at(a.spans);
   const int64_t t = at.row;
-  if (t >= a.tokens) return;
+  if (t >= a.tokens) {
+    const int64_t first = ((t - a.tokens) * a.spans + at.span) * 32;
+    if (!a.rest || first >= a.rows) return;
+    for (uint32_t left = unowned(a.order, a.position, a.tokens * a.k, a.rows, first, lane); left; left &= left - 1) {
+      uint4 *const to = static_cast<uint4 *>(a.out) + (first + __ffs(left) - 1) * a.out_stride;
+      for (int64_t c = lane; c < a.cols; c += 32) to[c] = make_uint4(0, 0, 0, 0);
+    }
+    return;
+  }
   const int64_t c0 = at.span * kSpan + lane;
   const uint4 *const from = static_cast<const uint4 *>(a.x) + t * a.stride;
   uint4 v[kAhead];
@@ -131,8 +151,15 @@ template <typename T>
 __global__ void __launch_bounds__(kRowThreads) reshard_permute_any_kernel(Permute a) {
   grid_enter();
   const Where at(a.spans);
-  const int64_t s = at.row;
-  if (s >= a.tokens * a.k) return;
+  const int64_t s = at.row, slots = a.tokens * a.k;
+  if (s >= slots) {
+    const int64_t first = ((s - slots) * a.spans + at.span) * 32;
+    if (!a.rest || first >= a.rows) return;
+    for (uint32_t left = unowned(a.order, a.position, slots, a.rows, first, threadIdx.x & 31); left; left &= left - 1)
+      for (int c = 0; c < a.spans; ++c)
+        move_span<T, false, false>(nullptr, static_cast<T *>(a.out) + (first + __ffs(left) - 1) * a.out_stride, a.cols, c * kSpan, threadIdx.x & 31, 1.0f);
+    return;
+  }
   const int p = place_of(a.position, s, a.rows);
   if (p < 0 || a.order[p] != s) return;
   move_span<T, false, false>(static_cast<const T *>(a.x) + s / a.k * a.stride, static_cast<T *>(a.out) + (int64_t)p * a.out_stride, a.cols, at.span * kSpan,
@@ -293,13 +320,7 @@ struct CombineBackward {
 // Zeros in the rows of the gradient that no slot owns: a warp 32 rows, whose owners it looks up at once.
 template <typename TY, bool Wide>
 __device__ __forceinline__ void zero_unowned(const CombineBackward &a, int64_t first, int lane) {
-  const int64_t i = first + lane;
-  bool none = false;
-  if (i < a.rows) {
-    const int64_t s = a.order[i];      // not written behind the last place: whatever it holds there is no owner
-    none = s < 0 || s >= a.tokens * a.k || a.position[s] != i;
-  }
-  for (uint32_t left = __ballot_sync(kFull, none); left; left &= left - 1)
+  for (uint32_t left = unowned(a.order, a.position, a.tokens * a.k, a.rows, first, lane); left; left &= left - 1)
     for (int c = 0; c < a.pieces; c += kSpan)
       move_span<TY, Wide, false>(nullptr, static_cast<TY *>(a.grad_y) + (first + __ffs(left) - 1) * a.grad_y_stride, a.cols, c, lane, 1.0f);
 }
@@ -521,31 +542,34 @@ using namespace reshard;
 using namespace reshard::ops;
 
 extern "C" int reshard_permute(const void *x, int dtype, int64_t tokens, int64_t cols, int64_t row_stride, const int32_t *order,
-                               const int32_t *position, int k, void *out, int64_t rows, int64_t out_stride, reshard_stream_t stream_) try {
+                               const int32_t *position, int k, void *out, int64_t rows, int64_t out_stride, int zero_rest, reshard_stream_t stream_) try {
   Checks c("reshard_permute");
   check_slots(c, tokens, cols, k, rows);
   c.invalid(!element_bytes(dtype), "dtype must be BF16, F16 or F32");
   c.invalid(row_stride < cols || out_stride < cols, "a row stride is shorter than the row");
   const int es = element_bytes(dtype);
-  const bool work = tokens > 0 && cols > 0 && rows > 0;
+  const bool work = (tokens > 0 || zero_rest) && cols > 0 && rows > 0;
   if (work && c.ok()) {
-    c.pointer(x, "x", (uintptr_t)es);
+    if (tokens > 0) {
+      c.pointer(x, "x", (uintptr_t)es);
+      c.pointer(position, "position", 4);
+    }
     c.pointer(order, "order", 4);
-    c.pointer(position, "position", 4);
     c.pointer(out, "out", (uintptr_t)es);
   }
   if (!c.ok()) return c.report();
   if (!work) return RESHARD_OK;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
-  Permute a{x, tokens, cols, row_stride, order, position, k, out, rows, out_stride, 0};
+  Permute a{x, tokens, cols, row_stride, order, position, k, out, rows, out_stride, 0, zero_rest != 0};
+  const int64_t rest = zero_rest ? ceil_div(rows, 32) : 0;      // warps
   if (aligned16(x, row_stride, es) && aligned16(out, out_stride, es) && cols * es % 16 == 0) {
     a.cols = cols * es / 16, a.stride = row_stride * es / 16, a.out_stride = out_stride * es / 16;
     a.spans = (int)ceil_div(a.cols, kSpan);
-    return launched(launch_warps(reshard_permute_kernel, tokens * a.spans, stream, a), "launching reshard_permute_kernel");
+    return launched(launch_warps(reshard_permute_kernel, tokens * a.spans + rest, stream, a), "launching reshard_permute_kernel");
   }
   // values are copied as they are: the types of a size share a kernel
   a.spans = (int)ceil_div(piece_count(cols, 16 / es, false), kSpan);
-  return launched(launch_warps(es == 4 ? reshard_permute_any_kernel<float> : reshard_permute_any_kernel<__half>, tokens * k * a.spans, stream, a),
+  return launched(launch_warps(es == 4 ? reshard_permute_any_kernel<float> : reshard_permute_any_kernel<__half>, tokens * k * a.spans + rest, stream, a),
                   "launching reshard_permute_any_kernel");
 } OPS_CATCH
 

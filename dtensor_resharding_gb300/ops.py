@@ -53,7 +53,7 @@ _SIGNATURES = {
     "reshard_linear_fp8": [_p, _i, _l, _l, _l, _p, _l, _p, _l, _p, _l, _p, _l, _p],
     "reshard_experts_fp8_workspace": [_l, _i, _i, _l, _l, _i],
     "reshard_experts_fp8": [_p, _i, _l, _l, _l, _p, _p, _i, _i, _i, _l, _p, _l, _l, _p, _p, _l, _l, _p, _p, _l, _p, _l, _p],
-    "reshard_permute": [_p, _i, _l, _l, _l, _p, _p, _i, _p, _l, _l, _p],
+    "reshard_permute": [_p, _i, _l, _l, _l, _p, _p, _i, _p, _l, _l, _i, _p],
     "reshard_combine": [_p, _i, _l, _l, _l, _p, _p, _l, _i, _p, _i, _l, _p],
     "reshard_combine_backward": [_p, _i, _l, _p, _i, _l, _l, _l, _p, _p, _p, _l, _i, _p, _l, _p, _p],
     "reshard_embedding": [_p, _i, _l, _p, _i, _l, _l, _l, _l, _f, _p, _l, _p],
@@ -81,7 +81,7 @@ _QUANTIZE_BLOCKS = Struct("=12q").pack
 _MATMUL_FP8 = Struct("=18q").pack
 _LINEAR_FP8 = Struct("=14q").pack
 _EXPERTS_FP8 = Struct("=24q").pack
-_PERMUTE = Struct("=12q").pack
+_PERMUTE = Struct("=13q").pack
 _COMBINE = Struct("=13q").pack
 _COMBINE_BACKWARD = Struct("=17q").pack
 _EMBEDDING = Struct("=9qd3q").pack
@@ -479,7 +479,7 @@ def reshard_permute(x: torch.Tensor, sort: Sort, *, out: Optional[torch.Tensor] 
     """y [slots, cols] with y[position[t * k + j]] = x[t]: each token's row at the places of its experts.
 
     ``sort`` is what ``reshard_dispatch`` gave for these tokens' ids. Rows of no slot (from offsets[-1] on: other ranks' experts') are
-    left as they are in ``out``, which may have more or fewer rows than slots, and undefined in a new tensor. Values
+    left as they are in ``out``, which may have more or fewer rows than slots, and 0 in a new tensor. Values
     are copied bit for bit; differentiable in ``x``."""
     here = _here(x, stream)
     if here is None:
@@ -492,11 +492,11 @@ def reshard_permute(x: torch.Tensor, sort: Sort, *, out: Optional[torch.Tensor] 
     code = _code(x, "x")
     at_order, places, at_position, slots = _sorted(sort, x)
     k = _choices(slots, T)
-    rows = places if out is None else out.shape[0]
+    rows, zero_rest = (places, 1) if out is None else (out.shape[0], 0)
     out, to_step = _output(out, rows, H, x.dtype, x)
     if rows > places:      # places that the sort does not have are nobody's
         rows = places
-    _call(8, _PERMUTE(x.data_ptr(), code, T, H, step, at_order, at_position, k, out.data_ptr(), rows, to_step, here))
+    _call(8, _PERMUTE(x.data_ptr(), code, T, H, step, at_order, at_position, k, out.data_ptr(), rows, to_step, zero_rest, here))
     return out
 
 

@@ -133,11 +133,13 @@ int reshard_experts_fp8(const void *x, int dtype, int64_t tokens, int64_t hidden
  * reshard_permute -- tokens' rows to their experts' places: out[position[s]] = x[t] for the slots s = t * k + j.
  * x [tokens, cols] in dtype, out [rows, cols] in the same; order [rows] and position [tokens * k] as reshard_dispatch gave
  * them (the places and slots of one another): a slot whose position is negative, beyond the rows, or another's (order
- * names another slot there) writes nothing. Rows that no slot writes stay as they were: those behind the last expert.
+ * names another slot there) writes nothing. Rows that no slot writes (those behind the last expert) stay as they were, or
+ * with zero_rest become 0.
  * Values are copied bit for bit. The gradient to x is reshard_combine without weights.
  */
 int reshard_permute(const void *x, int dtype, int64_t tokens, int64_t cols, int64_t row_stride, const int32_t *order,
-                    const int32_t *position, int k, void *out, int64_t rows, int64_t out_stride, reshard_stream_t stream);
+                    const int32_t *position, int k, void *out, int64_t rows, int64_t out_stride, int zero_rest,
+                    reshard_stream_t stream);
 
 /*
  * reshard_combine -- experts' rows back to their tokens: out[t] = sum over j of weights[t, j] * y[position[t * k + j]].

@@ -23,8 +23,8 @@ def refused(rc, code, *words):
 
 
 def test_empty_calls_need_no_device():
-    assert L.reshard_permute(None, 1, 0, 8, 8, None, None, 2, None, 4, 8, None) == 0
-    assert L.reshard_permute(None, 1, 4, 8, 8, None, None, 2, None, 0, 8, None) == 0
+    assert L.reshard_permute(None, 1, 0, 8, 8, None, None, 2, None, 4, 8, 0, None) == 0
+    assert L.reshard_permute(None, 1, 4, 8, 8, None, None, 2, None, 0, 8, 0, None) == 0
     assert L.reshard_combine(None, 1, 4, 8, 8, None, None, 0, 2, None, 1, 8, None) == 0
     assert L.reshard_combine_backward(None, 1, 8, None, 1, 0, 8, 8, None, None, None, 0, 2, None, 8, None, None) == 0
     assert L.reshard_combine_backward(None, 1, 8, None, 1, 4, 8, 8, None, None, None, 2, 2, None, 8, None, None) == 0      # neither is wanted
@@ -36,12 +36,12 @@ def test_empty_calls_need_no_device():
 
 
 def test_every_violation_is_listed():
-    refused(L.reshard_permute(None, 4, 2, 8, 4, None, None, 0, None, 4, 7, None), BAD, "k >= 1", "dtype", "row stride")
-    refused(L.reshard_permute(None, 1, 2, 8, 8, None, None, 2, None, 4, 8, None), BAD, "x is NULL", "order is NULL", "position is NULL", "out is NULL")
-    refused(L.reshard_permute(None, 1, 1 << 31, 8, 8, None, None, 2, None, 4, 8, None), UNSUP, "2^30")
-    refused(L.reshard_permute(None, 1, 1 << 30, 8, 8, None, None, 2, None, 4, 8, None), UNSUP, "2^30 slots")
-    refused(L.reshard_permute(None, 1, 1 << 62, 1 << 62, 1 << 62, None, None, 1 << 30, None, 4, 1 << 62, None), UNSUP, "2^30")
-    refused(L.reshard_permute(None, 1, 1 << 28, 1 << 30, 1 << 30, None, None, 2, None, 4, 1 << 30, None), UNSUP, "one launch")
+    refused(L.reshard_permute(None, 4, 2, 8, 4, None, None, 0, None, 4, 7, 0, None), BAD, "k >= 1", "dtype", "row stride")
+    refused(L.reshard_permute(None, 1, 2, 8, 8, None, None, 2, None, 4, 8, 0, None), BAD, "x is NULL", "order is NULL", "position is NULL", "out is NULL")
+    refused(L.reshard_permute(None, 1, 1 << 31, 8, 8, None, None, 2, None, 4, 8, 0, None), UNSUP, "2^30")
+    refused(L.reshard_permute(None, 1, 1 << 30, 8, 8, None, None, 2, None, 4, 8, 0, None), UNSUP, "2^30 slots")
+    refused(L.reshard_permute(None, 1, 1 << 62, 1 << 62, 1 << 62, None, None, 1 << 30, None, 4, 1 << 62, 0, None), UNSUP, "2^30")
+    refused(L.reshard_permute(None, 1, 1 << 28, 1 << 30, 1 << 30, None, None, 2, None, 4, 1 << 30, 0, None), UNSUP, "one launch")
     refused(L.reshard_combine(None, 0, -1, 8, 4, None, None, 3, 2, None, 9, 4, None), BAD, ">= 0", "dtype", "row stride")
     refused(L.reshard_combine(None, 1, 4, 8, 8, None, None, 3, 2, None, 1, 8, None), BAD, "y is NULL", "position is NULL", "out is NULL")
     refused(L.reshard_combine_backward(None, 7, 4, None, 1, 4, 8, 4, None, None, None, 3, 2, 16, 4, 16, None), BAD, "grad_dtype", "row stride")
@@ -136,7 +136,7 @@ def test_words_of_the_row_calls(words):
     assert [op for op, _ in words] == [8, 9, 10]
     at_order, at_position = sort[1].data_ptr(), sort[2].data_ptr()
     # places that the sort does not have are left out
-    assert words[0][1] == (x.data_ptr(), 1, 3, 16, 24, at_order, at_position, 2, out.data_ptr(), 6, 40, 0)
+    assert words[0][1] == (x.data_ptr(), 1, 3, 16, 24, at_order, at_position, 2, out.data_ptr(), 6, 40, 0, 0)
     assert words[1][1] == (y.data_ptr(), 3, 6, 16, 16, at_position, w.data_ptr(), 3, 2, back.data_ptr(), 2, 16, 0)
     assert words[2][1] == (x.data_ptr(), 1, 24, y.data_ptr(), 3, 6, 16, 16, at_order, at_position, w.data_ptr(), 3, 2, dy.data_ptr(), 16, dw.data_ptr(), 0)
 

@@ -73,7 +73,7 @@ def test_permute(T, k, E, H, dtype, how, share):
     offsets, order, position = sort
     held = int(offsets[-1])
     got = R.reshard_permute(x, sort)
-    assert got.shape == (T * k, H) and torch.equal(got[:held], x[order[:held].long() // k])
+    assert got.shape == (T * k, H) and torch.equal(got[:held], x[order[:held].long() // k]) and not bool(got[held:].any())
     # rows behind the last expert, of a longer and of a shorter buffer, stay as they were
     for rows in (T * k + 3, max(1, held - 1)):
         to = laid(torch.full((rows, H), 7.0, dtype=x.dtype, device="cuda"), how)
@@ -109,6 +109,9 @@ def test_sorts_that_are_none(H):
     R.reshard_permute(x, sort, out=to)
     for p in range(12):
         assert torch.equal(to[p], x[owners[p] // k] if p in owners else torch.full((H,), 7.0, device="cuda")), p
+    fresh = R.reshard_permute(x, sort)
+    for p in range(12):
+        assert torch.equal(fresh[p], x[owners[p] // k] if p in owners else torch.zeros(H, device="cuda")), p
     y, w, g = randn(gen(2), 12, H), randn(gen(3), T, k), randn(gen(4), T, H)
     close(R.reshard_combine(y, sort, w), X.combine(y, position, w, k), k * U * X.combine(y, position, w, k, True))
     dy, dw = R.reshard_combine_backward(g, y, sort, w)
@@ -160,7 +163,7 @@ def test_nothing_is_here(T):
     _, ids, sort = case(1, T, 2, 8, 16, "f32", first=100, local=4)
     x, y = randn(gen(2), T, 16), randn(gen(3), 2 * T, 16)
     to = torch.full((2 * T + 1, 16), 3.0, device="cuda")
-    assert bool((R.reshard_permute(x, sort, out=to) == 3.0).all())
+    assert bool((R.reshard_permute(x, sort, out=to) == 3.0).all()) and not bool(R.reshard_permute(x, sort).any())
     w = torch.rand(T, 2, device="cuda")
     assert not bool(R.reshard_combine(y, sort, w).any()) and R.reshard_combine(y, sort, w).shape == (T, 16)
     dy, dw = R.reshard_combine_backward(x, y, sort, w)
@@ -523,7 +526,7 @@ def test_refusals_name_what_is_wrong():
             call()
         assert word in str(e.value), (i, word, str(e.value))
     host = torch.zeros(4, 16)
-    rc = R.binding.LIB.reshard_permute(host.data_ptr(), 3, 4, 16, 16, order.data_ptr(), position.data_ptr(), 2, y.data_ptr(), 8, 16, None)
+    rc = R.binding.LIB.reshard_permute(host.data_ptr(), 3, 4, 16, 16, order.data_ptr(), position.data_ptr(), 2, y.data_ptr(), 8, 16, 0, None)
     assert rc == R.RESHARD_ERR_INVALID_ARG and "pageable" in R.reshard_last_error()
 
 
