@@ -180,14 +180,23 @@ __global__ void __launch_bounds__(kZeroThreads) reshard_zero_kernel(uint8_t *bas
 // -------------------------------------------------------------------------------------------------------------- sum --
 
 constexpr int kSumThreads = 128;
-constexpr int kJoinThreads = 128, kJoinColumns = kJoinThreads * 4;
 
 // The sorted tokens go in runs, one to each CTA (of a slice of the columns): at least kMinRun tokens, and as many runs as give the
-// GPU one round of CTAs, kSumCtas of each of 152 SMs (a second round of a few CTAs took a third longer). How many tokens are of this
-// shard, the device knows. Each run leaves up to two rows in the workspace.
-constexpr int64_t kMinRun = 16, kMostRuns = 512;
+// GPU one round of CTAs, kSumCtas of each of 152 SMs, or more of fewer warps (a second round of a few CTAs took a third longer). How
+// many tokens are of this shard, the device knows. Each run leaves up to two rows in the workspace.
+constexpr int64_t kMinRun = 16, kMostRuns = 1024;
 constexpr int kSumCtas = 6;
-int runs_of(int64_t slices) { return (int)std::max<int64_t>(64, std::min<int64_t>(kMostRuns, 152 * kSumCtas / slices)); }
+struct Slices {                      // of rows of so many columns, a piece of `values` a thread
+  int threads, count;
+  Slices(int64_t cols, int values) : threads(kSumThreads) {
+    while (threads > 32 && threads / 2 * values >= cols) threads /= 2;
+    count = (int)((cols + threads * values - 1) / (threads * values));
+  }
+  int64_t runs(int64_t tokens) const {
+    const int64_t round = 152 * kSumCtas * (kSumThreads / threads) / count;
+    return std::min((tokens + kMinRun - 1) / kMinRun, std::max<int64_t>(64, std::min(kMostRuns, round)));
+  }
+};
 
 struct Sum {
   const uint2 *sorted;
@@ -234,7 +243,7 @@ __global__ void __launch_bounds__(kSumThreads, Wide ? kSumCtas : 5) reshard_sum_
   grid_enter();
   const int lane = threadIdx.x & 31;
   const int64_t number = blockIdx.x / (uint32_t)a.slices;
-  const int64_t c = ((int64_t)(blockIdx.x % (uint32_t)a.slices) * kSumThreads + threadIdx.x) * kN;
+  const int64_t c = ((int64_t)(blockIdx.x % (uint32_t)a.slices) * blockDim.x + threadIdx.x) * kN;
   const int64_t held = *a.held, run = a.run_of(held), lo = number * run, hi = min(lo + run, held);
   if (lo >= held || c - lane * kN >= a.cols) return;       // whole warps
   uint2 mine = lo + lane < hi ? a.sorted[lo + lane] : make_uint2(0, 0);
@@ -288,11 +297,11 @@ __global__ void __launch_bounds__(kSumThreads, Wide ? kSumCtas : 5) reshard_sum_
 
 // The rows that end in another run than they begin in: the CTAs of the run that such a row begins in.
 template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) reshard_join_rows_kernel(Sum a) {
+__global__ void __launch_bounds__(kSumThreads) reshard_join_rows_kernel(Sum a) {
   grid_enter();
   const int lane = threadIdx.x & 31;
   const int64_t number = blockIdx.x / (uint32_t)a.slices;
-  const int64_t c = (int64_t)(blockIdx.x % (uint32_t)a.slices) * kJoinColumns + threadIdx.x * 4;
+  const int64_t c = ((int64_t)(blockIdx.x % (uint32_t)a.slices) * blockDim.x + threadIdx.x) * 4;
   const int64_t held = *a.held, run = a.run_of(held), lo = number * run, hi = lo + run;
   if (hi >= held) return;
   const uint32_t row = a.sorted[hi - 1].x, after = a.sorted[hi].x, before = lo > 0 ? a.sorted[lo - 1].x : ~0u;
@@ -396,7 +405,7 @@ __global__ void __launch_bounds__(kSumThreads, Wide ? kSumCtas : 5) reshard_sum_
 struct Layout {
   int64_t sorted, held, runs, pitch, part;
   Layout(int64_t tokens, int64_t cols)
-      : sorted(up(8 * tokens, kAlign)), held(kAlign), runs(std::min<int64_t>(kMostRuns, (tokens + kMinRun - 1) / kMinRun)), pitch(up(cols, 8)),
+      : sorted(up(8 * tokens, kAlign)), held(kAlign), runs(Slices(cols, 8).runs(tokens)), pitch(up(cols, 8)),
         part(up(2 * runs * pitch * 4, kAlign)) {}
   int64_t bytes() const { return 2 * sorted + held + part; }
 };
@@ -424,7 +433,7 @@ extern "C" int reshard_embedding_backward(const void *grad, int grad_dtype, int6
   c.invalid(!element_bytes(grad_dtype) || !element_bytes(table_dtype), "grad_dtype and table_dtype must be BF16, F16 or F32");
   c.invalid(grad_stride < cols || table_stride < cols, "a row stride is shorter than the row");
   if (c.ok() && tokens > 0)
-    c.unsupported(Layout(tokens, cols).runs * ((cols + kJoinColumns - 1) / kJoinColumns) > INT32_MAX, "too many columns for one launch");
+    c.unsupported(Layout(tokens, cols).runs * Slices(cols, 4).count > INT32_MAX, "too many columns for one launch");
   const bool work = rows > 0 && cols > 0 && (tokens > 0 || !accumulate);
   if (work && c.ok()) {
     c.pointer(grad_table, "grad_table", (uintptr_t)element_bytes(table_dtype));
@@ -474,20 +483,23 @@ extern "C" int reshard_embedding_backward(const void *grad, int grad_dtype, int6
     using TG = decltype(g);
     return by_type(table_dtype, [&](auto t) {
       using T = decltype(t);
-      a.slices = (int)((cols + kSumThreads * kPieceOf<TG, T> - 1) / (kSumThreads * kPieceOf<TG, T>));
+      const Slices s(cols, kPieceOf<TG, T>);
+      a.slices = s.count;
       if (few) {
+        a.slices = (int)((cols + kSumThreads * kPieceOf<TG, T> - 1) / (kSumThreads * kPieceOf<TG, T>));
         const FewSum f{ids, id_bits == 64, (int)tokens, first_row, rows, a};
         return launch(wide ? reshard_sum_few_rows_kernel<TG, T, true> : reshard_sum_few_rows_kernel<TG, T, false>, dim3((unsigned)(tokens * a.slices)),
                       kSumThreads, 0, 1, stream, f);
       }
-      a.runs = (int)std::min<int64_t>(l.runs, runs_of(a.slices));
-      return launch(wide ? reshard_sum_rows_kernel<TG, T, true> : reshard_sum_rows_kernel<TG, T, false>, dim3((unsigned)(a.runs * a.slices)), kSumThreads, 0,
+      a.runs = (int)s.runs(tokens);
+      return launch(wide ? reshard_sum_rows_kernel<TG, T, true> : reshard_sum_rows_kernel<TG, T, false>, dim3((unsigned)(a.runs * a.slices)), s.threads, 0,
                     1, stream, a);
     });
   }), "launching reshard_sum_rows_kernel");
   if (rc || few || a.runs == 1) return rc;
-  a.slices = (int)((cols + kJoinColumns - 1) / kJoinColumns);
+  const Slices s(cols, 4);
+  a.slices = s.count;
   return launched(by_type(table_dtype, [&](auto t) {
-    return launch(reshard_join_rows_kernel<decltype(t)>, dim3((unsigned)((a.runs - 1) * a.slices)), kJoinThreads, 0, 1, stream, a);
+    return launch(reshard_join_rows_kernel<decltype(t)>, dim3((unsigned)((a.runs - 1) * a.slices)), s.threads, 0, 1, stream, a);
   }), "launching reshard_join_rows_kernel");
 } OPS_CATCH
