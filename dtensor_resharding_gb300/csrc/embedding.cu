@@ -183,7 +183,8 @@ constexpr int kSumThreads = 128;
 
 // The sorted tokens go in runs, one to each CTA (of a slice of the columns): at least kMinRun tokens, and as many runs as give the
 // GPU one round of CTAs, kSumCtas of each of 152 SMs, or more of fewer warps (a second round of a few CTAs took a third longer). How
-// many tokens are of this shard, the device knows. Each run leaves up to two rows in the workspace.
+// many tokens are of this shard, the device knows. Each run leaves up to two rows in the workspace. (59,088 x 176 bf16 into 25,645
+// rows: 58 us, of which the sort 27; CTAs of four warps, one of them with columns, and 512 runs 68.)
 constexpr int64_t kMinRun = 16, kMostRuns = 1024;
 constexpr int kSumCtas = 6;
 struct Slices {                      // of rows of so many columns, a piece of `values` a thread
