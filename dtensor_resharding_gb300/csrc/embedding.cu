@@ -433,9 +433,9 @@ extern "C" int reshard_embedding_backward(const void *grad, int grad_dtype, int6
   c.invalid(id_bits != 32 && id_bits != 64, "id_bits must be 32 or 64");
   c.invalid(!element_bytes(grad_dtype) || !element_bytes(table_dtype), "grad_dtype and table_dtype must be BF16, F16 or F32");
   c.invalid(grad_stride < cols || table_stride < cols, "a row stride is shorter than the row");
-  if (c.ok() && tokens > 0)
+  const bool work = rows > 0 && cols > 0 && (tokens > 0 || !accumulate);      // a layout is of rows that have columns
+  if (work && c.ok() && tokens > 0)
     c.unsupported(Layout(tokens, cols).runs * Slices(cols, 4).count > INT32_MAX, "too many columns for one launch");
-  const bool work = rows > 0 && cols > 0 && (tokens > 0 || !accumulate);
   if (work && c.ok()) {
     c.pointer(grad_table, "grad_table", (uintptr_t)element_bytes(table_dtype));
     if (tokens > 0) {

@@ -35,6 +35,16 @@ def test_empty_calls_need_no_device():
     assert L.reshard_tensors_destroy(None) == 0
 
 
+def test_gradients_of_no_columns_are_nothing():
+    """Rows of no columns have no slices: their gradients are calls without work, of few tokens and of many, whole or accumulated."""
+    for tokens in (1, 5, 256, 257, 300, 1 << 30):
+        for rows in (0, 9):
+            for accumulate in (0, 1):
+                assert L.reshard_embedding_backward(None, 1, tokens, 0, 0, None, 64, 0, rows, 1.0, None, 1, 0, accumulate, None, 0, None) == 0
+    assert L.reshard_embedding_backward_workspace(300, 0) == 0
+    assert L.reshard_combine_backward(None, 1, 0, None, 1, 4, 0, 0, None, None, None, 0, 2, None, 0, None, None) == 0
+
+
 def test_every_violation_is_listed():
     refused(L.reshard_permute(None, 4, 2, 8, 4, None, None, 0, None, 4, 7, 0, None), BAD, "k >= 1", "dtype", "row stride")
     refused(L.reshard_permute(None, 1, 2, 8, 8, None, None, 2, None, 4, 8, 0, None), BAD, "x is NULL", "order is NULL", "position is NULL", "out is NULL")

@@ -616,3 +616,25 @@ def test_a_captured_training_step():
         for a, b in zip(captured, step()):
             # torch's own indexing gradient adds in any order
             assert float((a - b).abs().max()) <= 1e-5 * float(b.abs().max())
+
+
+# ------------------------------------------------------------------------------------------------------- no columns
+
+@pytest.mark.parametrize("T", [0, 1, 5, 300])
+@pytest.mark.parametrize("wide_ids", [False, True])
+def test_rows_of_no_columns(T, wide_ids):
+    """Tables and rows without columns: results and gradients of the right shape, through autograd too; a weight's gradient is 0."""
+    ids = torch.arange(T, device="cuda", dtype=torch.int64 if wide_ids else torch.int32) % 9
+    table = torch.zeros(9, 0, device="cuda", requires_grad=True)
+    out = R.reshard_embedding(ids, table)
+    out.sum().backward()
+    assert out.shape == (T, 0) and table.grad.shape == (9, 0)
+    grad = torch.zeros(T, 0, device="cuda")
+    for accumulate in (False, True):
+        main = torch.zeros(9, 0, device="cuda")
+        assert R.reshard_embedding_backward(grad, ids, 9, out=main, accumulate=accumulate) is main
+    sort = R.reshard_dispatch((ids % 4).int().view(T, 1), 4)
+    x, w = torch.zeros(T, 0, device="cuda", requires_grad=True), torch.rand(T, 1, device="cuda", requires_grad=True)
+    y = R.reshard_combine(R.reshard_permute(x, sort), sort, w)
+    y.sum().backward()
+    assert y.shape == x.grad.shape == (T, 0) and w.grad.shape == (T, 1) and not bool(w.grad.any())
