@@ -709,6 +709,10 @@ class TensorList:
             _check(LIB.reshard_tensors_create((ctypes.c_void_p * n)(*at), (ctypes.c_int64 * n)(*sizes), (ctypes.c_int32 * n)(*types), n, ctypes.byref(handle)))
         self._handle = handle.value
 
+    def __reduce__(self):
+        """A copy, deep copy or pickle is a list of its own: the library's list is freed with the object that made it."""
+        return type(self), (self.tensors,)
+
     def get_device(self) -> int:
         return self.device.index
 

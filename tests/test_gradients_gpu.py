@@ -5,7 +5,9 @@ one rounding, and what follows carries its roundings along or has 64 bits; with 
 of it of the root, and the root's rounding to fp32: 7 u. The factor adds its rounding and takes over the norm's error, the
 product its own: 9 u of the value, and half a step of the type that it is rounded to.
 """
+import copy
 import math
+import pickle
 
 import pytest
 import torch
@@ -275,3 +277,21 @@ def test_refusals_name_what_is_wrong():
             call()
         assert word in str(e.value), (i, word, str(e.value))
     assert float(R.reshard_grad_norm([x + 1, x + 1])) == math.sqrt(128) or abs(float(R.reshard_grad_norm([x + 1, x + 1])) - math.sqrt(128)) < 1e-5
+
+
+# ----------------------------------------------------------------------------------------------------- lists that are kept
+
+@pytest.mark.parametrize("how", ["copy", "deepcopy", "pickle"])
+def test_a_copied_list_outlives_its_source(how):
+    ts = tensors(3, [300, 5000, 0, 7], ["bf16", "f32"])
+    a = R.reshard_tensor_list(ts)
+    n = check_norm(ts, R.reshard_grad_norm(a))
+    b = {"copy": copy.copy, "deepcopy": copy.deepcopy, "pickle": lambda t: pickle.loads(pickle.dumps(t))}[how](a)
+    assert len(b) == 4 and b.device == a.device and b._handle != a._handle
+    assert [x.data_ptr() == y.data_ptr() for x, y in zip(a.tensors, b.tensors) if x.numel()] == [how == "copy"] * 3
+    keep = [t.clone() for t in ts]
+    del a
+    assert torch.equal(R.reshard_clip_grads(b, 0.5 * float(n)), n)
+    check_clipped(b.tensors, keep, 0.5 * float(n), n)
+    if how != "copy":                                        # a deep copy's tensors are its own
+        assert all(torch.equal(x, y) for x, y in zip(ts, keep))

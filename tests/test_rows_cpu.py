@@ -1,6 +1,9 @@
 """Rows by index, embedding, norm and clipping without a GPU: the calls' refusals, the words that the binding hands over, and
 the 64-bit oracle against other definitions of the same things."""
+import contextlib
+import copy
 import ctypes
+import pickle
 import struct
 
 import pytest
@@ -89,6 +92,24 @@ def test_a_list_of_nothing():
         refused(L.reshard_grad_norm(handle, None, None, 0, None), BAD, "norm is NULL", "workspace is NULL", "workspace is smaller")
         refused(L.reshard_clip_grads(handle, None, 1.0, None, None, None, 0, None), BAD, "norm_out is NULL")
         assert L.reshard_tensors_destroy(handle) == 0
+
+
+def test_copies_of_a_list_are_lists_of_their_own(monkeypatch):
+    """A list that is copied, deeply copied or pickled (with the optimizer that holds it) makes another in the library, and each is
+    freed once."""
+    freed = []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: contextlib.nullcontext())
+    monkeypatch.setattr(ops, "LIB", type("Lib", (), {"reshard_tensors_create": staticmethod(L.reshard_tensors_create),
+                                                     "reshard_tensors_destroy": staticmethod(lambda h: freed.append(h) or L.reshard_tensors_destroy(h))}))
+    first = R.reshard_tensor_list([])
+    lists = [first, copy.copy(first), copy.deepcopy({"of": [first]})["of"][0], pickle.loads(pickle.dumps(first))]
+    handles = {t._handle for t in lists}
+    assert len(handles) == 4 and all(type(t) is R.TensorList and t.tensors == [] for t in lists)
+    del first
+    while lists:
+        lists.pop()
+    assert sorted(freed) == sorted(handles)
 
 
 def test_workspace_sizes():
