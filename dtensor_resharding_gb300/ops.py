@@ -681,14 +681,16 @@ def _packed(t: torch.Tensor) -> bool:
 
 class TensorList:
     """Dense tensors of one device for ``reshard_grad_norm`` and ``reshard_clip_grads``, looked over once: for tensors that
-    stay where they are from step to step (the list keeps them alive; one whose storage is replaced needs a new list)."""
+    stay where they are from step to step (``zero_grad(set_to_none=False)``). The list keeps them and their memory alive, and
+    goes on with that memory where a tensor is given other (``t.data = ...``) or a parameter another gradient: then make a new
+    list. Storages that are resized in place must not be in one."""
 
     is_cuda = True
 
     def __init__(self, tensors: Iterable[torch.Tensor]):
         self._handle = None
         self.tensors = tensors = list(tensors)
-        at, sizes, types, self._order = [], [], [], {}
+        at, sizes, types, self._order, self._memory = [], [], [], {}, []
         self.device = device = tensors[0].device if tensors else torch.device("cuda", torch.cuda.current_device())
         if device.type != "cuda":
             _bad(f"tensors must be on a CUDA device, not on {device}")
@@ -702,6 +704,7 @@ class TensorList:
                     _bad(f"tensor {i} of shape {tuple(t.shape)}, strides {t.stride()} is not dense")
                 self._order[i] = (t.shape, t.stride())
             at.append(t.data_ptr())
+            self._memory.append(t.untyped_storage())      # what the addresses are of, whatever the tensor is given later
             sizes.append(t.numel())
             types.append(_code(t, "a tensor"))
         n, handle = len(tensors), ctypes.c_void_p()

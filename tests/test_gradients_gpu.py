@@ -295,3 +295,17 @@ def test_a_copied_list_outlives_its_source(how):
     check_clipped(b.tensors, keep, 0.5 * float(n), n)
     if how != "copy":                                        # a deep copy's tensors are its own
         assert all(torch.equal(x, y) for x, y in zip(ts, keep))
+
+
+def test_a_list_keeps_the_memory_that_it_was_made_of():
+    """A tensor that is given other memory leaves its own to the list: calls do not write what belongs to others by then."""
+    ts = [torch.randn(n, generator=gen(4), device="cuda") for n in (70000, 500)]
+    t, at = ts[0], ts[0].data_ptr()
+    a = R.reshard_tensor_list(ts)
+    n = check_norm(ts, R.reshard_grad_norm(a))
+    t.data = torch.zeros(70000, device="cuda")
+    others = [torch.full((70000,), 7.0, device="cuda") for _ in range(20)]
+    assert all(not o.data_ptr() <= at < o.data_ptr() + 4 * o.numel() for o in others)
+    assert torch.equal(R.reshard_grad_norm(a), n)
+    R.reshard_clip_grads(a, 0.5 * float(n))
+    assert all(bool((o == 7.0).all()) for o in others) and not bool(t.any())
