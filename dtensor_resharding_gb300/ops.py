@@ -17,7 +17,8 @@ looks at: ``reshard_ops_status`` reads it.
 Gradients: ``reshard_route``'s weights carry the gradient to its logits (``reshard_route_backward``); ``reshard_permute``,
 ``reshard_combine`` and ``reshard_embedding`` carry theirs, which are also calls of their own. ``reshard_linear_fp8`` and
 ``reshard_experts_fp8`` have none: of an input that requires one, their result raises when a gradient is asked of it. Codes and
-scales (the quantizations, ``reshard_matmul_fp8`` over them) carry none.
+scales (the quantizations, ``reshard_matmul_fp8`` over them) carry none. In forward mode (``torch.autograd.forward_ad``) there
+are no derivatives: an input with a tangent is refused.
 """
 from __future__ import annotations
 
@@ -27,6 +28,7 @@ from struct import Struct
 from typing import Iterable, Optional, Tuple, Union
 
 import torch
+from torch.autograd import forward_ad as _forward
 
 from .binding import LIB, ReshardError, RESHARD_ERR_INVALID_ARG, RESHARD_ERR_UNSUPPORTED, _check, reshard_last_error
 
@@ -177,6 +179,14 @@ class _on:
             e.__exit__(*exc)
 
 
+# Forward mode reads a result without a tangent as one that does not depend on its inputs. The calls ask for tangents only
+# inside a level of forward mode (the number of the innermost, -1 outside).
+
+def _no_tangent(name: str, *inputs: Optional[torch.Tensor]) -> None:
+    if any(t is not None and _forward.unpack_dual(t).tangent is not None for t in inputs):
+        raise ReshardError(RESHARD_ERR_UNSUPPORTED, f"{name} has no derivative in forward mode: call it on the primal, or use reverse mode")
+
+
 def _score(score) -> int:
     if isinstance(score, str):
         if score not in SCORES:
@@ -195,6 +205,8 @@ def reshard_route(logits: torch.Tensor, k: int, *, score="softmax", bias: Option
     the chosen scores without the bias, divided by their sum if ``renormalize``, times ``scale``. A logit of -inf or NaN
     is never chosen: missing choices have id -1 and weight 0. The weights are differentiable in the logits, the choice and
     the bias that makes it are not."""
+    if _forward._current_level >= 0:
+        _no_tangent("reshard_route", logits, bias)
     here = _here(logits, stream)
     if here is None:
         with _on(logits, stream):
@@ -249,6 +261,8 @@ def reshard_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, ids
     """The gradient to ``logits`` of ``reshard_route``'s weights, the choice ``ids`` held fixed, in the logits' type.
 
     ``grad_weights`` is copied where it is not contiguous (a broadcast gradient)."""
+    if _forward._current_level >= 0:
+        _no_tangent("reshard_route_backward", grad_weights, logits)
     here = _here(logits, stream)
     if here is None:
         with _on(logits, stream):
@@ -376,6 +390,8 @@ def reshard_matmul_fp8(a: torch.Tensor, a_scale: torch.Tensor, w: torch.Tensor, 
 def reshard_linear_fp8(x: torch.Tensor, w: torch.Tensor, w_scale: torch.Tensor, *, out: Optional[torch.Tensor] = None,
                        stream=None) -> torch.Tensor:
     """out [m, n] = Q(x) w^T in x's type: x [m, k] is quantized by rows, ``w`` [n, k] holds 8-bit values and block scales."""
+    if _forward._current_level >= 0:
+        _no_tangent("reshard_linear_fp8", x, w_scale)
     here = _here(x, stream)
     if here is None:
         with _on(x, stream):
@@ -404,6 +420,8 @@ def reshard_experts_fp8(x: torch.Tensor, ids: torch.Tensor, weights: torch.Tenso
     x [tokens, hidden]; ids int32 and weights float32 [tokens, k] (``reshard_route``); w13 [experts, 2 ffn, hidden] (gate rows,
     then up rows) and w2 [experts, hidden, ffn] with their block scales; ffn a multiple of 128. Ids outside this
     rank's experts first_expert .. first_expert + experts - 1 add nothing."""
+    if _forward._current_level >= 0:
+        _no_tangent("reshard_experts_fp8", x, weights, w13_scale, w2_scale)
     here = _here(x, stream)
     if here is None:
         with _on(x, stream):
@@ -481,6 +499,8 @@ def reshard_permute(x: torch.Tensor, sort: Sort, *, out: Optional[torch.Tensor] 
     ``sort`` is what ``reshard_dispatch`` gave for these tokens' ids. Rows of no slot (from offsets[-1] on: other ranks' experts') are
     left as they are in ``out``, which may have more or fewer rows than slots, and 0 in a new tensor. Values
     are copied bit for bit; differentiable in ``x``."""
+    if _forward._current_level >= 0:
+        _no_tangent("reshard_permute", x)
     here = _here(x, stream)
     if here is None:
         with _on(x, stream):
@@ -502,6 +522,8 @@ def reshard_permute(x: torch.Tensor, sort: Sort, *, out: Optional[torch.Tensor] 
 
 def reshard_permute_backward(grad: torch.Tensor, sort: Sort, k: int, *, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """The gradient to ``x`` of ``reshard_permute``: each token's sum over its k places, in ``grad``'s type."""
+    if _forward._current_level >= 0:
+        _no_tangent("reshard_permute_backward", grad)
     return reshard_combine(grad.detach(), sort, k=k, out=out, stream=stream)
 
 
@@ -524,6 +546,8 @@ def reshard_combine(y: torch.Tensor, sort: Sort, weights: Optional[torch.Tensor]
 
     ``weights`` [tokens, k] float32 (``reshard_route``), or None with ``k`` given: plain sums. Slots without a place add nothing.
     The sum is fp32 and rounded once, to ``out_dtype`` (y's type if None). Differentiable in ``y`` and ``weights``."""
+    if _forward._current_level >= 0:
+        _no_tangent("reshard_combine", y, weights)
     here = _here(y, stream)
     if here is None:
         with _on(y, stream):
@@ -548,6 +572,8 @@ def reshard_combine_backward(grad: torch.Tensor, y: torch.Tensor, sort: Sort, we
 
     Rows of ``y`` that belong to no slot have gradient 0, and so have weights of slots without a place. ``needs``: which of the two
     are wanted (the other is None). Without ``weights`` there is no gradient to them."""
+    if _forward._current_level >= 0:
+        _no_tangent("reshard_combine_backward", grad, y, weights)
     here = _here(grad, stream)
     if here is None:
         with _on(grad, stream):
@@ -603,6 +629,8 @@ def reshard_embedding(ids: torch.Tensor, table: torch.Tensor, *, scale: float = 
 
     ``ids`` int64 or int32 of any shape (copied where not contiguous), ``table`` [rows, cols] the rows first_row .. first_row +
     rows - 1 of the vocabulary: the shards' results sum to the whole lookup. Differentiable in ``table``."""
+    if _forward._current_level >= 0:
+        _no_tangent("reshard_embedding", table)
     here = _here(table, stream)
     if here is None:
         with _on(table, stream):
@@ -634,6 +662,8 @@ def reshard_embedding_backward(grad: torch.Tensor, ids: torch.Tensor, rows: int,
 
     Sums are fp32 in the order of the tokens, rounded once to ``dtype`` (``grad``'s if None). Rows without a token get 0; with
     ``accumulate`` the sums are added to ``out`` instead (a main gradient of a training step), and other rows not touched."""
+    if _forward._current_level >= 0:
+        _no_tangent("reshard_embedding_backward", grad, out if accumulate else None)
     here = _here(grad, stream)
     if here is None:
         with _on(grad, stream):
@@ -741,6 +771,8 @@ def reshard_grad_norm(tensors: Tensors, *, stream=None) -> torch.Tensor:
     Other ranks' shards: the root of the sum of their norms' squares is the whole norm."""
     if not isinstance(tensors, TensorList):
         tensors = TensorList(tensors)
+    if _forward._current_level >= 0:
+        _no_tangent("reshard_grad_norm", *tensors.tensors)
     here = _here(tensors, stream)
     if here is None:
         with _on(tensors, stream):
@@ -760,6 +792,8 @@ def reshard_clip_grads(tensors: Tensors, limit: float, *, norm: Optional[torch.T
     any write through a pointer, autograd is not told."""
     if not isinstance(tensors, TensorList):
         tensors = TensorList(tensors)
+    if _forward._current_level >= 0:
+        _no_tangent("reshard_clip_grads", *tensors.tensors, norm)
     if out is not None and not isinstance(out, TensorList):
         out = TensorList(out)
     here = _here(tensors, stream)

@@ -11,6 +11,7 @@ import pickle
 
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 from oracle import rows as X
 
@@ -309,3 +310,18 @@ def test_a_list_keeps_the_memory_that_it_was_made_of():
     assert torch.equal(R.reshard_grad_norm(a), n)
     R.reshard_clip_grads(a, 0.5 * float(n))
     assert all(bool((o == 7.0).all()) for o in others) and not bool(t.any())
+
+
+# ------------------------------------------------------------------------------------------------------- derivatives
+
+def test_tangents_are_refused():
+    ts = [torch.ones(8, device="cuda"), torch.ones(3, device="cuda")]
+    a = R.reshard_tensor_list(ts)
+    with forward_ad.dual_level():
+        duals = [ts[0], forward_ad.make_dual(ts[1], torch.ones_like(ts[1]))]
+        for call in (lambda: R.reshard_grad_norm(duals), lambda: R.reshard_clip_grads(duals, 1.0),
+                     lambda: R.reshard_clip_grads(ts, 1.0, norm=forward_ad.make_dual(torch.ones((), device="cuda"), torch.ones((), device="cuda")))):
+            with pytest.raises(R.ReshardError, match="forward mode"):
+                call()
+        assert float(R.reshard_grad_norm(a)) == math.sqrt(11.0) or abs(float(R.reshard_grad_norm(a)) - math.sqrt(11.0)) <= 7 * U * 4
+    assert all(bool((t == 1.0).all()) for t in ts)

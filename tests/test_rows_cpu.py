@@ -8,6 +8,7 @@ import struct
 
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 import dtensor_resharding_gb300 as R
 from dtensor_resharding_gb300 import binding as B, ops
@@ -191,6 +192,51 @@ def test_dense_in_any_order():
         assert t.is_contiguous() or ops._packed(t), t.shape
     for t in (x[:, ::2], x[:, :, :3], x[:, :, :1], x.expand(2, 4, 6, 5), torch.zeros(3, 1).expand(3, 4), x.permute(2, 0, 1)[:3]):
         assert not t.is_contiguous() and not ops._packed(t), (t.shape, t.stride())
+
+
+# ---------------------------------------------------------------------------------------------------------- derivatives
+
+def _sort():
+    return tuple(torch.zeros(4, dtype=torch.int32) for _ in range(3))
+
+
+TANGENTS = {
+    "reshard_route": lambda d: R.reshard_route(d(2, 4), 2),
+    "reshard_route bias": lambda d: R.reshard_route(torch.zeros(2, 4), 2, bias=d(4)),
+    "reshard_route_backward": lambda d: R.reshard_route_backward(d(2, 2), torch.zeros(2, 4), torch.zeros(2, 2, dtype=torch.int32)),
+    "reshard_route_backward logits": lambda d: R.reshard_route_backward(torch.zeros(2, 2), d(2, 4), torch.zeros(2, 2, dtype=torch.int32)),
+    "reshard_linear_fp8": lambda d: R.reshard_linear_fp8(d(2, 128), torch.zeros(8, 128, dtype=torch.uint8), torch.zeros(1, 1)),
+    "reshard_experts_fp8": lambda d: R.reshard_experts_fp8(torch.zeros(2, 128), torch.zeros(2, 1, dtype=torch.int32), d(2, 1), None, None, None, None),
+    "reshard_permute": lambda d: R.reshard_permute(d(2, 8), _sort()),
+    "reshard_permute_backward": lambda d: R.reshard_permute_backward(d(4, 8), _sort(), 2),
+    "reshard_combine": lambda d: R.reshard_combine(d(4, 8), _sort(), torch.zeros(2, 2)),
+    "reshard_combine weights": lambda d: R.reshard_combine(torch.zeros(4, 8), _sort(), d(2, 2)),
+    "reshard_combine_backward": lambda d: R.reshard_combine_backward(torch.zeros(2, 8), d(4, 8), _sort(), torch.zeros(2, 2)),
+    "reshard_embedding": lambda d: R.reshard_embedding(torch.zeros(3, dtype=torch.int64), d(2, 8)),
+    "reshard_embedding_backward": lambda d: R.reshard_embedding_backward(d(3, 8), torch.zeros(3, dtype=torch.int64), 4),
+    "reshard_embedding_backward out": lambda d: R.reshard_embedding_backward(torch.zeros(3, 8), torch.zeros(3, dtype=torch.int64), 4, out=d(4, 8), accumulate=True),
+}
+
+
+@pytest.mark.parametrize("name", TANGENTS)
+@pytest.mark.parametrize("requires_grad", [False, True])
+def test_tangents_are_refused(name, requires_grad):
+    """Forward mode would read a result without a tangent as a constant; without a tangent, or outside the level, nothing is
+    refused for it."""
+    call = TANGENTS[name]
+
+    def dual(*shape):
+        return forward_ad.make_dual(torch.zeros(*shape, requires_grad=requires_grad), torch.ones(*shape))
+
+    with forward_ad.dual_level():
+        for grad in (True, False):
+            with torch.set_grad_enabled(grad), pytest.raises(R.ReshardError, match="forward mode") as e:
+                call(dual)
+            assert e.value.code == UNSUP
+        with pytest.raises(R.ReshardError, match="CUDA device"):
+            call(torch.zeros)
+    with pytest.raises(R.ReshardError, match="CUDA device"):
+        call(torch.zeros)
 
 
 # ------------------------------------------------------------------------------------------------ the oracle itself

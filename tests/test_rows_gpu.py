@@ -9,6 +9,7 @@ What is copied is compared bit for bit.
 """
 import pytest
 import torch
+from torch.autograd import forward_ad
 
 from oracle import rows as X
 
@@ -638,3 +639,24 @@ def test_rows_of_no_columns(T, wide_ids):
     y = R.reshard_combine(R.reshard_permute(x, sort), sort, w)
     y.sum().backward()
     assert y.shape == x.grad.shape == (T, 0) and w.grad.shape == (T, 1) and not bool(w.grad.any())
+
+
+# ------------------------------------------------------------------------------------------------------- derivatives
+
+def test_tangents_are_refused():
+    """A dual tensor that requires no gradient does not go past: its result would have no tangent."""
+    x, ids, sort = case(1, 6, 2, 4, 16, "f32")
+    y, w, table, tokens = randn(gen(1), 12, 16), torch.rand(6, 2, device="cuda"), randn(gen(2), 9, 16), torch.arange(5, device="cuda")
+    logits = randn(gen(3), 6, 8)
+    calls = [(logits, lambda t: R.reshard_route(t, 2)), (x, lambda t: R.reshard_permute(t, sort)), (y, lambda t: R.reshard_combine(t, sort, w)),
+             (w, lambda t: R.reshard_combine(y, sort, t)), (table, lambda t: R.reshard_embedding(tokens, t)), (x, lambda t: R.reshard_combine_backward(t, y, sort, w))]
+    for t, call in calls:
+        with forward_ad.dual_level():
+            want = call(t)
+            with pytest.raises(R.ReshardError, match="forward mode"):
+                call(forward_ad.make_dual(t, torch.ones_like(t)))
+            with pytest.raises(R.ReshardError, match="forward mode"):
+                call(forward_ad.make_dual(t.clone().requires_grad_(), torch.ones_like(t)))
+        got = call(t)
+        for a, b in zip(*((v if isinstance(v, tuple) else (v,)) for v in (got, want))):
+            assert torch.equal(a, b)
