@@ -15,8 +15,9 @@ A wait inside a product kernel that gives up (it does not on a working GPU) leav
 looks at: ``reshard_ops_status`` reads it.
 
 Gradients: ``reshard_route``'s weights carry the gradient to its logits (``reshard_route_backward``); ``reshard_permute``,
-``reshard_combine`` and ``reshard_embedding`` carry theirs, which are also calls of their own. ``reshard_linear_fp8`` and
-``reshard_experts_fp8`` have none: of an input that requires one, their result raises when a gradient is asked of it. Codes and
+``reshard_combine`` and ``reshard_embedding`` carry theirs, which are also calls of their own. ``reshard_linear_fp8``,
+``reshard_experts_fp8``, ``reshard_grad_norm`` and the gradients' own calls have none (that of ``reshard_permute`` is a
+``reshard_combine``): of an input that requires one, their result raises when a gradient is asked of it. Codes and
 scales (the quantizations, ``reshard_matmul_fp8`` over them) carry none. In forward mode (``torch.autograd.forward_ad``) there
 are no derivatives: an input with a tangent is refused.
 """
@@ -255,6 +256,7 @@ class _Undifferentiable(torch.autograd.Function):
         raise ReshardError(RESHARD_ERR_UNSUPPORTED, f"{ctx.name} has no gradient: call it under torch.no_grad(), or detach its inputs")
 
 
+
 def reshard_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, *, score="softmax",
                            renormalize: bool = True, scale: float = 1.0, out: Optional[torch.Tensor] = None,
                            stream=None) -> torch.Tensor:
@@ -276,6 +278,8 @@ def reshard_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor, ids
     out, to_step = _output(out, T, E, logits.dtype, logits)
     _call(1, _ROUTE_BACKWARD(at_grad, logits.data_ptr(), code, T, E, step, at_ids, k, _score(score), renormalize, scale,
                              out.data_ptr(), to_step, here))
+    if (grad_weights.requires_grad or logits.requires_grad) and torch.is_grad_enabled():
+        return _Undifferentiable.apply("reshard_route_backward", out, grad_weights, logits)
     return out
 
 
@@ -521,10 +525,9 @@ def reshard_permute(x: torch.Tensor, sort: Sort, *, out: Optional[torch.Tensor] 
 
 
 def reshard_permute_backward(grad: torch.Tensor, sort: Sort, k: int, *, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-    """The gradient to ``x`` of ``reshard_permute``: each token's sum over its k places, in ``grad``'s type."""
-    if _forward._current_level >= 0:
-        _no_tangent("reshard_permute_backward", grad)
-    return reshard_combine(grad.detach(), sort, k=k, out=out, stream=stream)
+    """The gradient to ``x`` of ``reshard_permute``: each token's sum over its k places, in ``grad``'s type; differentiable in
+    ``grad``, as ``reshard_combine`` is."""
+    return reshard_combine(grad, sort, k=k, out=out, stream=stream)
 
 
 class _Permute(torch.autograd.Function):
@@ -595,6 +598,8 @@ def reshard_combine_backward(grad: torch.Tensor, y: torch.Tensor, sort: Sort, we
     _call(10, _COMBINE_BACKWARD(grad.data_ptr(), _code(grad, "grad"), grad_step, y.data_ptr(), _code(y, "y"), rows, H, step, at_order, at_position,
                                 at_weights, T, k, 0 if grad_y is None else grad_y.data_ptr(), H,
                                 0 if grad_weights is None else grad_weights.data_ptr(), here))
+    if (grad.requires_grad or y.requires_grad or (weights is not None and weights.requires_grad)) and torch.is_grad_enabled():
+        grad_y, grad_weights = (t if t is None else _Undifferentiable.apply("reshard_combine_backward", t, grad, y, weights) for t in (grad_y, grad_weights))
     return grad_y, grad_weights
 
 
@@ -680,6 +685,8 @@ def reshard_embedding_backward(grad: torch.Tensor, ids: torch.Tensor, rows: int,
     space = torch.empty(need, dtype=torch.uint8, device=grad.device) if need else None
     _call(12, _EMBEDDING_BACKWARD(grad.data_ptr(), _code(grad, "grad"), T, H, step, ids.data_ptr(), bits, first_row, rows, scale, out.data_ptr(),
                                   _code(out, "out"), to_step, accumulate, space.data_ptr() if need else 0, need, here))
+    if grad.requires_grad and torch.is_grad_enabled():
+        return _Undifferentiable.apply("reshard_embedding_backward", out, grad)
     return out
 
 
@@ -720,7 +727,7 @@ class TensorList:
     def __init__(self, tensors: Iterable[torch.Tensor]):
         self._handle = None
         self.tensors = tensors = list(tensors)
-        at, sizes, types, self._order, self._memory = [], [], [], {}, []
+        at, sizes, types, self._order, self._memory, self._wanting = [], [], [], {}, [], []
         self.device = device = tensors[0].device if tensors else torch.device("cuda", torch.cuda.current_device())
         if device.type != "cuda":
             _bad(f"tensors must be on a CUDA device, not on {device}")
@@ -735,6 +742,8 @@ class TensorList:
                 self._order[i] = (t.shape, t.stride())
             at.append(t.data_ptr())
             self._memory.append(t.untyped_storage())      # what the addresses are of, whatever the tensor is given later
+            if t.requires_grad:
+                self._wanting.append(t)
             sizes.append(t.numel())
             types.append(_code(t, "a tensor"))
         n, handle = len(tensors), ctypes.c_void_p()
@@ -768,7 +777,8 @@ Tensors = Union[TensorList, Iterable[torch.Tensor]]
 def reshard_grad_norm(tensors: Tensors, *, stream=None) -> torch.Tensor:
     """The norm sqrt(sum x^2) over all elements of ``tensors`` (a ``TensorList`` or tensors), a float32 scalar on their device.
 
-    Other ranks' shards: the root of the sum of their norms' squares is the whole norm."""
+    Other ranks' shards: the root of the sum of their norms' squares is the whole norm. It has no gradient: of tensors that
+    require one (when their list is made) the result raises when it is asked for, outside ``torch.no_grad()``."""
     if not isinstance(tensors, TensorList):
         tensors = TensorList(tensors)
     if _forward._current_level >= 0:
@@ -780,6 +790,8 @@ def reshard_grad_norm(tensors: Tensors, *, stream=None) -> torch.Tensor:
     norm = torch.empty((), dtype=torch.float32, device=tensors.device)
     space = torch.empty(_norm_space, dtype=torch.uint8, device=tensors.device)
     _call(13, _GRAD_NORM(tensors._handle, norm.data_ptr(), space.data_ptr(), _norm_space, here))
+    if tensors._wanting and torch.is_grad_enabled():
+        return _Undifferentiable.apply("reshard_grad_norm", norm, *tensors._wanting)
     return norm
 
 
@@ -789,7 +801,7 @@ def reshard_clip_grads(tensors: Tensors, limit: float, *, norm: Optional[torch.T
 
     ``norm``: a float32 scalar on the device (the norm over all ranks), or None: ``reshard_grad_norm`` of the tensors. Nothing is
     read back: a step with a NaN norm makes every value NaN, one with an infinite norm 0 (see include/reshard_ops.h). As with
-    any write through a pointer, autograd is not told."""
+    any write through a pointer, autograd is not told: neither what is written nor the norm carries a gradient."""
     if not isinstance(tensors, TensorList):
         tensors = TensorList(tensors)
     if _forward._current_level >= 0:

@@ -325,3 +325,17 @@ def test_tangents_are_refused():
                 call()
         assert float(R.reshard_grad_norm(a)) == math.sqrt(11.0) or abs(float(R.reshard_grad_norm(a)) - math.sqrt(11.0)) <= 7 * U * 4
     assert all(bool((t == 1.0).all()) for t in ts)
+
+
+def test_a_norm_has_no_gradient_and_says_so():
+    ts = [torch.ones(n, device="cuda", requires_grad=i != 1) for i, n in enumerate((8, 3, 5))]
+    for of in (ts, R.reshard_tensor_list(ts)):
+        norm = R.reshard_grad_norm(of)
+        assert float(norm.detach()) == 4.0
+        for t in (ts[0], ts[2]):
+            with pytest.raises(R.ReshardError, match="reshard_grad_norm has no gradient"):
+                torch.autograd.grad(norm * 2.0 + t.sum(), t)
+        with torch.no_grad():
+            assert not R.reshard_grad_norm(of).requires_grad
+    assert not R.reshard_grad_norm([t.detach() for t in ts]).requires_grad
+    assert not R.reshard_clip_grads([t.detach() for t in ts], 1.0).requires_grad

@@ -660,3 +660,44 @@ def test_tangents_are_refused():
         got = call(t)
         for a, b in zip(*((v if isinstance(v, tuple) else (v,)) for v in (got, want))):
             assert torch.equal(a, b)
+
+
+def test_results_that_have_no_gradient_raise_when_it_is_asked_for():
+    """The gradients' own calls: nothing is lost without a word, and under no_grad, or of inputs that require none, they are plain."""
+    x, ids, sort = case(1, 6, 2, 4, 16, "f32")
+    logits, dw = randn(gen(3), 6, 8), randn(gen(4), 6, 2)
+    y, w, tokens = randn(gen(1), 12, 16), torch.rand(6, 2, device="cuda"), torch.arange(5, device="cuda") % 3
+    routed = R.reshard_route(logits, 2)[1]
+    calls = [([dw, logits], lambda a, b: R.reshard_route_backward(a, b, routed)),
+             ([x, y, w], lambda a, b, c: R.reshard_combine_backward(a, b, sort, c)),
+             ([randn(gen(5), 5, 16)], lambda a: R.reshard_embedding_backward(a, tokens, 4)),
+             ([randn(gen(6), 5, 1, 16).transpose(0, 1)], lambda a: R.reshard_embedding_backward(a, tokens.view(1, 5), 4))]
+    for inputs, call in calls:
+        want = call(*inputs)
+        want = want if isinstance(want, tuple) else (want,)
+        assert not any(t.requires_grad for t in want)
+        for i in range(len(inputs)):
+            leaf = inputs[i].clone().requires_grad_()
+            these = [*inputs[:i], leaf, *inputs[i + 1:]]
+            with torch.no_grad():
+                got = call(*these)
+            assert not any(t.requires_grad for t in (got if isinstance(got, tuple) else (got,)))
+            got = call(*these)
+            for a, b in zip(got if isinstance(got, tuple) else (got,), want):
+                assert torch.equal(a, b)
+                with pytest.raises(R.ReshardError, match="has no gradient"):
+                    torch.autograd.grad(a.sum(), leaf)
+
+
+def test_the_permutations_gradient_is_differentiable():
+    """It is linear in what comes in: its own gradient takes each token's row to its places."""
+    x, ids, sort = case(1, 6, 2, 4, 16, "f32", 1, 2)
+    dy = randn(gen(1), 12, 16).requires_grad_()
+    pull = randn(gen(2), 6, 16)
+    R.reshard_permute_backward(dy, sort, 2).backward(pull)
+    assert torch.equal(dy.grad, R.reshard_permute(pull, sort))
+    with pytest.raises(R.ReshardError, match="cannot be written to out"):
+        R.reshard_permute_backward(dy, sort, 2, out=torch.empty(6, 16, device="cuda"))
+    with torch.no_grad():
+        to = torch.empty(6, 16, device="cuda")
+        assert R.reshard_permute_backward(dy, sort, 2, out=to) is to
