@@ -548,7 +548,8 @@ def reshard_combine(y: torch.Tensor, sort: Sort, weights: Optional[torch.Tensor]
     """out[t] = sum_j weights[t, j] * y[position[t * k + j]]: experts' rows back to their tokens.
 
     ``weights`` [tokens, k] float32 (``reshard_route``), or None with ``k`` given: plain sums. Slots without a place add nothing.
-    The sum is fp32 and rounded once, to ``out_dtype`` (y's type if None). Differentiable in ``y`` and ``weights``."""
+    ``y`` may have more rows than the sort has places (a padded buffer): those belong to no slot and their gradient is 0. The sum
+    is fp32 and rounded once, to ``out_dtype`` (y's type if None). Differentiable in ``y`` and ``weights``."""
     if _forward._current_level >= 0:
         _no_tangent("reshard_combine", y, weights)
     here = _here(y, stream)
@@ -577,10 +578,22 @@ def reshard_combine_backward(grad: torch.Tensor, y: torch.Tensor, sort: Sort, we
     are wanted (the other is None). Without ``weights`` there is no gradient to them."""
     if _forward._current_level >= 0:
         _no_tangent("reshard_combine_backward", grad, y, weights)
+    rows, places = _matrix(y, "y")[0], sort[1].numel()
+    if places < rows:
+        _bad(f"y has {rows} rows, the sort {places} places")
+    grad_y, grad_weights = _combine_gradients(grad, y, sort, weights, k, needs, stream)
+    if (grad.requires_grad or y.requires_grad or (weights is not None and weights.requires_grad)) and torch.is_grad_enabled():
+        grad_y, grad_weights = (t if t is None else _Undifferentiable.apply("reshard_combine_backward", t, grad, y, weights) for t in (grad_y, grad_weights))
+    return grad_y, grad_weights
+
+
+def _combine_gradients(grad: torch.Tensor, y: torch.Tensor, sort: Sort, weights: Optional[torch.Tensor], k: Optional[int],
+                       needs: Tuple[bool, bool], stream=None) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """(grad_y, grad_weights), the one that is not needed None. Rows of y behind the sort's places are no slot's."""
     here = _here(grad, stream)
     if here is None:
         with _on(grad, stream):
-            return reshard_combine_backward(grad, y, sort, weights, k=k, needs=needs)
+            return _combine_gradients(grad, y, sort, weights, k, needs)
     grad = _rows(grad)
     T, k = _tokens(sort, weights, k)
     G, H, grad_step = _matrix(grad, "grad")
@@ -590,16 +603,16 @@ def reshard_combine_backward(grad: torch.Tensor, y: torch.Tensor, sort: Sort, we
     if y.get_device() != grad.get_device():
         _bad(f"y is on {y.device}, not on {grad.device}")
     at_order, places, at_position, _ = _sorted(sort, grad)
-    if places < rows:
-        _bad(f"y has {rows} rows, the sort {places} places")
     at_weights = 0 if weights is None else _dense(weights, "weights", torch.float32, (T, k), grad)
     grad_y = torch.empty((rows, H), dtype=y.dtype, device=y.device) if needs[0] else None
+    if rows > places:
+        if needs[0]:
+            grad_y[places:].zero_()
+        rows = places
     grad_weights = torch.empty((T, k), dtype=torch.float32, device=y.device) if needs[1] and weights is not None else None
     _call(10, _COMBINE_BACKWARD(grad.data_ptr(), _code(grad, "grad"), grad_step, y.data_ptr(), _code(y, "y"), rows, H, step, at_order, at_position,
                                 at_weights, T, k, 0 if grad_y is None else grad_y.data_ptr(), H,
                                 0 if grad_weights is None else grad_weights.data_ptr(), here))
-    if (grad.requires_grad or y.requires_grad or (weights is not None and weights.requires_grad)) and torch.is_grad_enabled():
-        grad_y, grad_weights = (t if t is None else _Undifferentiable.apply("reshard_combine_backward", t, grad, y, weights) for t in (grad_y, grad_weights))
     return grad_y, grad_weights
 
 
@@ -614,7 +627,7 @@ class _Combine(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         y, weights, *sort = ctx.saved_tensors
-        grad_y, grad_weights = reshard_combine_backward(grad, y, tuple(sort), weights, k=ctx.k, needs=ctx.needs_input_grad[:2])
+        grad_y, grad_weights = _combine_gradients(grad, y, tuple(sort), weights, ctx.k, ctx.needs_input_grad[:2])
         return (grad_y, grad_weights, *[None] * 5)
 
 

@@ -701,3 +701,31 @@ def test_the_permutations_gradient_is_differentiable():
     with torch.no_grad():
         to = torch.empty(6, 16, device="cuda")
         assert R.reshard_permute_backward(dy, sort, 2, out=to) is to
+
+
+@pytest.mark.parametrize("H", [64, 67])
+@pytest.mark.parametrize("more", [0, 1, 40])
+@pytest.mark.parametrize("share", [False, True])
+def test_autograd_of_padded_rows(H, more, share):
+    """Experts' rows in a buffer that is longer than the sort: their weighted sum and its gradients are those of the places, rows
+    behind them have gradient 0."""
+    T, k = 9, 2
+    g = gen(H + more)
+    first, local = (1, 2) if share else (0, 4)
+    _, ids, sort = case(5, T, k, 4, 1, "f32", first, local)
+    y = randn(g, T * k + more, H)
+    y[int(sort[0][-1]):] = float("nan")
+    pull, w = randn(g, T, H), torch.softmax(randn(g, T, k), 1)
+    for needs in ((True, True), (True, False), (False, True)):
+        leaf, weights = y.clone().requires_grad_(needs[0]), w.clone().requires_grad_(needs[1])
+        out = R.reshard_combine(leaf, sort, weights)
+        assert torch.equal(out, R.reshard_combine(y[:T * k].contiguous(), sort, w))
+        out.backward(pull)
+        dy, dw = R.reshard_combine_backward(pull, y[:T * k], sort, w)
+        if needs[0]:
+            assert leaf.grad.shape == y.shape and torch.equal(leaf.grad[:T * k], dy) and not bool(leaf.grad[T * k:].any())
+        if needs[1]:
+            assert torch.equal(weights.grad, dw)
+    leaf = y.clone().requires_grad_()
+    R.reshard_combine(leaf, sort, k=k).backward(pull)
+    assert torch.equal(leaf.grad[:T * k], R.reshard_combine_backward(pull, y[:T * k], sort, k=k)[0]) and not bool(leaf.grad[T * k:].any())
