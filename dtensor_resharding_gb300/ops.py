@@ -581,36 +581,43 @@ def reshard_combine_backward(grad: torch.Tensor, y: torch.Tensor, sort: Sort, we
     rows, places = _matrix(y, "y")[0], sort[1].numel()
     if places < rows:
         _bad(f"y has {rows} rows, the sort {places} places")
-    grad_y, grad_weights = _combine_gradients(grad, y, sort, weights, k, needs, stream)
+    grad_y, grad_weights = _combine_gradients(grad, y, (y.shape, y.dtype), sort, weights, k, needs, stream)
     if (grad.requires_grad or y.requires_grad or (weights is not None and weights.requires_grad)) and torch.is_grad_enabled():
         grad_y, grad_weights = (t if t is None else _Undifferentiable.apply("reshard_combine_backward", t, grad, y, weights) for t in (grad_y, grad_weights))
     return grad_y, grad_weights
 
 
-def _combine_gradients(grad: torch.Tensor, y: torch.Tensor, sort: Sort, weights: Optional[torch.Tensor], k: Optional[int],
-                       needs: Tuple[bool, bool], stream=None) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
-    """(grad_y, grad_weights), the one that is not needed None. Rows of y behind the sort's places are no slot's."""
+def _combine_gradients(grad: torch.Tensor, y: Optional[torch.Tensor], like: Tuple[torch.Size, torch.dtype], sort: Sort, weights: Optional[torch.Tensor],
+                       k: Optional[int], needs: Tuple[bool, bool], stream=None) -> Tuple[Optional[torch.Tensor], Optional[torch.Tensor]]:
+    """(grad_y, grad_weights), the one that is not needed None. Rows of y behind the sort's places are no slot's. `like`: y's shape
+    and type; y itself is read for grad_weights only."""
     here = _here(grad, stream)
     if here is None:
         with _on(grad, stream):
-            return _combine_gradients(grad, y, sort, weights, k, needs)
+            return _combine_gradients(grad, y, like, sort, weights, k, needs)
     grad = _rows(grad)
     T, k = _tokens(sort, weights, k)
     G, H, grad_step = _matrix(grad, "grad")
-    rows, cols, step = _matrix(y, "y")
+    (rows, cols), dtype = like
     if (G, H) != (T, cols):
-        _bad(f"grad {tuple(grad.shape)} does not fit {T} tokens and y {tuple(y.shape)}")
-    if y.get_device() != grad.get_device():
-        _bad(f"y is on {y.device}, not on {grad.device}")
+        _bad(f"grad {tuple(grad.shape)} does not fit {T} tokens and y {(rows, cols)}")
+    at_y, step = 0, cols
+    if y is not None:
+        at_y, step = y.data_ptr(), _matrix(y, "y")[2]
+        if y.get_device() != grad.get_device():
+            _bad(f"y is on {y.device}, not on {grad.device}")
+    code = _CODES.get(dtype)
+    if code is None:
+        _bad(f"y must be bfloat16, float16 or float32, not {dtype}")
     at_order, places, at_position, _ = _sorted(sort, grad)
     at_weights = 0 if weights is None else _dense(weights, "weights", torch.float32, (T, k), grad)
-    grad_y = torch.empty((rows, H), dtype=y.dtype, device=y.device) if needs[0] else None
+    grad_y = torch.empty((rows, H), dtype=dtype, device=grad.device) if needs[0] else None
     if rows > places:
         if needs[0]:
             grad_y[places:].zero_()
         rows = places
-    grad_weights = torch.empty((T, k), dtype=torch.float32, device=y.device) if needs[1] and weights is not None else None
-    _call(10, _COMBINE_BACKWARD(grad.data_ptr(), _code(grad, "grad"), grad_step, y.data_ptr(), _code(y, "y"), rows, H, step, at_order, at_position,
+    grad_weights = torch.empty((T, k), dtype=torch.float32, device=grad.device) if needs[1] and weights is not None else None
+    _call(10, _COMBINE_BACKWARD(grad.data_ptr(), _code(grad, "grad"), grad_step, at_y, code, rows, H, step, at_order, at_position,
                                 at_weights, T, k, 0 if grad_y is None else grad_y.data_ptr(), H,
                                 0 if grad_weights is None else grad_weights.data_ptr(), here))
     return grad_y, grad_weights
@@ -619,15 +626,17 @@ def _combine_gradients(grad: torch.Tensor, y: torch.Tensor, sort: Sort, weights:
 class _Combine(torch.autograd.Function):
     @staticmethod
     def forward(ctx, y, weights, k, out_dtype, *sort):
-        ctx.save_for_backward(y, weights, *sort)
-        ctx.k = k
+        # y is kept only for a gradient that reads it: tokens * k rows
+        keep = y if weights is not None and ctx.needs_input_grad[1] else None
+        ctx.save_for_backward(keep, weights, *sort)
+        ctx.k, ctx.like = k, (y.shape, y.dtype)
         return reshard_combine(y.detach(), sort, None if weights is None else weights.detach(), k=k, out_dtype=out_dtype)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         y, weights, *sort = ctx.saved_tensors
-        grad_y, grad_weights = _combine_gradients(grad, y, tuple(sort), weights, ctx.k, ctx.needs_input_grad[:2])
+        grad_y, grad_weights = _combine_gradients(grad, y, ctx.like, tuple(sort), weights, ctx.k, ctx.needs_input_grad[:2])
         return (grad_y, grad_weights, *[None] * 5)
 
 

@@ -729,3 +729,29 @@ def test_autograd_of_padded_rows(H, more, share):
     leaf = y.clone().requires_grad_()
     R.reshard_combine(leaf, sort, k=k).backward(pull)
     assert torch.equal(leaf.grad[:T * k], R.reshard_combine_backward(pull, y[:T * k], sort, k=k)[0]) and not bool(leaf.grad[T * k:].any())
+
+
+def test_the_weighted_sum_keeps_its_rows_only_for_the_weights():
+    """The gradient to y does not read y: it may be written anew before the backward pass, and its memory is not held."""
+    T, k, H = 64, 2, 4096
+    _, ids, sort = case(5, T, k, 8, 1, "f32")
+    w, pull = torch.softmax(randn(gen(1), T, k), 1), randn(gen(2), T, H)
+    for weights in (w, None):
+        source = randn(gen(3), T * k, H).requires_grad_()
+        y = source * 2.0
+        out = R.reshard_combine(y, sort, weights, k=k)
+        with torch.no_grad():
+            y.zero_()
+        out.backward(pull)
+        want = R.reshard_combine_backward(pull, y.detach(), sort, weights, k=k)[0]
+        assert torch.equal(source.grad, 2.0 * want)
+    source = randn(gen(3), T * k, H).requires_grad_()
+    before = torch.cuda.memory_allocated()
+    out = R.reshard_combine(source * 2.0, sort, w)
+    assert torch.cuda.memory_allocated() - before < T * k * H * 4
+    # of a weight that has a gradient y is kept, and a change of it is seen
+    y, weights = source.detach().clone(), w.clone().requires_grad_()
+    out = R.reshard_combine(y, sort, weights)
+    y.zero_()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.backward(pull)
