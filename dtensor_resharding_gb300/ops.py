@@ -7,7 +7,7 @@ scales (``reshard_plan_blockwise_fp8``), or with BF16 weights that ``reshard_qua
 these calls compute with them.
 
 Argument marshalling only, as in ``binding``: the checks on values are the library's, which lists every violation.
-Outputs are allocated unless given (``out``). Work is enqueued on ``stream`` (a cudaStream_t as int, or a
+Outputs are allocated unless given (``out``, written in place as far as autograd knows). Work is enqueued on ``stream`` (a cudaStream_t as int, or a
 ``torch.cuda.Stream``; the current stream if None) and is asynchronous. What a call allocates belongs to that stream; an
 input made on another stream must be ready there (an event), as for any torch operation.
 
@@ -30,6 +30,7 @@ from typing import Iterable, Optional, Tuple, Union
 
 import torch
 from torch.autograd import forward_ad as _forward
+from torch.autograd.graph import increment_version as _written
 
 from .binding import LIB, ReshardError, RESHARD_ERR_INVALID_ARG, RESHARD_ERR_UNSUPPORTED, _check, reshard_last_error
 
@@ -139,7 +140,9 @@ def _output(out: Optional[torch.Tensor], rows: int, cols: int, dtype: torch.dtyp
         return torch.empty((rows, cols), dtype=dtype, device=like.device), cols
     if out.dtype is not dtype or out.shape != (rows, cols) or out.get_device() != like.get_device():
         _bad(f"out must be {dtype} of shape {(rows, cols)} on {like.device}, not {out.dtype} of shape {tuple(out.shape)} on {out.device}")
-    return out, _matrix(out, "out")[2]
+    step = _matrix(out, "out")[2]
+    _written(out)      # a backward pass that kept what was there is told, as by torch's own operations
+    return out, step
 
 
 # Workspace sizes by sizes: asking the library each time costs a call.

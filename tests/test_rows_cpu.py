@@ -186,6 +186,30 @@ def test_words_of_the_embedding_calls(words):
     assert w[15] == L.reshard_embedding_backward_workspace(6, 16) and w[16] == 0
 
 
+def test_a_given_output_counts_as_written(words):
+    """Autograd keeps tensors by their version: a buffer that a call writes has another one afterwards, through any of its views."""
+    x, sort = torch.zeros(2, 8), _sort()
+    logits, ids2, tokens = torch.zeros(2, 4), torch.zeros(2, 2, dtype=torch.int32), torch.zeros(3, dtype=torch.int64)
+    w8, s8 = torch.zeros(8, 128, dtype=torch.uint8), torch.zeros(1, 1)
+    calls = [(torch.zeros(4, 8), lambda o: R.reshard_permute(x, sort, out=o)), (torch.zeros(2, 8), lambda o: R.reshard_combine(torch.zeros(4, 8), sort, k=2, out=o)),
+             (torch.zeros(2, 8), lambda o: R.reshard_permute_backward(torch.zeros(4, 8), sort, 2, out=o)), (torch.zeros(3, 8), lambda o: R.reshard_embedding(tokens, x, out=o)),
+             (torch.zeros(1, 3, 8), lambda o: R.reshard_embedding(tokens.view(1, 3), x, out=o)), (torch.zeros(2, 8), lambda o: R.reshard_embedding_backward(torch.zeros(3, 8), tokens, 2, out=o)),
+             (torch.zeros(2, 8), lambda o: R.reshard_embedding_backward(torch.zeros(3, 8), tokens, 2, out=o, accumulate=True)),
+             (torch.zeros(2, 4), lambda o: R.reshard_route_backward(torch.zeros(2, 2), logits, ids2, out=o)), (torch.zeros(2, 8), lambda o: R.reshard_linear_fp8(torch.zeros(2, 128), w8, s8, out=o)),
+             (torch.zeros(2, 8), lambda o: R.reshard_matmul_fp8(torch.zeros(2, 128, dtype=torch.uint8), torch.zeros(2, 1), w8, s8, out=o))]
+    for i, (out, call) in enumerate(calls):
+        base = torch.zeros(4, *out.shape)
+        for to in (out, base[2]):
+            leaf = torch.ones(out.shape, requires_grad=True)
+            product = leaf * to                       # keeps `to`
+            version = to._version
+            assert call(to) is to and to._version > version and len(words) > 0, i
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                product.sum().backward()
+        with torch.inference_mode():
+            assert call(torch.zeros(out.shape)).is_inference()
+
+
 def test_dense_in_any_order():
     x = torch.zeros(4, 6, 5)
     for t in (x, x.permute(2, 0, 1), x.transpose(0, 1), x[:1], x[:, :, :1].contiguous(), torch.zeros(()), torch.zeros(0)):
