@@ -197,10 +197,10 @@ __global__ void __launch_bounds__(kRowThreads) reshard_embedding_kernel(Lookup a
 // ---------------------------------------------------------------------------------------------------------- combine --
 
 // A warp a span of a token's columns. Lanes look up the places of up to 32 slots at once; those that have one are taken in
-// order, kSlots rows in flight together. Bound by the read of y: 8 places a token, 8,192 x 2048 fp32, 84 us, 6.8 TB/s; where few
+// order, kSlots rows in flight together. Bound by the read of y: 8 places a token, 8,192 x 2048 bf16, 50 us, 6.0 TB/s; where few
 // slots have a place by the chain places, rows, output of each span, so that warps stay and look up the next span's places
-// before this one's rows (16,383 tokens with one place of eight on average, 4096 fp32: 70 us; a warp a span: 78). Rows that start
-// anywhere are bound by instructions (8,191 x 2867 fp16, four places each: 48 us, of 2872 columns 43; with two words read by
+// before this one's rows (16,383 tokens with one place of eight on average, 4096 bf16: 54 us; fp32 72, a warp a span: 86). Rows that start
+// anywhere are bound by instructions (8,191 x 2867 fp16, four places each: 48 us, of 2872 columns 42; with two words read by
 // each lane, without its neighbour's: 59).
 template <typename TY, typename TO>
 struct CombineShape {
@@ -296,6 +296,40 @@ __global__ void __launch_bounds__(kRowThreads, CombineShape<TY, TO>::kCtas) resh
       }
     }
   } while (Wide && (unit += step) < units);
+}
+
+// fp32 rows of whole pieces, a few places a token: a thread eight columns, without anything shared in a warp, so that more of them
+// are in flight. 4,095 x 4096 to bf16, one of eight places here, 20.9 us where warps that stay take 21.9 (after the experts' products 33.6
+// and 35.9), 1,000 x 4096 with eight places 23.6 and 26.0; with 12 of them it depends (6,000 x 1000 47.9 and 50.2, 1,000 x 1000 12.7 and
+// 11.9), of many tokens' share with 32 it loses (26.1 and 23.0), and 16-bit rows are 5 to 25% slower so.
+constexpr int kThreadPlaces = 8;
+template <typename TO>
+__global__ void __launch_bounds__(kRowThreads) reshard_combine_f32_kernel(Combine a, int chunks) {
+  grid_enter();
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= a.tokens * chunks) return;
+  const int64_t t = a.tokens * chunks <= 0xffffffffll ? (uint32_t)i / (uint32_t)chunks : i / chunks;
+  const int64_t c = (i - t * chunks) * 8;
+  const int left = (int)min((int64_t)8, a.cols - c);
+  float sum[8] = {};
+#pragma unroll 4
+  for (int j = 0; j < a.k; ++j) {
+    const int p = a.position[t * a.k + j];
+    if (p < 0 || p >= a.rows) continue;
+    const float w = a.weights ? a.weights[t * a.k + j] : 1.0f;
+    float x[8];
+    load_values<float, 8>(static_cast<const float *>(a.y) + (int64_t)p * a.y_stride + c, left, true, x);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) sum[u] = fmaf(w, x[u], sum[u]);
+  }
+  TO *const to = static_cast<TO *>(a.out) + t * a.out_stride + c;
+  if (left == 8) {
+    store_piece(to, sum);
+  } else {
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (u < left) to[u] = from_f32<TO>(sum[u]);
+  }
 }
 
 // ------------------------------------------------------------------------------------------------- combine backward --
@@ -507,6 +541,13 @@ int enqueue_combine(const Combine &a, cudaStream_t stream) {
   int sms = 0;
   if (const int rc = device_sms(&sms)) return rc;
   const bool wide = aligned16(a.y, a.y_stride, element_bytes(a.dtype)) && aligned16(a.out, a.out_stride, element_bytes(a.out_dtype));
+  if (wide && a.dtype == RESHARD_F32 && a.k <= kThreadPlaces) {
+    const int chunks = (int)ceil_div(a.cols, 8);
+    const int block = a.tokens * chunks <= 32768 ? kFewThreads : kRowThreads;      // a few tokens' columns spread over the SMs
+    return launched(by_type(a.out_dtype, [&](auto o) {
+      return launch(reshard_combine_f32_kernel<decltype(o)>, dim3((unsigned)ceil_div(a.tokens * chunks, block)), block, 0, 1, stream, a, chunks);
+    }), "launching reshard_combine_f32_kernel");
+  }
   return launched(by_type(a.dtype, [&](auto y) {
     using TY = decltype(y);
     return by_type(a.out_dtype, [&](auto o) {

@@ -755,3 +755,30 @@ def test_the_weighted_sum_keeps_its_rows_only_for_the_weights():
     y.zero_()
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         out.backward(pull)
+
+
+# ------------------------------------------------------------------------------------------ one sum, several kernels
+
+@pytest.mark.parametrize("T,k,E,H", [(1, 1, 4, 8), (3, 8, 16, 4), (5, 8, 8, 1003), (130, 8, 64, 520), (900, 8, 32, 2048), (40, 9, 16, 72), (700, 3, 8, 4100)])
+@pytest.mark.parametrize("to", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("share", [False, True])
+def test_the_sum_is_the_same_however_its_rows_lie(T, k, E, H, to, share):
+    """Rows of whole pieces, few places or many, rows that start anywhere: fp32 terms added in the order of the choices."""
+    g = gen(T + H)
+    first, local = (E // 4, max(1, E // 2)) if share else (0, E)
+    _, ids, sort = case(T + k, T, k, E, 1, "f32", first, local)
+    y, w = randn(g, T * k, H), torch.softmax(randn(g, T, k), 1)
+    position = sort[2].view(T, k)
+    for weights in (w, None):
+        want = torch.zeros(T, H, device="cuda", dtype=F64)
+        for j in range(k):                            # a product of 24-bit numbers is exact in 64 bits, and so each sum rounds once but for 2^-53
+            here = (position[:, j] >= 0)[:, None]
+            term = y[position[:, j].clamp_min(0).long()].to(F64) * (w[:, j:j + 1] if weights is not None else 1.0)
+            want = torch.where(here, (want + term).float().to(F64), want)
+        close(R.reshard_combine(y, sort, weights, k=k, out_dtype=DT[to]), want, 2 * U * X.combine(y, position.reshape(-1), weights, k, True))
+        outs = [R.reshard_combine(laid(y, how), sort, weights, k=k, out=laid(torch.zeros(T, H, device="cuda", dtype=DT[to]), how)) for how in ("dense", "pitch", "odd")]
+        assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+        many = torch.cat([w, torch.zeros(T, 9 - k, device="cuda")], 1) if k < 9 else w      # the same sum with nine choices
+        padded = torch.cat([position, torch.full((T, max(0, 9 - k)), -1, dtype=torch.int32, device="cuda")], 1).contiguous().view(-1)
+        if weights is not None:
+            assert torch.equal(outs[0], R.reshard_combine(y, (sort[0], sort[1], padded), many.contiguous(), out_dtype=DT[to]))
