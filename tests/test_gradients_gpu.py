@@ -339,3 +339,20 @@ def test_a_norm_has_no_gradient_and_says_so():
             assert not R.reshard_grad_norm(of).requires_grad
     assert not R.reshard_grad_norm([t.detach() for t in ts]).requires_grad
     assert not R.reshard_clip_grads([t.detach() for t in ts], 1.0).requires_grad
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+def test_an_infinite_limit_leaves_every_bit(bad, kind):
+    """Whatever the norm is, NaN among it: in place nothing is written, other tensors get the values as they are."""
+    ts = tensors(5, [40, 9000], [kind])
+    ts[1][8001] = bad
+    bits = {4: torch.int32, 2: torch.int16}[ts[0].element_size()]
+    keep = [t.clone() for t in ts]
+    out = [torch.empty_like(t) for t in ts]
+    R.reshard_clip_grads(ts, math.inf)
+    R.reshard_clip_grads(ts, math.inf, out=out)
+    for t, o, k in zip(ts, out, keep):
+        assert torch.equal(t.view(bits), k.view(bits))
+        finite = torch.isfinite(k)
+        assert torch.equal(o[finite], k[finite]) and torch.equal(torch.isnan(o), torch.isnan(k)) and torch.equal(torch.isinf(o), torch.isinf(k))

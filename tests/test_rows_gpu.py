@@ -782,3 +782,60 @@ def test_the_sum_is_the_same_however_its_rows_lie(T, k, E, H, to, share):
         padded = torch.cat([position, torch.full((T, max(0, 9 - k)), -1, dtype=torch.int32, device="cuda")], 1).contiguous().view(-1)
         if weights is not None:
             assert torch.equal(outs[0], R.reshard_combine(y, (sort[0], sort[1], padded), many.contiguous(), out_dtype=DT[to]))
+
+
+# -------------------------------------------------------------------------------------------- the other pairs of types
+
+@pytest.mark.parametrize("T,k,E,H", [(5, 2, 4, 7), (64, 4, 8, 1000), (33, 8, 8, 2867), (9, 12, 40, 8200)])
+@pytest.mark.parametrize("types", [("bf16", "f16"), ("f16", "bf16"), ("f16", "f32")])
+@pytest.mark.parametrize("how", ["dense", "odd"])
+def test_combine_and_its_gradients_of_other_types(T, k, E, H, types, how):
+    g = gen(T * H + k)
+    _, ids, sort = case(T + k, T, k, E, 1, "f32", E // 4, max(1, E // 2))
+    offsets, order, position = sort
+    held = int(offsets[-1])
+    y, grad = laid(randn(g, T * k, H).to(DT[types[0]]), how), laid(randn(g, T, H).to(DT[types[1]]), how)
+    w = torch.softmax(randn(g, T, k), 1)
+    out = R.reshard_combine(y, sort, w, out_dtype=DT[types[1]])
+    assert out.dtype is DT[types[1]]
+    close(out, X.combine(y, position, w, k), k * U * X.combine(y, position, w, k, True))
+    dy, dw = R.reshard_combine_backward(grad, y, sort, w)
+    want_y, want_w = X.combine_backward(grad, y, position, w, k)
+    assert dy.dtype is DT[types[0]] and not bool(dy[held:].any())
+    close(dy, want_y, U * want_y.abs())
+    close(dw, want_w, (H / 32 + 32) * U * X.combine_backward(grad, y, position, w, k, True)[1])
+
+
+@pytest.mark.parametrize("T,rows,H", [(40, 30, 520), (200, 7, 33), (256, 9, 2867), (300, 40, 520), (3000, 50, 2867), (5000, 3000, 72)])
+@pytest.mark.parametrize("types", [("f32", "bf16"), ("f32", "f16"), ("f16", "f32"), ("bf16", "f16"), ("f16", "bf16")])
+@pytest.mark.parametrize("how", ["dense", "odd"])
+def test_embedding_backward_of_other_types(T, rows, H, types, how):
+    """Whole and accumulated, few tokens and many, the table's rows on 16 bytes or not."""
+    g = gen(T + H)
+    ids = torch.randint(0, 2 * rows, (T,), generator=g, device="cuda")
+    grad = laid(randn(g, T, H).to(DT[types[0]]), how)
+    whole = laid(torch.full((rows, H), 7.0, device="cuda", dtype=DT[types[1]]), how)
+    want, size = X.embedding_backward(grad, ids, rows, 0.3, rows // 2), X.embedding_backward(grad, ids, rows, 0.3, rows // 2, True)
+    most = int(torch.bincount(ids).max())
+    R.reshard_embedding_backward(grad, ids, rows, scale=0.3, first_row=rows // 2, out=whole)
+    close(whole, want, (most + 2) * U * size)
+    base = randn(g, rows, H).to(DT[types[1]])
+    main = laid(base, how)
+    R.reshard_embedding_backward(grad, ids, rows, scale=0.3, first_row=rows // 2, out=main, accumulate=True)
+    close(main, want + base.to(F64), (most + 2) * U * size + U * (want + base.to(F64)).abs())
+
+
+def test_embedding_backward_when_other_tokens_change():
+    """Runs are cut from all tokens of the shard: other tokens may regroup a row's sum, whose distance stays bounded; what does not
+    change the ids changes no bit of it."""
+    g = gen(19)
+    ids = torch.randint(0, 50, (20000,), generator=g, device="cuda")
+    grad = randn(g, 20000, 128)
+    first = check_embedding_backward(grad, ids, 50)
+    mine = ids == 49
+    for change in (lambda i: torch.where(mine, i, i // 2), lambda i: torch.where(mine, i, 50), lambda i: torch.where(mine, i, i + 100)):
+        other = check_embedding_backward(grad, change(ids.clone()), 50)
+        want = X.embedding_backward(grad, ids, 50)[49]
+        size = X.embedding_backward(grad, ids, 50, magnitudes=True)[49]
+        close(other[49], want, (int(mine.sum()) + 2) * U * size)
+    assert torch.equal(first, R.reshard_embedding_backward(grad, ids, 50))
