@@ -462,8 +462,11 @@ Sort = Tuple[torch.Tensor, torch.Tensor, torch.Tensor]
 def _sorted(sort: Sort, like: torch.Tensor) -> Tuple[int, int, int, int]:
     """(address of order, its length, address of position, its length) of what reshard_dispatch gave."""
     _, order, position = sort
-    return (_dense(order, "the sort's order", torch.int32, order.shape, like), order.numel(),
-            _dense(position, "the sort's position", torch.int32, position.shape, like), position.numel())
+    device = like.get_device()
+    for t, name in ((order, "the sort's order"), (position, "the sort's position")):
+        if t.dtype is not torch.int32 or not t.is_contiguous() or t.get_device() != device:
+            _dense(t, name, torch.int32, t.shape, like)      # which says what is wrong
+    return order.data_ptr(), order.numel(), position.data_ptr(), position.numel()
 
 
 def _choices(slots: int, tokens: int) -> int:
