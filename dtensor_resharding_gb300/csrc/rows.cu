@@ -67,7 +67,8 @@ __device__ __forceinline__ uint32_t unowned(const int32_t *order, const int32_t 
 }
 
 // Rows of whole 16-byte pieces: a warp reads 2 KB of a token's row once and writes it to each of its places. Bound by the writes:
-// 8,192 x 2048 bf16 to 8 places each, 47 us, 6.4 TB/s.
+// 8,192 x 2048 bf16 to 8 places each, 47 us, 6.4 TB/s. Zeros are written row after row by a warp for 32 of them: of 16,383 tokens' 8
+// places of 4096 bf16, one in eight taken, 230 us (floor 178), 41 without the zeros.
 __global__ void __launch_bounds__(kRowThreads) reshard_permute_kernel(Permute a) {
   grid_enter();
   const int lane = threadIdx.x & 31;
@@ -146,7 +147,8 @@ __device__ __forceinline__ void move_span(const T *from, T *to, int64_t cols, in
   }
 }
 
-// Rows that start anywhere: a warp a span of a slot's row, which starts elsewhere than the token's does.
+// Rows that start anywhere: a warp a span of a slot's row, which starts elsewhere than the token's does. Bound by instructions (shuffles,
+// funnel shifts): 8,191 x 2867 bf16 to 4 places each, 53 us, floor 35.
 template <typename T>
 __global__ void __launch_bounds__(kRowThreads) reshard_permute_any_kernel(Permute a) {
   grid_enter();
@@ -299,8 +301,8 @@ __global__ void __launch_bounds__(kRowThreads, CombineShape<TY, TO>::kCtas) resh
 }
 
 // fp32 rows of whole pieces, a few places a token: a thread eight columns, without anything shared in a warp, so that more of them
-// are in flight. 4,095 x 4096 to bf16, one of eight places here, 20.9 us where warps that stay take 21.9 (after the experts' products 33.6
-// and 35.9), 1,000 x 4096 with eight places 23.6 and 26.0; with 12 of them it depends (6,000 x 1000 47.9 and 50.2, 1,000 x 1000 12.7 and
+// are in flight. 4,095 x 4096 to bf16, one of eight places here, 20.9 us where warps that stay take 21.9 (after the experts' products 34
+// and 36), 1,000 x 4096 with eight places 23.6 and 26.0; with 12 of them it depends (6,000 x 1000 47.9 and 50.2, 1,000 x 1000 12.7 and
 // 11.9), of many tokens' share with 32 it loses (26.1 and 23.0), and 16-bit rows are 5 to 25% slower so.
 constexpr int kThreadPlaces = 8;
 template <typename TO>
@@ -451,7 +453,7 @@ __global__ void __launch_bounds__(kRowThreads, kBackCtas) reshard_combine_backwa
   }
 }
 
-// Rows that start anywhere: a warp a slot (8,191 x 2867 bf16, four places each: 103 us).
+// Rows that start anywhere: a warp a slot (8,191 x 2867 bf16, four places each: 102 us).
 template <typename TG, typename TY>
 __global__ void __launch_bounds__(kRowThreads) reshard_combine_backward_any_kernel(CombineBackward a) {
   constexpr int kN = kPieceOf<TG, TY>, kU = 2;

@@ -507,8 +507,9 @@ def reshard_permute(x: torch.Tensor, sort: Sort, *, out: Optional[torch.Tensor] 
     """y [slots, cols] with y[position[t * k + j]] = x[t]: each token's row at the places of its experts.
 
     ``sort`` is what ``reshard_dispatch`` gave for these tokens' ids. Rows of no slot (from offsets[-1] on: other ranks' experts') are
-    left as they are in ``out``, which may have more or fewer rows than slots, and 0 in a new tensor. Values
-    are copied bit for bit; differentiable in ``x``."""
+    left as they are in ``out``, which may have more or fewer rows than slots, and 0 in a new tensor (all tokens * k rows are
+    written then: for a small share of the experts an ``out`` saves most of that). Values are copied bit for bit;
+    differentiable in ``x``."""
     if _forward._current_level >= 0:
         _no_tangent("reshard_permute", x)
     here = _here(x, stream)
@@ -693,7 +694,8 @@ def reshard_embedding_backward(grad: torch.Tensor, ids: torch.Tensor, rows: int,
                                stream=None) -> torch.Tensor:
     """The gradient [rows, cols] to ``reshard_embedding``'s table: scale * the sum of ``grad`` over each row's tokens.
 
-    Sums are fp32 in the order of the tokens, rounded once to ``dtype`` (``grad``'s if None). Rows without a token get 0; with
+    Sums are fp32, rounded once to ``dtype`` (``grad``'s if None): runs of a row's tokens in their order, then the runs; the same
+    ids, columns and types give the same bits (tokens of other rows can regroup a row's). Rows without a token get 0; with
     ``accumulate`` the sums are added to ``out`` instead (a main gradient of a training step), and other rows not touched."""
     if _forward._current_level >= 0:
         _no_tangent("reshard_embedding_backward", grad, out if accumulate else None)
@@ -795,7 +797,8 @@ class TensorList:
 
 
 def reshard_tensor_list(tensors: Iterable[torch.Tensor]) -> TensorList:
-    """A list of tensors for the calls below (bfloat16, float16 and float32, mixed as they come; dense in any order of dimensions)."""
+    """A list of tensors for the calls below (bfloat16, float16 and float32, mixed as they come; dense in any order of dimensions).
+    Making one looks at each tensor (10,000: some 9 ms), so lists that are used again are worth keeping."""
     return TensorList(tensors)
 
 

@@ -144,7 +144,8 @@ int reshard_permute(const void *x, int dtype, int64_t tokens, int64_t cols, int6
 /*
  * reshard_combine -- experts' rows back to their tokens: out[t] = sum over j of weights[t, j] * y[position[t * k + j]].
  * y [rows, cols] in dtype, weights [tokens, k] fp32 (NULL: 1), out [tokens, cols] in out_dtype. Slots without a place (a
- * position that is negative or beyond the rows) add nothing, whatever their weight. Summed in fp32 in the order of j and rounded once.
+ * position that is negative or beyond the rows) add nothing, whatever their weight. y may have more rows than slots. Summed in
+ * fp32 in the order of j and rounded once.
  */
 int reshard_combine(const void *y, int dtype, int64_t rows, int64_t cols, int64_t row_stride, const int32_t *position,
                     const float *weights, int64_t tokens, int k, void *out, int out_dtype, int64_t out_stride,
@@ -172,8 +173,9 @@ int reshard_embedding(const void *ids, int id_bits, int64_t tokens, const void *
 
 /*
  * reshard_embedding_backward -- the gradient to the table: grad_table[r] = scale * (sum of grad[t] over the tokens with
- * ids[t] = first_row + r), fp32 sums rounded once to table_dtype. Written whole, 0 for rows without a token; or, with
- * accumulate, added to the rows that have one, the others not touched.
+ * ids[t] = first_row + r), fp32 sums (runs of a row's tokens in their order, then the runs, which all tokens' ids cut) rounded
+ * once to table_dtype. Written whole, 0 for rows without a token; or, with accumulate, added to the rows that have one, the
+ * others not touched. Rows of no columns are nothing to do.
  * workspace: reshard_embedding_backward_workspace(tokens, cols) bytes, 256-byte aligned; 0 bytes (NULL will do) for a few tokens.
  */
 int64_t reshard_embedding_backward_workspace(int64_t tokens, int64_t cols);
