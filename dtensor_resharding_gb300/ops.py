@@ -141,6 +141,8 @@ def _output(out: Optional[torch.Tensor], rows: int, cols: int, dtype: torch.dtyp
     if out.dtype is not dtype or out.shape != (rows, cols) or out.get_device() != like.get_device():
         _bad(f"out must be {dtype} of shape {(rows, cols)} on {like.device}, not {out.dtype} of shape {tuple(out.shape)} on {out.device}")
     step = _matrix(out, "out")[2]
+    if _forward._current_level >= 0:
+        _no_tangent("what is written to out", out)
     _written(out)      # a backward pass that kept what was there is told, as by torch's own operations
     return out, step
 
@@ -835,10 +837,10 @@ def reshard_clip_grads(tensors: Tensors, limit: float, *, norm: Optional[torch.T
     any write through a pointer, autograd is not told: neither what is written nor the norm carries a gradient."""
     if not isinstance(tensors, TensorList):
         tensors = TensorList(tensors)
-    if _forward._current_level >= 0:
-        _no_tangent("reshard_clip_grads", *tensors.tensors, norm)
     if out is not None and not isinstance(out, TensorList):
         out = TensorList(out)
+    if _forward._current_level >= 0:
+        _no_tangent("reshard_clip_grads", *tensors.tensors, norm, *(() if out is None else out.tensors))
     here = _here(tensors, stream)
     if here is None:
         with _on(tensors, stream):

@@ -319,7 +319,7 @@ def test_tangents_are_refused():
     a = R.reshard_tensor_list(ts)
     with forward_ad.dual_level():
         duals = [ts[0], forward_ad.make_dual(ts[1], torch.ones_like(ts[1]))]
-        for call in (lambda: R.reshard_grad_norm(duals), lambda: R.reshard_clip_grads(duals, 1.0),
+        for call in (lambda: R.reshard_grad_norm(duals), lambda: R.reshard_clip_grads(duals, 1.0), lambda: R.reshard_clip_grads([t + 1.0 for t in ts], 1.0, out=duals),
                      lambda: R.reshard_clip_grads(ts, 1.0, norm=forward_ad.make_dual(torch.ones((), device="cuda"), torch.ones((), device="cuda")))):
             with pytest.raises(R.ReshardError, match="forward mode"):
                 call()

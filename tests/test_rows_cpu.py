@@ -263,6 +263,17 @@ def test_tangents_are_refused(name, requires_grad):
         call(torch.zeros)
 
 
+def test_a_given_output_has_no_tangent(words):
+    """What is written is not what the tangent was of."""
+    with forward_ad.dual_level():
+        out = forward_ad.make_dual(torch.zeros(4, 8), torch.ones(4, 8))
+        for call in (lambda: R.reshard_permute(torch.zeros(2, 8), _sort(), out=out), lambda: R.reshard_embedding(torch.zeros(4, dtype=torch.int64), torch.zeros(2, 8), out=out),
+                     lambda: R.reshard_combine(torch.zeros(4, 8), _sort(), k=1, out=out), lambda: R.reshard_embedding_backward(torch.zeros(3, 8), torch.zeros(3, dtype=torch.int64), 4, out=out)):
+            with pytest.raises(R.ReshardError, match="forward mode"):
+                call()
+        assert words == [] and R.reshard_permute(torch.zeros(2, 8), _sort(), out=torch.zeros(4, 8)).shape == (4, 8)
+
+
 # ------------------------------------------------------------------------------------------------ the oracle itself
 
 def test_oracle_sort_and_rows_by_hand():
